@@ -36,6 +36,9 @@ EXPORTED = [
     "moe_profile_report", "moe_status_string",
     "moe_dispatch_noalloc", "moe_dispatch_noalloc_scratch_bytes",
     "moe_dispatch_quant", "moe_grouped_ffn_q", "moe_wait_selftest",
+    "moe_add_rms_norm", "moe_gate",
+    "moe_grouped_gemm_fp8_workspace_size", "moe_grouped_gemm_fp8",
+    "moe_grouped_ffn_fp8_workspace_size", "moe_grouped_ffn_fp8",
 ]
 
 
@@ -58,6 +61,21 @@ class MoeShape(ctypes.Structure):
 FFN_PATH_AUTO, FFN_PATH_LARGE, FFN_PATH_SMALL, FFN_PATH_LARGE_PAIR = 0, 1, 2, 3
 FFN_PATHS = {"auto": FFN_PATH_AUTO, "large": FFN_PATH_LARGE, "small": FFN_PATH_SMALL,
              "large_pair": FFN_PATH_LARGE_PAIR}
+
+
+class MoeGateDesc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("num_experts", ctypes.c_int64),
+                ("topk", ctypes.c_int64), ("num_groups", ctypes.c_int64),
+                ("topk_groups", ctypes.c_int64), ("logits_stride", ctypes.c_int64),
+                ("logits_dtype", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+GATE_SCORES = {"softmax": 0, "sigmoid": 1}
+GATE_GROUP_SCORES = {"max": 0, "top2": 1}
+DTYPE_F32, DTYPE_BF16 = 0, 1
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
 
 class StageViews(ctypes.Structure):
@@ -100,6 +118,13 @@ def lib():
         "moe_dispatch_quant": [SP, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
         "moe_grouped_ffn_q": [SP, P, P, P, P, P, P, P, P, P, SZ, P],
         "moe_wait_selftest": [P, SZ, ctypes.c_uint64, P],
+        "moe_add_rms_norm": [I64, I64, P, P, P, ctypes.c_int, ctypes.c_float, P, P, P, P, P],
+        "moe_gate": [ctypes.POINTER(MoeGateDesc), P, P, P, P, P, P, P],
+        "moe_grouped_gemm_fp8_workspace_size": [I64, I64, I64, I64, ctypes.POINTER(SZ)],
+        "moe_grouped_gemm_fp8": [I64, I64, I64, I64, P, P, P, P, P, P, ctypes.c_int, ctypes.c_int,
+                                 P, SZ, P],
+        "moe_grouped_ffn_fp8_workspace_size": [SP, ctypes.POINTER(SZ)],
+        "moe_grouped_ffn_fp8": [SP, P, P, P, P, P, P, P, P, P, P, SZ, P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -427,6 +452,144 @@ def grouped_gemm_s32(expert_offsets, A, W, ws=None, C=None, stream=None, path="a
     _call("moe_grouped_gemm_s32", rows, E, N, Kd, _ptr(expert_offsets), _ptr(A), _ptr(W), _ptr(C),
           FFN_PATHS[path], _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream))
     return C, ws
+
+
+# ----------------------------------------------------------------- fp8 expert path
+
+FP8_BLOCK = 128
+
+
+def _blocks(n):
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def add_rms_norm(x, weight, residual=None, eps=1e-6, out=None, with_y=True, with_q=True,
+                 stream=None):
+    """moe_add_rms_norm: residual addition, RMS norm and block-scaled e4m3 codes.
+    Returns a dict with residual_out (bf16, when there is a residual), y (bf16)
+    and q, scales (e4m3 [T, H], fp32 [T, ceil(H/128)]).  Given `out`, a dict of
+    some of these tensors, exactly those are computed; residual_out may be the
+    residual itself and y may be x itself."""
+    T, H = x.shape
+    if weight.dtype not in _DTYPES:
+        raise TypeError(f"weight: dtype {weight.dtype}, expected float32 or bfloat16")
+    _check(x, torch.bfloat16, (T, H), "x")
+    _check(residual, torch.bfloat16, (T, H), "residual")
+    _check(weight, weight.dtype, (H,), "weight")
+    if out is None:
+        out = {}
+        if residual is not None:
+            out["residual_out"] = torch.empty_like(x)
+        if with_y:
+            out["y"] = torch.empty_like(x)
+        if with_q:
+            out["q"] = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=x.device)
+            out["scales"] = torch.empty((T, _blocks(H)), dtype=torch.float32, device=x.device)
+    else:
+        _check(out.get("residual_out"), torch.bfloat16, (T, H), "residual_out")
+        _check(out.get("y"), torch.bfloat16, (T, H), "y")
+        _check(out.get("q"), torch.float8_e4m3fn, (T, H), "q")
+        _check(out.get("scales"), torch.float32, (T, _blocks(H)), "scales")
+    _call("moe_add_rms_norm", T, H, _ptr(x), _ptr(residual), _ptr(weight), _DTYPES[weight.dtype],
+          float(eps), _ptr(out.get("residual_out")), _ptr(out.get("y")), _ptr(out.get("q")),
+          _ptr(out.get("scales")), _stream(stream))
+    return out
+
+
+def gate(logits, topk, bias=None, mask=None, score="softmax", groups=1, topk_groups=None,
+         group_score="max", renormalize=True, scale=1.0, out=None, stream=None):
+    """moe_gate: routes from router logits [T, E] (fp32 or bf16; rows may be
+    strided).  Returns dict(expert_ids, expert_scales, route_mask): the first
+    two feed dispatch and combine, route_mask is their per-route mask where a
+    token may get fewer than topk experts.  An `out` without route_mask leaves
+    it out."""
+    T, E = logits.shape
+    K = int(topk)
+    if logits.dtype not in _DTYPES:
+        raise TypeError(f"logits: dtype {logits.dtype}, expected float32 or bfloat16")
+    if not logits.is_cuda:
+        raise ValueError("logits: must be a CUDA tensor")
+    if E > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: a token's logits must be contiguous")
+    _check(bias, torch.float32, (E,), "bias")
+    _check(mask, torch.uint8, (T,), "mask")
+    if out is None:
+        dev = logits.device
+        out = dict(expert_ids=torch.empty((T, K), dtype=torch.int32, device=dev),
+                   expert_scales=torch.empty((T, K), dtype=torch.float32, device=dev),
+                   route_mask=torch.empty((T, K), dtype=torch.uint8, device=dev))
+    else:
+        _check(out["expert_ids"], torch.int32, (T, K), "expert_ids")
+        _check(out["expert_scales"], torch.float32, (T, K), "expert_scales")
+        _check(out.get("route_mask"), torch.uint8, (T, K), "route_mask")
+    groups = int(groups)
+    desc = MoeGateDesc(T, E, K, groups, groups if topk_groups is None else int(topk_groups),
+                       logits.stride(0) if T > 1 else E, _DTYPES[logits.dtype],
+                       GATE_SCORES[score], GATE_GROUP_SCORES[group_score],
+                       int(bool(renormalize)), float(scale), 0)
+    _call("moe_gate", ctypes.byref(desc), _ptr(logits), _ptr(bias), _ptr(mask),
+          _ptr(out["expert_ids"]), _ptr(out["expert_scales"]), _ptr(out.get("route_mask")),
+          _stream(stream))
+    return out
+
+
+def grouped_gemm_fp8(expert_offsets, a, a_scales, w, w_scales, ws=None, out=None,
+                     out_dtype=torch.bfloat16, stream=None, path="auto"):
+    """moe_grouped_gemm_fp8: rows of expert e times w[e]^T on block-scaled e4m3
+    operands.  Returns (out [rows, N], workspace); `out`'s dtype (or out_dtype)
+    is bfloat16 or float32."""
+    rows, Kd = a.shape
+    E, N, _ = w.shape
+    _check(a, torch.float8_e4m3fn, (rows, Kd), "a")
+    _check(a_scales, torch.float32, (rows, _blocks(Kd)), "a_scales")
+    _check(w, torch.float8_e4m3fn, (E, N, Kd), "w")
+    _check(w_scales, torch.float32, (E, _blocks(N), _blocks(Kd)), "w_scales")
+    _check(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=a.device)
+    if out.dtype not in _DTYPES:
+        raise TypeError(f"out: dtype {out.dtype}, expected float32 or bfloat16")
+    _check(out, out.dtype, (rows, N), "out")
+    if ws is None:
+        n = ctypes.c_size_t()
+        _call("moe_grouped_gemm_fp8_workspace_size", rows, E, N, Kd, ctypes.byref(n))
+        _, ws = _alloc_ws(n.value, a.device)
+    _call("moe_grouped_gemm_fp8", rows, E, N, Kd, _ptr(expert_offsets), _ptr(a), _ptr(a_scales),
+          _ptr(w), _ptr(w_scales), _ptr(out), _DTYPES[out.dtype], FFN_PATHS[path], _ptr(ws),
+          ctypes.c_size_t(ws.numel()), _stream(stream))
+    return out, ws
+
+
+def grouped_ffn_fp8_workspace_size(shape: MoeShape) -> int:
+    n = ctypes.c_size_t()
+    _call("moe_grouped_ffn_fp8_workspace_size", ctypes.byref(shape), ctypes.byref(n))
+    return n.value
+
+
+def grouped_ffn_fp8(shape: MoeShape, x, x_scales, expert_offsets, w1, w1_scales, w2, w2_scales,
+                    assist=None, ws=None, y=None, stream=None):
+    """moe_grouped_ffn_fp8: the experts' FFN on block-scaled e4m3.  With the
+    dispatch's `assist`, x [T, H] and x_scales are the tokens; without it,
+    expert-major rows [T*K, H].  Returns (y bf16 [T*K, H], workspace)."""
+    T, K, H, E, N = shape.num_tokens, shape.topk, shape.hidden, shape.num_experts, shape.ffn
+    R = T * K if assist is None else T
+    _check(x, torch.float8_e4m3fn, (R, H), "x")
+    _check(x_scales, torch.float32, (R, _blocks(H)), "x_scales")
+    _check(assist, torch.int32, (T * K, 3), "assist")
+    _check(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    _check(w1, torch.float8_e4m3fn, (E, N, H), "w1")
+    _check(w1_scales, torch.float32, (E, N // FP8_BLOCK, _blocks(H)), "w1_scales")
+    _check(w2, torch.float8_e4m3fn, (E, H, N // 2), "w2")
+    _check(w2_scales, torch.float32, (E, _blocks(H), N // 2 // FP8_BLOCK), "w2_scales")
+    if y is None:
+        y = torch.empty((T * K, H), dtype=torch.bfloat16, device=x.device)
+    _check(y, torch.bfloat16, (T * K, H), "y")
+    if ws is None:
+        _, ws = _alloc_ws(grouped_ffn_fp8_workspace_size(shape), x.device)
+    _call("moe_grouped_ffn_fp8", ctypes.byref(shape), _ptr(x), _ptr(x_scales), _ptr(assist),
+          _ptr(expert_offsets), _ptr(w1), _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(y),
+          _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream))
+    return y, ws
 
 
 def wait_selftest(limit_ns, ws=None, stream=None):

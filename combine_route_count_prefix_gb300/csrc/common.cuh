@@ -320,4 +320,31 @@ moe_status launch_grouped_gemm(Epi epi, const GemmArgs &a, cudaStream_t stream,
 // SwiGLU epilogue).
 moe_status launch_grouped_gemm_small(Epi epi, const GemmArgs &a, cudaStream_t stream);
 
+// ---------------------------------------------------------------- fp8 expert path
+moe_status launch_gate(const moe_gate_desc &d, const void *logits, const float *bias,
+                       const uint8_t *mask, int32_t *ids, float *scales, uint8_t *route_mask,
+                       cudaStream_t stream);
+moe_status launch_add_rms_norm(int64_t T, int64_t H, const void *x, const void *residual,
+                               const void *weight, bool w_bf16, float eps, void *residual_out,
+                               void *y, void *q, float *scales, cudaStream_t stream);
+
+// Grouped product of block-scaled e4m3 operands.
+struct Fp8GemmArgs {
+    const void *a;             // e4m3 [cap_rows, Kd]
+    const float *a_scales;     // [cap_rows, ceil(Kd/128)]
+    const void *w;             // e4m3 [E, N, Kd]
+    const float *w_scales;     // [E, ceil(N/128), ceil(Kd/128)]
+    const int32_t *offsets;    // [E+1]; rows >= cap_rows are never stored
+    int64_t cap_rows, E, N, Kd;
+    void *c;                   // [cap_rows, N], bf16 or fp32
+    bool out_bf16;
+};
+moe_status launch_gemm_fp8(const Fp8GemmArgs &a, cudaStream_t stream);
+moe_status launch_swiglu_quant(const float *h, const int32_t *offsets, int64_t E, void *q, float *s,
+                               int64_t cap_rows, int64_t Nh, cudaStream_t stream);
+// Rows and scales of the tokens named by the dispatch's triplets.
+moe_status launch_gather_fp8(const void *x, const float *xs, const int32_t *assist,
+                             const int32_t *offsets, int64_t E, int64_t T, int64_t M, void *rows,
+                             float *rs, int64_t cap_rows, int64_t H, cudaStream_t stream);
+
 }  // namespace moe

@@ -1,0 +1,28 @@
+// fp8.cuh -- block-scaled e4m3: the quantisation of 128 columns shared by the
+// norm and the fp8 FFN, and the conversions.
+#pragma once
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+namespace moe {
+
+constexpr int kFp8Block = 128;               // columns per scale
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxFloor = 7.8886090522101181e-31f;   // 2^-100: 448 / it is finite
+
+// Two floats -> two e4m3 codes (lo in the low byte), round to nearest even,
+// saturating; NaN -> NaN.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+// Scale and its inverse for a block whose largest magnitude is amax.
+__device__ __forceinline__ void block_scale(float amax, float &s, float &inv) {
+    const float a = fmaxf(amax, kAmaxFloor);
+    s = __fdiv_rn(a, kE4m3Max);
+    inv = __fdiv_rn(kE4m3Max, a);
+}
+
+}  // namespace moe

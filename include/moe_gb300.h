@@ -351,6 +351,134 @@ moe_status moe_dispatch_noalloc(const moe_shape *shape, const void *x, const int
                                 int32_t *ep_recv_counts, int32_t *route_row,
                                 cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The fp8 expert path: what a block-scaled 8-bit checkpoint needs around the
+ * dispatch and the combine above.  moe_add_rms_norm makes the layer's input
+ * (and its e4m3 codes), moe_gate the routes, moe_grouped_ffn_fp8 the experts'
+ * outputs that moe_combine adds up; moe_grouped_gemm_fp8 is the product alone.
+ * The pages have no counterpart for it: it serves models whose experts are
+ * stored in 8-bit floating point.
+ *
+ * Block-scaled e4m3.  A tensor of codes c (FP8 E4M3, finite values up to 448)
+ * with fp32 scales s stands for c * s.  Activations have one scale per row and
+ * 128 consecutive columns, s [rows, ceil(cols / 128)]; weights [E, N, Kd] one
+ * per 128 x 128 block, s [E, ceil(N / 128), ceil(Kd / 128)].  The last block
+ * of a dimension may be short.
+ * Quantisation of a row v (fp32), per block of 128 columns:
+ *   a = max(max|v|, 2^-100);  s = a / 448;  c = e4m3(v * (448 / a))
+ * each operation rounded to nearest even in fp32, the last one to e4m3; a NaN
+ * becomes the NaN code and does not enter the maximum.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the calls below that take more than one. */
+#define MOE_DTYPE_F32  0
+#define MOE_DTYPE_BF16 1
+
+/* Residual addition and root-mean-square norm.  Per token, in fp32:
+ *   h = x + residual (h = x when residual is NULL)
+ *   v = h * rsqrt(sum(h^2) / hidden + eps) * weight
+ * residual_out = bf16(h); y = bf16(v); q, scales = v quantised as above.  All
+ * are computed from the fp32 values, so each output is rounded once.
+ * x, residual     bf16 [T, H]; H % 8 == 0, 8 <= H <= 16384
+ * weight          [H], fp32 or bf16 (weight_dtype)
+ * residual_out    bf16 [T, H] or NULL; may be the residual buffer itself, else
+ *                 overlaps no input.  Needs a residual.
+ * y               bf16 [T, H] or NULL (may be x itself)
+ * q, scales       e4m3 [T, H] and fp32 [T, ceil(H / 128)], or both NULL
+ * At least one of y and q is given.  eps >= 1e-30 (so that squares that fp32
+ * cannot hold are nothing beside it) and finite. */
+moe_status moe_add_rms_norm(int64_t num_tokens, int64_t hidden, const void *x,
+                            const void *residual, const void *weight, int weight_dtype, float eps,
+                            void *residual_out, void *y, void *q, float *scales,
+                            cudaStream_t stream);
+
+/* Router.  Scores of E experts from a token's logits, choice of K of them, and
+ * their weights; what moe_dispatch and moe_combine take as expert_ids and
+ * expert_scales.  Per token, in fp32:
+ *   open[i]  = the token is active and logit[i] > -1e30.  A closed expert (a
+ *              logit of -inf, NaN, or the lowest value of bf16 or fp32) is
+ *              never chosen.  +inf counts as the largest finite number.
+ *   score[i] = 1 / (1 + exp(-logit[i]))                          (SIGMOID)
+ *            = exp(logit[i] - max) / sum over the open experts   (SOFTMAX)
+ *   key[i]   = score[i] + bias[i] (score[i] when bias is NULL)
+ *   With num_groups > 1 the experts form groups of E / num_groups neighbours;
+ *   a group's value is its largest key (GROUP_MAX) or the sum of its two
+ *   largest keys (GROUP_TOP2; its only key where one expert is open), and the
+ *   topk_groups groups of the largest values take part.
+ *   The K experts of the largest keys are chosen, in descending order.  Equal
+ *   keys and equal groups: the lower index first.
+ *   weight   = score / (sum of the chosen scores + 1e-20) if renormalize, else
+ *              score; times scale.  (The bias moves the choice, not the weight.)
+ * Where fewer than K experts are open in the groups that take part, the routes
+ * left over get expert id -1, weight 0 and route mask 0. */
+#define MOE_GATE_SOFTMAX 0
+#define MOE_GATE_SIGMOID 1
+#define MOE_GATE_GROUP_MAX  0
+#define MOE_GATE_GROUP_TOP2 1
+typedef struct moe_gate_desc {
+    int64_t num_tokens;     /* T >= 0 */
+    int64_t num_experts;    /* E: 1..1024; counts zero and copy experts too */
+    int64_t topk;           /* K: 1..16, at most topk_groups * (E / num_groups) */
+    int64_t num_groups;     /* >= 1, divides E */
+    int64_t topk_groups;    /* 1..num_groups */
+    int64_t logits_stride;  /* elements from one token's logits to the next, >= E */
+    int32_t logits_dtype;   /* MOE_DTYPE_* */
+    int32_t score;          /* MOE_GATE_SOFTMAX or MOE_GATE_SIGMOID */
+    int32_t group_score;    /* MOE_GATE_GROUP_MAX or MOE_GATE_GROUP_TOP2 */
+    int32_t renormalize;    /* 0 or 1 */
+    float scale;
+    int32_t reserved;       /* must be 0 */
+} moe_gate_desc;
+/* logits          [T, E], rows logits_stride apart (element-aligned)
+ * bias            fp32 [E] or NULL
+ * x_active_mask   uint8 [T] or NULL; the logits of an inactive token are not
+ *                 looked at, all its routes are left over
+ * expert_ids      int32 [T, K]
+ * expert_scales   fp32 [T, K]
+ * route_mask      uint8 [T, K] or NULL: 1 for a chosen expert, 0 for a route
+ *                 left over; the per-route mask (mask_kind 2) of moe_dispatch */
+moe_status moe_gate(const moe_gate_desc *desc, const void *logits, const float *bias,
+                    const uint8_t *x_active_mask, int32_t *expert_ids, float *expert_scales,
+                    uint8_t *route_mask, cudaStream_t stream);
+
+/* Grouped product of block-scaled e4m3 operands:
+ *   C[r, n] = sum_b a_scales[r, b] * w_scales[e, n / 128, b]
+ *                   * sum_{k in block b} A[r, k] * W[e, n, k]
+ * for the rows r of expert e, [expert_offsets[e], expert_offsets[e+1]); E = 1
+ * is a dense product.  Products are exact and summed in fp32.
+ * A e4m3 [rows, Kd]; a_scales fp32 [rows, ceil(Kd / 128)]; W e4m3 [E, N, Kd];
+ * w_scales fp32 [E, ceil(N / 128), ceil(Kd / 128)]; C [rows, N] in out_dtype;
+ * rows >= offsets[E] untouched.  N % 8 == 0, Kd % 16 == 0, N <= 1048576,
+ * Kd <= 131072.  path: MOE_FFN_PATH_* (which kernels; AUTO by rows per expert). */
+moe_status moe_grouped_gemm_fp8_workspace_size(int64_t rows, int64_t E, int64_t N, int64_t Kd,
+                                               size_t *bytes);
+moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
+                                const int32_t *expert_offsets, const void *A,
+                                const float *a_scales, const void *W, const float *w_scales,
+                                void *C, int out_dtype, int path, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+
+/* The experts' FFN on block-scaled e4m3 tokens and weights.  For a row of
+ * expert e, with moe_grouped_gemm_fp8's products:
+ *   h = x . W1[e]^T;  g = silu(h[:N/2]) * h[N/2:]     fp32
+ *   q2, s2 = g quantised per 128 columns;  y = bf16(q2 . W2[e]^T)
+ * x, x_scales     with assist: the tokens, e4m3 [T, H] and fp32
+ *                 [T, ceil(H / 128)]; row r is token assist[r][0] * (T / P) +
+ *                 assist[r][1].  With assist NULL: the rows themselves,
+ *                 [T*K, H] and [T*K, ceil(H / 128)], expert-major.
+ * assist          int32 [T*K, 3] from moe_dispatch (expand_x may be NULL there), or NULL
+ * expert_offsets  int32 [E+1] from moe_dispatch
+ * w1 e4m3 [E, N, H], w1_scales fp32 [E, N/128, ceil(H/128)]
+ * w2 e4m3 [E, H, N/2], w2_scales fp32 [E, ceil(H/128), N/256]
+ * y               bf16 [T*K, H] (rows [0, R) written)
+ * The weights are read as they are stored; shape->ffn_path picks the kernels. */
+moe_status moe_grouped_ffn_fp8_workspace_size(const moe_shape *shape, size_t *bytes);
+moe_status moe_grouped_ffn_fp8(const moe_shape *shape, const void *x, const float *x_scales,
+                               const int32_t *assist, const int32_t *expert_offsets,
+                               const void *w1, const float *w1_scales, const void *w2,
+                               const float *w2_scales, void *y, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+
 /* Reads the device status word of `workspace` (synchronising `stream`),
  * stores it in *status_host (0 = no device-side error, else MOE_DEV_* bits)
  * and clears it. */
