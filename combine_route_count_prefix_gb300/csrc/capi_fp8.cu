@@ -19,7 +19,6 @@ struct Fp8Layout {
     size_t sched = 0;    // int32 [E+1]
     size_t rows = 0;     // e4m3 [cap, H] gathered tokens
     size_t row_s = 0;    // fp32 [cap, ceil(H/128)]
-    size_t h = 0;        // fp32 [cap, N]
     size_t q2 = 0;       // e4m3 [cap, N/2]
     size_t s2 = 0;       // fp32 [cap, N/256]
     size_t total = 0;
@@ -51,11 +50,19 @@ Fp8Layout ffn_layout(const moe_shape &s) {
     L.sched = c.take((size_t)(s.num_experts + 1) * sizeof(int32_t));
     L.rows = c.take(cap * s.hidden);
     L.row_s = c.take(cap * ((s.hidden + 127) / 128) * sizeof(float));
-    L.h = c.take(cap * s.ffn * sizeof(float));
     L.q2 = c.take(cap * (s.ffn / 2));
     L.s2 = c.take(cap * (s.ffn / 256) * sizeof(float));
     L.total = c.off;
     return L;
+}
+
+// Rows per expert up to which reading the weights bounds the time.
+constexpr int64_t kSmallRowsPerExpert = 64;
+
+moe_status run_gemm(int path, const Fp8GemmArgs &a, cudaStream_t stream) {
+    const bool small = path == MOE_FFN_PATH_SMALL ||
+                       (path == MOE_FFN_PATH_AUTO && a.cap_rows <= kSmallRowsPerExpert * a.E);
+    return small ? launch_gemm_fp8_small(a, stream) : launch_gemm_fp8_large(a, stream);
 }
 
 }  // namespace
@@ -158,7 +165,8 @@ moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
     g.Kd = Kd;
     g.c = C;
     g.out_bf16 = out_dtype == MOE_DTYPE_BF16;
-    return launch_gemm_fp8(g, stream);
+    g.status = at<int32_t>(workspace, L.status);
+    return run_gemm(path, g, stream);
 }
 
 moe_status moe_grouped_ffn_fp8_workspace_size(const moe_shape *shape, size_t *bytes) {
@@ -208,12 +216,10 @@ moe_status moe_grouped_ffn_fp8(const moe_shape *shape, const void *x, const floa
     g1.E = E;
     g1.N = s.ffn;
     g1.Kd = H;
-    g1.c = at<void>(workspace, L.h);
-    g1.out_bf16 = false;
-    MOE_TRY(launch_gemm_fp8(g1, stream));
-    MOE_TRY(launch_swiglu_quant(at<float>(workspace, L.h), expert_offsets, E,
-                                at<void>(workspace, L.q2), at<float>(workspace, L.s2), cap, Nh,
-                                stream));
+    g1.q2 = at<void>(workspace, L.q2);
+    g1.s2 = at<float>(workspace, L.s2);
+    g1.status = at<int32_t>(workspace, L.status);
+    MOE_TRY(run_gemm(s.ffn_path, g1, stream));
     Fp8GemmArgs g2{};
     g2.a = at<void>(workspace, L.q2);
     g2.a_scales = at<float>(workspace, L.s2);
@@ -226,7 +232,8 @@ moe_status moe_grouped_ffn_fp8(const moe_shape *shape, const void *x, const floa
     g2.Kd = Nh;
     g2.c = y;
     g2.out_bf16 = true;
-    return launch_gemm_fp8(g2, stream);
+    g2.status = at<int32_t>(workspace, L.status);
+    return run_gemm(s.ffn_path, g2, stream);
 }
 
 }  // extern "C"

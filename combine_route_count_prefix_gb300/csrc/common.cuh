@@ -336,12 +336,16 @@ struct Fp8GemmArgs {
     const float *w_scales;     // [E, ceil(N/128), ceil(Kd/128)]
     const int32_t *offsets;    // [E+1]; rows >= cap_rows are never stored
     int64_t cap_rows, E, N, Kd;
-    void *c;                   // [cap_rows, N], bf16 or fp32
+    void *c;                   // [cap_rows, N], bf16 or fp32; or, when q2 is set,
     bool out_bf16;
+    void *q2;                  // silu(C[:, :N/2]) * C[:, N/2:], quantised: e4m3 [cap_rows, N/2]
+    float *s2;                 // and its scales [cap_rows, N/256] (N % 256 == 0)
+    int32_t *status;
 };
-moe_status launch_gemm_fp8(const Fp8GemmArgs &a, cudaStream_t stream);
-moe_status launch_swiglu_quant(const float *h, const int32_t *offsets, int64_t E, void *q, float *s,
-                               int64_t cap_rows, int64_t Nh, cudaStream_t stream);
+// For many rows per expert (256-row tiles on pairs of SMs) and for few (the
+// weights as the MMA's M side).
+moe_status launch_gemm_fp8_large(const Fp8GemmArgs &a, cudaStream_t stream);
+moe_status launch_gemm_fp8_small(const Fp8GemmArgs &a, cudaStream_t stream);
 // Rows and scales of the tokens named by the dispatch's triplets.
 moe_status launch_gather_fp8(const void *x, const float *xs, const int32_t *assist,
                              const int32_t *offsets, int64_t E, int64_t T, int64_t M, void *rows,
