@@ -10,16 +10,26 @@
 // block's scale and add to fp32 sums in registers, while the tensor cores work
 // on the next block in the other accumulator.
 //
-// Kernel shape (a cluster of two CTAs per 256-row x 256-channel tile, as many
-// clusters as fit, 320 threads):
-//   warp 0      TMA producer: the CTA's 128 rows and its 128 of the 256
-//               channels, 128 bytes of K each (16 + 16 KB), six-stage ring;
-//               both CTAs' loads complete on CTA 0's barrier
-//   warp 1      TMEM (two 256-column accumulators) and, in CTA 0, the MMA
-//               issuer: 4 x tcgen05.mma cta_group::2 M=256 N=256 K=32 a block
-//   warps 2..9  epilogue: TMEM lane quadrant q (32 rows) x column half
-// The pair's tile halves the weight bytes each SM stages, which a one-SM tile
-// of the same height would read twice.
+// Kernel shape (a cluster of two CTAs per 256-row x 256-channel tile, 128 rows
+// each, as many clusters as fit, 12 warps):
+//   warp 0      TMA producer, four-stage ring of 128 bytes of K: the CTA's 128
+//               rows (16 KB), and 128 of the tile's 256 channels (16 KB) that
+//               land in both CTAs, so that a channel is read once per pair
+//   warps 1, 3  MMA issuers: 4 x tcgen05.mma M=128 N=256 K=32 a block, even
+//               blocks into one 256-column accumulator and odd ones into the
+//               other (one thread spends about 450 cycles on the issue of a
+//               block, which the tensor cores finish in 512); warp 1 owns TMEM
+//   warp 2      scales: four blocks at a time, the products of the CTA's row
+//               scales and the two channel blocks' scales, for the epilogue in
+//               a shared-memory ring (one 16-byte load a row and four blocks;
+//               loads by the epilogue itself, a row a lane, stalled it)
+//   warps 4..11 epilogue: TMEM lane quadrant q (32 rows) x 128 columns, 128
+//               sums a thread
+// Every CTA multiplies its own rows: with one MMA over both (cta_group::2) the
+// release of an accumulator has to travel between the SMs, about 1000 cycles
+// from the end of a block's MMAs to the start of those that reuse its
+// accumulator, and with two accumulators that, not the tensor cores, set the
+// pace (630 ns a block against 270 for the MMAs).
 // SwiGLU form: CTA 0 stages 128 SiLU-half channels and CTA 1 the multiplier
 // channels of the same numbers, so a tile holds 128 complete channels of g and
 // the epilogue quantises them as one block; h never leaves the SM.
@@ -38,20 +48,28 @@ using namespace tc;
 constexpr int BM = 128;                 // rows per CTA (256 per pair)
 constexpr int BN = 256;                 // channels per tile
 constexpr int BK = 128;                 // bytes of K per block: one scale
-constexpr int STAGES = 6;
+constexpr int STAGES = 4;
 constexpr int A_BYTES = BM * BK;
-constexpr int B_BYTES = (BN / 2) * BK;
+constexpr int B_BYTES = BN * BK;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr size_t RING_BYTES = (size_t)STAGES * STAGE_BYTES;
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int CG = EPI_WARPS / 4;        // column groups
+constexpr int CPT = BN / CG;             // sums per epilogue thread
+constexpr int HC = CPT / 2;
+constexpr int EPI_WARP0 = 4;
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 constexpr uint32_t TMEM_COLS = 512;
 constexpr size_t kBarrierBytes = 512;
-constexpr size_t kAmaxBytes = 2 * 2 * BM * sizeof(float);
-constexpr size_t SMEM_BYTES =
-    RING_BYTES + 1024 + kBarrierBytes + kAmaxBytes + 2 * (kMaxExperts + 1) * sizeof(int32_t);
+constexpr size_t kAmaxBytes = 2 * CG * BM * sizeof(float);
+constexpr int SB = 4;                   // blocks of K per batch of scales
+constexpr int SC_STAGES = 3;
+constexpr int SC_FLOATS = SB * 2 * BM;  // [block][channel block][row]
+constexpr size_t kScaleBytes = SC_STAGES * SC_FLOATS * sizeof(float);
+constexpr size_t SMEM_BYTES = RING_BYTES + 1024 + kBarrierBytes + kAmaxBytes + kScaleBytes +
+                              2 * (kMaxExperts + 1) * sizeof(int32_t);
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-static_assert((2 * STAGES + 9) * 8 + 16 <= (int)kBarrierBytes, "barriers");
+static_assert((2 * STAGES + 9 + 2 * SC_STAGES) * 8 + 16 <= (int)kBarrierBytes, "barriers");
 
 enum { EPI_F32 = 0, EPI_BF16 = 1, EPI_SWIGLU = 2 };
 
@@ -69,6 +87,8 @@ struct LargeDev {
     uint8_t *q2;         // SwiGLU: [cap_rows, N/2]
     float *s2;           //         [cap_rows, N/256]
     int32_t *status;
+    int c_vec32;         // rows of C start on 32-byte boundaries
+    int vec_scales;      // rows of a_scales can be read 16 bytes at a time
 };
 
 // The pair's tile: expert, this CTA's first row, its rows there (may be <= 0
@@ -96,9 +116,10 @@ __device__ __forceinline__ Tile decode(int64_t tile, const LargeDev &p, const in
     return t;
 }
 
-// acc.xy += s.xy * d.xy, each lane one fp32 fused multiply-add.
+// acc += s * d on both numbers, each one an fp32 fused multiply-add.  Volatile,
+// to stay behind the wait that makes the loaded d valid.
 __device__ __forceinline__ void fma2(float2 &acc, float s, uint32_t d0, uint32_t d1) {
-    asm("{\n\t.reg .b64 a, b, c;\n\t"
+    asm volatile("{\n\t.reg .b64 a, b, c;\n\t"
         "mov.b64 a, {%2, %3};\n\t"
         "mov.b64 b, {%4, %4};\n\t"
         "mov.b64 c, {%0, %1};\n\t"
@@ -113,47 +134,59 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Columns of accumulator half `hf` that the epilogue warp's sums 64 j .. 64 j + 63
-// (j = 0, 1) come from: neighbours, or a SiLU quarter and its multipliers.
+// One 32-byte store to a 32-byte aligned global address: a whole sector.
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// First accumulator column of the epilogue warp's sums HC j .. HC j + HC - 1 (j =
+// 0, 1) in column group cg: neighbours, or SiLU channels and their multipliers.
 template <int EPI>
-__device__ __forceinline__ int half_col(int hf, int j) {
-    return EPI == EPI_SWIGLU ? 128 * j + 64 * hf : 128 * hf + 64 * j;
+__device__ __forceinline__ int group_col(int cg, int j) {
+    return EPI == EPI_SWIGLU ? 128 * j + HC * cg : CPT * cg + HC * j;
 }
 
 template <int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
-k_gemm_fp8_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 LargeDev p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING_BYTES);   // used in CTA 0
+    // aligned by its declaration, so that every address in it is a constant
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING_BYTES);
     uint64_t *empty = full + STAGES;
     uint64_t *acc_full = empty + STAGES;
-    uint64_t *acc_empty = acc_full + 2;                                 // used in CTA 0
+    uint64_t *acc_empty = acc_full + 2;
     uint64_t *drain = acc_empty + 2;
     uint64_t *amax_bar = drain + 1;                                     // [4], one per quadrant
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(amax_bar + 4);
+    uint64_t *sc_full = amax_bar + 4;
+    uint64_t *sc_empty = sc_full + SC_STAGES;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sc_empty + SC_STAGES);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    float *s_amax = reinterpret_cast<float *>(smem + RING_BYTES + kBarrierBytes);   // [2][2][BM]
-    int32_t *s_off = reinterpret_cast<int32_t *>(smem + RING_BYTES + kBarrierBytes + kAmaxBytes);
+    float *s_amax = reinterpret_cast<float *>(smem + RING_BYTES + kBarrierBytes);   // [2][CG][BM]
+    float *s_scale = s_amax + kAmaxBytes / sizeof(float);
+    int32_t *s_off = reinterpret_cast<int32_t *>(s_scale + kScaleBytes / sizeof(float));
     int32_t *s_blk = s_off + (kMaxExperts + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const bool leader = rank == 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1);        // CTA 0's producer arms it with both halves' bytes
-            mbar_init(&empty[s], 1);       // one commit per stage use
+            mbar_init(&full[s], 1);        // armed with the rows and both CTAs' channels
+            mbar_init(&empty[s], 2);       // both CTAs' MMAs have read it
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 2 * EPI_WARPS);   // both CTAs' epilogue warps
+            mbar_init(&acc_empty[b], EPI_WARPS);
         }
-        mbar_init(drain, 1);
-        for (int q = 0; q < 4; ++q) mbar_init(&amax_bar[q], 2);   // the quadrant's two warps
+        mbar_init(drain, 2);               // both issuers
+        for (int s = 0; s < SC_STAGES; ++s) {
+            mbar_init(&sc_full[s], 1);
+            mbar_init(&sc_empty[s], EPI_WARPS);
+        }
+        for (int q = 0; q < 4; ++q) mbar_init(&amax_bar[q], CG);   // the quadrant's warps
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -182,178 +215,235 @@ k_gemm_fp8_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         if (lane == 0) s_blk[p.E] = carry;
     }
     if (warp == 1) {
-        tmem_alloc_pair(tmem_slot, TMEM_COLS);
-        tmem_relinquish_pair();
+        tmem_alloc(tmem_slot, TMEM_COLS);
+        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // both CTAs' barriers and TMEM exist before any cross-CTA use
+    cluster_sync();   // both CTAs' barriers exist before any copy or commit reaches them
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int64_t total_tiles = (int64_t)s_blk[p.E] * p.n_blocks;
-    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;   // cluster index and count
+    // the cluster's tiles: its index, and every cluster count after it
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int my_tiles = first < total_tiles ? (int)((total_tiles - first + step - 1) / step) : 0;
 
-    if (warp == 0) {
+    if (warp < EPI_WARP0) {
+      if (warp == 0) {
         if (lane == 0) {
-            // ------------------------------------------------ TMA producer (both CTAs)
-            const uint32_t full0 = cluster_addr(full, 0);   // CTA 0's full[0]
+            // ------------------------------------------------ TMA producer
             int stage = 0;
             uint32_t phase = 0;
-            int armed_phase[STAGES];
-#pragma unroll
-            for (int s = 0; s < STAGES; ++s) armed_phase[s] = -1;
+            int64_t armed = 0;   // stage uses
             bool ok = true;
-            for (int64_t tile = first; ok && tile < total_tiles; tile += step) {
-                const Tile t = decode(tile, p, s_blk, s_off, (int)rank);
+            for (int i = 0; ok && i < my_tiles; ++i) {
+                const Tile t = decode(first + i * step, p, s_blk, s_off, (int)rank);
                 const int ch0 = EPI == EPI_SWIGLU ? (int)rank * (p.N / 2) + t.nb * 128
                                                   : t.nb * BN + (int)rank * (BN / 2);
                 for (int kb = 0; kb < p.num_kb; ++kb) {
-                    // freed by CTA 0's commit once the MMAs have read both halves
-                    if (!wait_bounded(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                    // free once both CTAs' MMAs have read what was there: the
+                    // channels are written to both
+                    if (!wait_bounded_inline(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     uint8_t *sa = smem + (size_t)stage * STAGE_BYTES;
-                    if (leader) {
-                        mbar_arrive_expect_tx(&full[stage], 2 * STAGE_BYTES);
-                        armed_phase[stage] = (int)phase;
-                    }
+                    mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+                    ++armed;
                     // rows past this CTA's half (or past the buffer) only reach
                     // accumulator rows that are never stored; bytes past K are 0
-                    const uint32_t fb = full0 + (uint32_t)(stage * sizeof(uint64_t));
-                    tma_load_2d_pair(sa, &tmA, fb, kb * BK, t.row0);
-                    tma_load_3d_pair(sa + A_BYTES, &tmB, fb, kb * BK, ch0, t.e);
+                    tma_load_2d(sa, &tmA, &full[stage], kb * BK, t.row0);
+                    tma_load_3d_multicast(sa + A_BYTES + rank * (B_BYTES / 2), &tmB, &full[stage],
+                                          kb * BK, ch0, t.e, 0x3);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
-            if (leader) {
-                // every armed stage must have landed (both CTAs' halves) before exit
-                for (int s = 0; s < STAGES; ++s)
-                    if (armed_phase[s] >= 0)
-                        wait_bounded(&full[s], (uint32_t)armed_phase[s], abort_flag, p.status, false);
-            } else if (!ok) {
-                // the peer's loads complete on CTA 0's barriers; after a give-up,
-                // leave the copies still in flight time to land before exit
+            // every armed stage must have landed (the peer's half too) before exit
+            for (int64_t u = armed > STAGES ? armed - STAGES : 0; u < armed; ++u)
+                wait_bounded_inline(&full[u % STAGES], (uint32_t)(u / STAGES) & 1u, abort_flag, p.status, false);
+            // and the peer's releases of them, which arrive on this CTA's barriers
+            for (int64_t u = armed > STAGES ? armed - STAGES : 0; ok && u < armed; ++u)
+                ok = wait_bounded_inline(&empty[u % STAGES], (uint32_t)(u / STAGES) & 1u, abort_flag, p.status);
+            if (!ok) {
+                // after a give-up, leave the copies still in flight to the peer
+                // time to land before either CTA exits
                 const uint64_t t0 = globaltimer();
                 while (globaltimer() - t0 < 100000ull) __nanosleep(2000);
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0 && leader) {
-            // ------------------------------------------------ MMA issuer (CTA 0)
-            constexpr uint32_t idesc = idesc_e4m3(2 * BM, BN);
-            int stage = 0;
-            uint32_t phase = 0;
-            int accb = 0;
-            uint32_t acc_phase = 0;
-            bool ok = true;
-            for (int64_t tile = first; ok && tile < total_tiles; tile += step) {
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!wait_bounded(&acc_empty[accb], acc_phase ^ 1u, abort_flag, p.status) ||
-                        !wait_bounded(&full[stage], phase, abort_flag, p.status)) {
+      } else if (warp == 2) {
+        // ---------------------------------------------------- scales
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int i = 0; ok && i < my_tiles; ++i) {
+            const Tile t = decode(first + i * step, p, s_blk, s_off, (int)rank);
+            // lane's rows lane + 32 u, clamped to rows that exist
+            const int64_t row0 = min((int64_t)t.row0, p.cap_rows - 1);
+            const int last = (int)min((int64_t)max(t.rows, 1), p.cap_rows - row0) - 1;
+            const float *sa = p.a_scales + row0 * p.num_kb;
+            int at[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) at[u] = min(lane + 32 * u, last) * p.num_kb;
+            const int wb0 = EPI == EPI_SWIGLU ? t.nb : 2 * t.nb;
+            const int wb1 = EPI == EPI_SWIGLU ? t.nb + p.w_blocks / 2 : min(2 * t.nb + 1, p.w_blocks - 1);
+            const float *sw0 = p.w_scales + ((int64_t)t.e * p.w_blocks + wb0) * p.num_kb;
+            const float *sw1 = p.w_scales + ((int64_t)t.e * p.w_blocks + wb1) * p.num_kb;
+            for (int kb = 0; kb < p.num_kb; kb += SB) {
+                float v[4][SB], w0[SB], w1[SB];
+                if (p.vec_scales) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float4 x = __ldg(reinterpret_cast<const float4 *>(sa + at[u] + kb));
+                        v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int b = 0; b < SB; ++b) v[u][b] = __ldg(sa + at[u] + min(kb + b, p.num_kb - 1));
+                }
+#pragma unroll
+                for (int b = 0; b < SB; ++b) {
+                    w0[b] = __ldg(sw0 + min(kb + b, p.num_kb - 1));
+                    w1[b] = __ldg(sw1 + min(kb + b, p.num_kb - 1));
+                }
+                if (!__all_sync(0xffffffffu, wait_bounded_inline(&sc_empty[stage], phase ^ 1u, abort_flag, p.status))) {
+                    ok = false;
+                    break;
+                }
+                float *dst = s_scale + stage * SC_FLOATS + lane;
+#pragma unroll
+                for (int b = 0; b < SB; ++b)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        dst[(2 * b) * BM + 32 * u] = v[u][b] * w0[b];
+                        dst[(2 * b + 1) * BM + 32 * u] = v[u][b] * w1[b];
+                    }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_full[stage]);
+                if (++stage == SC_STAGES) { stage = 0; phase ^= 1u; }
+            }
+        }
+      } else if (lane == 0) {
+        // ---------------------------------------------------- MMA issuers
+        constexpr uint32_t idesc = idesc_e4m3(BM, BN);
+        const int accb = warp >> 1;          // this issuer's accumulator: every second block
+        int stage = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        int turn = 0;                        // accumulator of the block at hand
+        bool ok = true;
+        const uint32_t d_tmem = tmem_base + (uint32_t)(accb * BN);
+        for (int i = 0; ok && i < my_tiles; ++i) {
+            for (int kb = 0; kb < p.num_kb; ++kb) {
+                if (turn == accb) {
+                    if (!wait_bounded_inline(&full[stage], phase, abort_flag, p.status) ||
+                        !wait_bounded_inline(&acc_empty[accb], acc_phase ^ 1u, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + (uint32_t)(accb * BN);
                     const uint32_t a_addr = smem_u32(smem + (size_t)stage * STAGE_BYTES);
                     const uint32_t b_addr = a_addr + A_BYTES;
 #pragma unroll
                     for (int k = 0; k < BK / 32; ++k)
-                        mma_f8_pair(d_tmem, desc_sw128(a_addr + 32 * k), desc_sw128(b_addr + 32 * k),
-                                    idesc, k > 0 ? 1u : 0u);
-                    mma_commit_pair(&empty[stage], 0x3);
-                    mma_commit_pair(&acc_full[accb], 0x3);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                    if (++accb == 2) { accb = 0; acc_phase ^= 1u; }
+                        mma_f8(d_tmem, desc_sw128(a_addr + 32 * k), desc_sw128(b_addr + 32 * k), idesc,
+                               k > 0 ? 1u : 0u);
+                    mma_commit(&acc_full[accb]);
+                    mma_commit_multicast(&empty[stage], 0x3);
+                    acc_phase ^= 1u;
                 }
+                turn ^= 1;
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
-            // no MMA may still be running when either CTA frees TMEM or exits
-            mma_commit_pair(drain, 0x1);
-            wait_bounded(drain, 0, abort_flag, p.status, false);
         }
+        // no MMA may still be running when TMEM is freed
+        mma_commit(drain);
+        wait_bounded_inline(drain, 0, abort_flag, p.status, false);
+      }
     } else {
-        // ---------------------------------------------------- epilogue warps (both CTAs)
+        // ---------------------------------------------------- epilogue warps
         const int q = warp & 3;
-        const int hf = (warp - 2) >> 2;
+        const int cg = (warp - EPI_WARP0) >> 2;   // column group
         const int rloc = q * 32 + lane;
         int accb = 0;
         uint32_t acc_phase = 0;
         uint32_t tile_par = 0;
-        for (int64_t tile = first; tile < total_tiles; tile += step) {
-            const Tile t = decode(tile, p, s_blk, s_off, (int)rank);
+        int sc_stage = 0;
+        uint32_t sc_phase = 0;
+        for (int it = 0; it < my_tiles; ++it) {
+            const Tile t = decode((int64_t)(blockIdx.x >> 1) + (int64_t)it * (gridDim.x >> 1), p, s_blk, s_off, (int)rank);
             const bool rows_here = q * 32 < t.rows;   // warp-uniform
-            // a row that exists, so that every lane may read its scales
-            const int64_t row = min((int64_t)t.row0 + (rloc < t.rows ? rloc : 0), p.cap_rows - 1);
-            const float *sa = p.a_scales + row * p.num_kb;
-            // scale rows of the two 64-column groups' channel blocks
-            const int wb0 = EPI == EPI_SWIGLU ? t.nb : min(2 * t.nb + hf, p.w_blocks - 1);
-            const float *sw0 = p.w_scales + ((int64_t)t.e * p.w_blocks + wb0) * p.num_kb;
-            const float *sw1 = EPI == EPI_SWIGLU ? sw0 + (int64_t)(p.w_blocks / 2) * p.num_kb : sw0;
-            float2 acc[64];
+            float2 acc[CPT / 2];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
-            float sa_n = 0.0f, sw0_n = 0.0f, sw1_n = 0.0f;
-            if (rows_here) {
-                sa_n = __ldg(sa);
-                sw0_n = __ldg(sw0);
-                sw1_n = __ldg(sw1);
-            }
+            for (int i = 0; i < CPT / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
             bool ok = true;
             for (int kb = 0; kb < p.num_kb; ++kb) {
-                const float s0 = sa_n * sw0_n, s1 = sa_n * sw1_n;
-                if (rows_here && kb + 1 < p.num_kb) {   // the next block's, while this one is awaited
-                    sa_n = __ldg(sa + kb + 1);
-                    sw0_n = __ldg(sw0 + kb + 1);
-                    if (EPI == EPI_SWIGLU) sw1_n = __ldg(sw1 + kb + 1);
-                    else sw1_n = sw0_n;
+                if ((kb & (SB - 1)) == 0) {
+                    const bool w = wait_bounded_inline(&sc_full[sc_stage], sc_phase, abort_flag, p.status);
+                    if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
                 }
-                const bool w = wait_bounded(&acc_full[accb], acc_phase, abort_flag, p.status);
+                const float *sc = s_scale + sc_stage * SC_FLOATS + (kb & (SB - 1)) * 2 * BM + rloc;
+                const float s0 = EPI == EPI_SWIGLU ? sc[0] : sc[cg * BM];
+                const float s1 = EPI == EPI_SWIGLU ? sc[BM] : s0;
+                const bool w = wait_bounded_inline(&acc_full[accb], acc_phase, abort_flag, p.status);
                 if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
                 tc_fence_after();
+                uint32_t r[16];
+                const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(accb * BN);
                 if (rows_here) {
-                    const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(accb * BN);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t r[32];
-                        tmem_ld32(taddr + half_col<EPI>(hf, j >> 1) + 32 * (j & 1), r);
+                    for (int j = 0; j < 8; ++j) {
+                        tmem_ld16(taddr + group_col<EPI>(cg, j >> 2) + 16 * (j & 3), r);
                         tmem_ld_wait();
-                        const float s = j < 2 ? s0 : s1;
+                        if (j == 7) break;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) fma2(acc[16 * j + i], s, r[2 * i], r[2 * i + 1]);
+                        for (int i = 0; i < 8; ++i)
+                            fma2(acc[8 * j + i], j < 4 ? s0 : s1, r[2 * i], r[2 * i + 1]);
                     }
                 }
+                // the accumulator is read: the next block but one may use it
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(&acc_empty[accb], 0);
+                if (lane == 0) mbar_arrive(&acc_empty[accb]);
+                if (rows_here) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) fma2(acc[56 + i], s1, r[2 * i], r[2 * i + 1]);
+                }
                 if (++accb == 2) { accb = 0; acc_phase ^= 1u; }
+                if ((kb & (SB - 1)) == SB - 1 || kb + 1 == p.num_kb) {
+                    if (lane == 0) mbar_arrive(&sc_empty[sc_stage]);   // read before the __syncwarp above
+                    if (++sc_stage == SC_STAGES) { sc_stage = 0; sc_phase ^= 1u; }
+                }
             }
             if (!ok) break;
             const bool store = rloc < t.rows && (int64_t)t.row0 + rloc < p.cap_rows;
             if (EPI == EPI_SWIGLU) {
                 if (rows_here) {
-                    // sums 0..31 (pairs) are SiLU-half channels, 32..63 their multipliers
+                    // the first half of the pairs are SiLU channels, the others their multipliers
                     float amax = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        acc[i].x = silu_f32(acc[i].x) * acc[32 + i].x;
-                        acc[i].y = silu_f32(acc[i].y) * acc[32 + i].y;
+                    for (int i = 0; i < HC / 2; ++i) {
+                        acc[i].x = silu_f32(acc[i].x) * acc[HC / 2 + i].x;
+                        acc[i].y = silu_f32(acc[i].y) * acc[HC / 2 + i].y;
                         amax = fmaxf(amax, fmaxf(fabsf(acc[i].x), fabsf(acc[i].y)));
                     }
-                    // the block's other 64 channels are the other warp's
-                    float *mine = s_amax + ((tile_par * 2 + hf) * BM) + rloc;
-                    const float *other = s_amax + ((tile_par * 2 + (hf ^ 1)) * BM) + rloc;
-                    *mine = amax;
+                    // the block's other channels are with the quadrant's other warps
+                    float *all = s_amax + tile_par * CG * BM + rloc;
+                    all[cg * BM] = amax;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&amax_bar[q]);
-                    const bool w = wait_bounded(&amax_bar[q], tile_par, abort_flag, p.status);
+                    const bool w = wait_bounded_inline(&amax_bar[q], tile_par, abort_flag, p.status);
                     if (!__all_sync(0xffffffffu, w)) break;
-                    amax = fmaxf(amax, *reinterpret_cast<const volatile float *>(other));
+                    const volatile float *m = all;
                     float s, inv;
+                    amax = m[0];
+#pragma unroll
+                    for (int g = 1; g < CG; ++g) amax = fmaxf(amax, m[g * BM]);
                     block_scale(amax, s, inv);
                     if (store) {
                         const int Nh = p.N / 2;
                         const int64_t r = (int64_t)t.row0 + rloc;
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.q2 + r * Nh + t.nb * 128 + hf * 64);
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.q2 + r * Nh + t.nb * 128 + cg * HC);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < HC / 16; ++i) {
                             uint32_t w4[4];
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {
@@ -362,26 +452,37 @@ k_gemm_fp8_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             }
                             dst[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
                         }
-                        if (hf == 0) p.s2[r * (Nh / kFp8Block) + t.nb] = s;
+                        if (cg == 0) p.s2[r * (Nh / kFp8Block) + t.nb] = s;
                     }
                     tile_par ^= 1u;
                 }
             } else if (store) {
                 const int64_t r = (int64_t)t.row0 + rloc;
-                const int c0 = t.nb * BN + hf * 128;
+                const int c0 = t.nb * BN + cg * CPT;
                 if (EPI == EPI_BF16) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.c) + r * p.N + c0);
+                    __nv_bfloat16 *row = static_cast<__nv_bfloat16 *>(p.c) + r * p.N + c0;
+                    if (p.c_vec32 && c0 + CPT <= p.N) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c0 + 8 * i < p.N)
-                            dst[i] = make_uint4(pack_bf16(acc[4 * i].x, acc[4 * i].y),
-                                                pack_bf16(acc[4 * i + 1].x, acc[4 * i + 1].y),
-                                                pack_bf16(acc[4 * i + 2].x, acc[4 * i + 2].y),
-                                                pack_bf16(acc[4 * i + 3].x, acc[4 * i + 3].y));
+                        for (int i = 0; i < CPT / 16; ++i) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) w[u] = pack_bf16(acc[8 * i + u].x, acc[8 * i + u].y);
+                            st_global_v8(row + 16 * i, w);
+                        }
+                    } else {
+                        uint4 *dst = reinterpret_cast<uint4 *>(row);
+#pragma unroll
+                        for (int i = 0; i < CPT / 8; ++i)
+                            if (c0 + 8 * i < p.N)
+                                dst[i] = make_uint4(pack_bf16(acc[4 * i].x, acc[4 * i].y),
+                                                    pack_bf16(acc[4 * i + 1].x, acc[4 * i + 1].y),
+                                                    pack_bf16(acc[4 * i + 2].x, acc[4 * i + 2].y),
+                                                    pack_bf16(acc[4 * i + 3].x, acc[4 * i + 3].y));
+                    }
                 } else {
                     float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.c) + r * p.N + c0);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
+                    for (int i = 0; i < CPT / 4; ++i)
                         if (c0 + 4 * i < p.N)
                             dst[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x,
                                                  acc[2 * i + 1].y);
@@ -394,14 +495,14 @@ k_gemm_fp8_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
 }
 
 // Clusters that fit on the GPU at once (0 if the kernel cannot run).
 template <int EPI>
 int clusters_that_fit() {
     static const int n = [] {
-        if (!set_smem_limit((const void *)k_gemm_fp8_pair<EPI>, SMEM_BYTES)) return 0;
+        if (!set_smem_limit((const void *)k_gemm_fp8_large<EPI>, SMEM_BYTES)) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
         cfg.blockDim = dim3(THREADS);
@@ -414,7 +515,7 @@ int clusters_that_fit() {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int c = 0;
-        if (cudaOccupancyMaxActiveClusters(&c, (const void *)k_gemm_fp8_pair<EPI>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&c, (const void *)k_gemm_fp8_large<EPI>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             c = 0;
         }
@@ -440,7 +541,7 @@ moe_status launch(const Fp8GemmArgs &a, const LargeDev &d, cudaStream_t stream) 
                          bstr, bbox))
         return MOE_ERR_CUDA;
     const char *names[3] = {"gemm_fp8_f32", "gemm_fp8_bf16", "gemm_fp8_swiglu"};
-    MOE_LAUNCH_CLUSTER(names[EPI], k_gemm_fp8_pair<EPI>, 2 * clusters, THREADS, SMEM_BYTES, stream, 2u,
+    MOE_LAUNCH_CLUSTER(names[EPI], k_gemm_fp8_large<EPI>, 2 * clusters, THREADS, SMEM_BYTES, stream, 2u,
                        ma, mb, d);
     return MOE_OK;
 }
@@ -462,6 +563,8 @@ moe_status launch_gemm_fp8_large(const Fp8GemmArgs &a, cudaStream_t stream) {
     d.q2 = static_cast<uint8_t *>(a.q2);
     d.s2 = a.s2;
     d.status = a.status;
+    d.c_vec32 = (uintptr_t)a.c % 32 == 0 && a.N * 2 % 32 == 0;
+    d.vec_scales = d.num_kb % SB == 0 && (uintptr_t)a.a_scales % 16 == 0;
     if (a.q2) return launch<EPI_SWIGLU>(a, d, stream);
     return a.out_bf16 ? launch<EPI_BF16>(a, d, stream) : launch<EPI_F32>(a, d, stream);
 }

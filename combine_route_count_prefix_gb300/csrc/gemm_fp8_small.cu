@@ -134,9 +134,8 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
                  SmallDev p) {
     using C = Cfg<EPI, TB_>;
     constexpr int TB = C::TB, NG = C::NG, CW = C::CW, NBUF = C::NBUF, STAGES = C::STAGES;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // aligned by its declaration, so that every address in it is a constant
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::RING_BYTES);
     uint64_t *empty = full + STAGES;
     uint64_t *acc_full = empty + STAGES;

@@ -141,4 +141,22 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, vol
     if (mbar_try_wait(bar, parity)) return true;
     return wait_bounded_loop(bar, parity, abort_flag, status, honour_abort);
 }
+// The same wait with its loop in line, for a warp that holds more live
+// registers than a call leaves it (a call from the sums of a 128-register
+// epilogue spills some of them on every wait).
+__device__ __forceinline__ bool wait_bounded_inline(uint64_t *bar, uint32_t parity,
+                                                    volatile int *abort_flag, int32_t *status,
+                                                    bool honour_abort = true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    for (;;) {
+        if (mbar_try_wait_sleep(bar, parity, kWaitSliceNs)) return true;
+        if (honour_abort && *abort_flag) return false;
+        if (globaltimer() - t0 > kTimeoutNs) {
+            *abort_flag = 1;
+            if (status) atomicOr(status, MOE_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
 }  // namespace moe
