@@ -9,6 +9,7 @@ fallback: if the library is missing, :func:`lib` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -141,7 +142,7 @@ def lib():
 
 
 def _call(name, *args):
-    rc = getattr(lib(), name)(*args)
+    rc = getattr(_lib or lib(), name)(*args)
     if rc != 0:
         raise MoeError(name, rc)
 
@@ -155,12 +156,25 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _addr(t):
+    """A tensor's address as a plain integer (None for None), and the raw handle
+    of the current or given stream: what ctypes converts at the least cost on
+    calls whose kernels take a few microseconds."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _check(t, dtype, shape, name):
     if t is None:
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
@@ -490,10 +504,16 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out=None, with_y=True, with
         _check(out.get("y"), torch.bfloat16, (T, H), "y")
         _check(out.get("q"), torch.float8_e4m3fn, (T, H), "q")
         _check(out.get("scales"), torch.float32, (T, _blocks(H)), "scales")
-    _call("moe_add_rms_norm", T, H, _ptr(x), _ptr(residual), _ptr(weight), _DTYPES[weight.dtype],
-          float(eps), _ptr(out.get("residual_out")), _ptr(out.get("y")), _ptr(out.get("q")),
-          _ptr(out.get("scales")), _stream(stream))
+    _call("moe_add_rms_norm", T, H, _addr(x), _addr(residual), _addr(weight),
+          _DTYPES[weight.dtype], eps, _addr(out.get("residual_out")), _addr(out.get("y")),
+          _addr(out.get("q")), _addr(out.get("scales")), _raw_stream(stream, x.device))
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _gate_desc(T, E, K, groups, topk_groups, stride, dtype, score, group_score, renormalize, scale):
+    return MoeGateDesc(T, E, K, groups, topk_groups, stride, _DTYPES[dtype], GATE_SCORES[score],
+                       GATE_GROUP_SCORES[group_score], renormalize, scale, 0)
 
 
 def gate(logits, topk, bias=None, mask=None, score="softmax", groups=1, topk_groups=None,
@@ -522,14 +542,12 @@ def gate(logits, topk, bias=None, mask=None, score="softmax", groups=1, topk_gro
         _check(out["expert_ids"], torch.int32, (T, K), "expert_ids")
         _check(out["expert_scales"], torch.float32, (T, K), "expert_scales")
         _check(out.get("route_mask"), torch.uint8, (T, K), "route_mask")
-    groups = int(groups)
-    desc = MoeGateDesc(T, E, K, groups, groups if topk_groups is None else int(topk_groups),
-                       logits.stride(0) if T > 1 else E, _DTYPES[logits.dtype],
-                       GATE_SCORES[score], GATE_GROUP_SCORES[group_score],
-                       int(bool(renormalize)), float(scale), 0)
-    _call("moe_gate", ctypes.byref(desc), _ptr(logits), _ptr(bias), _ptr(mask),
-          _ptr(out["expert_ids"]), _ptr(out["expert_scales"]), _ptr(out.get("route_mask")),
-          _stream(stream))
+    desc = _gate_desc(T, E, K, int(groups), int(groups if topk_groups is None else topk_groups),
+                      logits.stride(0) if T > 1 else E, logits.dtype, score, group_score,
+                      int(bool(renormalize)), float(scale))
+    _call("moe_gate", desc, _addr(logits), _addr(bias), _addr(mask), _addr(out["expert_ids"]),
+          _addr(out["expert_scales"]), _addr(out.get("route_mask")),
+          _raw_stream(stream, logits.device))
     return out
 
 
@@ -554,9 +572,9 @@ def grouped_gemm_fp8(expert_offsets, a, a_scales, w, w_scales, ws=None, out=None
         n = ctypes.c_size_t()
         _call("moe_grouped_gemm_fp8_workspace_size", rows, E, N, Kd, ctypes.byref(n))
         _, ws = _alloc_ws(n.value, a.device)
-    _call("moe_grouped_gemm_fp8", rows, E, N, Kd, _ptr(expert_offsets), _ptr(a), _ptr(a_scales),
-          _ptr(w), _ptr(w_scales), _ptr(out), _DTYPES[out.dtype], FFN_PATHS[path], _ptr(ws),
-          ctypes.c_size_t(ws.numel()), _stream(stream))
+    _call("moe_grouped_gemm_fp8", rows, E, N, Kd, _addr(expert_offsets), _addr(a), _addr(a_scales),
+          _addr(w), _addr(w_scales), _addr(out), _DTYPES[out.dtype], FFN_PATHS[path], _addr(ws),
+          ws.numel(), _raw_stream(stream, a.device))
     return out, ws
 
 
@@ -586,9 +604,9 @@ def grouped_ffn_fp8(shape: MoeShape, x, x_scales, expert_offsets, w1, w1_scales,
     _check(y, torch.bfloat16, (T * K, H), "y")
     if ws is None:
         _, ws = _alloc_ws(grouped_ffn_fp8_workspace_size(shape), x.device)
-    _call("moe_grouped_ffn_fp8", ctypes.byref(shape), _ptr(x), _ptr(x_scales), _ptr(assist),
-          _ptr(expert_offsets), _ptr(w1), _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(y),
-          _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream))
+    _call("moe_grouped_ffn_fp8", ctypes.byref(shape), _addr(x), _addr(x_scales), _addr(assist),
+          _addr(expert_offsets), _addr(w1), _addr(w1_scales), _addr(w2), _addr(w2_scales), _addr(y),
+          _addr(ws), ws.numel(), _raw_stream(stream, x.device))
     return y, ws
 
 

@@ -16,7 +16,6 @@ T *at(void *ws, size_t off) {
 
 struct Fp8Layout {
     size_t status = 0;   // int32 status word
-    size_t sched = 0;    // int32 [E+1]
     size_t rows = 0;     // e4m3 [cap, H] gathered tokens
     size_t row_s = 0;    // fp32 [cap, ceil(H/128)]
     size_t q2 = 0;       // e4m3 [cap, N/2]
@@ -33,11 +32,10 @@ struct Carve {
     }
 };
 
-Fp8Layout gemm_layout(int64_t E) {
+Fp8Layout gemm_layout() {
     Fp8Layout L;
     Carve c;
     L.status = c.take(4);
-    L.sched = c.take((size_t)(E + 1) * sizeof(int32_t));
     L.total = c.off;
     return L;
 }
@@ -47,7 +45,6 @@ Fp8Layout ffn_layout(const moe_shape &s) {
     Carve c;
     const size_t cap = (size_t)(s.num_tokens * s.topk);
     L.status = c.take(4);
-    L.sched = c.take((size_t)(s.num_experts + 1) * sizeof(int32_t));
     L.rows = c.take(cap * s.hidden);
     L.row_s = c.take(cap * ((s.hidden + 127) / 128) * sizeof(float));
     L.q2 = c.take(cap * (s.ffn / 2));
@@ -133,7 +130,7 @@ moe_status moe_grouped_gemm_fp8_workspace_size(int64_t rows, int64_t E, int64_t 
     if (rows < 0 || rows > INT32_MAX || E < 1 || E > kMaxExperts || N < 8 || N % 8 != 0 || Kd < 16 ||
         Kd % 16 != 0 || N > (1 << 20) || Kd > 131072)
         return MOE_FAIL(MOE_ERR_SHAPE);
-    *bytes = gemm_layout(E).total;
+    *bytes = gemm_layout().total;
     return MOE_OK;
 }
 
@@ -155,9 +152,7 @@ moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
         return MOE_FAIL(MOE_ERR_ALIGNMENT);
     if (workspace_bytes < need) return MOE_FAIL(MOE_ERR_WORKSPACE);
     if (empty) return MOE_OK;
-    const Fp8Layout L = gemm_layout(E);
-    MOE_TRY(launch_sched(expert_offsets, E, at<int32_t>(workspace, L.sched),
-                         at<int32_t>(workspace, L.status), stream));
+    const Fp8Layout L = gemm_layout();
     Fp8GemmArgs g{};
     g.a = A;
     g.a_scales = a_scales;
@@ -171,6 +166,7 @@ moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
     g.c = C;
     g.out_bf16 = out_dtype == MOE_DTYPE_BF16;
     g.status = at<int32_t>(workspace, L.status);
+    g.reset_status = true;
     return run_gemm(path, g, stream);
 }
 
@@ -200,14 +196,13 @@ moe_status moe_grouped_ffn_fp8(const moe_shape *shape, const void *x, const floa
     if (workspace_bytes < L.total) return MOE_FAIL(MOE_ERR_WORKSPACE);
     if (empty) return MOE_OK;
     const int64_t cap = s.num_tokens * s.topk, H = s.hidden, E = s.num_experts, Nh = s.ffn / 2;
-    MOE_TRY(launch_sched(expert_offsets, E, at<int32_t>(workspace, L.sched),
-                         at<int32_t>(workspace, L.status), stream));
     const void *rows = x;
     const float *row_s = x_scales;
     if (assist) {
         MOE_TRY(launch_gather_fp8(x, x_scales, assist, expert_offsets, E, s.num_tokens,
                                   s.num_tokens / s.num_partitions, at<void>(workspace, L.rows),
-                                  at<float>(workspace, L.row_s), cap, H, stream));
+                                  at<float>(workspace, L.row_s), cap, H,
+                                  at<int32_t>(workspace, L.status), stream));
         rows = at<void>(workspace, L.rows);
         row_s = at<float>(workspace, L.row_s);
     }
@@ -224,6 +219,7 @@ moe_status moe_grouped_ffn_fp8(const moe_shape *shape, const void *x, const floa
     g1.q2 = at<void>(workspace, L.q2);
     g1.s2 = at<float>(workspace, L.s2);
     g1.status = at<int32_t>(workspace, L.status);
+    g1.reset_status = assist == nullptr;   // the gather has done it
     MOE_TRY(run_gemm(s.ffn_path, g1, stream));
     Fp8GemmArgs g2{};
     g2.a = at<void>(workspace, L.q2);

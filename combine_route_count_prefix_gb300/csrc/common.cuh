@@ -341,14 +341,17 @@ struct Fp8GemmArgs {
     void *q2;                  // silu(C[:, :N/2]) * C[:, N/2:], quantised: e4m3 [cap_rows, N/2]
     float *s2;                 // and its scales [cap_rows, N/256] (N % 256 == 0)
     int32_t *status;
+    bool reset_status;         // the call's first kernel clears the status word
 };
 // For many rows per expert (256-row tiles on pairs of SMs) and for few (the
 // weights as the MMA's M side).
 moe_status launch_gemm_fp8_large(const Fp8GemmArgs &a, cudaStream_t stream);
 moe_status launch_gemm_fp8_small(const Fp8GemmArgs &a, cudaStream_t stream);
-// Rows and scales of the tokens named by the dispatch's triplets.
+// Rows and scales of the tokens named by the dispatch's triplets; clears the
+// status word.
 moe_status launch_gather_fp8(const void *x, const float *xs, const int32_t *assist,
                              const int32_t *offsets, int64_t E, int64_t T, int64_t M, void *rows,
-                             float *rs, int64_t cap_rows, int64_t H, cudaStream_t stream);
+                             float *rs, int64_t cap_rows, int64_t H, int32_t *status,
+                             cudaStream_t stream);
 
 }  // namespace moe

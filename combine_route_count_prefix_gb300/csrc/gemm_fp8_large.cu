@@ -87,6 +87,7 @@ struct LargeDev {
     uint8_t *q2;         // SwiGLU: [cap_rows, N/2]
     float *s2;           //         [cap_rows, N/256]
     int32_t *status;
+    int reset_status;    // first kernel of its call
     int c_vec32;         // rows of C start on 32-byte boundaries
     int vec_scales;      // rows of a_scales can be read 16 bytes at a time
 };
@@ -195,6 +196,9 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
     }
     pdl_wait();   // everything below may read what earlier kernels wrote
+    // Block 0 starts no later than any other, and no wait gives up before two
+    // seconds have passed, so no bit set by this call is lost.
+    if (p.reset_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x) s_off[i] = p.offsets[i];
     __syncthreads();
     if (warp == 0) {
@@ -563,6 +567,7 @@ moe_status launch_gemm_fp8_large(const Fp8GemmArgs &a, cudaStream_t stream) {
     d.q2 = static_cast<uint8_t *>(a.q2);
     d.s2 = a.s2;
     d.status = a.status;
+    d.reset_status = a.reset_status;
     d.c_vec32 = (uintptr_t)a.c % 32 == 0 && a.N * 2 % 32 == 0;
     d.vec_scales = d.num_kb % SB == 0 && (uintptr_t)a.a_scales % 16 == 0;
     if (a.q2) return launch<EPI_SWIGLU>(a, d, stream);

@@ -86,6 +86,7 @@ struct SmallDev {
     uint8_t *q2;
     float *s2;
     int32_t *status;
+    int reset_status;    // first kernel of its call
     int split;           // CTAs per tile (the cluster's size)
 };
 
@@ -178,6 +179,9 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmW) : "memory");
     }
     pdl_wait();   // everything below may read what earlier kernels wrote
+    // Block 0 starts no later than any other, and no wait gives up before two
+    // seconds have passed, so no bit set by this call is lost.
+    if (p.reset_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x) s_off[i] = p.offsets[i];
     __syncthreads();
     if (warp == 0) {
@@ -501,6 +505,7 @@ moe_status launch_gemm_fp8_small(const Fp8GemmArgs &a, cudaStream_t stream) {
     d.q2 = static_cast<uint8_t *>(a.q2);
     d.s2 = a.s2;
     d.status = a.status;
+    d.reset_status = a.reset_status;
     d.split = 1;
     if (a.q2) return launch_epi<EPI_SWIGLU>(a, d, stream);
     return a.out_bf16 ? launch_epi<EPI_BF16>(a, d, stream) : launch_epi<EPI_F32>(a, d, stream);
