@@ -220,6 +220,7 @@ moe_status moe_grouped_ffn_fp8(const moe_shape *shape, const void *x, const floa
     g1.s2 = at<float>(workspace, L.s2);
     g1.status = at<int32_t>(workspace, L.status);
     g1.reset_status = assist == nullptr;   // the gather has done it
+    g1.early = assist != nullptr;
     MOE_TRY(run_gemm(s.ffn_path, g1, stream));
     Fp8GemmArgs g2{};
     g2.a = at<void>(workspace, L.q2);
@@ -234,6 +235,7 @@ moe_status moe_grouped_ffn_fp8(const moe_shape *shape, const void *x, const floa
     g2.c = y;
     g2.out_bf16 = true;
     g2.status = at<int32_t>(workspace, L.status);
+    g2.early = true;
     return run_gemm(s.ffn_path, g2, stream);
 }
 

@@ -342,6 +342,8 @@ struct Fp8GemmArgs {
     float *s2;                 // and its scales [cap_rows, N/256] (N % 256 == 0)
     int32_t *status;
     bool reset_status;         // the call's first kernel clears the status word
+    bool early;                // not the call's first kernel: offsets, weights and their scales
+                               // were final before the kernel before this one began
 };
 // For many rows per expert (256-row tiles on pairs of SMs) and for few (the
 // weights as the MMA's M side).

@@ -10,10 +10,14 @@
 // here) and adds to fp32 sums in registers.
 //
 // Kernel shape (one persistent CTA per SM, 12 warps):
-//   warp 0       TMA producer: per block NG x 128 channels and TB rows,
-//                128 bytes of K each, one ring
-//   warps 1, 3   MMA issuers, one per 128-channel group (issuing a tcgen05.mma
-//                takes a thread about 130 cycles whatever its N); warp 1 owns TMEM
+//   warp 0       TMA producer of the weights: NG x 128 channels, 128 bytes of K
+//                each, per block, into the ring
+//   warp 2       TMA producer of the block's TB rows, into the same stages.  In a
+//                call's later kernels only these (and their scales) depend on
+//                the kernel before, so the weights start to come while it ends
+//   warps 1, 3   MMA issuers, one per 128-channel group, or taking turns on the
+//                blocks of the one group (issuing a tcgen05.mma takes a thread
+//                about 130 cycles whatever its N); warp 1 owns TMEM
 //   warps 4..11  epilogue: TMEM lane quadrant (32 channels) x half of the rows
 // Tiles are (expert, TB rows, NG x 128 channels), channel block fastest.
 // SwiGLU form (NG = 2): the groups are 128 SiLU-half channels and their
@@ -52,7 +56,7 @@ struct Cfg {
     static constexpr int TB = TB_;                       // rows per tile
     static constexpr int NG = EPI == EPI_SWIGLU ? 2 : 1;
     static constexpr int CW = TB / 2;                    // rows per epilogue warp
-    static constexpr int NBUF = TB == 32 ? 4 : 2;        // accumulators
+    static constexpr int NBUF = 4;                       // accumulators
     static constexpr uint32_t TMEM_COLS = NBUF * NG * TB < 32 ? 32 : NBUF * NG * TB;
     static constexpr int STAGE_BYTES = NG * W_BYTES + TB * BK;
     // partial sums of a shared tile; the 64-row SwiGLU tile has no room for them
@@ -88,6 +92,7 @@ struct SmallDev {
     int32_t *status;
     int reset_status;    // first kernel of its call
     int split;           // CTAs per tile (the cluster's size)
+    int early;           // offsets and weights were final before the previous kernel began
 };
 
 struct Tile {
@@ -129,6 +134,19 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return v;
 }
 
+// a0 += s0 * d0, a1 += s1 * d1, one instruction.  Volatile, to stay behind the
+// wait that makes the loaded d valid.
+__device__ __forceinline__ void fma2(float &a0, float &a1, float s0, float s1, uint32_t d0, uint32_t d1) {
+    asm volatile("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "r"(d0), "r"(d1), "f"(s0), "f"(s1));
+}
+
 template <int EPI, int TB_>
 __global__ void __launch_bounds__(THREADS, 1)
 k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__ CUtensorMap tmW,
@@ -166,7 +184,7 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
             mbar_init(&acc_full[b], NG);
             mbar_init(&acc_empty[b], EPI_WARPS);
         }
-        mbar_init(drain, NG);
+        mbar_init(drain, 2);
         mbar_init(part_full, S * EPI_WARPS);
         mbar_init(part_free, S * EPI_WARPS);
         mbar_init(&red_bar[0], 4);
@@ -178,7 +196,7 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmRows) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmW) : "memory");
     }
-    pdl_wait();   // everything below may read what earlier kernels wrote
+    if (!p.early) pdl_wait();   // everything below may read what earlier kernels wrote
     // Block 0 starts no later than any other, and no wait gives up before two
     // seconds have passed, so no bit set by this call is lost.
     if (p.reset_status && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
@@ -217,38 +235,56 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
 
     if (warp == 0) {
         if (lane == 0) {
-            // ------------------------------------------------ TMA producer
+            // ------------------------------------------------ weight producer
             int stage = 0;
             uint32_t phase = 0;
-            int armed_phase[STAGES];
-#pragma unroll
-            for (int s = 0; s < STAGES; ++s) armed_phase[s] = -1;
+            int64_t armed = 0;   // stage uses
             bool ok = true;
             for (int64_t tile = first; ok && tile < total_tiles; tile += step) {
                 const Tile t = decode(tile, p, TB, s_blk, s_off);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_bounded(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
-                    armed_phase[stage] = (int)phase;
+                    mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);   // the rows' bytes too
+                    ++armed;
                     uint8_t *dst = smem + (size_t)stage * C::STAGE_BYTES;
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
                         tma_load_3d(dst + g * W_BYTES, &tmW, &full[stage], kb * BK,
                                     g * (p.N / 2) + t.wb * BW, t.e);
-                    // rows past the tile's (another expert's, or zero fill) only
-                    // reach accumulator columns that are never read
-                    tma_load_2d(dst + NG * W_BYTES, &tmRows, &full[stage], kb * BK, t.row0);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
-            for (int s = 0; s < STAGES; ++s)
-                if (armed_phase[s] >= 0)
-                    wait_bounded(&full[s], (uint32_t)armed_phase[s], abort_flag, p.status, false);
+            for (int64_t u = armed > STAGES ? armed - STAGES : 0; u < armed; ++u)
+                ok = wait_bounded(&full[u % STAGES], (uint32_t)(u / STAGES) & 1u, abort_flag, p.status, false) && ok;
+            if (!ok) {   // after a give-up, leave row copies still in flight time to land
+                const uint64_t t0 = globaltimer();
+                while (globaltimer() - t0 < 100000ull) __nanosleep(2000);
+            }
         }
-    } else if (warp == 1 || (warp == 3 && NG == 2)) {
+    } else if (warp == 2) {
+        if (lane == 0) {
+            // ------------------------------------------------ row producer
+            if (p.early) pdl_wait();
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int64_t tile = first; ok && tile < total_tiles; tile += step) {
+                const Tile t = decode(tile, p, TB, s_blk, s_off);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!wait_bounded(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+                    // rows past the tile's (another expert's, or zero fill) only
+                    // reach accumulator columns that are never read
+                    tma_load_2d(smem + (size_t)stage * C::STAGE_BYTES + NG * W_BYTES, &tmRows,
+                                &full[stage], kb * BK, t.row0);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+        }
+    } else if (warp == 1 || warp == 3) {
         if (lane == 0) {
             // ------------------------------------------------ MMA issuers
-            const int g = warp >> 1;
+            const int me = warp >> 1;            // NG = 2: the group; NG = 1: every second block
+            const int g = NG == 2 ? me : 0;
             int stage = 0;
             uint32_t phase = 0;
             int accb = 0;
@@ -258,20 +294,22 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
                 const Tile t = decode(tile, p, TB, s_blk, s_off);
                 const uint32_t idesc = idesc_e4m3(BW, ((t.rows + 15) / 16) * 16);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!wait_bounded(&acc_empty[accb], acc_phase ^ 1u, abort_flag, p.status) ||
-                        !wait_bounded(&full[stage], phase, abort_flag, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + (uint32_t)((accb * NG + g) * TB);
-                    const uint32_t base = smem_u32(smem + (size_t)stage * C::STAGE_BYTES);
+                    if (NG == 2 || (accb & 1) == me) {
+                        if (!wait_bounded(&acc_empty[accb], acc_phase ^ 1u, abort_flag, p.status) ||
+                            !wait_bounded(&full[stage], phase, abort_flag, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t d_tmem = tmem_base + (uint32_t)((accb * NG + g) * TB);
+                        const uint32_t base = smem_u32(smem + (size_t)stage * C::STAGE_BYTES);
 #pragma unroll
-                    for (int k = 0; k < BK / 32; ++k)
-                        mma_f8(d_tmem, desc_sw128(base + g * W_BYTES + 32 * k),
-                               desc_sw128(base + NG * W_BYTES + 32 * k), idesc, k > 0 ? 1u : 0u);
-                    mma_commit(&empty[stage]);
-                    mma_commit(&acc_full[accb]);
+                        for (int k = 0; k < BK / 32; ++k)
+                            mma_f8(d_tmem, desc_sw128(base + g * W_BYTES + 32 * k),
+                                   desc_sw128(base + NG * W_BYTES + 32 * k), idesc, k > 0 ? 1u : 0u);
+                        mma_commit(&acc_full[accb]);
+                        mma_commit(&empty[stage]);
+                    }
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     if (++accb == NBUF) { accb = 0; acc_phase ^= 1u; }
                 }
@@ -281,10 +319,11 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
         }
     } else if (warp >= EPI_WARP0) {
         // ---------------------------------------------------- epilogue warps
+        if (p.early) pdl_wait();
         const int q = warp & 3;
         const int hf = (warp - EPI_WARP0) >> 2;
         const int c0 = hf * CW;                   // first row of this warp
-        constexpr int LDW = CW < 32 ? 16 : 32;    // columns per TMEM load
+        constexpr int LDW = CW < 32 || NG == 2 ? 16 : 32;   // columns per TMEM load
         constexpr int SPT = (CW + 31) / 32;       // row scales per lane
         float *my_scale = s_scale + (size_t)(warp - EPI_WARP0) * 2 * NG * CW;
         int accb = 0;
@@ -346,10 +385,8 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
                             for (int i = 0; i < LDW; i += 4) {
                                 const float4 s = *reinterpret_cast<const float4 *>(sb + g * CW + LDW * j + i);
                                 float *a = &acc[g][LDW * j + i];
-                                a[0] = fmaf(s.x, __uint_as_float(r[i]), a[0]);
-                                a[1] = fmaf(s.y, __uint_as_float(r[i + 1]), a[1]);
-                                a[2] = fmaf(s.z, __uint_as_float(r[i + 2]), a[2]);
-                                a[3] = fmaf(s.w, __uint_as_float(r[i + 3]), a[3]);
+                                fma2(a[0], a[1], s.x, s.y, r[i], r[i + 1]);
+                                fma2(a[2], a[3], s.z, s.w, r[i + 2], r[i + 3]);
                             }
                         }
                     }
@@ -507,6 +544,7 @@ moe_status launch_gemm_fp8_small(const Fp8GemmArgs &a, cudaStream_t stream) {
     d.status = a.status;
     d.reset_status = a.reset_status;
     d.split = 1;
+    d.early = a.early;
     if (a.q2) return launch_epi<EPI_SWIGLU>(a, d, stream);
     return a.out_bf16 ? launch_epi<EPI_BF16>(a, d, stream) : launch_epi<EPI_F32>(a, d, stream);
 }
