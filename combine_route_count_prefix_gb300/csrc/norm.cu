@@ -1,18 +1,26 @@
 // norm.cu -- residual addition, root-mean-square norm and block-scaled e4m3.
 //
-// One CTA per token.  Thread i holds the 16-byte vectors i, i + 256, ... of the
-// row (eight channels each) in registers from the load to the stores, so every
-// input is read once.  A block of 128 channels is 16 neighbouring vectors, half
-// a warp: its maximum is four shuffles.
+// Memory bounds it: every input is read once and every output written once
+// (9 bytes an element with a residual and all outputs).  Persistent CTAs walk
+// the tokens; a token's rows of x and residual come by bulk copies into a
+// shared-memory ring, the next tokens' on their way while this one is summed
+// and written, and stay in registers from the sum to the stores.  Thread i
+// holds the 16-byte vectors i, i + threads, ... (eight channels each), with as
+// many threads as make the row come out even.  A block of 128 channels is 16
+// neighbouring vectors, half a warp: its maximum is four shuffles.
 #include "common.cuh"
 #include "fp8.cuh"
+#include "ptx.cuh"
+
+#include <algorithm>
 
 namespace moe {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kNormThreads = 256;
 constexpr float kF32Max = 3.402823466e38f;
+constexpr int kNormMaxThreads = 512;
+constexpr int kStages = 3;
 
 struct NormDev {
     const uint4 *x, *residual;
@@ -21,7 +29,7 @@ struct NormDev {
     uint2 *q;
     float *scales;
     int64_t T;
-    int H, H8, nb;
+    int H8, nb;
     float eps, inv_h;
 };
 
@@ -41,47 +49,94 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
 }
 
-// Sum over the CTA, the same in every thread.
-__device__ __forceinline__ float block_sum(float v, float *part) {
+// Sum over the CTA, the same in every thread.  `fail` from any thread makes
+// `failed` true in all.  Every thread's earlier shared-memory reads are done
+// when it returns.
+__device__ __forceinline__ float block_sum(float v, float *part, bool fail, bool &failed) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.0f;
+    failed = __syncthreads_or(fail);
+    // places of warps that the block does not have hold 0
+    const float4 *p4 = reinterpret_cast<const float4 *>(part);
+    float4 a = p4[0];
 #pragma unroll
-    for (int w = 0; w < kNormThreads / 32; ++w) v += part[w];
-    return v;
+    for (int w = 1; w < kNormMaxThreads / 128; ++w) {
+        const float4 b = p4[w];
+        a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+    }
+    return (a.x + a.y) + (a.z + a.w);
 }
 
-template <int V, bool W_BF16>
-__global__ void __launch_bounds__(kNormThreads)
+template <int V, bool W_BF16, bool RES>
+__global__ void __launch_bounds__(kNormMaxThreads)
 k_add_rms_norm(NormDev p) {
-    __shared__ float part[kNormThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31;
+    extern __shared__ __align__(128) uint8_t smem[];   // [kStages][x, residual][H]
+    __shared__ __align__(16) float part[2][kNormMaxThreads / 32];
+    __shared__ uint64_t full[kStages];
+    __shared__ volatile int abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, nt = blockDim.x;
+    const uint32_t row_bytes = (uint32_t)p.H8 * 16u;
+    constexpr int IN = RES ? 2 : 1;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+        abort_flag = 0;
+        for (int w = nt >> 5; w < kNormMaxThreads / 32; ++w) part[0][w] = part[1][w] = 0.0f;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
     pdl_wait();
+    auto load = [&](int64_t t, int s) {
+        uint8_t *dst = smem + (size_t)s * IN * row_bytes;
+        mbar_arrive_expect_tx(&full[s], IN * row_bytes);
+        bulk_load(dst, p.x + t * p.H8, row_bytes, &full[s]);
+        if (RES) bulk_load(dst + row_bytes, p.residual + t * p.H8, row_bytes, &full[s]);
+    };
+    if (tid == 0)
+        for (int s = 0; s < kStages; ++s)
+            if (blockIdx.x + (int64_t)s * gridDim.x < p.T) load(blockIdx.x + (int64_t)s * gridDim.x, s);
+    // the thread's weights, for every token
+    constexpr int WN = W_BF16 ? 1 : 2;
+    uint4 wv[V][WN];
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+        if (u * nt + tid < p.H8)
+#pragma unroll
+            for (int k = 0; k < WN; ++k)
+                wv[u][k] = __ldg(static_cast<const uint4 *>(p.weight) + WN * (u * nt + tid) + k);
+
+    int s = 0, turn = 0;
+    uint32_t phase = 0;
+    bool failed = false;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const bool ok = wait_bounded(&full[s], phase, &abort_flag, nullptr);
+        const uint4 *sx = reinterpret_cast<const uint4 *>(smem + (size_t)s * IN * row_bytes);
         float h[V][8];
         float ss = 0.0f;
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            const int i = u * kNormThreads + tid;
+            const int i = u * nt + tid;
 #pragma unroll
             for (int c = 0; c < 8; ++c) h[u][c] = 0.0f;
             if (i < p.H8) {
-                unpack8(p.x[t * p.H8 + i], h[u]);
-                if (p.residual) {
+                unpack8(sx[i], h[u]);
+                if (RES) {
                     float r[8];
-                    unpack8(p.residual[t * p.H8 + i], r);
+                    unpack8(sx[p.H8 + i], r);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) h[u][c] += r[c];
-                    if (p.residual_out) p.residual_out[t * p.H8 + i] = pack8(h[u]);
+                    if (p.residual_out && ok) p.residual_out[t * p.H8 + i] = pack8(h[u]);
                 }
             }
 #pragma unroll
             for (int c = 0; c < 8; ++c) ss = fmaf(h[u][c], h[u][c], ss);
         }
-        ss = block_sum(ss, part);
+        ss = block_sum(ss, part[turn], !ok, failed);
+        if (failed) break;
+        turn ^= 1;
+        // everyone has read the stage: the token kStages ahead may land in it
+        if (tid == 0 && t + (int64_t)kStages * gridDim.x < p.T) load(t + (int64_t)kStages * gridDim.x, s);
+        if (++s == kStages) { s = 0; phase ^= 1u; }
         float r = __frsqrt_rn(fmaf(ss, p.inv_h, p.eps));
         if (!(ss <= kF32Max)) {
             // squares past fp32's range (|h| above about 1e17): the same sum of
@@ -95,22 +150,24 @@ k_add_rms_norm(NormDev p) {
                     const float d = h[u][c] * 0x1p-80f;
                     ss = fmaf(d, d, ss);
                 }
-            r = __frsqrt_rn(block_sum(ss, part) * p.inv_h) * 0x1p-80f;
+            r = __frsqrt_rn(block_sum(ss, part[turn], false, failed) * p.inv_h) * 0x1p-80f;
+            turn ^= 1;
         }
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            const int i = u * kNormThreads + tid;
+            const int i = u * nt + tid;
             const bool in = i < p.H8;
             float amax = 0.0f;
             if (in) {
                 float w[8];
                 if (W_BF16) {
-                    unpack8(static_cast<const uint4 *>(p.weight)[i], w);
+                    unpack8(wv[u][0], w);
                 } else {
-                    const float4 a = static_cast<const float4 *>(p.weight)[2 * i];
-                    const float4 b = static_cast<const float4 *>(p.weight)[2 * i + 1];
-                    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-                    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+                    const uint4 a = wv[u][0], b = wv[u][WN - 1];
+                    w[0] = __uint_as_float(a.x); w[1] = __uint_as_float(a.y);
+                    w[2] = __uint_as_float(a.z); w[3] = __uint_as_float(a.w);
+                    w[4] = __uint_as_float(b.x); w[5] = __uint_as_float(b.y);
+                    w[6] = __uint_as_float(b.z); w[7] = __uint_as_float(b.w);
                 }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -123,25 +180,41 @@ k_add_rms_norm(NormDev p) {
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
                 if (in) {
-                    float s, inv;
-                    block_scale(amax, s, inv);
+                    float sc, inv;
+                    block_scale(amax, sc, inv);
                     p.q[t * p.H8 + i] =
                         make_uint2(e4m3x4(h[u][0] * inv, h[u][1] * inv, h[u][2] * inv, h[u][3] * inv),
                                    e4m3x4(h[u][4] * inv, h[u][5] * inv, h[u][6] * inv, h[u][7] * inv));
-                    if ((lane & 15) == 0) p.scales[t * p.nb + (i >> 4)] = s;
+                    if ((lane & 15) == 0) p.scales[t * p.nb + (i >> 4)] = sc;
                 }
             }
         }
     }
+    if (failed) {   // copies still in flight get time to land before the block's memory goes
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 100000ull) __nanosleep(2000);
+    }
+}
+
+template <int V, bool W_BF16, bool RES>
+moe_status launch(const NormDev &p, cudaStream_t stream) {
+    auto kernel = k_add_rms_norm<V, W_BF16, RES>;
+    const size_t smem = (size_t)kStages * (RES ? 2 : 1) * p.H8 * 16;
+    if (!set_smem_limit((const void *)kernel, smem)) return MOE_ERR_CUDA;
+    const int threads = ((p.H8 + V - 1) / V + 31) / 32 * 32;
+    // as many blocks as fit beside each other on every SM
+    const size_t room = 224 * 1024;
+    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(room / (smem + 1024), 2048 / 3 * 2 / threads));
+    const int64_t cap = num_sms() * per_sm;
+    const unsigned grid = (unsigned)(p.T < cap ? p.T : cap);
+    MOE_LAUNCH("add_rms_norm", kernel, grid, threads, smem, stream, p);
+    return MOE_OK;
 }
 
 template <int V>
 moe_status launch_v(const NormDev &p, bool w_bf16, cudaStream_t stream) {
-    const int64_t cap = (int64_t)num_sms() * 8;
-    const unsigned grid = (unsigned)(p.T < cap ? p.T : cap);
-    if (w_bf16) MOE_LAUNCH("add_rms_norm", (k_add_rms_norm<V, true>), grid, kNormThreads, 0, stream, p);
-    else MOE_LAUNCH("add_rms_norm", (k_add_rms_norm<V, false>), grid, kNormThreads, 0, stream, p);
-    return MOE_OK;
+    if (p.residual) return w_bf16 ? launch<V, true, true>(p, stream) : launch<V, false, true>(p, stream);
+    return w_bf16 ? launch<V, true, false>(p, stream) : launch<V, false, false>(p, stream);
 }
 
 }  // namespace
@@ -158,16 +231,14 @@ moe_status launch_add_rms_norm(int64_t T, int64_t H, const void *x, const void *
     p.q = static_cast<uint2 *>(q);
     p.scales = scales;
     p.T = T;
-    p.H = (int)H;
     p.H8 = (int)(H / 8);
     p.nb = (int)((H + kFp8Block - 1) / kFp8Block);
     p.eps = eps;
     p.inv_h = 1.0f / (float)H;
-    const int v = (p.H8 + kNormThreads - 1) / kNormThreads;
-    if (v <= 1) return launch_v<1>(p, w_bf16, stream);
-    if (v <= 2) return launch_v<2>(p, w_bf16, stream);
-    if (v <= 4) return launch_v<4>(p, w_bf16, stream);
-    return launch_v<8>(p, w_bf16, stream);
+    // vectors a thread: few enough for registers, many enough for at most 512 threads
+    if (p.H8 <= 256) return launch_v<1>(p, w_bf16, stream);
+    if (p.H8 <= 1024) return launch_v<2>(p, w_bf16, stream);
+    return launch_v<4>(p, w_bf16, stream);
 }
 
 }  // namespace moe

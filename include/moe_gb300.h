@@ -366,8 +366,9 @@ moe_status moe_dispatch_noalloc(const moe_shape *shape, const void *x, const int
  * of a dimension may be short.
  * Quantisation of a row v (fp32), per block of 128 columns:
  *   a = max(max|v|, 2^-100);  s = a / 448;  c = e4m3(v * (448 / a))
- * each operation rounded to nearest even in fp32, the last one to e4m3; a NaN
- * becomes the NaN code and does not enter the maximum.
+ * in fp32 (the two quotients within two units in the last place), the
+ * conversion to e4m3 rounded to nearest even; a NaN becomes the NaN code and
+ * does not enter the maximum.
  * ------------------------------------------------------------------------ */
 
 /* Element types of the calls below that take more than one. */
