@@ -1,10 +1,14 @@
 // gate.cu -- router: scores, balance bias, expert groups, top-k, weights.
 //
-// One warp per token.  Lane l holds the keys of the VPL experts l * VPL ... in
-// registers.  The choice:
+// One warp per token.  A lane holds the keys of a run of up to VPL neighbouring
+// experts in registers; the runs are in the lanes' order, and with groups a
+// whole power of two of lanes holds a group, so that its value is a few
+// shuffles (where that would take runs of more than 32, the keys go through
+// shared memory instead).  The choice:
 //   1. K or a few more rounds over the lanes' largest keys (a warp-wide maximum
 //      by redux; the lanes that have it step out) give a lower bound of the
-//      K-th largest key.  Only keys at or above it can be chosen: about 9 of
+//      K-th largest key; over quarters of the lanes' keys where few lanes
+//      have any.  Only keys at or above it can be chosen: about 9 of
 //      256 for K = 8, 22 of 1000 for K = 16.
 //   2. Those candidates are collected in the order of their experts, one a lane.
 //   3. A candidate's place is the number of candidates before it (larger key,
@@ -39,8 +43,10 @@ struct GateDev {
     int64_t T, stride;
     int E, K, G, KG, per;     // per = E / G
     int bf16, sigmoid, top2, renorm;
-    int vec;                  // a lane's logits load as 16-byte vectors (or whole, if shorter)
-    int lanes_per_group;      // lanes a group fills exactly (a power of two), 0 if it does not
+    int run;                  // experts a lane holds at most
+    int padded;               // runs of VPL: in shared memory a float is left out after each
+    int vec;                  // runs of VPL that load as 16-byte vectors (or whole, if shorter)
+    int group_lanes;          // lanes that hold a group, 0 if runs do not end with the groups
     float scale;
 };
 
@@ -61,11 +67,6 @@ __device__ __forceinline__ float load_logit(const GateDev &p, int64_t at) {
                   : static_cast<const float *>(p.logits)[at];
 }
 
-// kSmemStride: floats between two lanes' registers in shared memory, odd so
-// that the lanes' reads fall into different banks.
-template <int VPL>
-constexpr int kSmemStride = VPL + (VPL > 1);
-
 template <int VPL>
 __device__ __forceinline__ float lane_max(const float (&key)[VPL]) {
     float m = key[0];
@@ -75,33 +76,47 @@ __device__ __forceinline__ float lane_max(const float (&key)[VPL]) {
 }
 
 template <int VPL>
-__global__ void __launch_bounds__(32 * kGateWarps)
+__global__ void __launch_bounds__(32 * kGateWarps, 8)
 k_gate(GateDev p) {
-    __shared__ float s_keys[kGateWarps][32 * kSmemStride<VPL>];
+    __shared__ float s_keys[kGateWarps][32 * VPL + 32];
+    __shared__ float s_bias[32 * VPL + 32];
     __shared__ __align__(16) float s_key[kGateWarps][32];   // candidates
     __shared__ int s_cand[kGateWarps][32];
     __shared__ int s_ids[kGateWarps][kMaxTopK];
-    extern __shared__ float s_groups[];         // [warps][G], groups that straddle lanes only
+    extern __shared__ float s_groups[];         // [warps][G], where group_lanes is 0
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float *sk = s_keys[warp];
-    const int e0 = lane * VPL;                  // the lane's first expert
+    // Shared memory holds the experts in order; runs of VPL, a power of two,
+    // with a float left out after each, so that the lanes' reads of their runs
+    // fall into different banks.
+    const int pad = p.padded ? 1 : 0;
+    const int store0 = lane + pad * (lane / VPL), store_step = 32 + pad * (32 / VPL);
+    // the lane's first expert, and how many it has
+    int e0 = lane * p.run, have = min(p.run, p.E - e0);
+    if (p.group_lanes) {
+        const int g = lane / p.group_lanes, l = lane % p.group_lanes;
+        e0 = g * p.per + l * p.run;
+        have = g < p.G ? min(p.run, p.per - l * p.run) : 0;
+    }
+    const int run0 = e0 + pad * lane;           // the run's place in shared memory
     pdl_wait();
+    if (p.bias) {
+        for (int i = threadIdx.x; i < p.E; i += 32 * kGateWarps) s_bias[i + pad * (i / VPL)] = p.bias[i];
+        __syncthreads();
+    }
     for (int64_t t = (int64_t)blockIdx.x * kGateWarps + warp; t < p.T;
          t += (int64_t)gridDim.x * kGateWarps) {
         const bool active = p.mask == nullptr || p.mask[t] != 0;
         const int64_t row = t * p.stride;
         float key[VPL];
-        // ---- logits
-        if (!active) {
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) key[j] = ninf();
-        } else if (VPL <= 8 && p.vec) {
-            const bool in = e0 < p.E;
+        // ---- logits: what is not loaded stays NaN, which closes it
+        if (VPL <= 8 && p.vec) {
+            const bool in = active && have > 0;
             if (p.bf16) {
                 const uint16_t *src = static_cast<const uint16_t *>(p.logits) + row + e0;
                 uint32_t w[VPL > 1 ? VPL / 2 : 1];
 #pragma unroll
-                for (int j = 0; j < (VPL > 1 ? VPL / 2 : 1); ++j) w[j] = 0;
+                for (int j = 0; j < (VPL > 1 ? VPL / 2 : 1); ++j) w[j] = 0xffffffffu;
                 if (in) {
                     if constexpr (VPL == 8) *reinterpret_cast<uint4 *>(w) = __ldg(reinterpret_cast<const uint4 *>(src));
                     else if constexpr (VPL == 4) *reinterpret_cast<uint2 *>(w) = __ldg(reinterpret_cast<const uint2 *>(src));
@@ -113,6 +128,8 @@ k_gate(GateDev p) {
                     key[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
             } else {
                 const float *src = static_cast<const float *>(p.logits) + row + e0;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) key[j] = __uint_as_float(0xffffffffu);
                 if (in) {
                     if constexpr (VPL >= 4) {
 #pragma unroll
@@ -125,23 +142,26 @@ k_gate(GateDev p) {
                     }
                 }
             }
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) key[j] = in ? open_logit(key[j]) : ninf();
         } else {
             // neighbours on neighbouring lanes (whole sectors whatever the
             // alignment), then through shared memory to the lanes that hold them
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) key[j] = 32 * j + lane < p.E ? load_logit(p, row + 32 * j + lane) : ninf();
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
-                const int i = 32 * j + lane;
-                sk[i / VPL * kSmemStride<VPL> + i % VPL] = open_logit(key[j]);
+                key[j] = __uint_as_float(0xffffffffu);
+                if (active && 32 * j + lane < p.E) key[j] = load_logit(p, row + 32 * j + lane);
             }
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) key[j] = sk[lane * kSmemStride<VPL> + j];
+            for (int j = 0; j < VPL; ++j) {
+                sk[store0 + j * store_step] = key[j];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                key[j] = j < have ? sk[run0 + j] : __uint_as_float(0xffffffffu);
         }
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) key[j] = open_logit(key[j]);
         // ---- scores and keys
         float top = 0.0f, sum = 1.0f;           // softmax: the largest logit, the exponentials' sum
         if (!p.sigmoid) {
@@ -161,8 +181,7 @@ k_gate(GateDev p) {
             for (int j = 0; j < VPL; ++j) {
                 const float s = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-key[j]))
                                           : __expf(fminf(key[j], kF32Max) - top) * inv;
-                const float b = e0 + j < p.E ? __ldg(p.bias + e0 + j) : 0.0f;
-                key[j] = key[j] == ninf() ? ninf() : s + b;
+                if (key[j] != ninf()) key[j] = s + s_bias[run0 + j];
             }
         }
         // ---- groups
@@ -176,23 +195,23 @@ k_gate(GateDev p) {
             auto group_value = [&](float a, float b) {
                 return p.top2 && b != ninf() ? value(a) + value(b) : value(a);
             };
-            if (p.lanes_per_group) {
+            if (p.group_lanes) {
                 float a = ninf(), b = ninf();   // the group's two largest keys
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
                     b = fmaxf(b, fminf(a, key[j]));
                     a = fmaxf(a, key[j]);
                 }
-                for (int o = 1; o < p.lanes_per_group; o <<= 1) {
+                for (int o = 1; o < p.group_lanes; o <<= 1) {
                     const float oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
                     b = fmaxf(fminf(a, oa), fmaxf(b, ob));
                     a = fmaxf(a, oa);
                 }
                 const float gv = group_value(a, b);
-                const int mine = lane / p.lanes_per_group;
+                const int mine = lane / p.group_lanes;
                 int rank = 0;                   // groups that come before the lane's
                 for (int g = 0; g < p.G; ++g) {
-                    const float v = __shfl_sync(kFull, gv, g * p.lanes_per_group);
+                    const float v = __shfl_sync(kFull, gv, g * p.group_lanes);
                     rank += v > gv || (v == gv && g < mine);
                 }
                 if (rank >= p.KG || mine >= p.G) {
@@ -203,12 +222,14 @@ k_gate(GateDev p) {
                 float *sg = s_groups + warp * p.G;
                 __syncwarp();
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) sk[lane * kSmemStride<VPL> + j] = key[j];
+                for (int j = 0; j < VPL; ++j)
+                    if (j < have) sk[run0 + j] = key[j];
                 __syncwarp();
                 for (int g = lane; g < p.G; g += 32) {
                     float a = ninf(), b = ninf();
+#pragma unroll 8
                     for (int i = g * p.per; i < (g + 1) * p.per; ++i) {
-                        const float v = sk[i / VPL * kSmemStride<VPL> + i % VPL];
+                        const float v = sk[i + pad * (i / VPL)];
                         b = fmaxf(b, fminf(a, v));
                         a = fmaxf(a, v);
                     }
@@ -230,10 +251,10 @@ k_gate(GateDev p) {
                 }
                 __syncwarp();
                 const uint32_t *stay = reinterpret_cast<const uint32_t *>(sk);
-                int g = e0 / p.per, left = (g + 1) * p.per - e0;   // experts to the group's end
+                int g = have > 0 ? e0 / p.per : 0, left = (g + 1) * p.per - e0;   // experts to the group's end
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
-                    if (e0 + j < p.E && !((stay[g >> 5] >> (g & 31)) & 1u)) key[j] = ninf();
+                    if (j < have && !((stay[g >> 5] >> (g & 31)) & 1u)) key[j] = ninf();
                     if (--left == 0) { left = p.per; ++g; }
                 }
                 __syncwarp();
@@ -241,12 +262,31 @@ k_gate(GateDev p) {
         }
         // ---- the K best
         float bound = ninf(), cur = lane_max<VPL>(key);
-        for (int k = 0; k < p.K; k += 4)
+        if (VPL == 1 || __popc(__ballot_sync(kFull, cur > ninf())) >= 2 * p.K) {
+            for (int k = 0; k < p.K; k += 4)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                bound = warp_max(cur);
-                cur = cur == bound ? ninf() : cur;
+                for (int u = 0; u < 4; ++u) {
+                    bound = warp_max(cur);
+                    cur = cur == bound ? ninf() : cur;
+                }
+        } else {
+            // with few open lanes (the others' groups fell out) that bound would be
+            // low and the candidates many: the same over the largest keys of each
+            // lane's quarters
+            constexpr int Q = VPL < 4 ? VPL : 4;
+            float part[Q];
+#pragma unroll
+            for (int u = 0; u < Q; ++u) {
+                part[u] = key[u];
+#pragma unroll
+                for (int j = u + Q; j < VPL; j += Q) part[u] = fmaxf(part[u], key[j]);
             }
+            for (int k = 0; k < p.K; ++k) {
+                bound = warp_max(lane_max<Q>(part));
+#pragma unroll
+                for (int u = 0; u < Q; ++u) part[u] = part[u] == bound ? ninf() : part[u];
+            }
+        }
         // candidates of the lower lanes come first
         int own = 0;
 #pragma unroll
@@ -275,8 +315,11 @@ k_gate(GateDev p) {
             int place = 0;
             for (int i = 0; i < count; i += 4) {
                 const float4 o = *reinterpret_cast<const float4 *>(&s_key[warp][i]);
-                place += (o.x > mine || (o.x == mine && i < lane)) + (o.y > mine || (o.y == mine && i + 1 < lane)) +
-                         (o.z > mine || (o.z == mine && i + 2 < lane)) + (o.w > mine || (o.w == mine && i + 3 < lane));
+                // an equal key before the lane's own comes before it
+                if (i < lane ? o.x >= mine : o.x > mine) ++place;
+                if (i + 1 < lane ? o.y >= mine : o.y > mine) ++place;
+                if (i + 2 < lane ? o.z >= mine : o.z > mine) ++place;
+                if (i + 3 < lane ? o.w >= mine : o.w > mine) ++place;
             }
             if (lane < count && place < p.K) s_ids[warp][place] = s_cand[warp][lane];
         } else {
@@ -327,14 +370,12 @@ moe_status launch_vpl(GateDev &p, const moe_gate_desc &d, cudaStream_t stream) {
     const size_t align = lane_bytes < 16 ? lane_bytes : 16;
     // up to eight experts a lane a vector load of the lane's own logits uses
     // whole sectors; with more, or unaligned rows, they go through shared memory
-    p.vec = VPL <= 8 && p.E % VPL == 0 && (uintptr_t)p.logits % align == 0 &&
+    p.vec = VPL <= 8 && (VPL == 1 || (p.padded && p.E % VPL == 0)) && (uintptr_t)p.logits % align == 0 &&
             (size_t)d.logits_stride * esize % align == 0;
-    const int lanes = p.per % VPL == 0 ? p.per / VPL : 0;
-    p.lanes_per_group = lanes > 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     const int64_t want = (p.T + kGateWarps - 1) / kGateWarps;
     const int64_t cap = (int64_t)num_sms() * 16;
     const unsigned grid = (unsigned)(want < cap ? want : cap);
-    const size_t smem = p.G > 1 && !p.lanes_per_group ? (size_t)kGateWarps * p.G * sizeof(float) : 0;
+    const size_t smem = p.G > 1 && !p.group_lanes ? (size_t)kGateWarps * p.G * sizeof(float) : 0;
     MOE_LAUNCH("gate", k_gate<VPL>, grid, 32 * kGateWarps, smem, stream, p);
     return MOE_OK;
 }
@@ -363,7 +404,22 @@ moe_status launch_gate(const moe_gate_desc &d, const void *logits, const float *
     p.top2 = d.group_score == MOE_GATE_GROUP_TOP2;
     p.renorm = d.renormalize;
     p.scale = d.scale;
-    const int vpl = (p.E + 31) / 32;
+    // Lanes for a group: the most that 32 lanes give each, in powers of two.
+    p.group_lanes = 0;
+    p.run = (p.E + 31) / 32;
+    if (p.G > 1 && p.G <= 32) {
+        int lanes = 32;
+        while (lanes * p.G > 32) lanes /= 2;
+        const int run = (p.per + lanes - 1) / lanes;
+        if (run <= 32) {
+            p.group_lanes = lanes;
+            p.run = run;
+        }
+    }
+    int vpl = 1;
+    while (vpl < p.run) vpl *= 2;
+    if (!p.group_lanes) p.run = vpl;   // whole vectors
+    p.padded = p.run == vpl && vpl > 1 && (!p.group_lanes || p.per == p.group_lanes * p.run);
     if (vpl <= 1) return launch_vpl<1>(p, d, stream);
     if (vpl <= 2) return launch_vpl<2>(p, d, stream);
     if (vpl <= 4) return launch_vpl<4>(p, d, stream);
