@@ -2,6 +2,7 @@
 // argument checks, workspace layout and the order of kernels.
 #include "common.cuh"
 
+#include <algorithm>
 #include <cmath>
 
 namespace moe {
@@ -53,17 +54,31 @@ Fp8Layout ffn_layout(const moe_shape &s) {
     return L;
 }
 
-// Where the small-row kernel is the faster one: up to this many rows per expert
-// (128 experts, FFN 7168 x 4096: 1286 us against 1324 at 48 rows, 1642 against
-// 1342 at 64), and up to this many rows in all, which the large tiles spread
-// over too few SMs (one 4096 x 7168 product: 33 us against 38 at 128 rows).
-constexpr int64_t kSmallRowsPerExpert = 48;
-constexpr int64_t kSmallRows = 128;
+// AUTO's choice for a product, by an estimate of both kernels' time where the
+// weights' bytes do not bound it: tiles a multiprocessor (pair) works through x
+// blocks of K x the time a block takes it.  Measured times per block: a pair's
+// 256 x 256 (or 128 x 512) tile 0.52 us; 128 channels against up to 64 rows
+// 0.32 us; 128 channels of g against up to 32 rows 0.3 us and 64 rows 0.85 us
+// (two accumulators to read back for each).  Rows are taken as spread evenly.
+// What it chooses, measured (us, small against large): one product of 4096 x
+// 7168 with 256 rows 27/37, with 512 rows 43/37; 128 experts, 7168 x 4096 FFN,
+// 8 rows each 839/898, 32 rows each 1019/915.
+bool small_is_faster(const Fp8GemmArgs &a) {
+    const int64_t experts = std::min(a.E, a.cap_rows), rows = (a.cap_rows + experts - 1) / experts;
+    const int64_t num_kb = (a.Kd + 127) / 128, wblocks = (a.N + 127) / 128 / (a.q2 ? 2 : 1);
+    const int64_t blocks = (rows + 127) / 128, cols = (a.N + 255) / 256;
+    const int64_t pairs = std::max(1, num_sms() / 2), sms = num_sms();
+    const int64_t large_tiles = experts * (blocks / 2 * cols + blocks % 2 * ((cols + 1) / 2));
+    const double large = (double)((large_tiles + pairs - 1) / pairs * num_kb) * 0.52;
+    const int64_t tb = gemm_fp8_small_tile_rows(a);
+    const int64_t small_tiles = experts * ((rows + tb - 1) / tb) * wblocks;
+    const double small = (double)((small_tiles + sms - 1) / sms * num_kb) / gemm_fp8_small_split(a) *
+                         (a.q2 ? (tb > 32 ? 0.85 : 0.3) : 0.32);
+    return small <= 1.2 * large;   // a tie goes to the one that also prefetches its weights
+}
 
 moe_status run_gemm(int path, const Fp8GemmArgs &a, cudaStream_t stream) {
-    const bool small = path == MOE_FFN_PATH_SMALL ||
-                       (path == MOE_FFN_PATH_AUTO &&
-                        (a.cap_rows <= kSmallRowsPerExpert * a.E || a.cap_rows <= kSmallRows));
+    const bool small = path == MOE_FFN_PATH_SMALL || (path == MOE_FFN_PATH_AUTO && small_is_faster(a));
     return small ? launch_gemm_fp8_small(a, stream) : launch_gemm_fp8_large(a, stream);
 }
 

@@ -349,6 +349,9 @@ struct Fp8GemmArgs {
 // weights as the MMA's M side).
 moe_status launch_gemm_fp8_large(const Fp8GemmArgs &a, cudaStream_t stream);
 moe_status launch_gemm_fp8_small(const Fp8GemmArgs &a, cudaStream_t stream);
+// The small kernel's rows per tile, and the CTAs that share a tile's K.
+int gemm_fp8_small_tile_rows(const Fp8GemmArgs &a);
+int gemm_fp8_small_split(const Fp8GemmArgs &a);
 // Rows and scales of the tokens named by the dispatch's triplets; clears the
 // status word.
 moe_status launch_gather_fp8(const void *x, const float *xs, const int32_t *assist,

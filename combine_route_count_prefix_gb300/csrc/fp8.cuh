@@ -31,4 +31,10 @@ __device__ __forceinline__ void block_scale(float amax, float &s, float &inv) {
     inv = r * (kE4m3Max * 0x1p-9f);
 }
 
+// silu(a) * b; within a few units in the last place (expf and the hardware's
+// approximate division).
+__device__ __forceinline__ float swiglu(float a, float b) {
+    return __fdividef(a, 1.0f + expf(-a)) * b;
+}
+
 }  // namespace moe

@@ -10,11 +10,13 @@
 // block's scale and add to fp32 sums in registers, while the tensor cores work
 // on the next block in the other accumulator.
 //
-// Kernel shape (a cluster of two CTAs per 256-row x 256-channel tile, 128 rows
-// each, as many clusters as fit, 12 warps):
-//   warp 0      TMA producer, four-stage ring of 128 bytes of K: the CTA's 128
-//               rows (16 KB), and 128 of the tile's 256 channels (16 KB) that
-//               land in both CTAs, so that a channel is read once per pair
+// Kernel shape (clusters of two CTAs, as many as fit, 12 warps each): every CTA
+// computes 128 rows x 256 channels; a tall tile is 256 rows x 256 channels, and
+// an expert's last 128 rows, if their number of 128-row blocks is odd, make
+// wide tiles of 128 rows x 512 channels.
+//   warp 0      TMA producer, four-stage ring of 128 bytes of K: what the two
+//               CTAs share is read once, half by each, into both: a tall
+//               tile's channels (16 KB a half), a wide tile's rows (8 KB)
 //   warps 1, 3  MMA issuers: 4 x tcgen05.mma M=128 N=256 K=32 a block, even
 //               blocks into one 256-column accumulator and odd ones into the
 //               other (one thread spends about 450 cycles on the issue of a
@@ -92,28 +94,45 @@ struct LargeDev {
     int vec_scales;      // rows of a_scales can be read 16 bytes at a time
 };
 
-// The pair's tile: expert, this CTA's first row, its rows there (may be <= 0
-// or more than BM) and the column block.
+// A cluster's tile as one CTA sees it: expert, its first row, its rows there
+// (may be <= 0 or more than BM), its column block, and whether it is a wide one.
 struct Tile {
     int e, row0, rows, nb;
+    bool wide;
 };
 
+// Tiles of an expert with `rows` rows.
+__device__ __forceinline__ int tiles_of(int rows, int n_blocks) {
+    const int blocks = (rows + BM - 1) / BM;
+    return (blocks >> 1) * n_blocks + (blocks & 1) * ((n_blocks + 1) >> 1);
+}
+
 // Column-block-major within an expert: the clusters in flight share few weight
-// tiles, each read by all of the expert's row blocks while it is in L2.
-__device__ __forceinline__ Tile decode(int64_t tile, const LargeDev &p, const int32_t *s_blk,
+// tiles, each read by all of the expert's row blocks while it is in L2.  Not
+// inlined: once per tile a call costs nothing, and its registers would push
+// some of the epilogue's sums to memory.
+__device__ __noinline__ Tile decode(int64_t tile, const LargeDev &p, const int32_t *s_tile,
                                        const int32_t *s_off, int rank) {
     int lo = 0, hi = p.E - 1;
     while (lo < hi) {   // last expert whose first tile is <= tile
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)s_blk[mid] * p.n_blocks <= tile) lo = mid; else hi = mid - 1;
+        if (s_tile[mid] <= tile) lo = mid; else hi = mid - 1;
     }
-    const int nm = s_blk[lo + 1] - s_blk[lo];   // >= 1: an expert with no rows owns no tile
-    const int64_t local = tile - (int64_t)s_blk[lo] * p.n_blocks;
+    const int rows = s_off[lo + 1] - s_off[lo];
+    const int pairs = (rows + BM - 1) / BM >> 1;   // tall row blocks
+    const int local = (int)tile - s_tile[lo];
     Tile t;
     t.e = lo;
-    t.nb = (int)(local / nm);
-    t.row0 = s_off[lo] + (int)(local % nm) * (2 * BM) + rank * BM;
-    t.rows = s_off[lo + 1] - t.row0;
+    t.wide = local >= pairs * p.n_blocks;
+    if (!t.wide) {
+        t.nb = local / pairs;
+        t.row0 = s_off[lo] + (local % pairs) * (2 * BM) + rank * BM;
+        t.rows = s_off[lo + 1] - t.row0;
+    } else {
+        t.nb = 2 * (local - pairs * p.n_blocks) + rank;
+        t.row0 = s_off[lo] + pairs * (2 * BM);
+        t.rows = t.nb < p.n_blocks ? s_off[lo + 1] - t.row0 : 0;
+    }
     return t;
 }
 
@@ -151,7 +170,8 @@ __device__ __forceinline__ int group_col(int cg, int j) {
 
 template <int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
-k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA64,
+                 const __grid_constant__ CUtensorMap tmB,
                 LargeDev p) {
     // aligned by its declaration, so that every address in it is a constant
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -168,7 +188,7 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     float *s_amax = reinterpret_cast<float *>(smem + RING_BYTES + kBarrierBytes);   // [2][CG][BM]
     float *s_scale = s_amax + kAmaxBytes / sizeof(float);
     int32_t *s_off = reinterpret_cast<int32_t *>(s_scale + kScaleBytes / sizeof(float));
-    int32_t *s_blk = s_off + (kMaxExperts + 1);
+    int32_t *s_tile = s_off + (kMaxExperts + 1);
 
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -193,6 +213,7 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
     if (warp == 0 && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA64) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
     }
     pdl_wait();   // everything below may read what earlier kernels wrote
@@ -202,21 +223,21 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x) s_off[i] = p.offsets[i];
     __syncthreads();
     if (warp == 0) {
-        // s_blk[e] = 256-row blocks of the experts before e (warp scan)
+        // s_tile[e] = tiles of the experts before e (warp scan)
         int carry = 0;
         for (int base = 0; base < p.E; base += 32) {
             const int e = base + lane;
-            const int c = e < p.E ? (s_off[e + 1] - s_off[e] + 2 * BM - 1) / (2 * BM) : 0;
+            const int c = e < p.E ? tiles_of(s_off[e + 1] - s_off[e], p.n_blocks) : 0;
             int x = c;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, d);
                 if (lane >= d) x += y;
             }
-            if (e < p.E) s_blk[e] = carry + x - c;
+            if (e < p.E) s_tile[e] = carry + x - c;
             carry += __shfl_sync(0xffffffffu, x, 31);
         }
-        if (lane == 0) s_blk[p.E] = carry;
+        if (lane == 0) s_tile[p.E] = carry;
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, TMEM_COLS);
@@ -227,7 +248,7 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     cluster_sync();   // both CTAs' barriers exist before any copy or commit reaches them
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int64_t total_tiles = (int64_t)s_blk[p.E] * p.n_blocks;
+    const int64_t total_tiles = s_tile[p.E];
     // the cluster's tiles: its index, and every cluster count after it
     const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const int my_tiles = first < total_tiles ? (int)((total_tiles - first + step - 1) / step) : 0;
@@ -241,9 +262,10 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int64_t armed = 0;   // stage uses
             bool ok = true;
             for (int i = 0; ok && i < my_tiles; ++i) {
-                const Tile t = decode(first + i * step, p, s_blk, s_off, (int)rank);
-                const int ch0 = EPI == EPI_SWIGLU ? (int)rank * (p.N / 2) + t.nb * 128
-                                                  : t.nb * BN + (int)rank * (BN / 2);
+                const Tile t = decode(first + i * step, p, s_tile, s_off, (int)rank);
+                // the tile's two 128-channel halves
+                const int ch0 = EPI == EPI_SWIGLU ? t.nb * 128 : t.nb * BN;
+                const int ch1 = EPI == EPI_SWIGLU ? ch0 + p.N / 2 : ch0 + BN / 2;
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     // free once both CTAs' MMAs have read what was there: the
                     // channels are written to both
@@ -251,11 +273,18 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     uint8_t *sa = smem + (size_t)stage * STAGE_BYTES;
                     mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
                     ++armed;
-                    // rows past this CTA's half (or past the buffer) only reach
+                    // rows past this CTA's (or past the buffer) only reach
                     // accumulator rows that are never stored; bytes past K are 0
-                    tma_load_2d(sa, &tmA, &full[stage], kb * BK, t.row0);
-                    tma_load_3d_multicast(sa + A_BYTES + rank * (B_BYTES / 2), &tmB, &full[stage],
-                                          kb * BK, ch0, t.e, 0x3);
+                    if (!t.wide) {
+                        tma_load_2d(sa, &tmA, &full[stage], kb * BK, t.row0);
+                        tma_load_3d_multicast(sa + A_BYTES + rank * (B_BYTES / 2), &tmB, &full[stage],
+                                              kb * BK, rank ? ch1 : ch0, t.e, 0x3);
+                    } else {
+                        tma_load_2d_multicast(sa + rank * (A_BYTES / 2), &tmA64, &full[stage], kb * BK,
+                                              t.row0 + (int)rank * (BM / 2), 0x3);
+                        tma_load_3d(sa + A_BYTES, &tmB, &full[stage], kb * BK, ch0, t.e);
+                        tma_load_3d(sa + A_BYTES + B_BYTES / 2, &tmB, &full[stage], kb * BK, ch1, t.e);
+                    }
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
@@ -278,7 +307,7 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         uint32_t phase = 0;
         bool ok = true;
         for (int i = 0; ok && i < my_tiles; ++i) {
-            const Tile t = decode(first + i * step, p, s_blk, s_off, (int)rank);
+            const Tile t = decode(first + i * step, p, s_tile, s_off, (int)rank);
             // lane's rows lane + 32 u, clamped to rows that exist
             const int64_t row0 = min((int64_t)t.row0, p.cap_rows - 1);
             const int last = (int)min((int64_t)max(t.rows, 1), p.cap_rows - row0) - 1;
@@ -286,8 +315,9 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int at[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) at[u] = min(lane + 32 * u, last) * p.num_kb;
-            const int wb0 = EPI == EPI_SWIGLU ? t.nb : 2 * t.nb;
-            const int wb1 = EPI == EPI_SWIGLU ? t.nb + p.w_blocks / 2 : min(2 * t.nb + 1, p.w_blocks - 1);
+            // (clamped: a wide tile's second column block may lie past the last)
+            const int wb0 = min(EPI == EPI_SWIGLU ? t.nb : 2 * t.nb, p.w_blocks - 1);
+            const int wb1 = min(EPI == EPI_SWIGLU ? t.nb + p.w_blocks / 2 : 2 * t.nb + 1, p.w_blocks - 1);
             const float *sw0 = p.w_scales + ((int64_t)t.e * p.w_blocks + wb0) * p.num_kb;
             const float *sw1 = p.w_scales + ((int64_t)t.e * p.w_blocks + wb1) * p.num_kb;
             for (int kb = 0; kb < p.num_kb; kb += SB) {
@@ -373,7 +403,7 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         int sc_stage = 0;
         uint32_t sc_phase = 0;
         for (int it = 0; it < my_tiles; ++it) {
-            const Tile t = decode((int64_t)(blockIdx.x >> 1) + (int64_t)it * (gridDim.x >> 1), p, s_blk, s_off, (int)rank);
+            const Tile t = decode((int64_t)(blockIdx.x >> 1) + (int64_t)it * (gridDim.x >> 1), p, s_tile, s_off, (int)rank);
             const bool rows_here = q * 32 < t.rows;   // warp-uniform
             float2 acc[CPT / 2];
 #pragma unroll
@@ -425,8 +455,8 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     float amax = 0.0f;
 #pragma unroll
                     for (int i = 0; i < HC / 2; ++i) {
-                        acc[i].x = silu_f32(acc[i].x) * acc[HC / 2 + i].x;
-                        acc[i].y = silu_f32(acc[i].y) * acc[HC / 2 + i].y;
+                        acc[i].x = swiglu(acc[i].x, acc[HC / 2 + i].x);
+                        acc[i].y = swiglu(acc[i].y, acc[HC / 2 + i].y);
                         amax = fmaxf(amax, fmaxf(fabsf(acc[i].x), fabsf(acc[i].y)));
                     }
                     // the block's other channels are with the quadrant's other warps
@@ -532,21 +562,23 @@ template <int EPI>
 moe_status launch(const Fp8GemmArgs &a, const LargeDev &d, cudaStream_t stream) {
     const int clusters = clusters_that_fit<EPI>();
     if (clusters <= 0) return MOE_ERR_UNSUPPORTED;
-    CUtensorMap ma, mb;
+    CUtensorMap ma, ma64, mb;
     const uint64_t adims[2] = {(uint64_t)a.Kd, (uint64_t)a.cap_rows};
     const uint64_t astr[1] = {(uint64_t)a.Kd};
-    const uint32_t abox[2] = {BK, BM};
+    const uint32_t abox[2] = {BK, BM}, abox64[2] = {BK, BM / 2};
     const uint64_t bdims[3] = {(uint64_t)a.Kd, (uint64_t)a.N, (uint64_t)a.E};
     const uint64_t bstr[2] = {(uint64_t)a.Kd, (uint64_t)a.Kd * a.N};
     const uint32_t bbox[3] = {BK, BN / 2, 1};
     if (!make_tensor_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, a.a, 2, adims,
                          astr, abox) ||
+        !make_tensor_map(&ma64, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, a.a, 2, adims,
+                         astr, abox64) ||
         !make_tensor_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, a.w, 3, bdims,
                          bstr, bbox))
         return MOE_ERR_CUDA;
     const char *names[3] = {"gemm_fp8_f32", "gemm_fp8_bf16", "gemm_fp8_swiglu"};
     MOE_LAUNCH_CLUSTER(names[EPI], k_gemm_fp8_large<EPI>, 2 * clusters, THREADS, SMEM_BYTES, stream, 2u,
-                       ma, mb, d);
+                       ma, ma64, mb, d);
     return MOE_OK;
 }
 

@@ -439,7 +439,7 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
                 for (int i = 0; i < CW; ++i) {
                     const int c = cf + cs * i;
                     if (c >= t.rows) break;
-                    const float g = silu_f32(acc[0][i]) * acc[NG - 1][i];
+                    const float g = swiglu(acc[0][i], acc[NG - 1][i]);
                     acc[0][i] = g;
                     // magnitudes order as unsigned integers; a NaN counts as 0
                     const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(g), 0.0f)));
@@ -502,14 +502,7 @@ moe_status launch(const Fp8GemmArgs &a, SmallDev d, cudaStream_t stream) {
         !make_tensor_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, a.w, 3, wdims,
                          wstr, wbox))
         return MOE_ERR_CUDA;
-    // Tiles at most this call can have: share them among clusters of 2, 4 or 8
-    // CTAs while that still leaves no SM with a second tile.
-    const int64_t row_tiles = std::min<int64_t>(a.E, a.cap_rows) + a.cap_rows / TB;
-    const int64_t tiles = row_tiles * d.n_wblocks;
-    d.split = 1;
-    if (C::SPLIT)
-        while (d.split < kMaxSplit && tiles * d.split * 2 <= num_sms() && d.split * 2 <= d.num_kb)
-            d.split *= 2;
+    d.split = gemm_fp8_small_split(a);
     const char *names[3] = {"gemm_fp8_small_f32", "gemm_fp8_small_bf16", "gemm_fp8_small_swiglu"};
     const unsigned grid = (unsigned)(num_sms() / d.split * d.split);
     if (d.split == 1)
@@ -522,10 +515,25 @@ moe_status launch(const Fp8GemmArgs &a, SmallDev d, cudaStream_t stream) {
 
 template <int EPI>
 moe_status launch_epi(const Fp8GemmArgs &a, const SmallDev &d, cudaStream_t stream) {
-    return a.cap_rows > 16 * a.E ? launch<EPI, 64>(a, d, stream) : launch<EPI, 32>(a, d, stream);
+    return gemm_fp8_small_tile_rows(a) == 64 ? launch<EPI, 64>(a, d, stream) : launch<EPI, 32>(a, d, stream);
 }
 
 }  // namespace
+
+// 32 rows where they average at most 16 an expert: few experts then have more.
+int gemm_fp8_small_tile_rows(const Fp8GemmArgs &a) { return a.cap_rows > 16 * a.E ? 64 : 32; }
+
+int gemm_fp8_small_split(const Fp8GemmArgs &a) {
+    const int tb = gemm_fp8_small_tile_rows(a);
+    if (a.q2 && !(tb == 32 ? Cfg<EPI_SWIGLU, 32>::SPLIT : Cfg<EPI_SWIGLU, 64>::SPLIT)) return 1;
+    // Tiles at most this call can have: share them among clusters of 2, 4 or 8
+    // CTAs while that still leaves no SM with a second tile.
+    const int64_t wblocks = (a.N + BW - 1) / BW / (a.q2 ? 2 : 1), num_kb = (a.Kd + BK - 1) / BK;
+    const int64_t tiles = (std::min<int64_t>(a.E, a.cap_rows) + a.cap_rows / tb) * wblocks;
+    int split = 1;
+    while (split < kMaxSplit && tiles * split * 2 <= num_sms() && split * 2 <= num_kb) split *= 2;
+    return split;
+}
 
 moe_status launch_gemm_fp8_small(const Fp8GemmArgs &a, cudaStream_t stream) {
     SmallDev d;
