@@ -31,10 +31,14 @@ __device__ __forceinline__ void block_scale(float amax, float &s, float &inv) {
     inv = r * (kE4m3Max * 0x1p-9f);
 }
 
-// silu(a) * b; within a few units in the last place (expf and the hardware's
-// approximate division).
+// silu(a) * b, with the hardware's approximate exponential and reciprocal
+// (relative error about 1e-7 + 1e-7 |a|, before a rounding to e4m3 at 6e-2):
+// with expf and a division it was twice the instructions.
 __device__ __forceinline__ float swiglu(float a, float b) {
-    return __fdividef(a, 1.0f + expf(-a)) * b;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return a * r * b;
 }
 
 }  // namespace moe
