@@ -42,10 +42,9 @@ struct GateDev {
     uint8_t *route_mask;
     int64_t T, stride;
     int E, K, G, KG, per;     // per = E / G
-    int bf16, sigmoid, top2, renorm;
+    int sigmoid, top2, renorm;
     int run;                  // experts a lane holds at most
     int padded;               // runs of VPL: in shared memory a float is left out after each
-    int vec;                  // runs of VPL that load as 16-byte vectors (or whole, if shorter)
     int group_lanes;          // lanes that hold a group, 0 if runs do not end with the groups
     float scale;
 };
@@ -62,8 +61,9 @@ __device__ __forceinline__ float warp_max(float v) {
 // A logit as the keys see it: closed experts (NaN included) at -inf.
 __device__ __forceinline__ float open_logit(float v) { return v > kClosed ? v : ninf(); }
 
+template <bool BF16>
 __device__ __forceinline__ float load_logit(const GateDev &p, int64_t at) {
-    return p.bf16 ? bf16_bits_to_float(static_cast<const uint16_t *>(p.logits)[at])
+    return BF16 ? bf16_bits_to_float(static_cast<const uint16_t *>(p.logits)[at])
                   : static_cast<const float *>(p.logits)[at];
 }
 
@@ -75,13 +75,13 @@ __device__ __forceinline__ float lane_max(const float (&key)[VPL]) {
     return m;
 }
 
-template <int VPL>
+// VEC: runs load as vectors.
+template <int VPL, bool BF16, bool VEC>
 __global__ void __launch_bounds__(32 * kGateWarps, 8)
 k_gate(GateDev p) {
     __shared__ float s_keys[kGateWarps][32 * VPL + 32];
     __shared__ float s_bias[32 * VPL + 32];
-    __shared__ __align__(16) float s_key[kGateWarps][32];   // candidates
-    __shared__ int s_cand[kGateWarps][32];
+    __shared__ __align__(16) float2 s_cand[kGateWarps][32];   // candidates: key, expert
     __shared__ int s_ids[kGateWarps][kMaxTopK];
     extern __shared__ float s_groups[];         // [warps][G], where group_lanes is 0
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -110,9 +110,9 @@ k_gate(GateDev p) {
         const int64_t row = t * p.stride;
         float key[VPL];
         // ---- logits: what is not loaded stays NaN, which closes it
-        if (VPL <= 8 && p.vec) {
+        if constexpr (VEC) {
             const bool in = active && have > 0;
-            if (p.bf16) {
+            if constexpr (BF16) {
                 const uint16_t *src = static_cast<const uint16_t *>(p.logits) + row + e0;
                 uint32_t w[VPL > 1 ? VPL / 2 : 1];
 #pragma unroll
@@ -148,7 +148,7 @@ k_gate(GateDev p) {
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 key[j] = __uint_as_float(0xffffffffu);
-                if (active && 32 * j + lane < p.E) key[j] = load_logit(p, row + 32 * j + lane);
+                if (active && 32 * j + lane < p.E) key[j] = load_logit<BF16>(p, row + 32 * j + lane);
             }
             __syncwarp();
 #pragma unroll
@@ -287,10 +287,12 @@ k_gate(GateDev p) {
                 for (int u = 0; u < Q; ++u) part[u] = part[u] == bound ? ninf() : part[u];
             }
         }
+        bound = fmaxf(bound, -kF32Max);         // closed experts are no candidates
         // candidates of the lower lanes come first
         int own = 0;
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) own += key[j] >= bound && key[j] > ninf();
+        for (int j = 0; j < VPL; ++j)
+            if (key[j] >= bound) ++own;
         int upto = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -300,28 +302,28 @@ k_gate(GateDev p) {
         const int count = __shfl_sync(kFull, upto, 31);
         const int n = min(count, p.K);          // experts that are chosen
         if (count <= 32) {
-            s_key[warp][lane] = ninf();
+            float2 *cand = s_cand[warp];
+            cand[lane] = make_float2(ninf(), 0.0f);
             __syncwarp();
-            int at = upto - own;
+            float2 *to = cand + (upto - own);
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
-                if (key[j] >= bound && key[j] > ninf()) {
-                    s_key[warp][at] = key[j];
-                    s_cand[warp][at] = e0 + j;
-                    ++at;
-                }
+                if (key[j] >= bound) *to++ = make_float2(key[j], __int_as_float(e0 + j));
             __syncwarp();
-            const float mine = s_key[warp][lane];
+            const float2 own_cand = cand[lane];
+            const float mine = own_cand.x;
             int place = 0;
             for (int i = 0; i < count; i += 4) {
-                const float4 o = *reinterpret_cast<const float4 *>(&s_key[warp][i]);
+                const float4 a = *reinterpret_cast<const float4 *>(cand + i);
+                const float4 b = *reinterpret_cast<const float4 *>(cand + i + 2);
+                const float4 o = make_float4(a.x, a.z, b.x, b.z);
                 // an equal key before the lane's own comes before it
                 if (i < lane ? o.x >= mine : o.x > mine) ++place;
                 if (i + 1 < lane ? o.y >= mine : o.y > mine) ++place;
                 if (i + 2 < lane ? o.z >= mine : o.z > mine) ++place;
                 if (i + 3 < lane ? o.w >= mine : o.w > mine) ++place;
             }
-            if (lane < count && place < p.K) s_ids[warp][place] = s_cand[warp][lane];
+            if (lane < count && place < p.K) s_ids[warp][place] = __float_as_int(own_cand.y);
         } else {
             uint32_t used = 0;
             for (int k = 0; k < n; ++k) {
@@ -344,7 +346,7 @@ k_gate(GateDev p) {
         float w = 0.0f;
         if (lane < n) {
             id = s_ids[warp][lane];
-            const float l = fminf(load_logit(p, row + id), kF32Max);
+            const float l = fminf(load_logit<BF16>(p, row + id), kF32Max);
             w = __fdividef(p.sigmoid ? 1.0f : expf(l - top), p.sigmoid ? 1.0f + expf(-l) : sum);
         }
         __syncwarp();
@@ -363,21 +365,34 @@ k_gate(GateDev p) {
     }
 }
 
-template <int VPL>
-moe_status launch_vpl(GateDev &p, const moe_gate_desc &d, cudaStream_t stream) {
-    const size_t esize = p.bf16 ? 2 : 4;
-    const size_t lane_bytes = VPL * esize;
+template <int VPL, bool BF16>
+moe_status launch_vpl(const GateDev &p, cudaStream_t stream) {
+    const size_t lane_bytes = VPL * (BF16 ? 2 : 4);
     const size_t align = lane_bytes < 16 ? lane_bytes : 16;
     // up to eight experts a lane a vector load of the lane's own logits uses
     // whole sectors; with more, or unaligned rows, they go through shared memory
-    p.vec = VPL <= 8 && (VPL == 1 || (p.padded && p.E % VPL == 0)) && (uintptr_t)p.logits % align == 0 &&
-            (size_t)d.logits_stride * esize % align == 0;
+    const bool vec = VPL <= 8 && (VPL == 1 || (p.padded && p.E % VPL == 0)) &&
+                     (uintptr_t)p.logits % align == 0 &&
+                     (size_t)p.stride * (BF16 ? 2 : 4) % align == 0;
     const int64_t want = (p.T + kGateWarps - 1) / kGateWarps;
     const int64_t cap = (int64_t)num_sms() * 16;
     const unsigned grid = (unsigned)(want < cap ? want : cap);
     const size_t smem = p.G > 1 && !p.group_lanes ? (size_t)kGateWarps * p.G * sizeof(float) : 0;
-    MOE_LAUNCH("gate", k_gate<VPL>, grid, 32 * kGateWarps, smem, stream, p);
+    auto kernel = vec ? k_gate<VPL, BF16, VPL <= 8> : k_gate<VPL, BF16, false>;
+    MOE_LAUNCH("gate", kernel, grid, 32 * kGateWarps, smem, stream, p);
     return MOE_OK;
+}
+
+template <bool BF16>
+moe_status launch_type(const GateDev &p, int vpl, cudaStream_t stream) {
+    switch (vpl) {
+        case 1: return launch_vpl<1, BF16>(p, stream);
+        case 2: return launch_vpl<2, BF16>(p, stream);
+        case 4: return launch_vpl<4, BF16>(p, stream);
+        case 8: return launch_vpl<8, BF16>(p, stream);
+        case 16: return launch_vpl<16, BF16>(p, stream);
+    }
+    return launch_vpl<32, BF16>(p, stream);
 }
 
 }  // namespace
@@ -399,7 +414,6 @@ moe_status launch_gate(const moe_gate_desc &d, const void *logits, const float *
     p.G = (int)d.num_groups;
     p.KG = (int)d.topk_groups;
     p.per = p.E / p.G;
-    p.bf16 = d.logits_dtype == MOE_DTYPE_BF16;
     p.sigmoid = d.score == MOE_GATE_SIGMOID;
     p.top2 = d.group_score == MOE_GATE_GROUP_TOP2;
     p.renorm = d.renormalize;
@@ -420,12 +434,8 @@ moe_status launch_gate(const moe_gate_desc &d, const void *logits, const float *
     while (vpl < p.run) vpl *= 2;
     if (!p.group_lanes) p.run = vpl;   // whole vectors
     p.padded = p.run == vpl && vpl > 1 && (!p.group_lanes || p.per == p.group_lanes * p.run);
-    if (vpl <= 1) return launch_vpl<1>(p, d, stream);
-    if (vpl <= 2) return launch_vpl<2>(p, d, stream);
-    if (vpl <= 4) return launch_vpl<4>(p, d, stream);
-    if (vpl <= 8) return launch_vpl<8>(p, d, stream);
-    if (vpl <= 16) return launch_vpl<16>(p, d, stream);
-    return launch_vpl<32>(p, d, stream);
+    return d.logits_dtype == MOE_DTYPE_BF16 ? launch_type<true>(p, vpl, stream)
+                                            : launch_type<false>(p, vpl, stream);
 }
 
 }  // namespace moe
