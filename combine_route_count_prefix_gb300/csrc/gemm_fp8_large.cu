@@ -216,6 +216,10 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA64) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
     }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, TMEM_COLS);
+        tmem_relinquish();
+    }
     pdl_wait();   // everything below may read what earlier kernels wrote
     // Block 0 starts no later than any other, and no wait gives up before two
     // seconds have passed, so no bit set by this call is lost.
@@ -238,10 +242,6 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             carry += __shfl_sync(0xffffffffu, x, 31);
         }
         if (lane == 0) s_tile[p.E] = carry;
-    }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, TMEM_COLS);
-        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();

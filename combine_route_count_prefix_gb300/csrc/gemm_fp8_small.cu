@@ -121,12 +121,27 @@ __device__ __forceinline__ void arrive_cluster(uint64_t *bar, uint32_t rank) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank))
                  : "memory");
 }
-// wait_bounded that also acquires what other CTAs of the cluster released.
+// The bounded wait that also acquires what other CTAs of the cluster released.
 __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                              int32_t *status) {
-    const bool ok = wait_bounded(bar, parity, abort_flag, status);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    return ok;
+    const uint64_t t0 = globaltimer();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSliceNs)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        if (globaltimer() - t0 > kTimeoutNs) {
+            *abort_flag = 1;
+            if (status) atomicOr(status, MOE_DEV_TIMEOUT);
+            return false;
+        }
+    }
 }
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     float v;
@@ -196,6 +211,10 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmRows) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmW) : "memory");
     }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
     if (!p.early) pdl_wait();   // everything below may read what earlier kernels wrote
     // Block 0 starts no later than any other, and no wait gives up before two
     // seconds have passed, so no bit set by this call is lost.
@@ -219,13 +238,11 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
         }
         if (lane == 0) s_blk[p.E] = carry;
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, C::TMEM_COLS);
-        tmem_relinquish();
-    }
     tc_fence_before();
     __syncthreads();
-    if (S > 1) cluster_sync();   // every CTA's barriers exist before any remote arrival
+    // every CTA's barriers exist before any remote arrival: awaited only there
+    if (S > 1) cluster_arrive();
+    bool met = S == 1;   // this thread has waited for it
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int64_t total_tiles = (int64_t)s_blk[p.E] * p.n_wblocks;
@@ -359,6 +376,14 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
                     if (lane + 32 * u < CW)
 #pragma unroll
                         for (int g = 0; g < NG; ++g) sb[g * CW + lane + 32 * u] = sa_n[u] * sw_n[g];
+                __syncwarp();
+                // in registers before the wait, where they fit
+                constexpr int EARLY = CW <= 16 ? NG * CW : 4;
+                float se[EARLY];
+                if constexpr (CW <= 16)
+#pragma unroll
+                    for (int i = 0; i < NG * CW; i += 4)
+                        *reinterpret_cast<float4 *>(se + i) = *reinterpret_cast<const float4 *>(sb + i);
                 if (kb + 1 < kb1) {   // the next block's scales, while this one is awaited
 #pragma unroll
                     for (int u = 0; u < SPT; ++u) sa_n[u] = __ldg(sa[u] + kb + 1);
@@ -366,10 +391,9 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
                     for (int g = 0; g < NG; ++g)
                         sw_n[g] = __ldg(sw + (int64_t)g * (p.w_blocks / 2) * p.num_kb + kb + 1);
                 }
-                const bool w = wait_bounded(&acc_full[accb], acc_phase, abort_flag, p.status);
+                const bool w = wait_bounded_inline(&acc_full[accb], acc_phase, abort_flag, p.status);
                 if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
                 tc_fence_after();
-                __syncwarp();
                 const uint32_t taddr =
                     tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(accb * NG * TB + c0);
 #pragma unroll
@@ -383,7 +407,8 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
                             tmem_ld_wait();
 #pragma unroll
                             for (int i = 0; i < LDW; i += 4) {
-                                const float4 s = *reinterpret_cast<const float4 *>(sb + g * CW + LDW * j + i);
+                                const float4 s = *reinterpret_cast<const float4 *>(
+                                    (CW <= 16 ? se : sb) + g * CW + LDW * j + i);
                                 float *a = &acc[g][LDW * j + i];
                                 fma2(a[0], a[1], s.x, s.y, r[i], r[i + 1]);
                                 fma2(a[2], a[3], s.z, s.w, r[i + 2], r[i + 3]);
@@ -403,6 +428,8 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
             // cluster's sums are joined, to row rank + S * (2 i + hf)
             if constexpr (C::SPLIT) {
                 if (S > 1) {
+                    if (!met) cluster_wait();
+                    met = true;
                     if (!__all_sync(0xffffffffu, wait_cluster(part_free, tile_par ^ 1u, abort_flag, p.status)))
                         break;
 #pragma unroll
@@ -414,16 +441,24 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
                     if (lane < S) arrive_cluster(part_full, (uint32_t)lane);
                     if (!__all_sync(0xffffffffu, wait_cluster(part_full, tile_par, abort_flag, p.status)))
                         break;
+                    // a row's S partial sums are fetched together, then added in rank order
 #pragma unroll
                     for (int i = 0; i < CW; ++i) {
                         const int c = rank + S * (2 * i + hf);
                         if (c >= t.rows) break;
+                        float v[NG][kMaxSplit];
+#pragma unroll
+                        for (int g = 0; g < NG; ++g)
+#pragma unroll
+                            for (int s = 0; s < kMaxSplit; ++s)
+                                v[g][s] = s < S ? ld_cluster(cluster_addr(s_part + (g * TB + c) * BW + q * 32 + lane,
+                                                                          (uint32_t)s))
+                                                : 0.0f;
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
-                            const float *src = s_part + (g * TB + c) * BW + q * 32 + lane;
-                            float v = 0.0f;
-                            for (int s = 0; s < S; ++s) v += ld_cluster(cluster_addr(src, (uint32_t)s));
-                            acc[g][i] = v;
+                            acc[g][i] = v[g][0];
+#pragma unroll
+                            for (int s = 1; s < kMaxSplit; ++s) acc[g][i] += v[g][s];
                         }
                     }
                     __syncwarp();
@@ -481,6 +516,7 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
 
     tc_fence_before();
     __syncthreads();
+    if (!met) cluster_wait();
     if (S > 1) cluster_sync();   // peers may still read this CTA's partial sums
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
