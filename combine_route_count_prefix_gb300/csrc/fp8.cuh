@@ -18,17 +18,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
 }
-// Scale a / 448 and its inverse 448 / a for a block whose largest magnitude is
-// amax, each within two units in the last place (the hardware's approximate
-// reciprocal: two IEEE divisions per thread were half of the norm's
-// instructions).  The reciprocal is taken of a / 512, so that no finite a makes
-// it a denormal.
+// 448 / a within two units in the last place, for a >= 2^-100.  The reciprocal
+// is taken of a / 512, so that no finite a makes it a denormal.
+__device__ __forceinline__ float inverse_scale(float a) {
+    return __frcp_rn(a * 0x1p-9f) * (kE4m3Max * 0x1p-9f);
+}
+// Scale a / 448 and its inverse for a block whose largest magnitude is amax.
+// (Two IEEE divisions per thread were half of the norm's instructions.)
 __device__ __forceinline__ void block_scale(float amax, float &s, float &inv) {
     const float a = fmaxf(amax, kAmaxFloor);
     s = a * (1.0f / kE4m3Max);
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * 0x1p-9f));
-    inv = r * (kE4m3Max * 0x1p-9f);
+    inv = inverse_scale(a);
 }
 
 // silu(a) * b, with the hardware's approximate exponential and reciprocal

@@ -61,6 +61,12 @@ constexpr int CPT = BN / CG;             // sums per epilogue thread
 constexpr int HC = CPT / 2;
 constexpr int EPI_WARP0 = 4;
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+// Registers: the block is launched with 168 a thread (65536 / 384, in steps of
+// 8); the first warpgroup gives up what the two epilogue warpgroups take.  With
+// 168 the epilogue's 128 sums and what it loads did not fit, and a few spilled
+// words a block cost a tenth of the time.
+constexpr int REGS_LAUNCH = 168, REGS_ISSUE = 72, REGS_EPI = 216;
+static_assert(REGS_ISSUE + 2 * REGS_EPI <= 3 * REGS_LAUNCH, "register split");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr size_t kBarrierBytes = 512;
 constexpr size_t kAmaxBytes = 2 * CG * BM * sizeof(float);
@@ -108,10 +114,8 @@ __device__ __forceinline__ int tiles_of(int rows, int n_blocks) {
 }
 
 // Column-block-major within an expert: the clusters in flight share few weight
-// tiles, each read by all of the expert's row blocks while it is in L2.  Not
-// inlined: once per tile a call costs nothing, and its registers would push
-// some of the epilogue's sums to memory.
-__device__ __noinline__ Tile decode(int64_t tile, const LargeDev &p, const int32_t *s_tile,
+// tiles, each read by all of the expert's row blocks while it is in L2.
+__device__ __forceinline__ Tile decode(int64_t tile, const LargeDev &p, const int32_t *s_tile,
                                        const int32_t *s_off, int rank) {
     int lo = 0, hi = p.E - 1;
     while (lo < hi) {   // last expert whose first tile is <= tile
@@ -254,6 +258,7 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int my_tiles = first < total_tiles ? (int)((total_tiles - first + step - 1) / step) : 0;
 
     if (warp < EPI_WARP0) {
+      regs_dec<REGS_ISSUE>();
       if (warp == 0) {
         if (lane == 0) {
             // ------------------------------------------------ TMA producer
@@ -394,6 +399,7 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       }
     } else {
         // ---------------------------------------------------- epilogue warps
+        regs_inc<REGS_EPI>();
         const int q = warp & 3;
         const int cg = (warp - EPI_WARP0) >> 2;   // column group
         const int rloc = q * 32 + lane;

@@ -139,18 +139,18 @@ k_add_rms_norm(NormDev p) {
         if (++s == kStages) { s = 0; phase ^= 1u; }
         float r = __frsqrt_rn(fmaf(ss, p.inv_h, p.eps));
         if (!(ss <= kF32Max)) {
-            // squares past fp32's range (|h| above about 1e17): the same sum of
-            // (h * 2^-80)^2, beside which eps is nothing.  An infinite or NaN
-            // h leaves r at 0 or NaN, as the formula does.
+            // squares past fp32's range (|h| above about 1e17): the same with
+            // h * 2^-80, beside which eps is nothing.  An infinite or NaN h
+            // leaves r at 0 or NaN, as the formula does.
             ss = 0.0f;
 #pragma unroll
             for (int u = 0; u < V; ++u)
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    const float d = h[u][c] * 0x1p-80f;
-                    ss = fmaf(d, d, ss);
+                    h[u][c] *= 0x1p-80f;
+                    ss = fmaf(h[u][c], h[u][c], ss);
                 }
-            r = __frsqrt_rn(block_sum(ss, part[turn], false, failed) * p.inv_h) * 0x1p-80f;
+            r = __frsqrt_rn(block_sum(ss, part[turn], false, failed) * p.inv_h);
             turn ^= 1;
         }
 #pragma unroll
@@ -171,17 +171,27 @@ k_add_rms_norm(NormDev p) {
                 }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    h[u][c] = h[u][c] * r * w[c];
+                    h[u][c] *= w[c];
                     amax = fmaxf(amax, fabsf(h[u][c]));
                 }
-                if (p.y) p.y[t * p.H8 + i] = pack8(h[u]);
+                if (p.y) {
+                    float v[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[c] = h[u][c] * r;
+                    p.y[t * p.H8 + i] = pack8(v);
+                }
             }
             if (p.q) {
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
                 if (in) {
-                    float sc, inv;
-                    block_scale(amax, sc, inv);
+                    // v = r * (h w), and r is the same all over the block: the codes
+                    // are (h w) * 448 / max|h w|, one rounding fewer, unless the floor
+                    // or the range of h w says otherwise
+                    const float a = fmaxf(amax * r, kAmaxFloor);
+                    const float sc = a * (1.0f / kE4m3Max);
+                    const float inv = amax >= kAmaxFloor && amax * r >= kAmaxFloor
+                                          ? inverse_scale(amax) : inverse_scale(a) * r;
                     p.q[t * p.H8 + i] =
                         make_uint2(e4m3x4(h[u][0] * inv, h[u][1] * inv, h[u][2] * inv, h[u][3] * inv),
                                    e4m3x4(h[u][4] * inv, h[u][5] * inv, h[u][6] * inv, h[u][7] * inv));

@@ -159,4 +159,14 @@ __device__ __forceinline__ bool wait_bounded_inline(uint64_t *bar, uint32_t pari
         }
     }
 }
+// Moves registers between the warpgroups of a block; what all of them hold
+// together stays what the block was launched with.
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 }  // namespace moe
