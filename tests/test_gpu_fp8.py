@@ -194,6 +194,44 @@ def test_ffn_on_rows_equals_ffn_on_tokens(B, path):
     assert torch.equal(a[:n].view(torch.int16), b[:n].view(torch.int16))
 
 
+@pytest.mark.parametrize("E,K,P,mask_p,skew", [
+    (5, 2, 1, 1.0, 0.0),
+    (5, 2, 4, 0.3, 0.0),                      # most routes masked
+    (40, 3, 2, 0.9, 0.95),                    # almost every token's first route to one expert
+    (1, 1, 1, 1.0, 0.0),
+    (700, 2, 5, 1.0, 0.0),                    # fewer rows per expert than a segment's
+    (6, 2, 1, 0.0, 0.0),                      # no rows
+])
+def test_ffn_on_many_tokens_takes_every_row(B, E, K, P, mask_p, skew):
+    """More tokens than are copied in the rows' own order: the same rows, bit for bit."""
+    T, H, N = 4700, 7168, 256
+    g = torch.Generator(device="cuda").manual_seed(E + K)
+    score = torch.rand(T, E, generator=g, device="cuda")
+    score[:, E // 2] += (torch.rand(T, generator=g, device="cuda") < skew).float()
+    ids = score.argsort(1, descending=True)[:, :K].int().contiguous()
+    mask = (torch.rand(T, K, generator=g, device="cuda") < mask_p).to(torch.uint8)
+    d = B.dispatch(None, ids, E, P, mask=mask, with_rows=False)
+    x, xs = codes(g, T, H), scales(g, 0.01, T, H // 128)
+    w = (codes(g, E, N, H), scales(g, 2e-4, E, 2, H // 128), codes(g, E, H, N // 2),
+         scales(g, 2e-4, E, H // 128, 1))
+    shape = B.make_shape(T, P, H, E, K, N)
+    n = int(d["expert_offsets"][-1])
+    assert n == int(mask.sum())
+    as_ = d["assist"][:n].long()
+    tok = as_[:, 0] * (T // P) + as_[:, 1]
+    rows = torch.zeros(T * K, H, dtype=torch.uint8, device="cuda")
+    rs = torch.zeros(T * K, H // 128, device="cuda")
+    rows[:n] = x.view(torch.uint8)[tok]
+    rs[:n] = xs[tok]
+    y = torch.full((T * K, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    a, ws = B.grouped_ffn_fp8(shape, x, xs, d["expert_offsets"], *w, assist=d["assist"], y=y)
+    b, _ = B.grouped_ffn_fp8(shape, rows.view(torch.float8_e4m3fn), rs, d["expert_offsets"], *w)
+    torch.cuda.synchronize()
+    assert B.read_device_status(ws) == 0
+    assert torch.equal(a[:n].view(torch.int16), b[:n].view(torch.int16))
+    assert bool((a[n:] == 7.0).all())
+
+
 def test_ffn_no_tokens(B):
     s = B.make_shape(0, 1, 128, 4, 2, 256)
     z = torch.zeros
