@@ -17,7 +17,9 @@
 // K rounds of a full arg-max, each lane looking through its registers after a
 // win, measured 26 us against 11 for this (32768 tokens, 256 experts, K = 8).
 //
-// A warp's instructions bound it, not memory: so nothing is computed for
+// A warp's instructions bound it, not memory (32768 tokens, 256 experts of
+// bf16 logits, K = 8: 11 us with the logits in L2, where their bytes would take
+// 2.9 us from HBM): so nothing is computed for
 // experts that is not needed for the choice.  Without a bias the keys are the
 // logits themselves (scores order as they do); with one, the scores behind the
 // keys use the hardware's approximate exponential and reciprocal (a few units

@@ -27,6 +27,11 @@
 // each takes a range of K, and the partial sums are added in rank order (so
 // repeats are bitwise equal) through distributed shared memory, every CTA
 // finishing the rows c = rank mod S.
+// What bounds it: the weights' bytes from HBM where there are many (an FFN of
+// 128 experts of 7168 x 4096, 8 rows each: 829 us, 6.8 TB/s), the fixed steps
+// where there are few (16 rows, 4096 x 7168: 8.9 us a kernel, of which 2.2 go to
+// the set-up, 1.2 to the first data, 1.4 to the join of a shared tile and 0.9
+// to the exit; the weights' bytes alone take 4.4).
 // Every wait is bounded (about two seconds) and sets MOE_DEV_TIMEOUT.
 #include "common.cuh"
 #include "fp8.cuh"

@@ -387,7 +387,8 @@ moe_status moe_dispatch_noalloc(const moe_shape *shape, const void *x, const int
  * y               bf16 [T, H] or NULL (may be x itself)
  * q, scales       e4m3 [T, H] and fp32 [T, ceil(H / 128)], or both NULL
  * At least one of y and q is given.  eps >= 1e-30 (so that squares that fp32
- * cannot hold are nothing beside it) and finite. */
+ * cannot hold are nothing beside it) and finite.  h * weight is formed before
+ * the factor rsqrt(...) joins it: it has to be within fp32's range. */
 moe_status moe_add_rms_norm(int64_t num_tokens, int64_t hidden, const void *x,
                             const void *residual, const void *weight, int weight_dtype, float eps,
                             void *residual_out, void *y, void *q, float *scales,
