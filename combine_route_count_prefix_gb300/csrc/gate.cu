@@ -1,38 +1,46 @@
 // gate.cu -- router: scores, balance bias, expert groups, top-k, weights.
 //
 // One warp per token.  A lane holds the keys of a run of up to VPL neighbouring
-// experts in registers; the runs are in the lanes' order, and with groups a
-// whole power of two of lanes holds a group, so that its value is a few
-// shuffles (where that would take runs of more than 32, the keys go through
-// shared memory instead).  The choice:
+// experts; the runs are in the lanes' order, and with groups a whole power of
+// two of lanes holds a group where that leaves runs of at most 32, so that its
+// value is a few shuffles.  Otherwise a group no shorter than a run is joined
+// from its lanes' parts, and shorter ones are looked through in shared memory.
+// The choice:
 //   1. K or a few more rounds over the lanes' largest keys (a warp-wide maximum
 //      by redux; the lanes that have it step out) give a lower bound of the
 //      K-th largest key; over quarters of the lanes' keys where few lanes
 //      have any.  Only keys at or above it can be chosen: about 9 of
 //      256 for K = 8, 22 of 1000 for K = 16.
 //   2. Those candidates are collected in the order of their experts, one a lane.
-//   3. A candidate's place is the number of candidates before it (larger key,
-//      or equal key and lower expert).
+//   3. A candidate's place is the number of larger candidates and of equal ones
+//      in lower lanes; its lane computes its weight and writes it there.
 // More than 32 candidates (many equal keys) are chosen one by one instead.
-// K rounds of a full arg-max, each lane looking through its registers after a
-// win, measured 26 us against 11 for this (32768 tokens, 256 experts, K = 8).
+// K rounds of a full arg-max, each lane looking through its keys after a win,
+// took 2.4 times as long.
 //
-// A warp's instructions bound it, not memory (32768 tokens, 256 experts of
-// bf16 logits, K = 8: 11 us with the logits in L2, where their bytes would take
-// 2.9 us from HBM): so nothing is computed for
-// experts that is not needed for the choice.  Without a bias the keys are the
-// logits themselves (scores order as they do); with one, the scores behind the
-// keys use the hardware's approximate exponential and reciprocal (a few units
-// in the last place); the K scores that become weights are computed again from
-// their logits with expf.
+// A warp's instructions bound it, not memory, and of those the comparisons,
+// maxima and selections, which run at half the rate of the others (32768
+// tokens, 256 experts of bf16 logits, K = 8: 16.2 us a call, where the bytes
+// take 2.9 us; 4097 tokens, 1000 experts, 20 groups, K = 16: 14.4 us, 2.5).  So
+// nothing is computed for experts that is not needed for the choice, and counts
+// are kept in floats, which leaves that half-rate pipe one instruction a
+// comparison (18.6 -> 16.2 us together with the next token's logits on their
+// way).  Without a bias the keys are the logits themselves (scores order as
+// they do); with one, the scores behind the keys use the hardware's approximate
+// exponential and reciprocal (a few units in the last place); the K scores that
+// become weights are computed again from their logits with expf.
 #include "common.cuh"
+
+#include <type_traits>
 
 namespace moe {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kGateWarps = 4;
+constexpr int kGateBlocks = 7;             // on an SM: 72 registers a thread; 8 blocks of 64 spill
 constexpr float kClosed = -1e30f;          // a logit at or below this closes the expert
+constexpr float kLeastOpen = -0x1.93e592p+99f;   // the next float above it
 constexpr float kF32Max = 3.402823466e38f;
 
 struct GateDev {
@@ -46,8 +54,10 @@ struct GateDev {
     int E, K, G, KG, per;     // per = E / G
     int sigmoid, top2, renorm;
     int run;                  // experts a lane holds at most
-    int padded;               // runs of VPL: in shared memory a float is left out after each
+    int padded;               // runs of VPL, one after the other
+    int wide;                 // rows can be loaded 16 bytes at a time
     int group_lanes;          // lanes that hold a group, 0 if runs do not end with the groups
+    int scratch;              // floats a warp joins the groups' values in
     float scale;
 };
 
@@ -69,30 +79,60 @@ __device__ __forceinline__ float load_logit(const GateDev &p, int64_t at) {
                   : static_cast<const float *>(p.logits)[at];
 }
 
-template <int VPL>
-__device__ __forceinline__ float lane_max(const float (&key)[VPL]) {
-    float m = key[0];
+// N floats of a lane's run from shared memory: 16 bytes at a time where the runs
+// are whole (and so aligned), else the first `have`, the rest closed.
+template <int N>
+__device__ __forceinline__ void read_run(float (&v)[N], const float *from, bool whole, int have) {
+    if (N >= 4 && whole) {
 #pragma unroll
-    for (int j = 1; j < VPL; ++j) m = fmaxf(m, key[j]);
-    return m;
+        for (int j = 0; j + 3 < N; j += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(from + j);
+            v[j] = a.x; v[j + 1] = a.y; v[j + 2] = a.z; v[j + 3] = a.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = whole || j < have ? from[j] : ninf();
+    }
 }
 
-// VEC: runs load as vectors.
+template <int N>
+__device__ __forceinline__ void write_run(const float (&v)[N], float *to, bool whole, int have) {
+    if (N >= 4 && whole) {
+#pragma unroll
+        for (int j = 0; j + 3 < N; j += 4)
+            *reinterpret_cast<float4 *>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (whole || j < have) to[j] = v[j];
+    }
+}
+
+// 1 / (1 + exp(-x)) with the hardware's approximate exponential and reciprocal:
+// half the instructions of __expf and __fdividef.
+__device__ __forceinline__ float sigmoid_approx(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
+// VEC: runs load as vectors.  Runs of up to 16 keys stay in registers, longer
+// ones in shared memory, from where eight at a time are looked at (32 keys in
+// registers spill: 24 us against 20 for 4097 tokens of 1000 experts, flushed L2).
 template <int VPL, bool BF16, bool VEC>
-__global__ void __launch_bounds__(32 * kGateWarps, 8)
+__global__ void __launch_bounds__(32 * kGateWarps, kGateBlocks)
 k_gate(GateDev p) {
-    __shared__ float s_keys[kGateWarps][32 * VPL + 32];
-    __shared__ float s_bias[32 * VPL + 32];
-    __shared__ __align__(16) float2 s_cand[kGateWarps][32];   // candidates: key, expert
-    __shared__ int s_ids[kGateWarps][kMaxTopK];
-    extern __shared__ float s_groups[];         // [warps][G], where group_lanes is 0
+    __shared__ __align__(16) float s_keys[kGateWarps][32 * VPL + 128];
+    __shared__ __align__(16) float s_bias[32 * VPL + 128];
+    __shared__ __align__(16) float2 s_cand[kGateWarps][36];   // candidates: key, expert
+    extern __shared__ __align__(16) float s_groups[];   // [warps][scratch], where group_lanes is 0
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float *sk = s_keys[warp];
-    // Shared memory holds the experts in order; runs of VPL, a power of two,
-    // with a float left out after each, so that the lanes' reads of their runs
-    // fall into different banks.
-    const int pad = p.padded ? 1 : 0;
-    const int store0 = lane + pad * (lane / VPL), store_step = 32 + pad * (32 / VPL);
+    // Shared memory holds the experts in order; whole runs of 8 and more, which
+    // are read 16 bytes at a time, with four floats left out after each, so that
+    // eight lanes' reads fall into different banks.
+    const int pad = p.padded && VPL >= 8 ? 4 : 0;
     // the lane's first expert, and how many it has
     int e0 = lane * p.run, have = min(p.run, p.E - e0);
     if (p.group_lanes) {
@@ -102,76 +142,153 @@ k_gate(GateDev p) {
     }
     const int run0 = e0 + pad * lane;           // the run's place in shared memory
     pdl_wait();
+    if (p.padded && !VEC)                       // whole runs are read past the last expert
+        for (int i = p.E + lane; i < 32 * VPL; i += 32) sk[i + pad * (i / VPL)] = ninf();
     if (p.bias) {
         for (int i = threadIdx.x; i < p.E; i += 32 * kGateWarps) s_bias[i + pad * (i / VPL)] = p.bias[i];
         __syncthreads();
     }
-    for (int64_t t = (int64_t)blockIdx.x * kGateWarps + warp; t < p.T;
-         t += (int64_t)gridDim.x * kGateWarps) {
-        const bool active = p.mask == nullptr || p.mask[t] != 0;
-        const int64_t row = t * p.stride;
-        float key[VPL];
-        // ---- logits: what is not loaded stays NaN, which closes it
+    // without a bias and groups the keys are the logits as they come: the bound
+    // keeps closed ones out
+    const bool raw_keys = !p.bias && p.G == 1 && (p.sigmoid || p.renorm);
+    // Where the runs do not end with the groups and a group is no shorter than
+    // a run: the group that the lane's run begins in, and how much of it
+    const bool two_groups = p.G > 1 && !p.group_lanes && p.per >= VPL;
+    const int first_group = two_groups ? e0 / p.per : 0;
+    const int in_first = two_groups ? (first_group + 1) * p.per - e0 : 0;
+    const int64_t step = (int64_t)gridDim.x * kGateWarps;
+    // a token's run, as it is stored; what is not loaded stays NaN, which closes it
+    constexpr int RAW = BF16 ? (VPL > 1 ? VPL / 2 : 1) : VPL;
+    uint32_t raw[VEC ? RAW : 1];
+    auto fetch = [&](int64_t t) {
         if constexpr (VEC) {
-            const bool in = active && have > 0;
-            if constexpr (BF16) {
-                const uint16_t *src = static_cast<const uint16_t *>(p.logits) + row + e0;
-                uint32_t w[VPL > 1 ? VPL / 2 : 1];
 #pragma unroll
-                for (int j = 0; j < (VPL > 1 ? VPL / 2 : 1); ++j) w[j] = 0xffffffffu;
-                if (in) {
-                    if constexpr (VPL == 8) *reinterpret_cast<uint4 *>(w) = __ldg(reinterpret_cast<const uint4 *>(src));
-                    else if constexpr (VPL == 4) *reinterpret_cast<uint2 *>(w) = __ldg(reinterpret_cast<const uint2 *>(src));
-                    else if constexpr (VPL == 2) w[0] = __ldg(reinterpret_cast<const uint32_t *>(src));
-                    else w[0] = __ldg(src);
-                }
-#pragma unroll
-                for (int j = 0; j < VPL; ++j)
-                    key[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+            for (int j = 0; j < RAW; ++j) raw[j] = 0xffffffffu;
+            if (t >= p.T || have <= 0 || (p.mask && p.mask[t] == 0)) return;
+            const uint8_t *src = static_cast<const uint8_t *>(p.logits) +
+                                 (t * p.stride + e0) * (BF16 ? 2 : 4);
+            if constexpr (BF16 && VPL == 1) raw[0] = __ldg(reinterpret_cast<const uint16_t *>(src));
+            else if constexpr (RAW == 1) raw[0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+            else if constexpr (RAW == 2) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+                raw[0] = v.x; raw[1] = v.y;
             } else {
-                const float *src = static_cast<const float *>(p.logits) + row + e0;
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) key[j] = __uint_as_float(0xffffffffu);
-                if (in) {
-                    if constexpr (VPL >= 4) {
-#pragma unroll
-                        for (int j = 0; j < VPL; j += 4)
-                            *reinterpret_cast<float4 *>(key + j) = __ldg(reinterpret_cast<const float4 *>(src + j));
-                    } else if constexpr (VPL == 2) {
-                        *reinterpret_cast<float2 *>(key) = __ldg(reinterpret_cast<const float2 *>(src));
-                    } else {
-                        key[0] = __ldg(src);
-                    }
+                for (int j = 0; j < RAW; j += 4) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + j / 4);
+                    raw[j] = v.x; raw[j + 1] = v.y; raw[j + 2] = v.z; raw[j + 3] = v.w;
                 }
             }
+        }
+    };
+    constexpr bool MEM = VPL > 16;
+    constexpr int C = MEM ? 8 : VPL;            // keys looked at together
+    float key[MEM ? 1 : VPL];
+    // f(keys, number of the first) over the lane's run; STORE: f changes them
+    auto each = [&](auto store, auto f) {
+        if constexpr (MEM) {
+#pragma unroll 2
+            for (int j0 = 0; j0 < VPL; j0 += C) {
+                float k[C];
+                read_run<C>(k, sk + run0 + j0, p.padded, have - j0);
+                f(k, j0);
+                if constexpr (decltype(store)::value) write_run<C>(k, sk + run0 + j0, p.padded, have - j0);
+            }
+        } else {
+            f(key, 0);
+        }
+    };
+    constexpr std::true_type change{};
+    constexpr std::false_type look{};
+    auto largest = [&]() {                      // of the lane's keys, NaN aside
+        float m = ninf();
+        each(look, [&](auto &k, int) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) m = fmaxf(m, k[j]);
+        });
+        return m;
+    };
+    int64_t t = (int64_t)blockIdx.x * kGateWarps + warp;
+    fetch(t);
+    for (; t < p.T; t += step) {
+        const int64_t row = t * p.stride;
+        // ---- logits
+        if constexpr (VEC) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                key[j] = __uint_as_float(!BF16 ? raw[j] : j & 1 ? raw[j / 2] & 0xffff0000u : raw[j / 2] << 16);
+            fetch(t + step);
+        } else if (p.mask && p.mask[t] == 0) {
+            each(change, [&](auto &k, int) {
+#pragma unroll
+                for (int j = 0; j < C; ++j) k[j] = ninf();
+            });
         } else {
             // neighbours on neighbouring lanes (whole sectors whatever the
             // alignment), then through shared memory to the lanes that hold them
+            constexpr int EV = BF16 ? 8 : 4;
+            if (VPL >= 16 && p.wide) {
+                constexpr int U = VPL / EV < 4 ? (VPL / EV > 0 ? VPL / EV : 1) : 4;
+#pragma unroll 1
+                for (int j0 = 0; j0 < VPL / EV; j0 += U) {
+                    uint4 v[U];
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                key[j] = __uint_as_float(0xffffffffu);
-                if (active && 32 * j + lane < p.E) key[j] = load_logit<BF16>(p, row + 32 * j + lane);
+                    for (int u = 0; u < U; ++u) {
+                        const int i = (32 * (j0 + u) + lane) * EV;
+                        if (i < p.E)
+                            v[u] = __ldg(reinterpret_cast<const uint4 *>(
+                                static_cast<const uint8_t *>(p.logits) + (row + i) * (BF16 ? 2 : 4)));
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int i = (32 * (j0 + u) + lane) * EV;
+                        if (i >= p.E) continue;
+                        uint4 *to = reinterpret_cast<uint4 *>(sk + i + pad * (i / VPL));
+                        if constexpr (BF16) {
+                            to[0] = make_uint4(v[u].x << 16, v[u].x & 0xffff0000u, v[u].y << 16, v[u].y & 0xffff0000u);
+                            to[1] = make_uint4(v[u].z << 16, v[u].z & 0xffff0000u, v[u].w << 16, v[u].w & 0xffff0000u);
+                        } else {
+                            to[0] = v[u];
+                        }
+                    }
+                }
+            } else {
+                constexpr int U = VPL < 8 ? VPL : 8;
+#pragma unroll 1
+                for (int j0 = 0; j0 < VPL; j0 += U) {
+                    float v[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (32 * (j0 + u) + lane < p.E) v[u] = load_logit<BF16>(p, row + 32 * (j0 + u) + lane);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int i = 32 * (j0 + u) + lane;
+                        if (i < p.E) sk[i + pad * (i / VPL)] = v[u];
+                    }
+                }
             }
             __syncwarp();
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                sk[store0 + j * store_step] = key[j];
+            if constexpr (!MEM) {
+                read_run<VPL>(key, sk + run0, p.padded, have);
+                __syncwarp();
             }
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                key[j] = j < have ? sk[run0 + j] : __uint_as_float(0xffffffffu);
         }
+        if (!raw_keys && !(p.bias && p.sigmoid))
+            each(change, [&](auto &k, int) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) key[j] = open_logit(key[j]);
+                for (int j = 0; j < C; ++j) k[j] = open_logit(k[j]);
+            });
         // ---- scores and keys
         float top = 0.0f, sum = 1.0f;           // softmax: the largest logit, the exponentials' sum
         if (!p.sigmoid) {
-            top = fminf(fmaxf(warp_max(lane_max<VPL>(key)), -kF32Max), kF32Max);
+            top = fminf(fmaxf(warp_max(largest()), -kF32Max), kF32Max);
             if (!p.renorm || p.bias) {          // renormalised weights do not need the sum
                 sum = 0.0f;
+                each(look, [&](auto &k, int) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) sum += __expf(fminf(key[j], kF32Max) - top);
+                    for (int j = 0; j < C; ++j)
+                        if (k[j] > kClosed) sum += __expf(fminf(k[j], kF32Max) - top);
+                });
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
                 sum = fmaxf(sum, 1e-30f);
@@ -179,12 +296,20 @@ k_gate(GateDev p) {
         }
         if (p.bias) {
             const float inv = __fdividef(1.0f, sum);
+            each(change, [&](auto &k, int j0) {
+                constexpr int D = C < 4 ? C : 4;
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const float s = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-key[j]))
-                                          : __expf(fminf(key[j], kF32Max) - top) * inv;
-                if (key[j] != ninf()) key[j] = s + s_bias[run0 + j];
-            }
+                for (int d = 0; d < C; d += D) {
+                    float bias[D];
+                    read_run<D>(bias, s_bias + run0 + j0 + d, p.padded, have - j0 - d);
+#pragma unroll
+                    for (int j = 0; j < D; ++j) {
+                        const float l = k[d + j];
+                        const float score = p.sigmoid ? sigmoid_approx(l) : __expf(fminf(l, kF32Max) - top) * inv;
+                        k[d + j] = l > kClosed ? score + bias[j] : ninf();
+                    }
+                }
+            });
         }
         // ---- groups
         if (p.G > 1) {
@@ -197,13 +322,19 @@ k_gate(GateDev p) {
             auto group_value = [&](float a, float b) {
                 return p.top2 && b != ninf() ? value(a) + value(b) : value(a);
             };
+            float *scratch = s_groups + warp * p.scratch;
             if (p.group_lanes) {
                 float a = ninf(), b = ninf();   // the group's two largest keys
+                if (p.top2)
+                    each(look, [&](auto &k, int) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) {
-                    b = fmaxf(b, fminf(a, key[j]));
-                    a = fmaxf(a, key[j]);
-                }
+                        for (int j = 0; j < C; ++j) {
+                            b = fmaxf(b, fminf(a, k[j]));
+                            a = fmaxf(a, k[j]);
+                        }
+                    });
+                else
+                    a = largest();
                 for (int o = 1; o < p.group_lanes; o <<= 1) {
                     const float oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
                     b = fmaxf(fminf(a, oa), fmaxf(b, ob));
@@ -216,16 +347,66 @@ k_gate(GateDev p) {
                     const float v = __shfl_sync(kFull, gv, g * p.group_lanes);
                     rank += v > gv || (v == gv && g < mine);
                 }
-                if (rank >= p.KG || mine >= p.G) {
+                if (rank >= p.KG || mine >= p.G)
+                    each(change, [&](auto &k, int) {
 #pragma unroll
-                    for (int j = 0; j < VPL; ++j) key[j] = ninf();
-                }
-            } else {
-                float *sg = s_groups + warp * p.G;
+                        for (int j = 0; j < C; ++j) k[j] = ninf();
+                    });
+            } else if (two_groups) {
+                // the two largest keys of the run's part in either group
+                float a0 = ninf(), b0 = ninf(), a1 = ninf(), b1 = ninf();
+                auto parts = [&](auto two) {
+                    each(look, [&](auto &k, int j0) {
+#pragma unroll
+                        for (int j = 0; j < C; ++j) {
+                            const bool first = j0 + j < in_first;
+                            const float k0 = first ? k[j] : ninf(), k1 = first ? ninf() : k[j];
+                            if constexpr (decltype(two)::value) {
+                                b0 = fmaxf(b0, fminf(a0, k0));
+                                b1 = fmaxf(b1, fminf(a1, k1));
+                            }
+                            a0 = fmaxf(a0, k0);
+                            a1 = fmaxf(a1, k1);
+                        }
+                    });
+                };
+                if (p.top2) parts(std::true_type{}); else parts(std::false_type{});
+                float4 *part = reinterpret_cast<float4 *>(scratch);
+                part[lane] = make_float4(a0, b0, a1, b1);
                 __syncwarp();
+                // lane g joins group g's parts: all but the first of its lanes
+                // begin in it
+                float a = ninf(), b = ninf();
+                const int begin = lane * p.per;
+                if (lane < p.G)
+                    for (int l = begin / VPL; l * VPL < begin + p.per; ++l) {
+                        const float4 v = part[l];
+                        const float oa = l * VPL < begin ? v.z : v.x, ob = l * VPL < begin ? v.w : v.y;
+                        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                        a = fmaxf(a, oa);
+                    }
+                const float gv = group_value(a, b);
+                int rank = 0;                   // groups that come before the lane's
+                for (int g = 0; g < p.G; ++g) {
+                    const float v = __shfl_sync(kFull, gv, g);
+                    rank += v > gv || (v == gv && g < lane);
+                }
+                const uint32_t stay = __ballot_sync(kFull, lane < p.G && rank < p.KG);
+                const bool stay0 = (stay >> first_group) & 1u;
+                const bool stay1 = first_group < 31 && ((stay >> (first_group + 1)) & 1u);
+                if (!stay0 || !stay1)
+                    each(change, [&](auto &k, int j0) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j)
-                    if (j < have) sk[run0 + j] = key[j];
+                        for (int j = 0; j < C; ++j)
+                            if (!(j0 + j < in_first ? stay0 : stay1)) k[j] = ninf();
+                    });
+            } else {
+                if constexpr (!MEM) {
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j)
+                        if (j < have) sk[run0 + j] = key[j];
+                }
                 __syncwarp();
                 for (int g = lane; g < p.G; g += 32) {
                     float a = ninf(), b = ninf();
@@ -235,35 +416,35 @@ k_gate(GateDev p) {
                         b = fmaxf(b, fminf(a, v));
                         a = fmaxf(a, v);
                     }
-                    sg[g] = group_value(a, b);
+                    scratch[g] = group_value(a, b);
                 }
                 __syncwarp();
                 // a group stays if fewer than KG come before it
+                uint32_t *stay = reinterpret_cast<uint32_t *>(scratch + p.G);
                 for (int g0 = 0; g0 < p.G; g0 += 32) {
                     const int g = g0 + lane;
-                    const float gv = g < p.G ? sg[g] : ninf();
+                    const float gv = g < p.G ? scratch[g] : ninf();
                     int rank = 0;
                     for (int o = 0; o < p.G; ++o) {
-                        const float v = sg[o];
+                        const float v = scratch[o];
                         rank += v > gv || (v == gv && o < g);
                     }
-                    __syncwarp();
-                    const uint32_t stay = __ballot_sync(kFull, g < p.G && rank < p.KG);
-                    if (lane == 0) sk[g0 / 32] = __uint_as_float(stay);
+                    const uint32_t word = __ballot_sync(kFull, g < p.G && rank < p.KG);
+                    if (lane == 0) stay[g0 / 32] = word;
                 }
                 __syncwarp();
-                const uint32_t *stay = reinterpret_cast<const uint32_t *>(sk);
                 int g = have > 0 ? e0 / p.per : 0, left = (g + 1) * p.per - e0;   // experts to the group's end
+                each(change, [&](auto &k, int j0) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j) {
-                    if (j < have && !((stay[g >> 5] >> (g & 31)) & 1u)) key[j] = ninf();
-                    if (--left == 0) { left = p.per; ++g; }
-                }
-                __syncwarp();
+                    for (int j = 0; j < C; ++j) {
+                        if (j0 + j < have && !((stay[g >> 5] >> (g & 31)) & 1u)) k[j] = ninf();
+                        if (--left == 0) { left = p.per; ++g; }
+                    }
+                });
             }
         }
         // ---- the K best
-        float bound = ninf(), cur = lane_max<VPL>(key);
+        float bound = ninf(), cur = largest();
         if (VPL == 1 || __popc(__ballot_sync(kFull, cur > ninf())) >= 2 * p.K) {
             for (int k = 0; k < p.K; k += 4)
 #pragma unroll
@@ -278,23 +459,29 @@ k_gate(GateDev p) {
             constexpr int Q = VPL < 4 ? VPL : 4;
             float part[Q];
 #pragma unroll
-            for (int u = 0; u < Q; ++u) {
-                part[u] = key[u];
+            for (int u = 0; u < Q; ++u) part[u] = ninf();
+            each(look, [&](auto &k, int) {
 #pragma unroll
-                for (int j = u + Q; j < VPL; j += Q) part[u] = fmaxf(part[u], key[j]);
-            }
+                for (int j = 0; j < C; ++j) part[j % Q] = fmaxf(part[j % Q], k[j]);
+            });
             for (int k = 0; k < p.K; ++k) {
-                bound = warp_max(lane_max<Q>(part));
+                float m = part[0];
+#pragma unroll
+                for (int u = 1; u < Q; ++u) m = fmaxf(m, part[u]);
+                bound = warp_max(m);
 #pragma unroll
                 for (int u = 0; u < Q; ++u) part[u] = part[u] == bound ? ninf() : part[u];
             }
         }
-        bound = fmaxf(bound, -kF32Max);         // closed experts are no candidates
+        bound = fmaxf(bound, raw_keys ? kLeastOpen : -kF32Max);   // closed experts are no candidates
         // candidates of the lower lanes come first
-        int own = 0;
+        float in_run = 0.0f;                    // counted where the comparisons do not run
+        each(look, [&](auto &k, int) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j)
-            if (key[j] >= bound) ++own;
+            for (int j = 0; j < C; ++j)
+                if (k[j] >= bound) in_run += 1.0f;
+        });
+        const int own = (int)in_run;
         int upto = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -303,67 +490,79 @@ k_gate(GateDev p) {
         }
         const int count = __shfl_sync(kFull, upto, 31);
         const int n = min(count, p.K);          // experts that are chosen
+        // the lane's choice, if it has one: expert, key and place in the order
+        int id = 0, place = p.K;
+        float mine = 0.0f;
         if (count <= 32) {
             float2 *cand = s_cand[warp];
-            cand[lane] = make_float2(ninf(), 0.0f);
-            __syncwarp();
+            if (lane < 3) cand[count + lane].x = ninf();
             float2 *to = cand + (upto - own);
+            if (!MEM || own)
+                each(look, [&](auto &k, int j0) {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (key[j] >= bound) *to++ = make_float2(key[j], __int_as_float(e0 + j));
+                    for (int j = 0; j < C; ++j)
+                        if (k[j] >= bound) *to++ = make_float2(k[j], __int_as_float(e0 + j0 + j));
+                });
             __syncwarp();
-            const float2 own_cand = cand[lane];
-            const float mine = own_cand.x;
-            int place = 0;
-            for (int i = 0; i < count; i += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(cand + i);
-                const float4 b = *reinterpret_cast<const float4 *>(cand + i + 2);
-                const float4 o = make_float4(a.x, a.z, b.x, b.z);
-                // an equal key before the lane's own comes before it
-                if (i < lane ? o.x >= mine : o.x > mine) ++place;
-                if (i + 1 < lane ? o.y >= mine : o.y > mine) ++place;
-                if (i + 2 < lane ? o.z >= mine : o.z > mine) ++place;
-                if (i + 3 < lane ? o.w >= mine : o.w > mine) ++place;
+            if (lane < count) {
+                const float2 own_cand = cand[lane];
+                mine = own_cand.x;
+                id = __float_as_int(own_cand.y);
+                float before = 0.0f;            // counted where the comparisons do not run
+                for (int i = 0; i < count; i += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(cand + i);
+                    const float4 b = *reinterpret_cast<const float4 *>(cand + i + 2);
+                    if (a.x > mine) before += 1.0f;
+                    if (a.z > mine) before += 1.0f;
+                    if (b.x > mine) before += 1.0f;
+                    if (b.z > mine) before += 1.0f;
+                }
+                place = (int)before;
+                // equal keys (0 and -0 among them): those of lower lanes come before
+                place += __popc(__match_any_sync(count < 32 ? (1u << count) - 1u : kFull, __float_as_uint(mine + 0.0f)) & lanemask_lt());
             }
-            if (lane < count && place < p.K) s_ids[warp][place] = __float_as_int(own_cand.y);
         } else {
             uint32_t used = 0;
             for (int k = 0; k < n; ++k) {
                 float m = ninf();
                 int j1 = 0;
+                each(look, [&](auto &k, int j0) {
 #pragma unroll
-                for (int j = 0; j < VPL; ++j)
-                    if (!((used >> j) & 1u) && key[j] > m) { m = key[j]; j1 = j; }
+                    for (int j = 0; j < C; ++j)
+                        if (!((used >> (j0 + j)) & 1u) && k[j] > m) { m = k[j]; j1 = j0 + j; }
+                });
                 const float best = warp_max(m);
-                const uint32_t have = __ballot_sync(kFull, m == best);
-                if (m == best && (have & lanemask_lt()) == 0) {
-                    s_ids[warp][k] = e0 + j1;
-                    used |= 1u << j1;
-                }
+                const uint32_t first = __ballot_sync(kFull, m == best);
+                const int expert = __shfl_sync(kFull, e0 + j1, __ffs(first) - 1);
+                if (m == best && (first & lanemask_lt()) == 0) used |= 1u << j1;
+                if (lane == k) { id = expert; place = k; mine = best; }
             }
         }
-        __syncwarp();
-        // ---- weights: lane k has the k-th choice
-        int id = -1;
+        // ---- weights
+        const bool chosen = place < p.K;
         float w = 0.0f;
-        if (lane < n) {
-            id = s_ids[warp][lane];
-            const float l = fminf(load_logit<BF16>(p, row + id), kF32Max);
+        if (chosen) {
+            const float l = fminf(p.bias ? load_logit<BF16>(p, row + id) : mine, kF32Max);
             w = __fdividef(p.sigmoid ? 1.0f : expf(l - top), p.sigmoid ? 1.0f + expf(-l) : sum);
         }
-        __syncwarp();
         if (p.renorm) {
             float s = w;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
             w = __fdividef(w, s + 1e-20f);
         }
-        if (lane < p.K) {
-            const int64_t at = t * p.K + lane;
-            p.ids[at] = id;
-            p.scales[at] = w * p.scale;
-            if (p.route_mask) p.route_mask[at] = id >= 0;
+        const int64_t at = t * p.K;
+        if (chosen) {
+            p.ids[at + place] = id;
+            p.scales[at + place] = w * p.scale;
+            if (p.route_mask) p.route_mask[at + place] = 1;
         }
+        if (n < p.K && lane >= n && lane < p.K) {
+            p.ids[at + lane] = -1;
+            p.scales[at + lane] = 0.0f;
+            if (p.route_mask) p.route_mask[at + lane] = 0;
+        }
+        __syncwarp();                           // the candidates' places are free again
     }
 }
 
@@ -377,9 +576,9 @@ moe_status launch_vpl(const GateDev &p, cudaStream_t stream) {
                      (uintptr_t)p.logits % align == 0 &&
                      (size_t)p.stride * (BF16 ? 2 : 4) % align == 0;
     const int64_t want = (p.T + kGateWarps - 1) / kGateWarps;
-    const int64_t cap = (int64_t)num_sms() * 16;
+    const int64_t cap = (int64_t)num_sms() * kGateBlocks;
     const unsigned grid = (unsigned)(want < cap ? want : cap);
-    const size_t smem = p.G > 1 && !p.group_lanes ? (size_t)kGateWarps * p.G * sizeof(float) : 0;
+    const size_t smem = p.G > 1 && !p.group_lanes ? (size_t)kGateWarps * p.scratch * sizeof(float) : 0;
     auto kernel = vec ? k_gate<VPL, BF16, VPL <= 8> : k_gate<VPL, BF16, false>;
     MOE_LAUNCH("gate", kernel, grid, 32 * kGateWarps, smem, stream, p);
     return MOE_OK;
@@ -422,6 +621,7 @@ moe_status launch_gate(const moe_gate_desc &d, const void *logits, const float *
     p.scale = d.scale;
     // Lanes for a group: the most that 32 lanes give each, in powers of two.
     p.group_lanes = 0;
+    p.scratch = (p.G + 3) / 4 * 4 + 128;
     p.run = (p.E + 31) / 32;
     if (p.G > 1 && p.G <= 32) {
         int lanes = 32;
@@ -435,7 +635,9 @@ moe_status launch_gate(const moe_gate_desc &d, const void *logits, const float *
     int vpl = 1;
     while (vpl < p.run) vpl *= 2;
     if (!p.group_lanes) p.run = vpl;   // whole vectors
-    p.padded = p.run == vpl && vpl > 1 && (!p.group_lanes || p.per == p.group_lanes * p.run);
+    p.padded = p.run == vpl && (!p.group_lanes || p.per == p.group_lanes * p.run);
+    const size_t size = d.logits_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+    p.wide = (uintptr_t)p.logits % 16 == 0 && p.stride * size % 16 == 0 && p.E * size % 16 == 0;
     return d.logits_dtype == MOE_DTYPE_BF16 ? launch_type<true>(p, vpl, stream)
                                             : launch_type<false>(p, vpl, stream);
 }

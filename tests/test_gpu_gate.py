@@ -86,6 +86,41 @@ def test_choice_and_weights(B, T, E, K, groups, topk_groups, group_score, bias, 
         check(out, ref, span=24.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score,bias", [("sigmoid", True), ("softmax", True), ("softmax", False)])
+@pytest.mark.parametrize("E,K,groups,topk_groups,group_score", [
+    (1000, 16, 20, 7, "top2"),                # groups that begin and end inside the lanes' runs
+    (660, 5, 20, 3, "top2"),                  # the last lanes without experts
+    (999, 16, 3, 1, "max"),                   # a group over eleven lanes; rows not 16-byte aligned
+    (900, 12, 30, 6, "top2"),                 # runs of 30
+    (800, 10, 100, 4, "top2"),                # groups shorter than a run
+    (513, 16, 1, 1, "max"),
+    (1024, 3, 16, 2, "max"),
+])
+def test_many_experts_and_masked_tokens(B, E, K, groups, topk_groups, group_score, score, bias, dtype):
+    T = 90
+    g = np.random.default_rng(E + groups)
+    b = (0.2 * g.normal(size=E)).astype(np.float32) if bias else None
+    kw = dict(score=score, groups=groups, topk_groups=topk_groups, group_score=group_score)
+    l = logits_without_near_ties(T, E, K, E, dtype, None if b is None else b.astype(np.float64), **kw)
+    m = (g.random(T) < 0.7).astype(np.uint8)
+    l[torch.from_numpy(m == 0).cuda()] = float("nan")
+    out, ref = run(B, l, K, bias=dev(b), mask=dev(m), **kw)
+    check(out, ref, span=24.0)
+
+
+@pytest.mark.parametrize("E,groups,topk_groups", [(64, 1, 1), (256, 8, 3), (512, 1, 1), (1000, 20, 4)])
+def test_zeros_of_both_signs_are_equal(B, E, groups, topk_groups):
+    """Many equal keys, 0 and -0 among them, in the order of the experts."""
+    g = np.random.default_rng(E)
+    l = g.choice(np.float32([-0.0, 0.0, 0.0, -1.0]), (200, E))
+    l[100:] = g.choice(np.float32([-3.0, -2.0, -1.0]), (100, E))
+    l[100:, g.permutation(E)[:6]] = g.choice(np.float32([-0.0, 0.0]), (100, 6))
+    for score in ("softmax", "sigmoid"):
+        out, ref = run(B, dev(l), 8, score=score, groups=groups, topk_groups=topk_groups)
+        check(out, ref)
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("groups,topk_groups,group_score", [(1, 1, "max"), (8, 3, "max"), (8, 3, "top2")])
 def test_ties_go_to_the_lowest_index(B, score, groups, topk_groups, group_score):
