@@ -38,7 +38,9 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kGateWarps = 4;
-constexpr int kGateBlocks = 7;             // on an SM: 72 registers a thread; 8 blocks of 64 spill
+// Blocks on an SM: 72 registers a thread.  With 8 blocks of 64 some forms spill
+// (4097 tokens of 1000 experts 24.8 us against 24.1, 32768 of 512 38.5 against 35.8).
+constexpr int kGateBlocks = 7;
 constexpr float kClosed = -1e30f;          // a logit at or below this closes the expert
 constexpr float kLeastOpen = -0x1.93e592p+99f;   // the next float above it
 constexpr float kF32Max = 3.402823466e38f;

@@ -33,9 +33,11 @@
 // accumulator, and with two accumulators that, not the tensor cores, set the
 // pace (630 ns a block; this form takes about 415, the MMAs alone 270).
 // Shared memory bounds the block loop: 48 KB of operands come in and are read
-// once by the MMAs, 96 KB a block or 768 cycles at 128 bytes a cycle; a block
-// takes about 785 cycles, about 905 in the SwiGLU form, and a tile about 4000
-// more for its start and its stores.  Measured, bf16 output: 8192 rows, 7168 x
+// once by the MMAs, 96 KB a block or 768 cycles at 128 bytes a cycle; and the
+// round of an accumulator: issue to the end of its MMAs 900 cycles, the last
+// epilogue warp's start 115 (SwiGLU form 340), drain 450 (500), release to the
+// next issue 230 (310), for every second block.  A block takes about 785 (905)
+// cycles, and a tile about 4000 more for its start and its stores.  Measured, bf16 output: 8192 rows, 7168 x
 // 7168, 320 us (2.6 PFLOP/s); 8192 rows, 7168 x 2048, 114 us (2.1).
 // SwiGLU form: CTA 0 stages 128 SiLU-half channels and CTA 1 the multiplier
 // channels of the same numbers, so a tile holds 128 complete channels of g and
