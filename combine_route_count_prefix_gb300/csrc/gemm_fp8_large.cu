@@ -58,6 +58,10 @@ constexpr int BM = 128;                 // rows per CTA (256 per pair)
 constexpr int BN = 256;                 // channels per tile
 constexpr int BK = 128;                 // bytes of K per block: one scale
 constexpr int STAGES = 4;
+// The two issuers take turns on the blocks.  With an even number of stages each
+// always waits on its own ones; with an odd number a stage would pass from one
+// to the other, and a wait could take the other's phase for its own.
+static_assert(STAGES % 2 == 0, "stages belong to one issuer");
 constexpr int A_BYTES = BM * BK;
 constexpr int B_BYTES = BN * BK;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;

@@ -317,6 +317,11 @@ k_gemm_fp8_small(const __grid_constant__ CUtensorMap tmRows, const __grid_consta
                 const uint32_t idesc = idesc_e4m3(BW, ((t.rows + 15) / 16) * 16);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (NG == 2 || (accb & 1) == me) {
+                        // The accumulator first: it is free once the block NBUF before
+                        // has been added, so the stage's use before this one, which
+                        // may have been the other issuer's, has landed by then and
+                        // the second wait cannot take that phase for its own.
+                        static_assert(STAGES >= NBUF, "a stage's last use is behind the accumulator's");
                         if (!wait_bounded(&acc_empty[accb], acc_phase ^ 1u, abort_flag, p.status) ||
                             !wait_bounded(&full[stage], phase, abort_flag, p.status)) {
                             ok = false;
