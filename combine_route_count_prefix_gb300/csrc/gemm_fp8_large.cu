@@ -38,7 +38,7 @@
 // epilogue warp's start 115 (SwiGLU form 340), drain 450 (500), release to the
 // next issue 230 (310), for every second block.  A block takes about 785 (905)
 // cycles, and a tile about 4000 more for its start and its stores.  Measured, bf16 output: 8192 rows, 7168 x
-// 7168, 320 us (2.6 PFLOP/s); 8192 rows, 7168 x 2048, 114 us (2.1).
+// 7168, 313 us (2.7 PFLOP/s); 8192 rows, 7168 x 2048, 113 us (2.1).
 // SwiGLU form: CTA 0 stages 128 SiLU-half channels and CTA 1 the multiplier
 // channels of the same numbers, so a tile holds 128 complete channels of g and
 // the epilogue quantises them as one block; h never leaves the SM.
