@@ -23,9 +23,8 @@
 // tokens, 256 experts of bf16 logits, K = 8: 16.2 us a call, where the bytes
 // take 2.9 us; 4097 tokens, 1000 experts, 20 groups, K = 16: 14.4 us, 2.5).  So
 // nothing is computed for experts that is not needed for the choice, and counts
-// are kept in floats, which leaves that half-rate pipe one instruction a
-// comparison (18.6 -> 16.2 us together with the next token's logits on their
-// way).  Without a bias the keys are the logits themselves (scores order as
+// are kept in floats, so that they are not added on that pipe too (18.6 -> 16.2 us
+// together with the next token's logits on their way).  Without a bias the keys are the logits themselves (scores order as
 // they do); with one, the scores behind the keys use the hardware's approximate
 // exponential and reciprocal (a few units in the last place); the K scores that
 // become weights are computed again from their logits with expf.
@@ -110,8 +109,8 @@ __device__ __forceinline__ void write_run(const float (&v)[N], float *to, bool w
     }
 }
 
-// 1 / (1 + exp(-x)) with the hardware's approximate exponential and reciprocal:
-// half the instructions of __expf and __fdividef.
+// 1 / (1 + exp(-x)) with the hardware's approximate exponential and reciprocal,
+// whose results at the ends of their ranges (0, infinity) are what is wanted here.
 __device__ __forceinline__ float sigmoid_approx(float x) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
