@@ -55,21 +55,20 @@ Fp8Layout ffn_layout(const moe_shape &s) {
 }
 
 // AUTO's choice for a product, by an estimate of both kernels' time where the
-// weights' bytes do not bound it: tiles a multiprocessor (pair) works through x
-// blocks of K x the time a block takes it.  Measured times per block: a pair's
-// 256 x 256 (or 128 x 512) tile 0.48 us; 128 channels against up to 64 rows
-// 0.32 us; 128 channels of g against up to 32 rows 0.3 us and 64 rows 0.85 us
-// (two accumulators to read back for each).  Rows are taken as spread evenly.
+// weights' bytes do not bound it: tiles a multiprocessor works through x
+// blocks of K x the time a block takes it.  Measured times per block: a 128 x
+// 256 tile 0.48 us; 128 channels against up to 64 rows 0.32 us; 128 channels
+// of g against up to 32 rows 0.3 us and 64 rows 0.85 us (two accumulators to
+// read back for each).  Rows are taken as spread evenly.
 // What it chooses, measured (us, small against large): one product of 4096 x
-// 7168 with 256 rows 27/37, with 512 rows 43/37; 128 experts, 7168 x 4096 FFN,
-// 8 rows each 839/898, 32 rows each 1019/915.
+// 7168 with 256 rows 27/33, with 512 rows 45/33; 128 experts, 7168 x 4096 FFN,
+// 8 rows each 839/861, 32 rows each 1037/882.
 bool small_is_faster(const Fp8GemmArgs &a) {
     const int64_t experts = std::min(a.E, a.cap_rows), rows = (a.cap_rows + experts - 1) / experts;
     const int64_t num_kb = (a.Kd + 127) / 128, wblocks = (a.N + 127) / 128 / (a.q2 ? 2 : 1);
     const int64_t blocks = (rows + 127) / 128, cols = (a.N + 255) / 256;
-    const int64_t pairs = std::max(1, num_sms() / 2), sms = num_sms();
-    const int64_t large_tiles = experts * (blocks / 2 * cols + blocks % 2 * ((cols + 1) / 2));
-    const double large = (double)((large_tiles + pairs - 1) / pairs * num_kb) * 0.48;
+    const int64_t sms = num_sms();
+    const double large = (double)((experts * blocks * cols + sms - 1) / sms * num_kb) * 0.48;
     const int64_t tb = gemm_fp8_small_tile_rows(a);
     const int64_t small_tiles = experts * ((rows + tb - 1) / tb) * wblocks;
     const double small = (double)((small_tiles + sms - 1) / sms * num_kb) / gemm_fp8_small_split(a) *

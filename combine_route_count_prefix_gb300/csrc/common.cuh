@@ -345,8 +345,7 @@ struct Fp8GemmArgs {
     bool early;                // not the call's first kernel: offsets, weights and their scales
                                // were final before the kernel before this one began
 };
-// For many rows per expert (256-row tiles on pairs of SMs) and for few (the
-// weights as the MMA's M side).
+// For many rows per expert and for few (the weights as the MMA's M side).
 moe_status launch_gemm_fp8_large(const Fp8GemmArgs &a, cudaStream_t stream);
 moe_status launch_gemm_fp8_small(const Fp8GemmArgs &a, cudaStream_t stream);
 // The small kernel's rows per tile, and the CTAs that share a tile's K.

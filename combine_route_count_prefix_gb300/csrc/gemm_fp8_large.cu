@@ -1,5 +1,5 @@
 // gemm_fp8_large.cu -- grouped products of block-scaled e4m3 operands for many
-// rows per expert, on pairs of SMs.
+// rows per expert.
 //
 //   C[r, n] = sum_b a_scales[r, b] * w_scales[e, n / 128, b]
 //                   * sum_{k in block b} A[r, k] * W[e, n, k]
@@ -10,38 +10,35 @@
 // block's scale and add to fp32 sums in registers, while the tensor cores work
 // on the next block in the other accumulator.
 //
-// Kernel shape (clusters of two CTAs, as many as fit, 12 warps each): every CTA
-// computes 128 rows x 256 channels; a tall tile is 256 rows x 256 channels, and
-// an expert's last 128 rows, if their number of 128-row blocks is odd, make
-// wide tiles of 128 rows x 512 channels.
-//   warp 0      TMA producer, four-stage ring of 128 bytes of K: what the two
-//               CTAs share is read once, half by each, into both: a tall
-//               tile's channels (16 KB a half), a wide tile's rows (8 KB)
+// Kernel shape (one persistent CTA per SM, 12 warps; tiles of 128 rows x 256
+// channels, every CTA fetching all of its tile's operands):
+//   warp 0      TMA producer, four-stage ring of 128 bytes of K
 //   warps 1, 3  MMA issuers: 4 x tcgen05.mma M=128 N=256 K=32 a block, even
 //               blocks into one 256-column accumulator and odd ones into the
 //               other (one thread spends about 450 cycles on the issue of a
 //               block, which the tensor cores finish in 512); warp 1 owns TMEM
-//   warp 2      scales: four blocks at a time, the products of the CTA's row
+//   warp 2      scales: four blocks at a time, the products of the rows'
 //               scales and the two channel blocks' scales, for the epilogue in
 //               a shared-memory ring (one 16-byte load a row and four blocks;
 //               loads by the epilogue itself, a row a lane, stalled it)
 //   warps 4..11 epilogue: TMEM lane quadrant q (32 rows) x 128 columns, 128
 //               sums a thread
-// Every CTA multiplies its own rows: with one MMA over both (cta_group::2) the
-// release of an accumulator has to travel between the SMs, about 1000 cycles
-// from the end of a block's MMAs to the start of those that reuse its
-// accumulator, and with two accumulators that, not the tensor cores, set the
-// pace (630 ns a block; this form takes about 415, the MMAs alone 270).
-// Shared memory bounds the block loop: 48 KB of operands come in and are read
-// once by the MMAs, 96 KB a block or 768 cycles at 128 bytes a cycle; and the
-// round of an accumulator: issue to the end of its MMAs 900 cycles, the last
-// epilogue warp's start 115 (SwiGLU form 340), drain 450 (500), release to the
-// next issue 230 (310), for every second block.  A block takes about 785 (905)
-// cycles, and a tile about 4000 more for its start and its stores.  Measured, bf16 output: 8192 rows, 7168 x
-// 7168, 313 us (2.7 PFLOP/s); 8192 rows, 7168 x 2048, 113 us (2.1).
-// SwiGLU form: CTA 0 stages 128 SiLU-half channels and CTA 1 the multiplier
-// channels of the same numbers, so a tile holds 128 complete channels of g and
-// the epilogue quantises them as one block; h never leaves the SM.
+// Two SMs on one tile (cta_group::2) would move a third less, but the release
+// of an accumulator then has to travel between them, about 1000 cycles from the
+// end of a block's MMAs to the start of those that reuse its accumulator, and
+// with two accumulators that, not the tensor cores, set the pace (630 ns a
+// block; this form takes about 415, the MMAs alone 270).
+// What bounds the block loop: 48 KB of operands come in from L2 (768 cycles at
+// 64 bytes a cycle) and are written to shared memory and read once by the MMAs
+// (96 KB, 768 cycles at 128 bytes a cycle); and the round of an accumulator:
+// issue to the end of its MMAs 900 cycles, the last epilogue warp's start 115
+// (SwiGLU form 340), drain 450 (500), release to the next issue 230 (310), for
+// every second block.  A block takes about 785 (905) cycles, and a tile about
+// 4900 more for its start and its stores.  Measured, bf16 output: 8192 rows,
+// 7168 x 7168, 309 us (2.7 PFLOP/s); 8192 rows, 7168 x 2048, 111 us (2.2).
+// SwiGLU form: a tile is 128 SiLU-half channels and the multiplier channels of
+// the same numbers, so it holds 128 complete channels of g and the epilogue
+// quantises them as one block; h never leaves the SM.
 // Every wait is bounded (about two seconds) and sets MOE_DEV_TIMEOUT.
 #include "common.cuh"
 #include "fp8.cuh"
@@ -54,7 +51,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int BM = 128;                 // rows per CTA (256 per pair)
+constexpr int BM = 128;                 // rows per tile
 constexpr int BN = 256;                 // channels per tile
 constexpr int BK = 128;                 // bytes of K per block: one scale
 constexpr int STAGES = 4;
@@ -111,43 +108,31 @@ struct LargeDev {
     int vec_scales;      // rows of a_scales can be read 16 bytes at a time
 };
 
-// A cluster's tile as one CTA sees it: expert, its first row, its rows there
-// (may be <= 0 or more than BM), its column block, and whether it is a wide one.
+// Expert, first row, rows from there to the expert's end (may be more than BM),
+// column block.
 struct Tile {
     int e, row0, rows, nb;
-    bool wide;
 };
 
 // Tiles of an expert with `rows` rows.
-__device__ __forceinline__ int tiles_of(int rows, int n_blocks) {
-    const int blocks = (rows + BM - 1) / BM;
-    return (blocks >> 1) * n_blocks + (blocks & 1) * ((n_blocks + 1) >> 1);
-}
+__device__ __forceinline__ int tiles_of(int rows, int n_blocks) { return (rows + BM - 1) / BM * n_blocks; }
 
-// Column-block-major within an expert: the clusters in flight share few weight
+// Column-block-major within an expert: the CTAs in flight share few weight
 // tiles, each read by all of the expert's row blocks while it is in L2.
-__device__ __forceinline__ Tile decode(int64_t tile, const LargeDev &p, const int32_t *s_tile,
-                                       const int32_t *s_off, int rank) {
+__device__ __forceinline__ Tile decode(int tile, const LargeDev &p, const int32_t *s_tile,
+                                       const int32_t *s_off) {
     int lo = 0, hi = p.E - 1;
     while (lo < hi) {   // last expert whose first tile is <= tile
         const int mid = (lo + hi + 1) >> 1;
         if (s_tile[mid] <= tile) lo = mid; else hi = mid - 1;
     }
-    const int rows = s_off[lo + 1] - s_off[lo];
-    const int pairs = (rows + BM - 1) / BM >> 1;   // tall row blocks
-    const int local = (int)tile - s_tile[lo];
+    const int blocks = (s_off[lo + 1] - s_off[lo] + BM - 1) / BM;
+    const int local = tile - s_tile[lo];
     Tile t;
     t.e = lo;
-    t.wide = local >= pairs * p.n_blocks;
-    if (!t.wide) {
-        t.nb = local / pairs;
-        t.row0 = s_off[lo] + (local % pairs) * (2 * BM) + rank * BM;
-        t.rows = s_off[lo + 1] - t.row0;
-    } else {
-        t.nb = 2 * (local - pairs * p.n_blocks) + rank;
-        t.row0 = s_off[lo] + pairs * (2 * BM);
-        t.rows = t.nb < p.n_blocks ? s_off[lo + 1] - t.row0 : 0;
-    }
+    t.nb = local / blocks;
+    t.row0 = s_off[lo] + local % blocks * BM;
+    t.rows = s_off[lo + 1] - t.row0;
     return t;
 }
 
@@ -202,9 +187,8 @@ __device__ __forceinline__ int group_col(int cg, int j) {
 
 template <int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
-k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA64,
-                 const __grid_constant__ CUtensorMap tmB,
-                LargeDev p) {
+k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 LargeDev p) {
     // aligned by its declaration, so that every address in it is a constant
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING_BYTES);
@@ -223,12 +207,11 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     int32_t *s_tile = s_off + (kMaxExperts + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1);        // armed with the rows and both CTAs' channels
-            mbar_init(&empty[s], 2);       // both CTAs' MMAs have read it
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -245,7 +228,6 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
     if (warp == 0 && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA64) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
     }
     if (warp == 1) {
@@ -277,13 +259,10 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // both CTAs' barriers exist before any copy or commit reaches them
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int64_t total_tiles = s_tile[p.E];
-    // the cluster's tiles: its index, and every cluster count after it
-    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
-    const int my_tiles = first < total_tiles ? (int)((total_tiles - first + step - 1) / step) : 0;
+    const int total_tiles = s_tile[p.E];   // C fits memory, so they are far below 2^31
+    const int my_tiles = (int)blockIdx.x < total_tiles ? (total_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
 
     if (warp < EPI_WARP0) {
       regs_dec<REGS_ISSUE>();
@@ -295,44 +274,26 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int64_t armed = 0;   // stage uses
             bool ok = true;
             for (int i = 0; ok && i < my_tiles; ++i) {
-                const Tile t = decode(first + i * step, p, s_tile, s_off, (int)rank);
+                const Tile t = decode((int)(blockIdx.x + i * gridDim.x), p, s_tile, s_off);
                 // the tile's two 128-channel halves
                 const int ch0 = EPI == EPI_SWIGLU ? t.nb * 128 : t.nb * BN;
                 const int ch1 = EPI == EPI_SWIGLU ? ch0 + p.N / 2 : ch0 + BN / 2;
                 for (int kb = 0; kb < p.num_kb; ++kb) {
-                    // free once both CTAs' MMAs have read what was there: the
-                    // channels are written to both
                     if (!wait_bounded_inline(&empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     uint8_t *sa = smem + (size_t)stage * STAGE_BYTES;
                     mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
                     ++armed;
-                    // rows past this CTA's (or past the buffer) only reach
-                    // accumulator rows that are never stored; bytes past K are 0
-                    if (!t.wide) {
-                        tma_load_2d(sa, &tmA, &full[stage], kb * BK, t.row0);
-                        tma_load_3d_multicast(sa + A_BYTES + rank * (B_BYTES / 2), &tmB, &full[stage],
-                                              kb * BK, rank ? ch1 : ch0, t.e, 0x3);
-                    } else {
-                        tma_load_2d_multicast(sa + rank * (A_BYTES / 2), &tmA64, &full[stage], kb * BK,
-                                              t.row0 + (int)rank * (BM / 2), 0x3);
-                        tma_load_3d(sa + A_BYTES, &tmB, &full[stage], kb * BK, ch0, t.e);
-                        tma_load_3d(sa + A_BYTES + B_BYTES / 2, &tmB, &full[stage], kb * BK, ch1, t.e);
-                    }
+                    // rows past the tile's (or past the buffer) only reach accumulator
+                    // rows that are never stored; bytes past K are 0
+                    tma_load_2d(sa, &tmA, &full[stage], kb * BK, t.row0);
+                    tma_load_3d(sa + A_BYTES, &tmB, &full[stage], kb * BK, ch0, t.e);
+                    tma_load_3d(sa + A_BYTES + B_BYTES / 2, &tmB, &full[stage], kb * BK, ch1, t.e);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
-            // every armed stage must have landed (the peer's half too) before exit
+            // every armed stage must have landed before exit
             for (int64_t u = armed > STAGES ? armed - STAGES : 0; u < armed; ++u)
                 wait_bounded_inline(&full[u % STAGES], (uint32_t)(u / STAGES) & 1u, abort_flag, p.status, false);
-            // and the peer's releases of them, which arrive on this CTA's barriers
-            for (int64_t u = armed > STAGES ? armed - STAGES : 0; ok && u < armed; ++u)
-                ok = wait_bounded_inline(&empty[u % STAGES], (uint32_t)(u / STAGES) & 1u, abort_flag, p.status);
-            if (!ok) {
-                // after a give-up, leave the copies still in flight to the peer
-                // time to land before either CTA exits
-                const uint64_t t0 = globaltimer();
-                while (globaltimer() - t0 < 100000ull) __nanosleep(2000);
-            }
         }
       } else if (warp == 2) {
         // ---------------------------------------------------- scales
@@ -340,7 +301,7 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         uint32_t phase = 0;
         bool ok = true;
         for (int i = 0; ok && i < my_tiles; ++i) {
-            const Tile t = decode(first + i * step, p, s_tile, s_off, (int)rank);
+            const Tile t = decode((int)(blockIdx.x + i * gridDim.x), p, s_tile, s_off);
             // lane's rows lane + 32 u, clamped to rows that exist
             const int64_t row0 = min((int64_t)t.row0, p.cap_rows - 1);
             const int last = (int)min((int64_t)max(t.rows, 1), p.cap_rows - row0) - 1;
@@ -348,8 +309,8 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int at[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) at[u] = min(lane + 32 * u, last) * p.num_kb;
-            // (clamped: a wide tile's second column block may lie past the last)
-            const int wb0 = min(EPI == EPI_SWIGLU ? t.nb : 2 * t.nb, p.w_blocks - 1);
+            const int wb0 = EPI == EPI_SWIGLU ? t.nb : 2 * t.nb;
+            // (clamped: the last tile may have only one block of 128 channels)
             const int wb1 = min(EPI == EPI_SWIGLU ? t.nb + p.w_blocks / 2 : 2 * t.nb + 1, p.w_blocks - 1);
             const float *sw0 = p.w_scales + ((int64_t)t.e * p.w_blocks + wb0) * p.num_kb;
             const float *sw1 = p.w_scales + ((int64_t)t.e * p.w_blocks + wb1) * p.num_kb;
@@ -414,7 +375,7 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         mma_f8(d_tmem, desc_sw128(a_addr + 32 * k), desc_sw128(b_addr + 32 * k), idesc,
                                k > 0 ? 1u : 0u);
                     mma_commit(&acc_full[accb]);
-                    mma_commit_multicast(&empty[stage], 0x3);
+                    mma_commit(&empty[stage]);
                     acc_phase ^= 1u;
                 }
                 turn ^= 1;
@@ -436,8 +397,8 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         uint32_t tile_par = 0;
         int sc_stage = 0;
         uint32_t sc_phase = 0;
-        for (int it = 0; it < my_tiles; ++it) {
-            const Tile t = decode((int64_t)(blockIdx.x >> 1) + (int64_t)it * (gridDim.x >> 1), p, s_tile, s_off, (int)rank);
+        for (int tile = (int)blockIdx.x; tile < total_tiles; tile += gridDim.x) {
+            const Tile t = decode(tile, p, s_tile, s_off);
             const bool rows_here = q * 32 < t.rows;   // warp-uniform
             float2 acc[CPT / 2];
 #pragma unroll
@@ -445,7 +406,8 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             bool ok = true;
             for (int kb = 0; kb < p.num_kb; ++kb) {
                 if ((kb & (SB - 1)) == 0) {
-                    const bool w = wait_bounded_inline(&sc_full[sc_stage], sc_phase, abort_flag, p.status);
+                    // (not in line: nothing spills with the call, 28 bytes without)
+                    const bool w = wait_bounded(&sc_full[sc_stage], sc_phase, abort_flag, p.status);
                     if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
                 }
                 const float *sc = s_scale + sc_stage * SC_FLOATS + (kb & (SB - 1)) * 2 * BM + rloc;
@@ -586,58 +548,27 @@ k_gemm_fp8_large(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
 }
 
-// Clusters that fit on the GPU at once (0 if the kernel cannot run).
-template <int EPI>
-int clusters_that_fit() {
-    static const int n = [] {
-        if (!set_smem_limit((const void *)k_gemm_fp8_large<EPI>, SMEM_BYTES)) return 0;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
-        cfg.blockDim = dim3(THREADS);
-        cfg.dynamicSmemBytes = SMEM_BYTES;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int c = 0;
-        if (cudaOccupancyMaxActiveClusters(&c, (const void *)k_gemm_fp8_large<EPI>, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            c = 0;
-        }
-        return c;
-    }();
-    return n;
-}
-
 template <int EPI>
 moe_status launch(const Fp8GemmArgs &a, const LargeDev &d, cudaStream_t stream) {
-    const int clusters = clusters_that_fit<EPI>();
-    if (clusters <= 0) return MOE_ERR_UNSUPPORTED;
-    CUtensorMap ma, ma64, mb;
+    if (!set_smem_limit((const void *)k_gemm_fp8_large<EPI>, SMEM_BYTES)) return MOE_ERR_CUDA;
+    CUtensorMap ma, mb;
     const uint64_t adims[2] = {(uint64_t)a.Kd, (uint64_t)a.cap_rows};
     const uint64_t astr[1] = {(uint64_t)a.Kd};
-    const uint32_t abox[2] = {BK, BM}, abox64[2] = {BK, BM / 2};
+    const uint32_t abox[2] = {BK, BM};
     const uint64_t bdims[3] = {(uint64_t)a.Kd, (uint64_t)a.N, (uint64_t)a.E};
     const uint64_t bstr[2] = {(uint64_t)a.Kd, (uint64_t)a.Kd * a.N};
     const uint32_t bbox[3] = {BK, BN / 2, 1};
     if (!make_tensor_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, a.a, 2, adims,
                          astr, abox) ||
-        !make_tensor_map(&ma64, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, a.a, 2, adims,
-                         astr, abox64) ||
         !make_tensor_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, a.w, 3, bdims,
                          bstr, bbox))
         return MOE_ERR_CUDA;
     const char *names[3] = {"gemm_fp8_f32", "gemm_fp8_bf16", "gemm_fp8_swiglu"};
-    MOE_LAUNCH_CLUSTER(names[EPI], k_gemm_fp8_large<EPI>, 2 * clusters, THREADS, SMEM_BYTES, stream, 2u,
-                       ma, ma64, mb, d);
+    MOE_LAUNCH(names[EPI], k_gemm_fp8_large<EPI>, (unsigned)num_sms(), THREADS, SMEM_BYTES, stream, ma, mb, d);
     return MOE_OK;
 }
 
