@@ -11,7 +11,8 @@
 //      K-th largest key; over quarters of the lanes' keys where few lanes
 //      have any.  Only keys at or above it can be chosen: about 9 of
 //      256 for K = 8, 22 of 1000 for K = 16.
-//   2. Those candidates are collected in the order of their experts, one a lane.
+//   2. Those candidates are collected in the order of their experts, one a lane,
+//      which computes its expert's score from the logit with expf.
 //   3. A candidate's place is the number of larger candidates and of equal ones
 //      in lower lanes; its lane computes its weight and writes it there.
 // More than 32 candidates (many equal keys) are chosen one by one instead.
@@ -20,14 +21,16 @@
 //
 // A warp's instructions bound it, not memory, and of those the comparisons,
 // maxima and selections, which run at half the rate of the others (32768
-// tokens, 256 experts of bf16 logits, K = 8: 16.2 us a call, where the bytes
-// take 2.9 us; 4097 tokens, 1000 experts, 20 groups, K = 16: 14.4 us, 2.5).  So
+// tokens, 256 experts of bf16 logits, K = 8: 16.9 us a call, where the bytes
+// take 2.9 us; 4097 tokens, 1000 experts, 20 groups, K = 16: 14.5 us, 2.5).  So
 // nothing is computed for experts that is not needed for the choice, and counts
 // are kept in floats, so that they are not added on that pipe too (18.6 -> 16.2 us
-// together with the next token's logits on their way).  Without a bias the keys are the logits themselves (scores order as
-// they do); with one, the scores behind the keys use the hardware's approximate
-// exponential and reciprocal (a few units in the last place); the K scores that
-// become weights are computed again from their logits with expf.
+// together with the next token's logits on their way).  Without a bias the keys
+// are the logits until the candidates are known, whose scores then decide (16.3
+// -> 16.9 us against the logits alone, whose order is another where scores are
+// equal).  With a bias, and for the groups' values, the scores behind the keys use the
+// hardware's approximate exponential and reciprocal (a few units in the last
+// place); the scores that become weights are always those with expf.
 #include "common.cuh"
 
 #include <type_traits>
@@ -116,6 +119,22 @@ __device__ __forceinline__ float sigmoid_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
+}
+
+// The keys without a bias are logits until the candidates are known.  Different
+// logits may have the same score in fp32 (1 above 16.6, 0 far below the largest
+// one), and then the lower index comes first, whichever logit is larger.  So
+// `b`, a lower bound of the K-th largest logit, goes down to where the scores
+// are smaller for certain: to where 1 + exp(-l), or exp(l - top), is off by
+// 2^-20 of itself and more, eight units in the last place.
+__device__ __forceinline__ float sigmoid_floor(float b) {
+    const float c = fminf(b, 12.0f);            // 1 - score(12) is 100 units in the last place
+    return c < -80.0f ? ninf() : c - fmaf(__expf(c), 0x1p-20f, 0x1p-20f);
+}
+__device__ __forceinline__ float softmax_floor(float b, float top) {
+    b = fminf(b, kF32Max);
+    const float d = top - b;                    // rounded to 2^-24 of itself in a score
+    return d > 80.0f ? ninf() : b - fmaf(d, 0x1p-21f, 0x1p-20f);
 }
 
 // VEC: runs load as vectors.  Runs of up to 16 keys stay in registers, longer
@@ -315,10 +334,9 @@ k_gate(GateDev p) {
         // ---- groups
         if (p.G > 1) {
             // Without a bias the keys are logits; a group's value is of scores.
-            const bool logit_keys = p.top2 && !p.bias;
             auto value = [&](float k) {
-                if (!logit_keys || k == ninf()) return k;
-                return p.sigmoid ? __fdividef(1.0f, 1.0f + expf(-k)) : expf(fminf(k, kF32Max) - top);
+                if (p.bias || k == ninf()) return k;
+                return p.sigmoid ? sigmoid_approx(k) : __expf(fminf(k, kF32Max) - top);
             };
             auto group_value = [&](float a, float b) {
                 return p.top2 && b != ninf() ? value(a) + value(b) : value(a);
@@ -474,6 +492,7 @@ k_gate(GateDev p) {
                 for (int u = 0; u < Q; ++u) part[u] = part[u] == bound ? ninf() : part[u];
             }
         }
+        if (!p.bias) bound = p.sigmoid ? sigmoid_floor(bound) : softmax_floor(bound, top);
         bound = fmaxf(bound, raw_keys ? kLeastOpen : -kF32Max);   // closed experts are no candidates
         // candidates of the lower lanes come first
         float in_run = 0.0f;                    // counted where the comparisons do not run
@@ -491,9 +510,13 @@ k_gate(GateDev p) {
         }
         const int count = __shfl_sync(kFull, upto, 31);
         const int n = min(count, p.K);          // experts that are chosen
-        // the lane's choice, if it has one: expert, key and place in the order
+        // the lane's choice, if it has one: expert, key, score (SOFTMAX: before the
+        // division by the sum) and place in the order
         int id = 0, place = p.K;
-        float mine = 0.0f;
+        float mine = 0.0f, score = 0.0f;
+        auto score_of = [&](float l) {
+            return p.sigmoid ? __frcp_rn(1.0f + expf(-l)) : expf(fminf(l, kF32Max) - top);
+        };
         if (count <= 32) {
             float2 *cand = s_cand[warp];
             if (lane < 3) cand[count + lane].x = ninf();
@@ -509,6 +532,11 @@ k_gate(GateDev p) {
                 const float2 own_cand = cand[lane];
                 mine = own_cand.x;
                 id = __float_as_int(own_cand.y);
+                score = score_of(p.bias ? load_logit<BF16>(p, row + id) : mine);
+                if (!p.bias) cand[lane].x = mine = score;   // logits so far: the scores decide
+            }
+            __syncwarp();
+            if (lane < count) {
                 float before = 0.0f;            // counted where the comparisons do not run
                 for (int i = 0; i < count; i += 4) {
                     const float4 a = *reinterpret_cast<const float4 *>(cand + i);
@@ -523,6 +551,16 @@ k_gate(GateDev p) {
                 place += __popc(__match_any_sync(count < 32 ? (1u << count) - 1u : kFull, __float_as_uint(mine + 0.0f)) & lanemask_lt());
             }
         } else {
+            if (!p.bias) {                      // scores in the logits' places, in shared memory: rare
+                if constexpr (!MEM) write_run(key, sk + run0, p.padded, have);
+                const int keys = p.padded ? VPL : have;
+#pragma unroll 1
+                for (int j = 0; j < keys; ++j) {
+                    const float l = sk[run0 + j];
+                    sk[run0 + j] = l >= bound ? score_of(l) : ninf();
+                }
+                if constexpr (!MEM) read_run(key, sk + run0, p.padded, have);
+            }
             uint32_t used = 0;
             for (int k = 0; k < n; ++k) {
                 float m = ninf();
@@ -538,14 +576,12 @@ k_gate(GateDev p) {
                 if (m == best && (first & lanemask_lt()) == 0) used |= 1u << j1;
                 if (lane == k) { id = expert; place = k; mine = best; }
             }
+            if (place < p.K) score = p.bias ? score_of(load_logit<BF16>(p, row + id)) : mine;
         }
         // ---- weights
         const bool chosen = place < p.K;
         float w = 0.0f;
-        if (chosen) {
-            const float l = fminf(p.bias ? load_logit<BF16>(p, row + id) : mine, kF32Max);
-            w = __fdividef(p.sigmoid ? 1.0f : expf(l - top), p.sigmoid ? 1.0f + expf(-l) : sum);
-        }
+        if (chosen) w = p.sigmoid ? score : __fdividef(score, sum);
         if (p.renorm) {
             float s = w;
 #pragma unroll

@@ -408,7 +408,11 @@ moe_status moe_add_rms_norm(int64_t num_tokens, int64_t hidden, const void *x,
  *   largest keys (GROUP_TOP2; its only key where one expert is open), and the
  *   topk_groups groups of the largest values take part.
  *   The K experts of the largest keys are chosen, in descending order.  Equal
- *   keys and equal groups: the lower index first.
+ *   keys and equal groups: the lower index first.  Logits whose scores are the
+ *   same number in fp32 make equal keys: sigmoids from 17 on, exponentials 104
+ *   and more below the largest.  The exponentials, quotients and sums are within
+ *   a few units in the last place (a score below 2^-126 may count as 0), so
+ *   different keys, or groups, that are as near as that may come in either order.
  *   weight   = score / (sum of the chosen scores + 1e-20) if renormalize, else
  *              score; times scale.  (The bias moves the choice, not the weight.)
  * Where fewer than K experts are open in the groups that take part, the routes
