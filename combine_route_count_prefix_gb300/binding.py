@@ -157,19 +157,31 @@ def _stream(stream=None):
 
 
 def _addr(t):
-    """A tensor's address as a plain integer (None for None), and the raw handle
-    of the current or given stream: what ctypes converts at the least cost on
-    calls whose kernels take a few microseconds."""
+    """The address of a tensor that may be None, as a plain integer: what ctypes
+    converts at the least cost on calls whose kernels take a few microseconds."""
     return None if t is None else t.data_ptr()
 
 
+_current_device = torch._C._cuda_getDevice
+
+
 def _raw_stream(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    """The launches go to the current device, so the tensors (on GPU number
+    `device`) and the stream have to be its own."""
+    if device < 0:
+        raise ValueError("must be CUDA tensors")
+    if device != _current_device():
+        raise ValueError(f"tensors on cuda:{device}, but cuda:{_current_device()} is the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"stream: of cuda:{stream.device_index}, but the tensors are on cuda:{device}")
+    return stream.cuda_stream
 
 
-def _check(t, dtype, shape, name):
+def _check(t, dtype, shape, name, device=None):
+    """device: number of the GPU that the call's first tensor is on (-1: on none,
+    which _raw_stream refuses); without it, the current one."""
     if t is None:
         return
     if t.dtype is not dtype:
@@ -178,8 +190,18 @@ def _check(t, dtype, shape, name):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if not t.is_cuda:
+    if t.get_device() != device:
+        _check_device(t, name, device)
+
+
+def _check_device(t, name, device=None):
+    at = t.get_device()
+    if at < 0:
         raise ValueError(f"{name}: must be a CUDA tensor")
+    if device is None:
+        device = _current_device()
+    if at != device:
+        raise ValueError(f"{name}: on cuda:{at}, expected cuda:{device}")
 
 
 def make_shape(T, P, H, E, K, N=0, mask_kind=0, has_shared=False, zero_experts=0,
@@ -485,11 +507,12 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out=None, with_y=True, with
     some of these tensors, exactly those are computed; residual_out may be the
     residual itself and y may be x itself."""
     T, H = x.shape
+    dev = x.get_device()
     if weight.dtype not in _DTYPES:
         raise TypeError(f"weight: dtype {weight.dtype}, expected float32 or bfloat16")
-    _check(x, torch.bfloat16, (T, H), "x")
-    _check(residual, torch.bfloat16, (T, H), "residual")
-    _check(weight, weight.dtype, (H,), "weight")
+    _check(x, torch.bfloat16, (T, H), "x", dev)
+    _check(residual, torch.bfloat16, (T, H), "residual", dev)
+    _check(weight, weight.dtype, (H,), "weight", dev)
     if out is None:
         out = {}
         if residual is not None:
@@ -500,13 +523,13 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out=None, with_y=True, with
             out["q"] = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=x.device)
             out["scales"] = torch.empty((T, _blocks(H)), dtype=torch.float32, device=x.device)
     else:
-        _check(out.get("residual_out"), torch.bfloat16, (T, H), "residual_out")
-        _check(out.get("y"), torch.bfloat16, (T, H), "y")
-        _check(out.get("q"), torch.float8_e4m3fn, (T, H), "q")
-        _check(out.get("scales"), torch.float32, (T, _blocks(H)), "scales")
-    _call("moe_add_rms_norm", T, H, _addr(x), _addr(residual), _addr(weight),
+        _check(out.get("residual_out"), torch.bfloat16, (T, H), "residual_out", dev)
+        _check(out.get("y"), torch.bfloat16, (T, H), "y", dev)
+        _check(out.get("q"), torch.float8_e4m3fn, (T, H), "q", dev)
+        _check(out.get("scales"), torch.float32, (T, _blocks(H)), "scales", dev)
+    _call("moe_add_rms_norm", T, H, x.data_ptr(), _addr(residual), weight.data_ptr(),
           _DTYPES[weight.dtype], eps, _addr(out.get("residual_out")), _addr(out.get("y")),
-          _addr(out.get("q")), _addr(out.get("scales")), _raw_stream(stream, x.device))
+          _addr(out.get("q")), _addr(out.get("scales")), _raw_stream(stream, dev))
     return out
 
 
@@ -527,27 +550,25 @@ def gate(logits, topk, bias=None, mask=None, score="softmax", groups=1, topk_gro
     K = int(topk)
     if logits.dtype not in _DTYPES:
         raise TypeError(f"logits: dtype {logits.dtype}, expected float32 or bfloat16")
-    if not logits.is_cuda:
-        raise ValueError("logits: must be a CUDA tensor")
+    dev = logits.get_device()
     if E > 1 and logits.stride(1) != 1:
         raise ValueError("logits: a token's logits must be contiguous")
-    _check(bias, torch.float32, (E,), "bias")
-    _check(mask, torch.uint8, (T,), "mask")
+    _check(bias, torch.float32, (E,), "bias", dev)
+    _check(mask, torch.uint8, (T,), "mask", dev)
     if out is None:
-        dev = logits.device
-        out = dict(expert_ids=torch.empty((T, K), dtype=torch.int32, device=dev),
-                   expert_scales=torch.empty((T, K), dtype=torch.float32, device=dev),
-                   route_mask=torch.empty((T, K), dtype=torch.uint8, device=dev))
+        out = dict(expert_ids=torch.empty((T, K), dtype=torch.int32, device=logits.device),
+                   expert_scales=torch.empty((T, K), dtype=torch.float32, device=logits.device),
+                   route_mask=torch.empty((T, K), dtype=torch.uint8, device=logits.device))
     else:
-        _check(out["expert_ids"], torch.int32, (T, K), "expert_ids")
-        _check(out["expert_scales"], torch.float32, (T, K), "expert_scales")
-        _check(out.get("route_mask"), torch.uint8, (T, K), "route_mask")
+        _check(out["expert_ids"], torch.int32, (T, K), "expert_ids", dev)
+        _check(out["expert_scales"], torch.float32, (T, K), "expert_scales", dev)
+        _check(out.get("route_mask"), torch.uint8, (T, K), "route_mask", dev)
     desc = _gate_desc(T, E, K, int(groups), int(groups if topk_groups is None else topk_groups),
                       logits.stride(0) if T > 1 else E, logits.dtype, score, group_score,
                       int(bool(renormalize)), float(scale))
-    _call("moe_gate", desc, _addr(logits), _addr(bias), _addr(mask), _addr(out["expert_ids"]),
-          _addr(out["expert_scales"]), _addr(out.get("route_mask")),
-          _raw_stream(stream, logits.device))
+    _call("moe_gate", desc, logits.data_ptr(), _addr(bias), _addr(mask),
+          out["expert_ids"].data_ptr(), out["expert_scales"].data_ptr(),
+          _addr(out.get("route_mask")), _raw_stream(stream, dev))
     return out
 
 
@@ -557,24 +578,27 @@ def grouped_gemm_fp8(expert_offsets, a, a_scales, w, w_scales, ws=None, out=None
     operands.  Returns (out [rows, N], workspace); `out`'s dtype (or out_dtype)
     is bfloat16 or float32."""
     rows, Kd = a.shape
+    dev = a.get_device()
     E, N, _ = w.shape
-    _check(a, torch.float8_e4m3fn, (rows, Kd), "a")
-    _check(a_scales, torch.float32, (rows, _blocks(Kd)), "a_scales")
-    _check(w, torch.float8_e4m3fn, (E, N, Kd), "w")
-    _check(w_scales, torch.float32, (E, _blocks(N), _blocks(Kd)), "w_scales")
-    _check(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    _check(a, torch.float8_e4m3fn, (rows, Kd), "a", dev)
+    _check(a_scales, torch.float32, (rows, _blocks(Kd)), "a_scales", dev)
+    _check(w, torch.float8_e4m3fn, (E, N, Kd), "w", dev)
+    _check(w_scales, torch.float32, (E, _blocks(N), _blocks(Kd)), "w_scales", dev)
+    _check(expert_offsets, torch.int32, (E + 1,), "expert_offsets", dev)
     if out is None:
         out = torch.empty((rows, N), dtype=out_dtype, device=a.device)
     if out.dtype not in _DTYPES:
         raise TypeError(f"out: dtype {out.dtype}, expected float32 or bfloat16")
-    _check(out, out.dtype, (rows, N), "out")
+    _check(out, out.dtype, (rows, N), "out", dev)
     if ws is None:
         n = ctypes.c_size_t()
         _call("moe_grouped_gemm_fp8_workspace_size", rows, E, N, Kd, ctypes.byref(n))
         _, ws = _alloc_ws(n.value, a.device)
-    _call("moe_grouped_gemm_fp8", rows, E, N, Kd, _addr(expert_offsets), _addr(a), _addr(a_scales),
-          _addr(w), _addr(w_scales), _addr(out), _DTYPES[out.dtype], FFN_PATHS[path], _addr(ws),
-          ws.numel(), _raw_stream(stream, a.device))
+    if ws.get_device() != dev:
+        _check_device(ws, "ws", dev)
+    _call("moe_grouped_gemm_fp8", rows, E, N, Kd, expert_offsets.data_ptr(), a.data_ptr(),
+          a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), out.data_ptr(),
+          _DTYPES[out.dtype], FFN_PATHS[path], ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     return out, ws
 
 
@@ -591,22 +615,26 @@ def grouped_ffn_fp8(shape: MoeShape, x, x_scales, expert_offsets, w1, w1_scales,
     expert-major rows [T*K, H].  Returns (y bf16 [T*K, H], workspace)."""
     T, K, H, E, N = shape.num_tokens, shape.topk, shape.hidden, shape.num_experts, shape.ffn
     R = T * K if assist is None else T
-    _check(x, torch.float8_e4m3fn, (R, H), "x")
-    _check(x_scales, torch.float32, (R, _blocks(H)), "x_scales")
-    _check(assist, torch.int32, (T * K, 3), "assist")
-    _check(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
-    _check(w1, torch.float8_e4m3fn, (E, N, H), "w1")
-    _check(w1_scales, torch.float32, (E, N // FP8_BLOCK, _blocks(H)), "w1_scales")
-    _check(w2, torch.float8_e4m3fn, (E, H, N // 2), "w2")
-    _check(w2_scales, torch.float32, (E, _blocks(H), N // 2 // FP8_BLOCK), "w2_scales")
+    dev = x.get_device()
+    _check(x, torch.float8_e4m3fn, (R, H), "x", dev)
+    _check(x_scales, torch.float32, (R, _blocks(H)), "x_scales", dev)
+    _check(assist, torch.int32, (T * K, 3), "assist", dev)
+    _check(expert_offsets, torch.int32, (E + 1,), "expert_offsets", dev)
+    _check(w1, torch.float8_e4m3fn, (E, N, H), "w1", dev)
+    _check(w1_scales, torch.float32, (E, N // FP8_BLOCK, _blocks(H)), "w1_scales", dev)
+    _check(w2, torch.float8_e4m3fn, (E, H, N // 2), "w2", dev)
+    _check(w2_scales, torch.float32, (E, _blocks(H), N // 2 // FP8_BLOCK), "w2_scales", dev)
     if y is None:
         y = torch.empty((T * K, H), dtype=torch.bfloat16, device=x.device)
-    _check(y, torch.bfloat16, (T * K, H), "y")
+    _check(y, torch.bfloat16, (T * K, H), "y", dev)
     if ws is None:
         _, ws = _alloc_ws(grouped_ffn_fp8_workspace_size(shape), x.device)
-    _call("moe_grouped_ffn_fp8", ctypes.byref(shape), _addr(x), _addr(x_scales), _addr(assist),
-          _addr(expert_offsets), _addr(w1), _addr(w1_scales), _addr(w2), _addr(w2_scales), _addr(y),
-          _addr(ws), ws.numel(), _raw_stream(stream, x.device))
+    if ws.get_device() != dev:
+        _check_device(ws, "ws", dev)
+    _call("moe_grouped_ffn_fp8", ctypes.byref(shape), x.data_ptr(), x_scales.data_ptr(),
+          _addr(assist), expert_offsets.data_ptr(), w1.data_ptr(), w1_scales.data_ptr(),
+          w2.data_ptr(), w2_scales.data_ptr(), y.data_ptr(), ws.data_ptr(), ws.numel(),
+          _raw_stream(stream, dev))
     return y, ws
 
 

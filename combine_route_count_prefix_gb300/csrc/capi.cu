@@ -2,6 +2,7 @@
 // layout, the order of kernels behind each entry point, launch counting and
 // per-kernel event profiling.
 #include "common.cuh"
+#include "limits.cuh"
 
 #include <atomic>
 #include <mutex>
@@ -71,28 +72,25 @@ void launch_end(int token, cudaStream_t stream) {
 }
 
 bool set_smem_limit(const void *kernel, size_t bytes) {
-    static std::mutex mu;
-    static std::vector<std::pair<const void *, size_t>> done;
-    std::lock_guard<std::mutex> lk(mu);
-    size_t *have = nullptr;
-    for (auto &d : done)
-        if (d.first == kernel) have = &d.second;
-    if (have && *have >= bytes) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-        cudaSuccess) {
+    static RaisedLimits raised;
+    return raised.ensure(current_device(), kernel, bytes, [&] {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+            cudaSuccess)
+            return true;
         cudaGetLastError();
         return false;
-    }
-    if (have) *have = bytes;
-    else done.emplace_back(kernel, bytes);
-    return true;
+    });
+}
+
+int current_device() {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    return dev < 0 || dev >= kMaxDevices ? 0 : dev;
 }
 
 int num_sms() {
-    static int cached[64] = {0};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) dev = 0;
+    static int cached[kMaxDevices] = {0};
+    const int dev = current_device();
     if (cached[dev] == 0) {
         int n = 0;
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);

@@ -649,14 +649,10 @@ moe_status launch_epi(const CUtensorMap &ma, const CUtensorMap &mb, const GemmDe
 // the persistent grid is twice that.
 template <int EPI>
 int pair_clusters() {
-    static int cached = -1;
-    if (cached < 0) {
-        cached = 0;
-        if (cudaFuncSetAttribute(k_grouped_gemm_pair<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)P_SMEM_BYTES) != cudaSuccess) {
-            cudaGetLastError();
-            return cached;
-        }
+    static int known[kMaxDevices];   // clusters + 1, 0 where not asked yet
+    int &cached = known[current_device()];
+    if (cached == 0) {
+        if (!set_smem_limit((const void *)k_grouped_gemm_pair<EPI>, P_SMEM_BYTES)) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
         cfg.blockDim = dim3(THREADS);
@@ -674,9 +670,9 @@ int pair_clusters() {
             cudaGetLastError();
             n = 0;
         }
-        cached = n;
+        cached = n + 1;
     }
-    return cached;
+    return cached - 1;
 }
 
 template <int EPI>
