@@ -40,7 +40,6 @@ class Fp8MoeBlock:
         self.norm_weight, self.router, self.bias = norm_weight, router, bias
         self.w1, self.w1_scales, self.w2, self.w2_scales = w1, w1_scales, w2, w2_scales
         self.topk, self.groups, self.topk_groups, self.scale = topk, groups, topk_groups, scale
-        self.ws = {}
 
     def __call__(self, x, residual, mask=None, stages=None):
         """x, residual bf16 [T, H]; mask uint8 [T] (0: padding).  Returns the new
@@ -55,9 +54,10 @@ class Fp8MoeBlock:
         # bookkeeping only: the FFN takes its rows straight from the tokens
         d = B.dispatch(None, r["expert_ids"], E, 1, mask=r["route_mask"], with_rows=False)
         shape = B.make_shape(T, 1, H, E, self.topk, N)
-        y, self.ws[T] = B.grouped_ffn_fp8(shape, n["q"], n["scales"], d["expert_offsets"], self.w1,
-                                          self.w1_scales, self.w2, self.w2_scales,
-                                          assist=d["assist"], ws=self.ws.get(T))
+        # its workspace, like the outputs, comes from the allocator for this call
+        # alone: calls on other streams, or of other lengths, share nothing with it
+        y, _ = B.grouped_ffn_fp8(shape, n["q"], n["scales"], d["expert_offsets"], self.w1,
+                                 self.w1_scales, self.w2, self.w2_scales, assist=d["assist"])
         # the residual joins the experts' weighted sum in the combine
         out = B.combine(y, d["route_row"], r["expert_scales"], E, 1, mask=r["route_mask"],
                         shared=n["residual_out"])
