@@ -28,8 +28,8 @@
 // end of a block's MMAs to the start of those that reuse its accumulator, and
 // with two accumulators that, not the tensor cores, set the pace (630 ns a
 // block; this form takes about 415, the MMAs alone 270).
-// What bounds the block loop: 48 KB of operands come in from L2 (768 cycles at
-// 64 bytes a cycle) and are written to shared memory and read once by the MMAs
+// What bounds the block loop: 48 KB of operands come in from L2 (61 bytes a
+// cycle, as measured) and are written to shared memory and read once by the MMAs
 // (96 KB, 768 cycles at 128 bytes a cycle); and the round of an accumulator:
 // issue to the end of its MMAs 900 cycles, the last epilogue warp's start 115
 // (SwiGLU form 340), drain 450 (500), release to the next issue 230 (310), for

@@ -24,7 +24,8 @@
  *     workspace; the offending route is treated as inactive.  Each call that
  *     takes a workspace resets the word before its first kernel and later
  *     kernels of the call OR bits into it, so it describes the most recent
- *     call.  moe_read_device_status reads and clears it.
+ *     call.  (Without tokens or rows a call that launches nothing leaves it as
+ *     it was.)  moe_read_device_status reads and clears it.
  *   - Every tensor pointer must be 16-byte aligned; workspace and packed
  *     weights must be 1024-byte aligned.
  *   - With T == 0 the per-token, per-route and per-row arrays are empty and
@@ -455,7 +456,8 @@ moe_status moe_gate(const moe_gate_desc *desc, const void *logits, const float *
  * A e4m3 [rows, Kd]; a_scales fp32 [rows, ceil(Kd / 128)]; W e4m3 [E, N, Kd];
  * w_scales fp32 [E, ceil(N / 128), ceil(Kd / 128)]; C [rows, N] in out_dtype;
  * rows >= offsets[E] untouched.  N % 8 == 0, Kd % 16 == 0, N <= 1048576,
- * Kd <= 131072.  path: MOE_FFN_PATH_* (which kernels; AUTO by rows per expert). */
+ * Kd <= 131072.  path: MOE_FFN_PATH_* (SMALL: the kernel for few rows an expert,
+ * LARGE and LARGE_PAIR: the one for many, AUTO: by an estimate of both). */
 moe_status moe_grouped_gemm_fp8_workspace_size(int64_t rows, int64_t E, int64_t N, int64_t Kd,
                                                size_t *bytes);
 moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
@@ -468,6 +470,9 @@ moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
  * expert e, with moe_grouped_gemm_fp8's products:
  *   h = x . W1[e]^T;  g = silu(h[:N/2]) * h[N/2:]     fp32
  *   q2, s2 = g quantised per 128 columns;  y = bf16(q2 . W2[e]^T)
+ * silu(a) = a / (1 + exp(-a)), the exponential and the quotient each within a few
+ * units in the last place and the exponential's argument rounded once, which a
+ * code's rounding (2^-4 of it) covers; a code may take its other neighbour for it.
  * x, x_scales     with assist: the tokens, e4m3 [T, H] and fp32
  *                 [T, ceil(H / 128)]; row r is token assist[r][0] * (T / P) +
  *                 assist[r][1].  With assist NULL: the rows themselves,
