@@ -1,0 +1,414 @@
+"""Measured cases of the operators around a MoE block that serves a few tokens.
+
+Three operators:
+
+  layer  a whole int8 MoE layer for a few tokens: quantised rows, both expert
+         products with SwiGLU between them, the weighted combine
+  gemm   grouped matrix product in 8-bit integers with one scale per token and
+         one per output channel; bf16 rows are quantised within the call
+  norm   the boundary between two blocks: norm of the block's output, its gate,
+         the scaled residual addition, and the next block's norm, with an e4m3
+         output that carries one scale per token and 128 channels
+
+``run`` computes each in its plain form (elementary torch operations in fp32,
+rounded once at the end), or, where ``own`` is set, through the package's
+public binding.  ``exact`` restates them in 64 bits.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+BLOCK = 128                      # channels per e4m3 scale
+E4M3_MAX = 448.0
+AMAX_FLOOR = 2.0 ** -100         # a block of zeros takes the scale of this amax
+
+# The experts of the repository's full-layer configuration.
+FULL = dict(H=7168, E=128, K=8, N=4096)
+
+
+def listed():
+    return [
+        # one decoded token through 8 of 128 large experts: reading them bounds it
+        dict(name="layer 1 token", op="layer", T=1, Z=0, C=0, mask=0, shared=False, **FULL),
+        # the same through small experts, where latency counts beside the bytes
+        dict(name="layer 1 token small", op="layer", T=1, H=2048, E=128, K=8, N=1536, Z=0, C=0,
+             mask=0, shared=True),
+        # a small decode batch with padding tokens and a shared expert's output
+        dict(name="layer 8 tokens", op="layer", T=8, Z=0, C=0, mask=1, shared=True, **FULL),
+        # a larger one: zero and copy experts, some routes inactive, widths that end inside a tile
+        dict(name="layer 32 tokens", op="layer", T=32, H=2000, E=64, K=6, N=2816, Z=2, C=1, mask=2,
+             shared=False),
+        # a projection of one decoded token, quantised on the way in
+        dict(name="gemm 1 row", op="gemm", rows=1, E=1, N=4096, Kd=7168, skew=0.0, a="bf16",
+             bias=False, out="bf16"),
+        # of a decode batch
+        dict(name="gemm 64 rows", op="gemm", rows=64, E=1, N=7168, Kd=2048, skew=0.0, a="int8",
+             bias=False, out="bf16"),
+        # of a prefill batch: the tensor cores bound it
+        dict(name="gemm 8192 rows", op="gemm", rows=8192, E=1, N=7168, Kd=7168, skew=0.0, a="bf16",
+             bias=False, out="bf16"),
+        # ragged groups, edges that end inside a tile, a bias, fp32 output
+        dict(name="gemm ragged", op="gemm", rows=1533, E=7, N=1000, Kd=1456, skew=1.0, a="int8",
+             bias=True, out="f32"),
+        # one decoded token between two blocks, both norms and a gate per channel
+        dict(name="norm 1 token", op="norm", T=1, H=7168, post=True, gates=1, act="none", y=True,
+             q=False),
+        # a prefill batch, all outputs, a gate per token from a projection: bounded by HBM
+        dict(name="norm prefill", op="norm", T=16384, H=7168, post=True, gates=16384,
+             act="sigmoid", y=True, q=True),
+        # a width that ends inside a block, no norm behind the block, gates of three sequences
+        dict(name="norm odd", op="norm", T=1023, H=1000, post=False, gates=3, act="none", y=False,
+             q=True),
+    ]
+
+
+def _log(rng, lo, hi, step=1):
+    """A multiple of `step`, its factor spread evenly over the logarithm of [lo, hi]."""
+    return step * int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["layer", "gemm", "norm"])
+    if op == "layer":
+        E = _log(rng, 8, 128)
+        c = dict(op=op, T=_log(rng, 1, 32), H=_log(rng, 16, 448, 16), E=E, K=rng.randint(1, 8),
+                 N=_log(rng, 1, 16, 256), Z=rng.choice([0, 0, 2]), C=rng.choice([0, 0, 1]),
+                 mask=rng.choice([0, 0, 1, 2]), shared=rng.random() < 0.5)
+        while c["T"] * c["K"] * c["N"] * c["H"] > 64 * FULL["N"] * FULL["H"]:
+            c["T"] = (c["T"] + 1) // 2
+        return c
+    if op == "gemm":
+        return dict(op=op, rows=_log(rng, 1, 8192), E=rng.choice([1, 1, _log(rng, 2, 16)]),
+                    N=_log(rng, 16, 896, 8), Kd=_log(rng, 8, 448, 16),
+                    skew=rng.choice([0.0, 0.5, 1.0]), a=rng.choice(["bf16", "int8"]),
+                    bias=rng.random() < 0.3, out=rng.choice(["bf16", "f32"]))
+    y, q = rng.choice([(True, True), (True, False), (False, True)])
+    T = _log(rng, 1, 16384)
+    return dict(op=op, T=T, H=_log(rng, 8, 896, 8), post=rng.random() < 0.7,
+                gates=rng.choice([0, 1, 1, T]), act=rng.choice(["none", "sigmoid"]), y=y, q=q)
+
+
+# ------------------------------------------------------------------ inputs
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed))
+    return g
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device=DEV)
+
+
+def _rand(g, *shape):
+    return torch.rand(*shape, generator=g, device=DEV)
+
+
+def _blocks(n):
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _int8(g, *shape):
+    return torch.randint(-127, 128, shape, generator=g, dtype=torch.int8, device=DEV)
+
+
+def _prepare_layer(c, seed):
+    g = _gen(seed)
+    T, H, E, K, N = c["T"], c["H"], c["E"], c["K"], c["N"]
+    # K distinct experts a token, zero and copy experts among them
+    ids = torch.argsort(_rand(g, T, E + c["Z"] + c["C"]), dim=1)[:, :K].int().contiguous()
+    mask = None
+    if c["mask"]:
+        mask = (_rand(g, *((T,) if c["mask"] == 1 else (T, K))) < 0.9).to(torch.uint8)
+        mask[0] = 1
+    s = dict(x=_randn(g, T, H).bfloat16(), ids=ids, probs=torch.softmax(_randn(g, T, K), dim=1),
+             mask=mask, shared=_randn(g, T, H).bfloat16() if c["shared"] else None,
+             w1=_int8(g, E, N, H), scale1=1e-3 + 9e-3 * _rand(g, E, N), w2=_int8(g, E, H, N // 2),
+             scale2=1e-3 + 9e-3 * _rand(g, E, H),
+             out=torch.empty(T, H, dtype=torch.bfloat16, device=DEV))
+    if own:                              # a program packs its weights once
+        from combine_route_count_prefix_gb300 import binding as B
+        s["shape"] = B.make_shape(T, 1, H, E, K, N, mask_kind=c["mask"], has_shared=c["shared"],
+                                  zero_experts=c["Z"], copy_experts=c["C"], ffn_path="small")
+        (_, s["w1"]), (_, s["w2"]) = B.pack_weights(s["shape"], s["w1"], s["w2"])
+    return s
+
+
+def _prepare_gemm(c, seed):
+    g = _gen(seed)
+    rows, E, N, Kd = c["rows"], c["E"], c["N"], c["Kd"]
+    p = torch.exp(c["skew"] * _randn(g, E)).cpu()
+    p = p / p.sum()
+    if E > 3 and c["skew"]:
+        p[2] = 0.0                       # a group without rows
+    pick = torch.multinomial(p, rows, replacement=True,
+                             generator=torch.Generator().manual_seed(int(seed)))
+    counts = torch.bincount(pick, minlength=E)
+    offsets = torch.zeros(E + 1, dtype=torch.int32)
+    offsets[1:] = counts.cumsum(0)
+    int8_rows = c["a"] == "int8"
+    s = dict(a=_int8(g, rows, Kd) if int8_rows else _randn(g, rows, Kd).bfloat16(),
+             a_scales=0.01 + 0.02 * _rand(g, rows) if int8_rows else None, w=_int8(g, E, N, Kd),
+             w_scales=1e-4 + 9e-4 * _rand(g, E, N), bias=_randn(g, E, N) if c["bias"] else None,
+             offsets=offsets.to(DEV), most=int(counts.max()),
+             out=torch.empty(rows, N, device=DEV,
+                             dtype=torch.bfloat16 if c["out"] == "bf16" else torch.float32))
+    if own:
+        from combine_route_count_prefix_gb300 import binding as B
+        _, s["w"] = B.pack_int8(s["w"])
+    return s
+
+
+def _prepare_norm(c, seed):
+    g = _gen(seed)
+    T, H = c["T"], c["H"]
+    # a few channels far larger than the rest, as hidden states have them
+    spread = torch.where(_rand(g, H) < 0.01, 20.0, 1.0)
+    s = dict(x=(_randn(g, T, H) * spread).bfloat16(),
+             residual=(3.0 * _randn(g, T, H) * spread).bfloat16(),
+             weight=(1.0 + 0.2 * _randn(g, H)).bfloat16(),
+             post_weight=(1.0 + 0.2 * _randn(g, H)).bfloat16() if c["post"] else None,
+             gate=_randn(g, c["gates"], H).bfloat16() if c["gates"] else None)
+    out = dict(residual_out=torch.empty(T, H, dtype=torch.bfloat16, device=DEV))
+    if c["y"]:
+        out["y"] = torch.empty(T, H, dtype=torch.bfloat16, device=DEV)
+    if c["q"]:
+        out["q"] = torch.empty(T, H, dtype=torch.float8_e4m3fn, device=DEV)
+        out["scales"] = torch.empty(T, _blocks(H), device=DEV)
+    s["out"] = out
+    return s
+
+
+def prepare(case, seed):
+    s = {"layer": _prepare_layer, "gemm": _prepare_gemm, "norm": _prepare_norm}[case["op"]](case, seed)
+    s["case"] = dict(case)
+    return s
+
+
+RESIDUAL_SCALE, BRANCH_SCALE, EPS = 0.9, 0.4, 1e-6
+
+
+# ------------------------------------------------------------------ plain forms
+
+def _quantise_rows(v):
+    """fp32 rows -> whole-number codes (in fp32) and one scale per row."""
+    s = v.abs().amax(1, keepdim=True) / torch.full((), 127.0, device=v.device)
+    q = torch.where(s > 0, v / torch.where(s > 0, s, 1.0), 0.0)
+    return torch.round(q).clamp(-127, 127), s[:, 0]
+
+
+def _kinds(s):
+    """Per route: whether it takes part, its expert (0 for a special one), and
+    whether it is a zero or a copy expert's."""
+    c, ids = s["case"], s["ids"].long()
+    on = torch.ones_like(ids, dtype=torch.bool)
+    if s["mask"] is not None:
+        on = on & (s["mask"] != 0).view(ids.shape[0], -1)
+    routed = on & (ids < c["E"])
+    return on, routed, torch.where(routed, ids, 0), on & (ids >= c["E"] + c["Z"])
+
+
+def _plain_layer(s):
+    c = s["case"]
+    T, K, Nh = c["T"], c["K"], c["N"] // 2
+    on, routed, e, copy = _kinds(s)
+    x = s["x"].float()
+    q1, s1 = _quantise_rows(x)
+    e = e.reshape(-1)
+    rows = torch.arange(T * K, device=DEV) // K
+    h = torch.bmm(s["w1"][e].float(), q1[rows][:, :, None])[:, :, 0]
+    h = h * s["scale1"][e] * s1[rows][:, None]
+    gate = h[:, :Nh]
+    q2, s2 = _quantise_rows(gate / (1.0 + torch.exp(-gate)) * h[:, Nh:])
+    y = torch.bmm(s["w2"][e].float(), q2[:, :, None])[:, :, 0] * s["scale2"][e] * s2[:, None]
+    y = torch.where(routed[:, :, None], y.view(T, K, -1),
+                    torch.where(copy[:, :, None], x[:, None, :], 0.0))
+    out = (y * s["probs"][:, :, None]).sum(1)
+    if s["shared"] is not None:
+        out = out + s["shared"].float()
+    return out.bfloat16()
+
+
+def _grouped32(rows, offsets, most, w):
+    """Row r of group e times w[e]^T: every group's rows padded to the fullest group's."""
+    E = offsets.numel() - 1
+    r = torch.arange(rows.shape[0], device=rows.device)
+    e = torch.searchsorted(offsets, r.int(), right=True) - 1
+    at = r - offsets[e]
+    padded = torch.zeros(E, most, rows.shape[1], device=rows.device)
+    padded[e, at] = rows
+    return torch.bmm(padded, w.transpose(1, 2))[e, at], e
+
+
+def _plain_gemm(s):
+    if s["a_scales"] is None:
+        q, qs = _quantise_rows(s["a"].float())
+    else:
+        q, qs = s["a"].float(), s["a_scales"]
+    acc, e = _grouped32(q, s["offsets"], s["most"], s["w"].float())
+    y = acc * s["w_scales"][e] * qs[:, None]
+    if s["bias"] is not None:
+        y = y + s["bias"][e]
+    return y.to(s["out"].dtype)
+
+
+def _quantise_blocks(v):
+    """fp32 rows -> e4m3 codes and one fp32 scale per row and 128 channels."""
+    n, H = v.shape
+    nb = _blocks(H)
+    p = torch.zeros(n, nb * BLOCK, device=v.device)
+    p[:, :H] = v
+    p = p.view(n, nb, BLOCK)
+    amax = p.abs().amax(2).clamp(min=AMAX_FLOOR)
+    q = (p * (E4M3_MAX / amax)[:, :, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+    return q.view(n, nb * BLOCK)[:, :H].contiguous(), amax / E4M3_MAX
+
+
+def _plain_norm(s):
+    c = s["case"]
+    T, H = c["T"], c["H"]
+    a = s["x"].float()
+    if c["post"]:
+        a = a * torch.rsqrt((a * a).mean(1, keepdim=True) + EPS) * s["post_weight"].float()
+    if c["gates"]:
+        gate = s["gate"].float()
+        if c["act"] == "sigmoid":
+            gate = 1.0 / (1.0 + torch.exp(-gate))
+        a = (a.view(c["gates"], -1, H) * gate[:, None, :]).view(T, H)
+    h = RESIDUAL_SCALE * s["residual"].float() + BRANCH_SCALE * a
+    v = h * torch.rsqrt((h * h).mean(1, keepdim=True) + EPS) * s["weight"].float()
+    out = dict(residual_out=h.bfloat16())
+    if c["y"]:
+        out["y"] = v.bfloat16()
+    if c["q"]:
+        out["q"], out["scales"] = _quantise_blocks(v)
+    return out
+
+
+# ------------------------------------------------------------------ the package's operators
+
+def _own_layer(s):
+    from combine_route_count_prefix_gb300 import binding as B
+    out, s["ws"] = B.layer_few_tokens(s["shape"], s["x"], s["ids"], s["probs"], s["w1"],
+                                      s["scale1"], s["w2"], s["scale2"], mask=s["mask"],
+                                      shared=s["shared"], ws=s.get("ws"), out=s["out"])
+    return out
+
+
+def _own_gemm(s):
+    from combine_route_count_prefix_gb300 import binding as B
+    out, s["ws"] = B.grouped_gemm_int8(s["offsets"], s["a"], s["w"], s["w_scales"],
+                                       a_scales=s["a_scales"], bias=s["bias"], ws=s.get("ws"),
+                                       out=s["out"])
+    return out
+
+
+def _own_norm(s):
+    from combine_route_count_prefix_gb300 import binding as B
+    return B.block_norm(s["x"], s["residual"], s["weight"], post_weight=s["post_weight"],
+                        gate=s["gate"], gate_act=s["case"]["act"], residual_scale=RESIDUAL_SCALE,
+                        branch_scale=BRANCH_SCALE, eps=EPS, out=s["out"])
+
+
+def run(state):
+    op = state["case"]["op"]
+    if own:
+        return {"layer": _own_layer, "gemm": _own_gemm, "norm": _own_norm}[op](state)
+    return {"layer": _plain_layer, "gemm": _plain_gemm, "norm": _plain_norm}[op](state)
+
+
+# ------------------------------------------------------------------ floors
+
+def work(case):
+    c = case
+    if c["op"] == "layer":
+        T, H, E, K, N = c["T"], c["H"], c["E"], c["K"], c["N"]
+        share = E / (E + c["Z"] + c["C"]) * (0.9 if c["mask"] and T > 1 else 1.0)
+        hit = E * (1 - (1 - K * share / E) ** T)      # experts with rows, on average
+        b = hit * (N * H + H * N // 2 + 4 * (N + H)) + T * H * (6 if c["shared"] else 4) + 8 * T * K
+        return {"bytes": b, "flops": T * K * share * (2 * N * H + N * H)}
+    if c["op"] == "gemm":
+        R, E, N, Kd = c["rows"], c["E"], c["N"], c["Kd"]
+        hit = E * (1 - (1 - 1 / E) ** R)
+        b = R * (2 * Kd if c["a"] == "bf16" else Kd + 4) + hit * N * (Kd + (8 if c["bias"] else 4))
+        return {"bytes": b + R * N * (2 if c["out"] == "bf16" else 4), "flops": 2 * R * N * Kd}
+    n = c["T"] * c["H"]
+    b = n * (6 + (2 if c["y"] else 0) + (1 if c["q"] else 0)) + 2 * c["gates"] * c["H"]
+    b += c["H"] * (4 if c["post"] else 2) + (4 * c["T"] * _blocks(c["H"]) if c["q"] else 0)
+    return {"bytes": b, "flops": 12 * n}
+
+
+# ------------------------------------------------------------------ 64 bits
+
+def _codes64(v):
+    """64-bit rows -> whole-number codes and scales, one scale per row."""
+    s = v.abs().amax(-1, keepdim=True) / 127.0
+    return torch.where(s > 0, torch.round(v / s.clamp(min=1e-300)), 0.0), s
+
+
+def _exact_layer(c, s):
+    T, K, E, Nh = c["T"], c["K"], c["E"], c["N"] // 2
+    x = s["x"].double()
+    q1, s1 = _codes64(x)
+    out = torch.zeros_like(x)
+    ids = s["ids"].tolist()
+    on = [[1] * K] * T if s["mask"] is None else s["mask"].view(T, -1).expand(T, K).tolist()
+    for t in range(T):
+        for k in range(K):
+            e = ids[t][k]
+            if not on[t][k] or E <= e < E + c["Z"]:
+                continue
+            if e >= E:
+                y = x[t]
+            else:
+                h = (s["w1"][e].double() @ q1[t]) * s["scale1"][e].double() * s1[t]
+                q2, s2 = _codes64(h[:Nh] * torch.special.expit(h[:Nh]) * h[Nh:])
+                y = (s["w2"][e].double() @ q2) * s["scale2"][e].double() * s2
+            out[t] += s["probs"][t, k].double() * y
+    return out if s["shared"] is None else out + s["shared"].double()
+
+
+def _exact_gemm(c, s):
+    if s["a_scales"] is None:
+        q, qs = _codes64(s["a"].double())
+    else:
+        q, qs = s["a"].double(), s["a_scales"].double()[:, None]
+    off, parts = s["offsets"].tolist(), []
+    for e, (lo, hi) in enumerate(zip(off, off[1:])):
+        y = (q[lo:hi] @ s["w"][e].double().T) * s["w_scales"][e].double() * qs[lo:hi]
+        parts.append(y if s["bias"] is None else y + s["bias"][e].double())
+    return torch.cat(parts)
+
+
+def _exact_norm(c, s):
+    T = c["T"]
+    a = s["x"].double()
+    if c["post"]:
+        a = a / (a.square().sum(1, keepdim=True) / c["H"] + EPS).sqrt() * s["post_weight"].double()
+    if c["gates"]:
+        gate = s["gate"].double()
+        gate = torch.special.expit(gate) if c["act"] == "sigmoid" else gate
+        a = a * gate.repeat_interleave(T // c["gates"], 0)
+    h = RESIDUAL_SCALE * s["residual"].double() + BRANCH_SCALE * a
+    v = h / (h.square().sum(1, keepdim=True) / c["H"] + EPS).sqrt() * s["weight"].double()
+    out = dict(residual_out=h)
+    if c["y"]:
+        out["y"] = v
+    if c["q"]:
+        q, scales = torch.empty_like(v), v.new_empty(T, _blocks(c["H"]))
+        for b in range(scales.shape[1]):
+            part = v[:, b * BLOCK:(b + 1) * BLOCK]
+            scales[:, b] = part.abs().amax(1).clamp(min=AMAX_FLOOR) / E4M3_MAX
+            u = part / scales[:, b:b + 1]
+            step = torch.exp2(torch.floor(torch.log2(u.abs().clamp(min=2.0 ** -6))) - 3)
+            q[:, b * BLOCK:(b + 1) * BLOCK] = torch.round(u / step) * step
+        out["q"], out["scales"] = q, scales
+    return out
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"layer": _exact_layer, "gemm": _exact_gemm, "norm": _exact_norm}[case["op"]](case, s)
