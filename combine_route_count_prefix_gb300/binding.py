@@ -40,6 +40,7 @@ EXPORTED = [
     "moe_add_rms_norm", "moe_gate",
     "moe_grouped_gemm_fp8_workspace_size", "moe_grouped_gemm_fp8",
     "moe_grouped_ffn_fp8_workspace_size", "moe_grouped_ffn_fp8",
+    "moe_layer_few_tokens_workspace_size", "moe_layer_few_tokens",
 ]
 
 
@@ -126,6 +127,8 @@ def lib():
                                  P, SZ, P],
         "moe_grouped_ffn_fp8_workspace_size": [SP, ctypes.POINTER(SZ)],
         "moe_grouped_ffn_fp8": [SP, P, P, P, P, P, P, P, P, P, P, SZ, P],
+        "moe_layer_few_tokens_workspace_size": [SP, ctypes.POINTER(SZ)],
+        "moe_layer_few_tokens": [SP, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -437,6 +440,47 @@ def layer(shape: MoeShape, x, expert_ids, expert_scales, w1p, scale1, w2p, scale
     _call("moe_layer", ctypes.byref(shape), _ptr(x), _ptr(expert_ids), _ptr(expert_scales),
           _ptr(mask), _ptr(shared), _ptr(w1p), _ptr(scale1), _ptr(w2p), _ptr(scale2), _ptr(out),
           _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream))
+    return out, ws
+
+
+def layer_few_tokens_workspace_size(shape: MoeShape) -> int:
+    n = ctypes.c_size_t()
+    _call("moe_layer_few_tokens_workspace_size", ctypes.byref(shape), ctypes.byref(n))
+    return n.value
+
+
+def layer_few_tokens(shape: MoeShape, x, expert_ids, expert_scales, w1p, scale1, w2p, scale2,
+                     mask=None, shared=None, ws=None, out=None, stream=None):
+    """moe_layer_few_tokens: :func:`layer` for at most 512 routes (T * K), the
+    same results in two to four kernels.  The shape's ffn_path is "small" or
+    "auto", and the weights are packed with it.  Returns (out, workspace)."""
+    T, K, H, E, N = shape.num_tokens, shape.topk, shape.hidden, shape.num_experts, shape.ffn
+    dev = x.get_device()
+    _check(x, torch.bfloat16, (T, H), "x", dev)
+    _check(expert_ids, torch.int32, (T, K), "expert_ids", dev)
+    _check(expert_scales, torch.float32, (T, K), "expert_scales", dev)
+    _check(scale1, torch.float32, (E, N), "scale1", dev)
+    _check(scale2, torch.float32, (E, H), "scale2", dev)
+    _check(shared, torch.bfloat16, (T, H), "shared", dev)
+    if mask is not None:
+        if mask_kind_of(mask, T, K) != shape.mask_kind:
+            raise ValueError(f"mask: shape {tuple(mask.shape)} is not that of mask_kind {shape.mask_kind}")
+        _check(mask, torch.uint8, mask.shape, "mask", dev)
+    per = 3 if shape.ffn_path == FFN_PATH_AUTO else 1
+    for name, t, n in (("w1p", w1p, E * N * H), ("w2p", w2p, E * H * N // 2)):
+        _check(t, torch.uint8, (per * n,), name, dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    else:
+        _check(out, torch.bfloat16, (T, H), "out", dev)
+    if ws is None:
+        _, ws = _alloc_ws(layer_few_tokens_workspace_size(shape), x.device)
+    if ws.get_device() != dev:
+        _check_device(ws, "ws", dev)
+    _call("moe_layer_few_tokens", shape, x.data_ptr(), expert_ids.data_ptr(),
+          expert_scales.data_ptr(), _addr(mask), _addr(shared), w1p.data_ptr(), scale1.data_ptr(),
+          w2p.data_ptr(), scale2.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(),
+          _raw_stream(stream, dev))
     return out, ws
 
 

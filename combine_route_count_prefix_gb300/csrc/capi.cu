@@ -198,6 +198,22 @@ static RouteDev route_dev(const moe_shape &s, const int32_t *ids, const uint8_t 
     return r;
 }
 
+// Formats a packed buffer holds, by the shape's ffn_path: fp16 images for the
+// large-tile kernels, biased bytes for the small-batch kernel, both for AUTO
+// (which picks by the row count of each call).  In a buffer holding both, the
+// bytes follow the images.
+static bool packs_f16(int32_t path) { return path != MOE_FFN_PATH_SMALL; }
+static bool packs_i8(int32_t path) {
+    return path == MOE_FFN_PATH_SMALL || path == MOE_FFN_PATH_AUTO;
+}
+
+// The biased-byte part of a packed buffer: after the fp16 images (E*rows*cols*2
+// bytes, a multiple of 1024 because N % 256 == 0 and H % 16 == 0) when the
+// buffer holds both formats, else at its start.
+const void *packed_i8(const void *packed, int32_t path, int64_t E, int64_t rows, int64_t cols) {
+    return static_cast<const uint8_t *>(packed) + (packs_f16(path) ? (size_t)E * rows * cols * 2 : 0);
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -364,15 +380,6 @@ moe_status moe_combine(const moe_shape *shape, const void *expand_x, const int32
 }
 
 // ---------------------------------------------------------------- weights
-// Formats a packed buffer holds, by the shape's ffn_path: fp16 images for the
-// large-tile kernels, biased bytes for the small-batch kernel, both for AUTO
-// (which picks by the row count of each call).  In a buffer holding both, the
-// bytes follow the images.
-static bool packs_f16(int32_t path) { return path != MOE_FFN_PATH_SMALL; }
-static bool packs_i8(int32_t path) {
-    return path == MOE_FFN_PATH_SMALL || path == MOE_FFN_PATH_AUTO;
-}
-
 moe_status moe_packed_weight_bytes(const moe_shape *shape, size_t *w1_bytes, size_t *w2_bytes) {
     MOE_TRY(check_shape(shape, true));
     if (!w1_bytes || !w2_bytes) return MOE_FAIL(MOE_ERR_NULLPTR);
@@ -381,14 +388,6 @@ moe_status moe_packed_weight_bytes(const moe_shape *shape, size_t *w1_bytes, siz
     *w1_bytes = (size_t)s.num_experts * s.ffn * s.hidden * per;
     *w2_bytes = (size_t)s.num_experts * s.hidden * (s.ffn / 2) * per;
     return MOE_OK;
-}
-
-// The biased-byte part of a packed buffer: after the fp16 images (E*rows*cols*2
-// bytes, a multiple of 1024 because N % 256 == 0 and H % 16 == 0) when the
-// buffer holds both formats, else at its start.
-static const void *packed_i8(const void *packed, int32_t path, int64_t E, int64_t rows,
-                             int64_t cols) {
-    return static_cast<const uint8_t *>(packed) + (packs_f16(path) ? (size_t)E * rows * cols * 2 : 0);
 }
 
 static bool use_small_path(int32_t path, int64_t rows, int64_t E) {

@@ -150,6 +150,8 @@ struct Layout {
 
 enum class Op { Dispatch, Combine, Ffn, Layer };
 
+// The biased-byte part of a buffer of packed weights ([E, rows, cols]) of an ffn_path that has one.
+const void *packed_i8(const void *packed, int32_t path, int64_t E, int64_t rows, int64_t cols);
 int64_t route_chunks(const moe_shape &s);
 moe_status check_shape(const moe_shape *s, bool need_ffn);
 Layout layout_for(const moe_shape &s, Op op);
@@ -321,6 +323,28 @@ moe_status launch_grouped_gemm(Epi epi, const GemmArgs &a, cudaStream_t stream,
 // side, only as many as present.  Kd % 16 == 0 (and Nout % 128 == 0 for the
 // SwiGLU epilogue).
 moe_status launch_grouped_gemm_small(Epi epi, const GemmArgs &a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- a few tokens
+// Rows [rows, n] in bf16 or fp32 -> int8 codes and one scale a row.
+moe_status launch_quant_rows_i8(const void *src, bool bf16, int64_t rows, int64_t n, int8_t *q,
+                                float *scales, cudaStream_t stream);
+// The whole layer for at most MOE_FEW_TOKENS_MAX_ROUTES routes.
+struct FewTokensArgs {
+    const void *x;             // bf16 [T, H]
+    const int32_t *ids;        // [T, K]
+    const float *probs;        // [T, K]
+    const uint8_t *mask;
+    const void *shared;        // bf16 [T, H] or NULL
+    const void *w1, *w2;       // biased bytes, as launch_pack_w1_i8 and launch_bias_i8 write them
+    const float *scale1, *scale2;
+    void *out;                 // bf16 [T, H]
+    float *g;                  // [T*K, N/2]
+    float *gmax;               // [T*K, N/16]
+    int8_t *q;                 // T * H (rounded up to kAlign) + T * K * N/2 bytes
+    float *qs;                 // [T + T*K]
+    int32_t *status;
+};
+moe_status launch_layer_few_tokens(const moe_shape &s, const FewTokensArgs &a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- fp8 expert path
 moe_status launch_gate(const moe_gate_desc &d, const void *logits, const float *bias,

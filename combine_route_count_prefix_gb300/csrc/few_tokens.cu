@@ -1,0 +1,713 @@
+// few_tokens.cu -- the whole int8 MoE layer for a few tokens.
+//
+// out[t] = bf16(sum_k p[t,k] * y(t,k) + shared[t]) with the stages of the
+// layer's other kernels, in the same arithmetic, so that the outputs are the
+// same bit for bit:
+//   q1, s1 = quantised x[t];  h = (float(q1 . W1[e]) * scale1) * s1
+//   g = silu(h_a) * h_b;      q2, s2 = quantised g
+//   y = bf16((float(q2 . W2[e]) * scale2) * s2)
+// ("PTO MegaMoE Dispatch + Combine Fusion Example": GMM1, SwiGLU, GMM2, Unpermute;
+// "aclnnMoeDistributeCombineV4": masks, shared, zero and copy experts.)
+//
+// Reading the chosen experts' weights bounds it (stream_i8.cuh), and for one
+// token of small experts the steps between the reads.  So there are two
+// kernels, and neither an expert-major copy of the rows nor a routing kernel:
+//   k_few_gate_up  quantises the tokens in every CTA (a few KB from L2) and
+//                  multiplies; its CTAs share out the (expert, 8 rows, 8 + 8
+//                  channels) units evenly, in the weights' order.  The integer sums are exact,
+//                  so warps and stages may be added in any order.
+//   k_few_down     is launched while the first runs and fetches its first
+//                  weights meanwhile; a CTA owns 16 output channels for every
+//                  expert and route, so the weighted sum needs no other CTA.
+//                  It quantises g itself, from row maxima that the first kernel left.
+// Every CTA finds the experts' rows from expert_ids by itself (at most 512
+// routes: five block barriers).
+// Where the quantised rows do not fit shared memory beside the rings (kLocalBytes), a small
+// kernel before each product quantises them once, and the codes travel through the rings
+// with the weights.
+#include "common.cuh"
+#include "quant.cuh"
+#include "stream_i8.cuh"
+#include "tcgen05.cuh"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+using namespace si8;
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kMaxRoutes = MOE_FEW_TOKENS_MAX_ROUTES;
+constexpr int kBatchUnits = 16;                 // units between two block barriers of the first kernel
+constexpr size_t kLocalBytes = 64 * 1024;       // codes that a CTA holds itself
+constexpr int kDepthLocal = 5, kDepthRing = 4;  // stages of a warp's ring
+
+struct FewDev {
+    const uint4 *x;            // bf16 [T, H]
+    const int32_t *ids;
+    const float *probs;
+    const uint8_t *mask;
+    const __nv_bfloat16 *shared;
+    const uint8_t *w1, *w2;    // biased bytes
+    const float *scale1, *scale2;
+    __nv_bfloat16 *out;
+    float *g;                  // [T*K, Nh]
+    float *gmax;               // [T*K, Nh / 8] largest |g| of 8 channels
+    const int8_t *q;           // codes of the rows (not LOCAL): [T, H] or [T*K, Nh]
+    const float *qs;           // and their scales
+    int32_t *status;
+    int T, K, R, E, Z, C, H, Nh, mask_kind;
+};
+
+// What a CTA knows of the routes, in shared memory.
+struct Routes {
+    int32_t code[kMaxRoutes];      // expert, -1 none, -2 zero expert, -3 copy expert
+    uint16_t list[kMaxRoutes];     // the routes of each expert, expert after expert
+    uint16_t place[kMaxRoutes];    // a route's place in that list
+    uint16_t blk_e[kMaxRoutes];    // blocks of up to 8 routes of one expert
+    uint16_t blk_first[kMaxRoutes];
+    uint8_t blk_n[kMaxRoutes];
+    uint32_t count[kMaxExperts];
+    uint32_t part[kWarps];
+    int32_t blocks, rows, bad;
+};
+
+__device__ void find_routes(const FewDev &p, Routes &r) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e < p.E; e += kThreads) r.count[e] = 0;
+    if (tid == 0) r.bad = 0;
+    __syncthreads();
+    constexpr int kOwn = (kMaxRoutes + kThreads - 1) / kThreads;
+    uint32_t pos[kOwn];
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+        const int i = o * kThreads + tid;
+        if (i >= p.R) break;
+        bool on = true;
+        if (p.mask_kind == 1) on = p.mask[i / p.K] != 0;
+        if (p.mask_kind == 2) on = p.mask[i] != 0;
+        const int e = p.ids[i];
+        int code = -1;
+        if (on) {
+            if (e >= 0 && e < p.E) code = e;
+            else if (e >= p.E && e < p.E + p.Z) code = -2;
+            else if (e >= p.E + p.Z && e < p.E + p.Z + p.C) code = -3;
+            else r.bad = 1;
+        }
+        r.code[i] = code;
+        if (code >= 0) pos[o] = atomicAdd(&r.count[code], 1u);
+    }
+    __syncthreads();
+    // exclusive sums over the experts of routes (upper half) and blocks (lower half)
+    const int per = (p.E + kThreads - 1) / kThreads;
+    const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
+    uint32_t own = 0;
+    for (int e = e0; e < e1; ++e) own += (r.count[e] << 16) | ((r.count[e] + kRows - 1) / kRows);
+    uint32_t sum = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(kFull, sum, d);
+        if (lane >= d) sum += v;
+    }
+    if (lane == 31) r.part[warp] = sum;
+    __syncthreads();
+    uint32_t at = sum - own;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        if (w < warp) at += r.part[w];
+    for (int e = e0; e < e1; ++e) {
+        const int n = (int)r.count[e], first = (int)(at >> 16), b0 = (int)(at & 0xffffu);
+        const int nb = (n + kRows - 1) / kRows;
+        for (int b = 0; b < nb; ++b) {
+            r.blk_e[b0 + b] = (uint16_t)e;
+            r.blk_first[b0 + b] = (uint16_t)(first + b * kRows);
+            r.blk_n[b0 + b] = (uint8_t)min(kRows, n - b * kRows);
+        }
+        r.count[e] = (uint32_t)(first | n << 16);
+        at += ((uint32_t)n << 16) | (uint32_t)nb;
+    }
+    if (tid == kThreads - 1) {
+        r.rows = (int)(at >> 16);
+        r.blocks = (int)(at & 0xffffu);
+    }
+    __syncthreads();
+    int several = 0;
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+        const int i = o * kThreads + tid;
+        if (i >= p.R) break;
+        const int code = r.code[i];
+        if (code >= 0) {
+            pos[o] += r.count[code] & 0xffffu;
+            several |= (r.count[code] >> 16) > kRows;
+            r.list[pos[o]] = (uint16_t)i;
+            r.place[i] = (uint16_t)pos[o];
+        }
+    }
+    // The order within an expert is that of the atomics, each CTA's own.  Where
+    // an expert has several blocks the CTAs have to agree on who is in which:
+    // ascending routes.
+    if (__syncthreads_or(several)) {
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            const int i = o * kThreads + tid;
+            if (i >= p.R) break;
+            const int code = r.code[i];
+            if (code < 0) continue;
+            const int first = (int)(r.count[code] & 0xffffu), n = (int)(r.count[code] >> 16);
+            pos[o] = first;
+            for (int j = 0; j < n; ++j) pos[o] += r.list[first + j] < i;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            const int i = o * kThreads + tid;
+            if (i >= p.R || r.code[i] < 0) continue;
+            r.list[pos[o]] = (uint16_t)i;
+            r.place[i] = (uint16_t)pos[o];
+        }
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ float max8(const float (&f)[8], float m) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+    return m;
+}
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s, float rs) {
+    float c[8];
+    quant_codes<8>(v, s, rs, c);
+    return make_uint2(pack_i8x4(c[0], c[1], c[2], c[3]), pack_i8x4(c[4], c[5], c[6], c[7]));
+}
+// Eight codes at column 8 i of row r of a CTA's own codes (rows of `pitch`
+// bytes, in 128-byte pieces swizzled as a stage's rows are).
+__device__ __forceinline__ void put_codes(uint8_t *codes, int r, int pitch, int i, uint2 v) {
+    uint8_t *at = codes + (size_t)r * pitch + (i >> 4) * kDepth + unit_at(r, (i >> 1) & 7) + (i & 1) * 8;
+    *reinterpret_cast<uint2 *>(at) = v;
+}
+
+__host__ __device__ inline int padded(int k) { return (k + kDepth - 1) / kDepth * kDepth; }
+
+// One warp's way through its stages: `kBytes` a stage, kD stages in the ring.
+template <int kD, int kBytes>
+struct Ring {
+    uint32_t base;
+    int put = 0, get = 0;
+    __device__ __forceinline__ uint32_t next_put() {
+        const uint32_t a = base + (uint32_t)put * kBytes;
+        put = put + 1 == kD ? 0 : put + 1;
+        return a;
+    }
+    __device__ __forceinline__ uint32_t next_get() {
+        const uint32_t a = base + (uint32_t)get * kBytes;
+        get = get + 1 == kD ? 0 : get + 1;
+        return a;
+    }
+};
+
+// ---------------------------------------------------------------- h = q1 . W1, g = silu(h_a) h_b
+// Unit u of block u / (Nh / 8): SiLU channels 8 j .. 8 j + 7 and their
+// multipliers (16 rows of the packed W1, two runs of eight).
+template <bool LOCAL>
+__global__ void __launch_bounds__(kThreads, 2)
+k_few_gate_up(FewDev p) {
+    constexpr int kD = LOCAL ? kDepthLocal : kDepthRing;
+    constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : kRowBytes);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ Routes r;
+    __shared__ int32_t acc[2][kBatchUnits][kRows][kChannels];
+    __shared__ uint32_t amax[kMaxRoutes];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t *codes = smem + (size_t)kWarps * kD * kBytes;
+    const int H = p.H, KS = (H + kDepth - 1) / kDepth, pitch = KS * kDepth, NU = p.Nh / 8;
+
+    for (int i = tid; i < 2 * kBatchUnits * kRows * kChannels; i += kThreads) (&acc[0][0][0][0])[i] = 0;
+    if (LOCAL) {
+        for (int i = tid; i < p.T; i += kThreads) amax[i] = 0;
+        pdl_wait();
+    }
+    // with LOCAL unset, the kernel before this one has waited for the inputs
+    find_routes(p, r);
+    const int64_t units = (int64_t)r.blocks * NU;
+    const int u_begin = (int)(units * blockIdx.x / gridDim.x), u_end = (int)(units * (blockIdx.x + 1) / gridDim.x);
+
+    // the stages to fetch: batch by batch, this warp's share of each
+    struct {
+        int batch, unit, ks, left;
+        const uint8_t *src;
+        const int8_t *row;
+        bool row_on[2];
+    } f;
+    auto share = [&](int first, int &unit, int &ks, int &n) {
+        const int total = min(kBatchUnits, u_end - first) * KS;
+        const int a = total * warp / kWarps, b = total * (warp + 1) / kWarps;
+        unit = first + a / KS;
+        ks = a % KS;
+        n = b - a;
+    };
+    const int cu = lane & 7, cr = lane >> 3;   // copies: 16-byte unit, row of a group of four
+    auto weights_of = [&](int unit) {
+        const int blk = unit / NU, j = (unit - blk * NU) * 8;
+        const int64_t prow = (int64_t)r.blk_e[blk] * (2 * p.Nh) + (j >> 6) * 128 + ((j >> 4) & 3) * 32 + (j & 15);
+        return p.w1 + (prow + cr) * H + cu * 16;
+    };
+    auto enter = [&]() {
+        f.src = weights_of(f.unit);
+    };
+    f.batch = u_begin;
+    f.left = 0;
+    if (u_begin < u_end) share(u_begin, f.unit, f.ks, f.left);
+    Ring<kD, kBytes> ring;
+    ring.base = smem_u32(smem) + (uint32_t)(warp * kD * kBytes);
+    if (f.left > 0) enter();
+    auto fetch_rows = [&](uint32_t dst, int unit, int ks) {
+        const int blk = unit / NU;
+        const bool in = ks * kDepth + cu * 16 < H;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = 4 * i + cr;
+            if (row < r.blk_n[blk]) {
+                const int t = r.list[r.blk_first[blk] + row] / p.K;
+                copy16(dst + kWeightBytes + row * kDepth + unit_at(row, cu),
+                       p.q + (int64_t)t * H + ks * kDepth + cu * 16, in);
+            }
+        }
+    };
+    auto fetch = [&](bool rows) {
+        while (f.left == 0 && f.batch + kBatchUnits < u_end) {
+            f.batch += kBatchUnits;
+            share(f.batch, f.unit, f.ks, f.left);
+            if (f.left > 0) enter();
+        }
+        if (f.left > 0) {
+            const uint32_t dst = ring.next_put();
+            const bool in = f.ks * kDepth + cu * 16 < H;
+            const uint8_t *src = f.src + f.ks * kDepth;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                copy16(dst + (4 * i + cr) * kDepth + unit_at(4 * i + cr, cu),
+                       src + (int64_t)(i < 2 ? 4 * i : 4 * i + 8) * H, in);
+            if (!LOCAL && rows) fetch_rows(dst, f.unit, f.ks);
+            --f.left;
+            if (++f.ks == KS) {
+                f.ks = 0;
+                ++f.unit;
+                if (f.left > 0) enter();
+            }
+        }
+    };
+    if (LOCAL) {
+        for (int i = 0; i < kD - 1; ++i) {
+            fetch(false);
+            copy_commit();
+        }
+        // the tokens' codes, in every CTA
+        const int H8 = H / 8;
+        for (int i = tid; i < p.T * H8; i += kThreads) {
+            const int t = i / H8;
+            float v[8];
+            unpack8(p.x[i], v);
+            const uint32_t m = __float_as_uint(max8(v, 0.0f));
+            const uint32_t act = __activemask();
+            if (__match_any_sync(act, t) == act) {
+                const uint32_t w = __reduce_max_sync(act, m);
+                if (lane == __ffs(act) - 1) atomicMax(&amax[t], w);
+            } else {
+                atomicMax(&amax[t], m);
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < p.T * (pitch / 8); i += kThreads) {
+            const int t = i / (pitch / 8), c = i % (pitch / 8);
+            uint2 q = make_uint2(0, 0);
+            if (c < H8) {
+                float v[8];
+                unpack8(p.x[(int64_t)t * H8 + c], v);
+                const float s = __fdiv_rn(__uint_as_float(amax[t]), 127.0f);
+                q = codes8(v, s, __frcp_rn(s));
+            }
+            put_codes(codes, t, pitch, c, q);
+        }
+        __syncthreads();
+    } else {
+        pdl_wait();
+        for (int i = 0; i < kD - 1; ++i) {
+            fetch(true);
+            copy_commit();
+        }
+    }
+
+    const int g = lane >> 2, tq = lane & 3;
+    int buf = 0;
+    for (int first = u_begin; first < u_end; first += kBatchUnits, buf ^= 1) {
+        const int nu = min(kBatchUnits, u_end - first);
+        // this thread's unit of the batch, for the epilogue: its scales come meanwhile
+        const int eu = tid >> 4, ej = tid & 7, eh = (tid >> 3) & 1;
+        int eblk = 0, ech = 0;
+        float sa = 0.0f, sb = 0.0f;
+        if (eu < nu) {
+            eblk = (first + eu) / NU;
+            ech = ((first + eu) - eblk * NU) * 8 + ej;
+            const float *sc = p.scale1 + (int64_t)r.blk_e[eblk] * (2 * p.Nh) + ech;
+            sa = __ldg(sc);
+            sb = __ldg(sc + p.Nh);
+        }
+        int unit, ks, n;
+        share(first, unit, ks, n);
+        while (n > 0) {
+            const int blk = unit / NU, nr = r.blk_n[blk];
+            // lanes of rows that are not there read the first row's codes
+            const int row = g < nr ? g : 0;
+            const int t = r.list[r.blk_first[blk] + row] / p.K;
+            int m = min(n, KS - ks);
+            n -= m;
+            Sums<1> sums;
+            sums.clear();
+            uint32_t crow[1] = {smem_u32(codes) + (uint32_t)(t * pitch + ks * kDepth)};
+            int swz[1] = {LOCAL ? t : row};
+            for (int i = 0; i < m; ++i) {
+                copy_wait<kD - 2>();
+                __syncwarp();
+                fetch(true);
+                copy_commit();
+                const uint32_t st = ring.next_get();
+                if (!LOCAL) crow[0] = st + kWeightBytes + row * kDepth;
+                sums.add_stage(st, crow, swz);
+                if (LOCAL) crow[0] += kDepth;
+                if (i % kExactStages == kExactStages - 1) sums.flush();
+            }
+            sums.flush();
+            int32_t (*a)[kChannels] = acc[buf][unit - first];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (2 * tq + (i & 1) < nr)
+                    atomicAdd(&a[2 * tq + (i & 1)][g + (i >> 1) * 8], sums.total[0][i]);
+            ks = 0;
+            ++unit;
+        }
+        __syncthreads();
+        if (eu < nu) {
+            const int nr = r.blk_n[eblk];
+            for (int row = eh; row < kRows; row += 2) {
+                float v = 0.0f;
+                const int route = row < nr ? r.list[r.blk_first[eblk] + row] : 0;
+                if (row < nr) {
+                    int32_t *a = acc[buf][eu][row];
+                    const int t = route / p.K;
+                    const float s1 = LOCAL ? __fdiv_rn(__uint_as_float(amax[t]), 127.0f) : p.qs[t];
+                    const float ha = __fmul_rn(__fmul_rn(__int2float_rn(a[ej]), sa), s1);
+                    const float hb = __fmul_rn(__fmul_rn(__int2float_rn(a[ej + 8]), sb), s1);
+                    a[ej] = 0;
+                    a[ej + 8] = 0;
+                    v = __fmul_rn(tc::silu_f32(ha), hb);
+                    p.g[(int64_t)route * p.Nh + ech] = v;
+                }
+                if (LOCAL) {
+                    float mx = fmaxf(0.0f, fabsf(v));
+                    const uint32_t eight = 0xffu << (lane & 24);   // the lanes of this unit and row
+#pragma unroll
+                    for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(eight, mx, o));
+                    if (ej == 0 && row < nr) p.gmax[(int64_t)route * NU + (ech >> 3)] = mx;
+                }
+            }
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0) *p.status = r.bad ? MOE_DEV_BAD_EXPERT_ID : 0;
+}
+
+// ---------------------------------------------------------------- y = q2 . W2, out
+template <bool LOCAL>
+__global__ void __launch_bounds__(kThreads, 2)
+k_few_down(FewDev p) {
+    constexpr int kD = LOCAL ? kDepthLocal : kDepthRing;
+    constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : kRowBytes);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ Routes r;
+    __shared__ float s2[kMaxRoutes];      // by place in the list
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int Nh = p.Nh, KS = (Nh + kDepth - 1) / kDepth, pitch = KS * kDepth;
+    uint8_t *codes = smem + (size_t)kWarps * kD * kBytes;
+    int32_t *acc = reinterpret_cast<int32_t *>(codes + (LOCAL ? (size_t)p.R * pitch : 0));   // [2][R][16]
+
+    for (int i = tid; i < 2 * p.R * kChannels; i += kThreads) acc[i] = 0;
+    // ids, mask and weights were there before the kernel before this one began
+    find_routes(p, r);
+    const int per_batch = r.blocks * KS;      // stages of 16 channels
+    const int mine_a = per_batch * warp / kWarps, mine_n = per_batch * (warp + 1) / kWarps - mine_a;
+    const int batches = p.H / kChannels;
+
+    const int cu = lane & 7, cr = lane >> 3;
+    struct {
+        int batch, blk, ks, left;
+        const uint8_t *src;
+    } f;
+    auto begin = [&]() {
+        f.left = mine_n;
+        f.blk = mine_a / KS;
+        f.ks = mine_a % KS;
+    };
+    auto enter = [&]() {
+        f.src = p.w2 + ((int64_t)r.blk_e[f.blk] * p.H + f.batch * kChannels + cr) * Nh + cu * 16;
+    };
+    f.batch = blockIdx.x;
+    begin();
+    if (f.left > 0 && f.batch < batches) enter();
+    Ring<kD, kBytes> ring;
+    ring.base = smem_u32(smem) + (uint32_t)(warp * kD * kBytes);
+    auto fetch = [&]() {
+        if (mine_n == 0) return;
+        if (f.left == 0) {
+            f.batch += gridDim.x;
+            begin();
+            if (f.batch < batches) enter();
+        }
+        if (f.batch >= batches) return;
+        const uint32_t dst = ring.next_put();
+        const bool in = f.ks * kDepth + cu * 16 < Nh;
+        const uint8_t *src = f.src + f.ks * kDepth;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            copy16(dst + (4 * i + cr) * kDepth + unit_at(4 * i + cr, cu), src + (int64_t)4 * i * Nh, in);
+        if (!LOCAL) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = 4 * i + cr;
+                if (row < r.blk_n[f.blk])
+                    copy16(dst + kWeightBytes + row * kDepth + unit_at(row, cu),
+                           p.q + (int64_t)r.list[r.blk_first[f.blk] + row] * Nh + f.ks * kDepth + cu * 16, in);
+            }
+        }
+        --f.left;
+        if (++f.ks == KS) {
+            f.ks = 0;
+            ++f.blk;
+            if (f.left > 0) enter();
+        }
+    };
+    if (LOCAL) {
+        for (int i = 0; i < kD - 1; ++i) {
+            fetch();
+            copy_commit();
+        }
+        pdl_wait();
+        // the routes' codes: a row to a warp, or part of one where there are fewer
+        const int parts = r.rows > 0 ? max(1, kWarps / r.rows) : 1, n8 = Nh / 8;
+        for (int it = warp; it < r.rows * parts; it += kWarps) {
+            const int at = it / parts, part = it - at * parts;
+            const int route = r.list[at];
+            const float *gm = p.gmax + (int64_t)route * n8;
+            float m = 0.0f;
+            for (int i = lane; i < n8; i += 32) m = fmaxf(m, __ldcg(gm + i));
+            m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
+            const float s = __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
+            if (lane == 0 && part == 0) s2[at] = s;
+            const float4 *src = reinterpret_cast<const float4 *>(p.g + (int64_t)route * Nh);
+            for (int i = part * 32 + lane; i < pitch / 8; i += 32 * parts) {
+                uint2 q = make_uint2(0, 0);
+                if (i < n8) {
+                    const float4 a = __ldcg(src + 2 * i), b = __ldcg(src + 2 * i + 1);
+                    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                    q = codes8(v, s, rs);
+                }
+                put_codes(codes, at, pitch, i, q);
+            }
+        }
+    } else {
+        pdl_wait();
+        for (int i = 0; i < kD - 1; ++i) {
+            fetch();
+            copy_commit();
+        }
+        for (int i = tid; i < r.rows; i += kThreads) s2[i] = __ldcg(p.qs + r.list[i]);
+    }
+    __syncthreads();
+
+    const int g = lane >> 2, tq = lane & 3;
+    int buf = 0;
+    for (int batch = blockIdx.x; batch < batches; batch += gridDim.x, buf ^= 1) {
+        int32_t *a = acc + (size_t)buf * p.R * kChannels;
+        int blk = mine_a / KS, ks = mine_a % KS, n = mine_n;
+        while (n > 0) {
+            const int nr = r.blk_n[blk], base = r.blk_first[blk];
+            const int row = g < nr ? g : 0;
+            const int m = min(n, KS - ks);
+            n -= m;
+            Sums<1> sums;
+            sums.clear();
+            uint32_t crow[1] = {smem_u32(codes) + (uint32_t)((base + row) * pitch + ks * kDepth)};
+            int swz[1] = {LOCAL ? base + row : row};
+            for (int i = 0; i < m; ++i) {
+                copy_wait<kD - 2>();
+                __syncwarp();
+                fetch();
+                copy_commit();
+                const uint32_t st = ring.next_get();
+                if (!LOCAL) crow[0] = st + kWeightBytes + row * kDepth;
+                sums.add_stage(st, crow, swz);
+                if (LOCAL) crow[0] += kDepth;
+                if (i % kExactStages == kExactStages - 1) sums.flush();
+            }
+            sums.flush();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rr = 2 * tq + (i & 1);
+                if (rr < nr) atomicAdd(&a[(base + rr) * kChannels + g + (i >> 1) * 8], sums.total[0][i]);
+            }
+            ks = 0;
+            ++blk;
+        }
+        __syncthreads();
+        for (int i = tid; i < p.T * kChannels; i += kThreads) {
+            const int t = i / kChannels, c = i % kChannels, col = batch * kChannels + c;
+            const int64_t o = (int64_t)t * p.H + col;
+            float v = 0.0f;
+            for (int k = 0; k < p.K; ++k) {
+                const int route = t * p.K + k, code = r.code[route];
+                if (code == -1) continue;
+                float y = 0.0f;
+                if (code >= 0) {
+                    const int at = r.place[route];
+                    int32_t *s = a + at * kChannels + c;
+                    const float sc = __ldg(p.scale2 + (int64_t)code * p.H + col);
+                    y = __bfloat162float(
+                        __float2bfloat16_rn(__fmul_rn(__fmul_rn(__int2float_rn(*s), sc), s2[at])));
+                    *s = 0;
+                } else if (code == -3) {
+                    y = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.x)[o]);
+                }
+                v = __fadd_rn(v, __fmul_rn(__ldg(p.probs + route), y));
+            }
+            if (p.shared) v = __fadd_rn(v, __bfloat162float(p.shared[o]));
+            p.out[o] = __float2bfloat16_rn(v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- codes of rows, once for all CTAs
+// bf16 or fp32 rows -> int8 codes and scales, a CTA a row.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, float *__restrict__ s_out) {
+    __shared__ float part[kWarps];
+    pdl_wait();
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const int n8 = (int)(n / 8);
+    auto load = [&](int i, float (&v)[8]) {
+        if constexpr (sizeof(T) == 2) {
+            unpack8(__ldcg(reinterpret_cast<const uint4 *>(src + row * n) + i), v);
+        } else {
+            const float4 *p = reinterpret_cast<const float4 *>(src + row * n);
+            const float4 a = __ldcg(p + 2 * i), b = __ldcg(p + 2 * i + 1);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        }
+    };
+    float m = 0.0f;
+    for (int i = tid; i < n8; i += kThreads) {
+        float v[8];
+        load(i, v);
+        m = max8(v, m);
+    }
+    m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
+    if ((tid & 31) == 0) part[tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, part[w]);
+    const float s = __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
+    for (int i = tid; i < n8; i += kThreads) {
+        float v[8];
+        load(i, v);
+        reinterpret_cast<uint2 *>(q + row * n)[i] = codes8(v, s, rs);
+    }
+    if (tid == 0) s_out[row] = s;
+}
+
+}  // namespace
+
+moe_status launch_quant_rows_i8(const void *src, bool bf16, int64_t rows, int64_t n, int8_t *q,
+                                float *scales, cudaStream_t stream) {
+    if (bf16) {
+        MOE_LAUNCH("quant_rows_i8", k_quant_rows_i8<__nv_bfloat16>, (unsigned)rows, kThreads, 0, stream,
+                   static_cast<const __nv_bfloat16 *>(src), n, q, scales);
+    } else {
+        MOE_LAUNCH("quant_rows_i8", k_quant_rows_i8<float>, (unsigned)rows, kThreads, 0, stream,
+                   static_cast<const float *>(src), n, q, scales);
+    }
+    return MOE_OK;
+}
+
+// The codes that each kernel's CTAs would hold themselves.
+static bool few_tokens_local(int64_t T, int64_t K, int64_t H, int64_t Nh) {
+    return T * padded((int)H) <= (int64_t)kLocalBytes && T * K * padded((int)Nh) <= (int64_t)kLocalBytes;
+}
+
+moe_status launch_layer_few_tokens(const moe_shape &s, const FewTokensArgs &a, cudaStream_t stream) {
+    const int64_t T = s.num_tokens, K = s.topk, H = s.hidden, Nh = s.ffn / 2, R = T * K;
+    FewDev p;
+    p.x = static_cast<const uint4 *>(a.x);
+    p.ids = a.ids;
+    p.probs = a.probs;
+    p.mask = a.mask;
+    p.shared = static_cast<const __nv_bfloat16 *>(a.shared);
+    p.w1 = static_cast<const uint8_t *>(a.w1);
+    p.w2 = static_cast<const uint8_t *>(a.w2);
+    p.scale1 = a.scale1;
+    p.scale2 = a.scale2;
+    p.out = static_cast<__nv_bfloat16 *>(a.out);
+    p.g = a.g;
+    p.gmax = a.gmax;
+    p.q = nullptr;
+    p.qs = nullptr;
+    p.status = a.status;
+    p.T = (int)T;
+    p.K = (int)K;
+    p.R = (int)R;
+    p.E = (int)s.num_experts;
+    p.Z = (int)s.zero_experts;
+    p.C = (int)s.copy_experts;
+    p.H = (int)H;
+    p.Nh = (int)Nh;
+    p.mask_kind = s.mask_kind;
+    const unsigned sms = (unsigned)num_sms();
+    const unsigned grid1 = (unsigned)std::min<int64_t>(sms, R * (Nh / 8));
+    const unsigned grid2 = (unsigned)std::min<int64_t>(sms, H / kChannels);
+    const size_t acc2 = (size_t)2 * R * kChannels * sizeof(int32_t);
+    if (few_tokens_local(T, K, H, Nh)) {
+        const size_t ring = (size_t)kWarps * kDepthLocal * kWeightBytes;
+        const size_t smem1 = ring + (size_t)T * padded((int)H);
+        const size_t smem2 = ring + (size_t)R * padded((int)Nh) + acc2;
+        if (!set_smem_limit((const void *)k_few_gate_up<true>, smem1) ||
+            !set_smem_limit((const void *)k_few_down<true>, smem2))
+            return MOE_ERR_CUDA;
+        MOE_LAUNCH("few_gate_up", k_few_gate_up<true>, grid1, kThreads, smem1, stream, p);
+        MOE_LAUNCH("few_down", k_few_down<true>, grid2, kThreads, smem2, stream, p);
+        return MOE_OK;
+    }
+    const size_t ring = (size_t)kWarps * kDepthRing * (kWeightBytes + kRowBytes);
+    if (!set_smem_limit((const void *)k_few_gate_up<false>, ring) ||
+        !set_smem_limit((const void *)k_few_down<false>, ring + acc2))
+        return MOE_ERR_CUDA;
+    MOE_TRY(launch_quant_rows_i8(a.x, true, T, H, a.q, a.qs, stream));
+    p.q = a.q;
+    p.qs = a.qs;
+    MOE_LAUNCH("few_gate_up", k_few_gate_up<false>, grid1, kThreads, ring, stream, p);
+    int8_t *q2 = a.q + align_up((size_t)(T * H), kAlign);
+    MOE_TRY(launch_quant_rows_i8(a.g, false, R, Nh, q2, a.qs + T, stream));
+    p.q = q2;
+    p.qs = a.qs + T;
+    MOE_LAUNCH("few_down", k_few_down<false>, grid2, kThreads, ring + acc2, stream, p);
+    return MOE_OK;
+}
+
+}  // namespace moe

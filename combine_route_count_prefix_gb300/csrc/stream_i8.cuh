@@ -1,0 +1,145 @@
+// stream_i8.cuh -- int8 products against a few rows, with the weights streamed
+// through rings of shared memory that belong to one warp each.
+//
+// With a few rows an int8 product is a read of its weights.  A warp takes the
+// weights in stages of 16 output channels x 128 of the inner dimension (2 KB:
+// whole 128-byte lines), which its lanes fetch with 16-byte cp.async copies
+// some stages ahead and read back themselves, so no barrier and no other
+// warp is involved and a wait always ends.  sm_103a has no fast int8 matrix
+// instruction (mma.sync s8: 158 Top/s, 0.08 of the fp16 rate of tcgen05), so
+// the bytes are widened to fp16 in registers, exactly, and multiplied with
+// mma.sync m16n8k16 (601 TFLOP/s measured; 16 channels by 8 rows, no
+// tensor memory to fill and drain), whose fp32 sums are exact below 2^24, that is
+// for 1024 products.
+// 16 channels x 8 rows x 128 take 4 + 2 shared loads, 96 integer and half
+// instructions for the widening and 8 mma per warp: about a third of the issue
+// slots at the rate the stages arrive at from HBM.
+#pragma once
+#include <stdint.h>
+
+#include "ptx.cuh"
+
+namespace moe {
+namespace si8 {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kChannels = 16;                      // output channels of a stage
+constexpr int kDepth = 128;                        // its share of the inner dimension
+constexpr int kWeightBytes = kChannels * kDepth;
+constexpr int kRows = 8;                           // rows of one mma
+constexpr int kRowBytes = kRows * kDepth;
+constexpr int kExactStages = 1024 / kDepth;        // stages that an fp32 sum holds exactly
+
+// 16 bytes global -> shared, zeros where `on` is false (src is not read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 16u : 0u)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Row r of a block of 128-byte rows keeps its 16-byte unit u at u ^ (r % 8):
+// lanes that read the same unit of eight neighbouring rows meet no bank twice.
+__device__ __forceinline__ uint32_t unit_at(int r, int u) { return (uint32_t)((u ^ (r & 7)) << 4); }
+
+// Two biased bytes b + 128 of `word` (bytes 0, 1 or 2, 3) -> the fp16 pair of
+// their b: the byte in the low mantissa bits of the fp16 number 1024 is 1024 +
+// (b + 128) exactly, and 1152 less is b.
+__device__ __forceinline__ uint32_t widen_lo(uint32_t word) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(__byte_perm(word, 0x64646464u, 0x4140)), "r"(0x64806480u));
+    return d;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t word) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(__byte_perm(word, 0x64646464u, 0x4342)), "r"(0x64806480u));
+    return d;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+                 "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Lane (g, t) = (lane / 4, lane % 4) multiplies bytes [32 t, 32 t + 32) of
+// channels g and g + 8 with the same bytes of row g: which of the 128 inner
+// positions an mma calls k does not matter as long as both operands agree.
+// c[n][p]: the sums of row block n (p splits them in two where there is one
+// block, so that an mma need not wait for the one before it); c[][][0..1] are
+// channel g of rows 2 t and 2 t + 1, [2..3] channel g + 8.
+// weights: the stage (biased bytes).  rows[n]: row g of block n at this stage's
+// 128 bytes (plain int8), swizzled by row_swz (its row index mod 8).
+template <int NB>
+struct Sums {
+    static constexpr int kSplit = NB == 1 ? 2 : 1;
+    float c[NB][kSplit][4];
+    int32_t total[NB][4];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) total[n][i] = 0;
+#pragma unroll
+            for (int p = 0; p < kSplit; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[n][p][i] = 0.0f;
+        }
+    }
+    // fp32 sums of at most 1024 products -> the int32 totals
+    __device__ __forceinline__ void flush() {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int p = 0; p < kSplit; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    total[n][i] += __float2int_rn(c[n][p][i]);
+                    c[n][p][i] = 0.0f;
+                }
+    }
+    __device__ __forceinline__ void add_stage(uint32_t weights, const uint32_t (&rows)[NB],
+                                              const int (&row_swz)[NB]) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 wa = lds16(weights + g * kDepth + unit_at(g, 2 * t + h));
+            const uint4 wb = lds16(weights + (g + 8) * kDepth + unit_at(g, 2 * t + h));
+            uint4 xr[NB];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) xr[n] = lds16(rows[n] + unit_at(row_swz[n], 2 * t + h));
+            const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a0 = widen_lo(a[i]), a1 = widen_lo(b[i]);
+                const uint32_t a2 = widen_hi(a[i]), a3 = widen_hi(b[i]);
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const uint32_t x4[4] = {xr[n].x, xr[n].y, xr[n].z, xr[n].w};
+                    const uint32_t x = x4[i] ^ 0x80808080u;
+                    mma_f16(c[n][i % kSplit], a0, a1, a2, a3, widen_lo(x), widen_hi(x));
+                }
+            }
+        }
+    }
+};
+
+}  // namespace si8
+}  // namespace moe

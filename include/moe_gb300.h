@@ -277,6 +277,26 @@ moe_status moe_layer(const moe_shape *shape, const void *x, const int32_t *exper
                      const void *w2_packed, const float *scale2, void *x_out,
                      void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* The whole layer for a few tokens: moe_layer's arguments and, for finite
+ * inputs and scales, its results bit for bit, in two kernels (four where the
+ * quantised rows of all tokens or routes pass 64 KB) and without its
+ * workspace's row images.  For the steps of a decoding batch, where the time is
+ * that of reading the chosen experts' weights.
+ *   - T * K <= MOE_FEW_TOKENS_MAX_ROUTES; more return MOE_ERR_SHAPE.
+ *   - shape->ffn_path SMALL or AUTO, and weights that moe_pack_weights packed
+ *     with it (the packed bytes are read); the others return
+ *     MOE_ERR_PARAM_INVALID.
+ *   - x_out may be the shared_expert_x buffer itself, and overlaps no other
+ *     argument. */
+#define MOE_FEW_TOKENS_MAX_ROUTES 512
+moe_status moe_layer_few_tokens_workspace_size(const moe_shape *shape, size_t *bytes);
+moe_status moe_layer_few_tokens(const moe_shape *shape, const void *x, const int32_t *expert_ids,
+                                const float *expert_scales, const uint8_t *x_active_mask,
+                                const void *shared_expert_x, const void *w1_packed,
+                                const float *scale1, const void *w2_packed, const float *scale2,
+                                void *x_out, void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
 /* Device pointers into a workspace used by moe_layer or moe_grouped_ffn, for
  * inspection of the intermediate stages after the stream has finished.  Any
  * field a given call does not produce is NULL.  Layout of each:
