@@ -40,8 +40,20 @@ using namespace si8;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxRoutes = MOE_FEW_TOKENS_MAX_ROUTES;
 constexpr int kBatchUnits = 16;                 // units between two block barriers of the first kernel
-constexpr size_t kLocalBytes = 64 * 1024;       // codes that a CTA holds itself
-constexpr int kDepthLocal = 5, kDepthRing = 4;  // stages of a warp's ring
+#ifndef MOE_LOCAL_KB
+#define MOE_LOCAL_KB 64
+#endif
+constexpr size_t kLocalBytes = MOE_LOCAL_KB * 1024;       // codes that a CTA holds itself
+#ifndef MOE_DL
+#define MOE_DL 3
+#endif
+#ifndef MOE_DL2
+#define MOE_DL2 3
+#endif
+#ifndef MOE_DR
+#define MOE_DR 3
+#endif
+constexpr int kDepthLocal = MOE_DL, kDepthLocal2 = MOE_DL2, kDepthRing = MOE_DR;  // stages of a warp's ring
 
 struct FewDev {
     const uint4 *x;            // bf16 [T, H]
@@ -198,28 +210,11 @@ __device__ __forceinline__ void put_codes(uint8_t *codes, int r, int pitch, int 
 
 __host__ __device__ inline int padded(int k) { return (k + kDepth - 1) / kDepth * kDepth; }
 
-// One warp's way through its stages: `kBytes` a stage, kD stages in the ring.
-template <int kD, int kBytes>
-struct Ring {
-    uint32_t base;
-    int put = 0, get = 0;
-    __device__ __forceinline__ uint32_t next_put() {
-        const uint32_t a = base + (uint32_t)put * kBytes;
-        put = put + 1 == kD ? 0 : put + 1;
-        return a;
-    }
-    __device__ __forceinline__ uint32_t next_get() {
-        const uint32_t a = base + (uint32_t)get * kBytes;
-        get = get + 1 == kD ? 0 : get + 1;
-        return a;
-    }
-};
-
 // ---------------------------------------------------------------- h = q1 . W1, g = silu(h_a) h_b
 // Unit u of block u / (Nh / 8): SiLU channels 8 j .. 8 j + 7 and their
 // multipliers (16 rows of the packed W1, two runs of eight).
 template <bool LOCAL>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 512 / kThreads)
 k_few_gate_up(FewDev p) {
     constexpr int kD = LOCAL ? kDepthLocal : kDepthRing;
     constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : kRowBytes);
@@ -230,6 +225,7 @@ k_few_gate_up(FewDev p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t *codes = smem + (size_t)kWarps * kD * kBytes;
     const int H = p.H, KS = (H + kDepth - 1) / kDepth, pitch = KS * kDepth, NU = p.Nh / 8;
+    const Lane l;
 
     for (int i = tid; i < 2 * kBatchUnits * kRows * kChannels; i += kThreads) (&acc[0][0][0][0])[i] = 0;
     if (LOCAL) {
@@ -241,13 +237,7 @@ k_few_gate_up(FewDev p) {
     const int64_t units = (int64_t)r.blocks * NU;
     const int u_begin = (int)(units * blockIdx.x / gridDim.x), u_end = (int)(units * (blockIdx.x + 1) / gridDim.x);
 
-    // the stages to fetch: batch by batch, this warp's share of each
-    struct {
-        int batch, unit, ks, left;
-        const uint8_t *src;
-        const int8_t *row;
-        bool row_on[2];
-    } f;
+    // this warp's share of a batch of units: first unit, its first stage, stages
     auto share = [&](int first, int &unit, int &ks, int &n) {
         const int total = min(kBatchUnits, u_end - first) * KS;
         const int a = total * warp / kWarps, b = total * (warp + 1) / kWarps;
@@ -255,62 +245,61 @@ k_few_gate_up(FewDev p) {
         ks = a % KS;
         n = b - a;
     };
-    const int cu = lane & 7, cr = lane >> 3;   // copies: 16-byte unit, row of a group of four
-    auto weights_of = [&](int unit) {
-        const int blk = unit / NU, j = (unit - blk * NU) * 8;
-        const int64_t prow = (int64_t)r.blk_e[blk] * (2 * p.Nh) + (j >> 6) * 128 + ((j >> 4) & 3) * 32 + (j & 15);
-        return p.w1 + (prow + cr) * H + cu * 16;
-    };
+    // the stages to fetch, batch by batch
+    int f_batch = u_begin, f_unit = 0, f_ks = 0, f_left = 0;
+    const uint8_t *f_src = nullptr;                      // the lane's bytes of the next stage
+    const int8_t *f_row[2] = {nullptr, nullptr};         // and of the rows, where they are
     auto enter = [&]() {
-        f.src = weights_of(f.unit);
-    };
-    f.batch = u_begin;
-    f.left = 0;
-    if (u_begin < u_end) share(u_begin, f.unit, f.ks, f.left);
-    Ring<kD, kBytes> ring;
-    ring.base = smem_u32(smem) + (uint32_t)(warp * kD * kBytes);
-    if (f.left > 0) enter();
-    auto fetch_rows = [&](uint32_t dst, int unit, int ks) {
-        const int blk = unit / NU;
-        const bool in = ks * kDepth + cu * 16 < H;
+        const int blk = f_unit / NU, j = (f_unit - blk * NU) * 8;
+        const int64_t prow = (int64_t)r.blk_e[blk] * (2 * p.Nh) + (j >> 6) * 128 + ((j >> 4) & 3) * 32 + (j & 15);
+        f_src = p.w1 + (prow + l.cr) * H + f_ks * kDepth + l.cu * 16;
+        if (!LOCAL) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = 4 * i + cr;
-            if (row < r.blk_n[blk]) {
-                const int t = r.list[r.blk_first[blk] + row] / p.K;
-                copy16(dst + kWeightBytes + row * kDepth + unit_at(row, cu),
-                       p.q + (int64_t)t * H + ks * kDepth + cu * 16, in);
+            for (int i = 0; i < 2; ++i) {
+                const int row = 4 * i + l.cr;
+                f_row[i] = nullptr;
+                if (row < r.blk_n[blk])
+                    f_row[i] = p.q + (int64_t)(r.list[r.blk_first[blk] + row] / p.K) * H + f_ks * kDepth + l.cu * 16;
             }
         }
     };
-    auto fetch = [&](bool rows) {
-        while (f.left == 0 && f.batch + kBatchUnits < u_end) {
-            f.batch += kBatchUnits;
-            share(f.batch, f.unit, f.ks, f.left);
-            if (f.left > 0) enter();
+    if (u_begin < u_end) share(u_begin, f_unit, f_ks, f_left);
+    if (f_left > 0) enter();
+    auto fetch = [&](uint32_t slot) {
+        if (f_left == 0) {
+            while (f_left == 0 && f_batch + kBatchUnits < u_end) {
+                f_batch += kBatchUnits;
+                share(f_batch, f_unit, f_ks, f_left);
+            }
+            if (f_left == 0) return;
+            enter();
         }
-        if (f.left > 0) {
-            const uint32_t dst = ring.next_put();
-            const bool in = f.ks * kDepth + cu * 16 < H;
-            const uint8_t *src = f.src + f.ks * kDepth;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                copy16(dst + (4 * i + cr) * kDepth + unit_at(4 * i + cr, cu),
-                       src + (int64_t)(i < 2 ? 4 * i : 4 * i + 8) * H, in);
-            if (!LOCAL && rows) fetch_rows(dst, f.unit, f.ks);
-            --f.left;
-            if (++f.ks == KS) {
-                f.ks = 0;
-                ++f.unit;
-                if (f.left > 0) enter();
+        const bool in = f_ks * kDepth + l.cu * 16 < H;
+        copy16(slot + l.to0, f_src, in);
+        copy16(slot + l.to1, f_src + (int64_t)4 * H, in);
+        copy16(slot + l.to0 + 8 * kDepth, f_src + (int64_t)16 * H, in);
+        copy16(slot + l.to1 + 8 * kDepth, f_src + (int64_t)20 * H, in);
+        f_src += kDepth;
+        if (!LOCAL) {
+            if (f_row[0]) {
+                copy16(slot + l.to0 + kWeightBytes, f_row[0], in);
+                f_row[0] += kDepth;
+            }
+            if (f_row[1]) {
+                copy16(slot + l.to1 + kWeightBytes, f_row[1], in);
+                f_row[1] += kDepth;
             }
         }
+        --f_left;
+        if (++f_ks == KS) {
+            f_ks = 0;
+            ++f_unit;
+            if (f_left > 0) enter();
+        }
     };
+    Walk<kD, kBytes, LOCAL> walk(smem_u32(smem) + (uint32_t)(warp * kD * kBytes));
     if (LOCAL) {
-        for (int i = 0; i < kD - 1; ++i) {
-            fetch(false);
-            copy_commit();
-        }
+        walk.first(fetch);
         // the tokens' codes, in every CTA
         const int H8 = H / 8;
         for (int i = tid; i < p.T * H8; i += kThreads) {
@@ -341,18 +330,15 @@ k_few_gate_up(FewDev p) {
         __syncthreads();
     } else {
         pdl_wait();
-        for (int i = 0; i < kD - 1; ++i) {
-            fetch(true);
-            copy_commit();
-        }
+        walk.first(fetch);
     }
 
-    const int g = lane >> 2, tq = lane & 3;
     int buf = 0;
     for (int first = u_begin; first < u_end; first += kBatchUnits, buf ^= 1) {
         const int nu = min(kBatchUnits, u_end - first);
         // this thread's unit of the batch, for the epilogue: its scales come meanwhile
-        const int eu = tid >> 4, ej = tid & 7, eh = (tid >> 3) & 1;
+        constexpr int kUnitThreads = kThreads / kBatchUnits;
+        const int eu = tid / kUnitThreads, ej = tid & 7, er = (tid % kUnitThreads) >> 3;
         int eblk = 0, ech = 0;
         float sa = 0.0f, sb = 0.0f;
         if (eu < nu) {
@@ -365,59 +351,38 @@ k_few_gate_up(FewDev p) {
         int unit, ks, n;
         share(first, unit, ks, n);
         while (n > 0) {
-            const int blk = unit / NU, nr = r.blk_n[blk];
-            // lanes of rows that are not there read the first row's codes
-            const int row = g < nr ? g : 0;
-            const int t = r.list[r.blk_first[blk] + row] / p.K;
-            int m = min(n, KS - ks);
-            n -= m;
-            Sums<1> sums;
-            sums.clear();
-            uint32_t crow[1] = {smem_u32(codes) + (uint32_t)(t * pitch + ks * kDepth)};
-            int swz[1] = {LOCAL ? t : row};
-            for (int i = 0; i < m; ++i) {
-                copy_wait<kD - 2>();
-                __syncwarp();
-                fetch(true);
-                copy_commit();
-                const uint32_t st = ring.next_get();
-                if (!LOCAL) crow[0] = st + kWeightBytes + row * kDepth;
-                sums.add_stage(st, crow, swz);
-                if (LOCAL) crow[0] += kDepth;
-                if (i % kExactStages == kExactStages - 1) sums.flush();
-            }
-            sums.flush();
+            const int blk = unit / NU, m = min(n, KS - ks);
             int32_t (*a)[kChannels] = acc[buf][unit - first];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (2 * tq + (i & 1) < nr)
-                    atomicAdd(&a[2 * tq + (i & 1)][g + (i >> 1) * 8], sums.total[0][i]);
+            auto row = [&](int i) -> uint32_t {
+                if (!LOCAL) return kWeightBytes + i * kDepth + l.of_row(i);
+                const int t = r.list[r.blk_first[blk] + i] / p.K;
+                return smem_u32(codes) + (uint32_t)(t * pitch + ks * kDepth) + l.of_row(t);
+            };
+            auto add = [&](int i, int c, int32_t v) { atomicAdd(&a[i][c], v); };
+            walk.run(l, m, r.blk_n[blk], fetch, row, add);
+            n -= m;
             ks = 0;
             ++unit;
         }
         __syncthreads();
         if (eu < nu) {
             const int nr = r.blk_n[eblk];
-            for (int row = eh; row < kRows; row += 2) {
-                float v = 0.0f;
-                const int route = row < nr ? r.list[r.blk_first[eblk] + row] : 0;
-                if (row < nr) {
-                    int32_t *a = acc[buf][eu][row];
-                    const int t = route / p.K;
-                    const float s1 = LOCAL ? __fdiv_rn(__uint_as_float(amax[t]), 127.0f) : p.qs[t];
-                    const float ha = __fmul_rn(__fmul_rn(__int2float_rn(a[ej]), sa), s1);
-                    const float hb = __fmul_rn(__fmul_rn(__int2float_rn(a[ej + 8]), sb), s1);
-                    a[ej] = 0;
-                    a[ej + 8] = 0;
-                    v = __fmul_rn(tc::silu_f32(ha), hb);
-                    p.g[(int64_t)route * p.Nh + ech] = v;
-                }
+            for (int row = er; row < nr; row += kUnitThreads / 8) {
+                const int route = r.list[r.blk_first[eblk] + row], t = route / p.K;
+                int32_t *a = acc[buf][eu][row];
+                const float s1 = LOCAL ? __fdiv_rn(__uint_as_float(amax[t]), 127.0f) : p.qs[t];
+                const float ha = __fmul_rn(__fmul_rn(__int2float_rn(a[ej]), sa), s1);
+                const float hb = __fmul_rn(__fmul_rn(__int2float_rn(a[ej + 8]), sb), s1);
+                a[ej] = 0;
+                a[ej + 8] = 0;
+                const float v = __fmul_rn(tc::silu_f32(ha), hb);
+                p.g[(int64_t)route * p.Nh + ech] = v;
                 if (LOCAL) {
                     float mx = fmaxf(0.0f, fabsf(v));
                     const uint32_t eight = 0xffu << (lane & 24);   // the lanes of this unit and row
 #pragma unroll
                     for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(eight, mx, o));
-                    if (ej == 0 && row < nr) p.gmax[(int64_t)route * NU + (ech >> 3)] = mx;
+                    if (ej == 0) p.gmax[(int64_t)route * NU + (ech >> 3)] = mx;
                 }
             }
         }
@@ -427,15 +392,16 @@ k_few_gate_up(FewDev p) {
 
 // ---------------------------------------------------------------- y = q2 . W2, out
 template <bool LOCAL>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 512 / kThreads)
 k_few_down(FewDev p) {
-    constexpr int kD = LOCAL ? kDepthLocal : kDepthRing;
+    constexpr int kD = LOCAL ? kDepthLocal2 : kDepthRing;
     constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : kRowBytes);
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Routes r;
     __shared__ float s2[kMaxRoutes];      // by place in the list
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Nh = p.Nh, KS = (Nh + kDepth - 1) / kDepth, pitch = KS * kDepth;
+    const Lane l;
     uint8_t *codes = smem + (size_t)kWarps * kD * kBytes;
     int32_t *acc = reinterpret_cast<int32_t *>(codes + (LOCAL ? (size_t)p.R * pitch : 0));   // [2][R][16]
 
@@ -446,59 +412,60 @@ k_few_down(FewDev p) {
     const int mine_a = per_batch * warp / kWarps, mine_n = per_batch * (warp + 1) / kWarps - mine_a;
     const int batches = p.H / kChannels;
 
-    const int cu = lane & 7, cr = lane >> 3;
-    struct {
-        int batch, blk, ks, left;
-        const uint8_t *src;
-    } f;
-    auto begin = [&]() {
-        f.left = mine_n;
-        f.blk = mine_a / KS;
-        f.ks = mine_a % KS;
-    };
+    int f_batch = blockIdx.x, f_blk = 0, f_ks = 0, f_left = 0;
+    const uint8_t *f_src = nullptr;
+    const int8_t *f_row[2] = {nullptr, nullptr};
     auto enter = [&]() {
-        f.src = p.w2 + ((int64_t)r.blk_e[f.blk] * p.H + f.batch * kChannels + cr) * Nh + cu * 16;
-    };
-    f.batch = blockIdx.x;
-    begin();
-    if (f.left > 0 && f.batch < batches) enter();
-    Ring<kD, kBytes> ring;
-    ring.base = smem_u32(smem) + (uint32_t)(warp * kD * kBytes);
-    auto fetch = [&]() {
-        if (mine_n == 0) return;
-        if (f.left == 0) {
-            f.batch += gridDim.x;
-            begin();
-            if (f.batch < batches) enter();
-        }
-        if (f.batch >= batches) return;
-        const uint32_t dst = ring.next_put();
-        const bool in = f.ks * kDepth + cu * 16 < Nh;
-        const uint8_t *src = f.src + f.ks * kDepth;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            copy16(dst + (4 * i + cr) * kDepth + unit_at(4 * i + cr, cu), src + (int64_t)4 * i * Nh, in);
+        f_src = p.w2 + ((int64_t)r.blk_e[f_blk] * p.H + f_batch * kChannels + l.cr) * Nh + f_ks * kDepth + l.cu * 16;
         if (!LOCAL) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int row = 4 * i + cr;
-                if (row < r.blk_n[f.blk])
-                    copy16(dst + kWeightBytes + row * kDepth + unit_at(row, cu),
-                           p.q + (int64_t)r.list[r.blk_first[f.blk] + row] * Nh + f.ks * kDepth + cu * 16, in);
+                const int row = 4 * i + l.cr;
+                f_row[i] = nullptr;
+                if (row < r.blk_n[f_blk])
+                    f_row[i] = p.q + (int64_t)r.list[r.blk_first[f_blk] + row] * Nh + f_ks * kDepth + l.cu * 16;
             }
         }
-        --f.left;
-        if (++f.ks == KS) {
-            f.ks = 0;
-            ++f.blk;
-            if (f.left > 0) enter();
+    };
+    auto begin = [&]() {
+        f_left = mine_n;
+        f_blk = mine_a / KS;
+        f_ks = mine_a % KS;
+        if (f_left > 0) enter();
+    };
+    if (f_batch < batches) begin();
+    auto fetch = [&](uint32_t slot) {
+        if (f_left == 0) {
+            if (mine_n == 0 || f_batch + (int)gridDim.x >= batches) return;
+            f_batch += gridDim.x;
+            begin();
+        }
+        const bool in = f_ks * kDepth + l.cu * 16 < Nh;
+        copy16(slot + l.to0, f_src, in);
+        copy16(slot + l.to1, f_src + (int64_t)4 * Nh, in);
+        copy16(slot + l.to0 + 8 * kDepth, f_src + (int64_t)8 * Nh, in);
+        copy16(slot + l.to1 + 8 * kDepth, f_src + (int64_t)12 * Nh, in);
+        f_src += kDepth;
+        if (!LOCAL) {
+            if (f_row[0]) {
+                copy16(slot + l.to0 + kWeightBytes, f_row[0], in);
+                f_row[0] += kDepth;
+            }
+            if (f_row[1]) {
+                copy16(slot + l.to1 + kWeightBytes, f_row[1], in);
+                f_row[1] += kDepth;
+            }
+        }
+        --f_left;
+        if (++f_ks == KS) {
+            f_ks = 0;
+            ++f_blk;
+            if (f_left > 0) enter();
         }
     };
+    Walk<kD, kBytes, LOCAL> walk(smem_u32(smem) + (uint32_t)(warp * kD * kBytes));
     if (LOCAL) {
-        for (int i = 0; i < kD - 1; ++i) {
-            fetch();
-            copy_commit();
-        }
+        walk.first(fetch);
         pdl_wait();
         // the routes' codes: a row to a warp, or part of one where there are fewer
         const int parts = r.rows > 0 ? max(1, kWarps / r.rows) : 1, n8 = Nh / 8;
@@ -524,45 +491,24 @@ k_few_down(FewDev p) {
         }
     } else {
         pdl_wait();
-        for (int i = 0; i < kD - 1; ++i) {
-            fetch();
-            copy_commit();
-        }
+        walk.first(fetch);
         for (int i = tid; i < r.rows; i += kThreads) s2[i] = __ldcg(p.qs + r.list[i]);
     }
     __syncthreads();
 
-    const int g = lane >> 2, tq = lane & 3;
     int buf = 0;
     for (int batch = blockIdx.x; batch < batches; batch += gridDim.x, buf ^= 1) {
         int32_t *a = acc + (size_t)buf * p.R * kChannels;
         int blk = mine_a / KS, ks = mine_a % KS, n = mine_n;
         while (n > 0) {
-            const int nr = r.blk_n[blk], base = r.blk_first[blk];
-            const int row = g < nr ? g : 0;
-            const int m = min(n, KS - ks);
+            const int base = r.blk_first[blk], m = min(n, KS - ks);
+            auto row = [&](int i) -> uint32_t {
+                if (!LOCAL) return kWeightBytes + i * kDepth + l.of_row(i);
+                return smem_u32(codes) + (uint32_t)((base + i) * pitch + ks * kDepth) + l.of_row(base + i);
+            };
+            auto add = [&](int i, int c, int32_t v) { atomicAdd(&a[(base + i) * kChannels + c], v); };
+            walk.run(l, m, r.blk_n[blk], fetch, row, add);
             n -= m;
-            Sums<1> sums;
-            sums.clear();
-            uint32_t crow[1] = {smem_u32(codes) + (uint32_t)((base + row) * pitch + ks * kDepth)};
-            int swz[1] = {LOCAL ? base + row : row};
-            for (int i = 0; i < m; ++i) {
-                copy_wait<kD - 2>();
-                __syncwarp();
-                fetch();
-                copy_commit();
-                const uint32_t st = ring.next_get();
-                if (!LOCAL) crow[0] = st + kWeightBytes + row * kDepth;
-                sums.add_stage(st, crow, swz);
-                if (LOCAL) crow[0] += kDepth;
-                if (i % kExactStages == kExactStages - 1) sums.flush();
-            }
-            sums.flush();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int rr = 2 * tq + (i & 1);
-                if (rr < nr) atomicAdd(&a[(base + rr) * kChannels + g + (i >> 1) * 8], sums.total[0][i]);
-            }
             ks = 0;
             ++blk;
         }
@@ -684,9 +630,8 @@ moe_status launch_layer_few_tokens(const moe_shape &s, const FewTokensArgs &a, c
     const unsigned grid2 = (unsigned)std::min<int64_t>(sms, H / kChannels);
     const size_t acc2 = (size_t)2 * R * kChannels * sizeof(int32_t);
     if (few_tokens_local(T, K, H, Nh)) {
-        const size_t ring = (size_t)kWarps * kDepthLocal * kWeightBytes;
-        const size_t smem1 = ring + (size_t)T * padded((int)H);
-        const size_t smem2 = ring + (size_t)R * padded((int)Nh) + acc2;
+        const size_t smem1 = (size_t)kWarps * kDepthLocal * kWeightBytes + (size_t)T * padded((int)H);
+        const size_t smem2 = (size_t)kWarps * kDepthLocal2 * kWeightBytes + (size_t)R * padded((int)Nh) + acc2;
         if (!set_smem_limit((const void *)k_few_gate_up<true>, smem1) ||
             !set_smem_limit((const void *)k_few_down<true>, smem2))
             return MOE_ERR_CUDA;

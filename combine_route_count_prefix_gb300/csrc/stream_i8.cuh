@@ -22,7 +22,10 @@
 namespace moe {
 namespace si8 {
 
-constexpr int kWarps = 8;
+#ifndef MOE_W
+#define MOE_W 16
+#endif
+constexpr int kWarps = MOE_W;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kChannels = 16;                      // output channels of a stage
 constexpr int kDepth = 128;                        // its share of the inner dimension
@@ -84,8 +87,8 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 // c[n][p]: the sums of row block n (p splits them in two where there is one
 // block, so that an mma need not wait for the one before it); c[][][0..1] are
 // channel g of rows 2 t and 2 t + 1, [2..3] channel g + 8.
-// weights: the stage (biased bytes).  rows[n]: row g of block n at this stage's
-// 128 bytes (plain int8), swizzled by row_swz (its row index mod 8).
+// at: the lane's first 16 bytes of channel g in the stage (biased bytes; the next
+// 16 are at at ^ 16).  row[n]: the same of row g of block n (plain int8).
 template <int NB>
 struct Sums {
     static constexpr int kSplit = NB == 1 ? 2 : 1;
@@ -115,16 +118,13 @@ struct Sums {
                     c[n][p][i] = 0.0f;
                 }
     }
-    __device__ __forceinline__ void add_stage(uint32_t weights, const uint32_t (&rows)[NB],
-                                              const int (&row_swz)[NB]) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    __device__ __forceinline__ void add_stage(uint32_t at, const uint32_t (&row)[NB]) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint4 wa = lds16(weights + g * kDepth + unit_at(g, 2 * t + h));
-            const uint4 wb = lds16(weights + (g + 8) * kDepth + unit_at(g, 2 * t + h));
+            const uint4 wa = lds16(at ^ (h << 4)), wb = lds16((at ^ (h << 4)) + 8 * kDepth);
             uint4 xr[NB];
 #pragma unroll
-            for (int n = 0; n < NB; ++n) xr[n] = lds16(rows[n] + unit_at(row_swz[n], 2 * t + h));
+            for (int n = 0; n < NB; ++n) xr[n] = lds16(row[n] ^ (h << 4));
             const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -136,6 +136,158 @@ struct Sums {
                     const uint32_t x = x4[i] ^ 0x80808080u;
                     mma_f16(c[n][i % kSplit], a0, a1, a2, a3, widen_lo(x), widen_hi(x));
                 }
+            }
+        }
+    }
+};
+
+// The same products for NR <= 4 rows with dp4a, on the integer pipe (64 lanes a
+// clock of an SM): 16 instructions a row and stage, against the 104 that the widening
+// and the mma take whatever the rows (even at about five).  Lane (g, t) adds
+// bytes [32 t, 32 t + 32) of channels g and g + 8; join() adds the four lanes.
+// row[n]: the lane's first 16 bytes of row n at this stage.
+template <int NR>
+struct Dots {
+    int32_t acc[2][NR];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int n = 0; n < NR; ++n) acc[0][n] = acc[1][n] = 0;
+    }
+    __device__ __forceinline__ void add_stage(uint32_t at, const uint32_t (&row)[NR]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 wa = lds16(at ^ (h << 4)), wb = lds16((at ^ (h << 4)) + 8 * kDepth);
+            const uint32_t a[4] = {wa.x ^ 0x80808080u, wa.y ^ 0x80808080u, wa.z ^ 0x80808080u,
+                                   wa.w ^ 0x80808080u};
+            const uint32_t b[4] = {wb.x ^ 0x80808080u, wb.y ^ 0x80808080u, wb.z ^ 0x80808080u,
+                                   wb.w ^ 0x80808080u};
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                const uint4 x = lds16(row[n] ^ (h << 4));
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[0][n] = __dp4a((int)a[i], (int)xs[i], acc[0][n]);
+                    acc[1][n] = __dp4a((int)b[i], (int)xs[i], acc[1][n]);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void join() {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                acc[c][n] += __shfl_xor_sync(0xffffffffu, acc[c][n], 1);
+                acc[c][n] += __shfl_xor_sync(0xffffffffu, acc[c][n], 2);
+            }
+    }
+};
+
+// What the lanes of a warp need to fetch and find their parts of a stage.
+struct Lane {
+    int cu, cr;           // copies: 16-byte unit of a 128-byte row, row of a group of four
+    uint32_t to0, to1;    // where rows cr and cr + 4 of a group of eight go
+    int g, t;             // products: channel (row) of eight, quarter of the 128 bytes
+    uint32_t from;        // its first 16 bytes of channel g
+    __device__ __forceinline__ Lane() {
+        const int lane = threadIdx.x & 31;
+        cu = lane & 7;
+        cr = lane >> 3;
+        to0 = (uint32_t)(cr * kDepth) + unit_at(cr, cu);
+        to1 = (uint32_t)((cr + 4) * kDepth) + unit_at(cr + 4, cu);
+        g = lane >> 2;
+        t = lane & 3;
+        from = (uint32_t)(g * kDepth) + unit_at(g, 2 * t);
+    }
+    // row r of a block of 128-byte rows: this lane's first 16 bytes
+    __device__ __forceinline__ uint32_t of_row(int r) const { return unit_at(r, 2 * t); }
+};
+
+// One warp's way through its stages.  The ring holds kD; stage i + kD - 1 is
+// fetched (fetch(slot)) once every lane has read stage i - 1, into its slot.
+// LOCAL: the rows' codes lie elsewhere in shared memory, stage after stage;
+// else they come with the weights, behind them in the slot.
+template <int kD, int kBytes, bool LOCAL>
+struct Walk {
+    uint32_t base, cur, prev;
+    __device__ __forceinline__ explicit Walk(uint32_t b)
+        : base(b), cur(b), prev(b + (uint32_t)((kD - 1) * kBytes)) {}
+    template <typename Fetch>
+    __device__ __forceinline__ void first(Fetch &fetch) {
+#pragma unroll 1
+        for (int i = 0; i < kD - 1; ++i) {
+            fetch(base + (uint32_t)(i * kBytes));
+            copy_commit();
+        }
+    }
+    template <typename Fetch>
+    __device__ __forceinline__ uint32_t next(Fetch &fetch) {
+        copy_wait<kD - 2>();
+        __syncwarp();
+        fetch(prev);
+        copy_commit();
+        prev = cur;
+        cur = cur + kBytes == base + kD * kBytes ? base : cur + kBytes;
+        return prev;
+    }
+    template <int NR, typename Fetch, typename Row, typename Add>
+    __device__ __forceinline__ void dots(const Lane &l, int stages, Fetch &fetch, Row &row, Add &add) {
+        Dots<NR> d;
+        d.clear();
+        uint32_t r[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) r[n] = row(n);
+#pragma unroll 1
+        for (int i = 0; i < stages; ++i) {
+            const uint32_t st = next(fetch);
+            uint32_t at[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                at[n] = LOCAL ? r[n] : st + r[n];
+                if (LOCAL) r[n] += kDepth;
+            }
+            d.add_stage(st + l.from, at);
+        }
+        d.join();
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+            if (n == l.t) {
+                add(n, l.g, d.acc[0][n]);
+                add(n, l.g + 8, d.acc[1][n]);
+            }
+    }
+    // `stages` stages of one unit with nr rows.  row(n): the lane's first bytes of
+    // row n (LOCAL: at the first stage; else in the slot); add(n, c, v) takes the
+    // sum of row n and channel c (0 .. 15), from one lane each.
+    template <typename Fetch, typename Row, typename Add>
+    __device__ __forceinline__ void run(const Lane &l, int stages, int nr, Fetch &fetch, Row &row, Add &add) {
+        if (nr == 1) {
+            dots<1>(l, stages, fetch, row, add);
+        } else if (nr == 2) {
+            dots<2>(l, stages, fetch, row, add);
+        } else if (nr == 3) {
+            dots<3>(l, stages, fetch, row, add);
+        } else if (nr == 4) {
+            dots<4>(l, stages, fetch, row, add);
+        } else {
+            Sums<1> s;
+            s.clear();
+            uint32_t r = row(l.g < nr ? l.g : 0);   // lanes of rows that are not there read the first
+#pragma unroll 1
+            for (int i = 0; i < stages; ++i) {
+                const uint32_t st = next(fetch);
+                const uint32_t at[1] = {LOCAL ? r : st + r};
+                if (LOCAL) r += kDepth;
+                s.add_stage(st + l.from, at);
+                if (i % kExactStages == kExactStages - 1) s.flush();
+            }
+            s.flush();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = 2 * l.t + (i & 1);
+                if (n < nr) add(n, l.g + (i >> 1) * 8, s.total[0][i]);
             }
         }
     }
