@@ -22,7 +22,7 @@ struct Carve {
 };
 
 struct FewLayout {
-    size_t status, g, gmax, q, qs, total;
+    size_t status, g, q, qs, total;
 };
 
 FewLayout few_layout(const moe_shape &s) {
@@ -31,7 +31,6 @@ FewLayout few_layout(const moe_shape &s) {
     const size_t T = (size_t)s.num_tokens, R = T * (size_t)s.topk, H = (size_t)s.hidden, Nh = (size_t)s.ffn / 2;
     L.status = c.take(4);
     L.g = c.take(R * Nh * sizeof(float));
-    L.gmax = c.take(R * (Nh / 8) * sizeof(float));
     L.q = c.take(align_up(T * H, kAlign) + R * Nh);
     L.qs = c.take((T + R) * sizeof(float));
     L.total = c.off;
@@ -95,7 +94,6 @@ moe_status moe_layer_few_tokens(const moe_shape *shape, const void *x, const int
     a.scale2 = scale2;
     a.out = x_out;
     a.g = at<float>(workspace, L.g);
-    a.gmax = at<float>(workspace, L.gmax);
     a.q = at<int8_t>(workspace, L.q);
     a.qs = at<float>(workspace, L.qs);
     a.status = at<int32_t>(workspace, L.status);

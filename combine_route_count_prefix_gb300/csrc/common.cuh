@@ -339,7 +339,6 @@ struct FewTokensArgs {
     const float *scale1, *scale2;
     void *out;                 // bf16 [T, H]
     float *g;                  // [T*K, N/2]
-    float *gmax;               // [T*K, N/16]
     int8_t *q;                 // T * H (rounded up to kAlign) + T * K * N/2 bytes
     float *qs;                 // [T + T*K]
     int32_t *status;

@@ -39,21 +39,26 @@ using namespace si8;
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxRoutes = MOE_FEW_TOKENS_MAX_ROUTES;
-constexpr int kBatchUnits = 16;                 // units between two block barriers of the first kernel
-#ifndef MOE_LOCAL_KB
-#define MOE_LOCAL_KB 64
-#endif
-constexpr size_t kLocalBytes = MOE_LOCAL_KB * 1024;       // codes that a CTA holds itself
-#ifndef MOE_DL
-#define MOE_DL 3
-#endif
-#ifndef MOE_DL2
-#define MOE_DL2 3
-#endif
-#ifndef MOE_DR
-#define MOE_DR 3
-#endif
-constexpr int kDepthLocal = MOE_DL, kDepthLocal2 = MOE_DL2, kDepthRing = MOE_DR;  // stages of a warp's ring
+
+// LOCAL: every CTA quantises what it multiplies, from registers.  Eight warps
+// and rings of 80 KB, so that a CTA of either kernel fits an SM beside one of the other.
+// Else the codes come through the rings.
+template <bool LOCAL, int D = 5>
+struct Cfg {
+    static constexpr int kWarps = LOCAL ? 8 : 12;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kD = D;                                 // stages of a warp's ring
+    static constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : kRowBytes);
+    static constexpr int kRing = kWarps * kD * kBytes;
+};
+template <bool LOCAL>
+constexpr int kUnits = LOCAL ? 8 : 16;          // of the first kernel, between two block barriers
+// Routes up to which the rings are five stages deep, else four (the sums of more
+// routes also need the room).  7168 x 4096, top-8, 128 experts (us, five against four): 2
+// tokens 112 / 115, 8 tokens 347 / 355, 16 tokens 566 / 568, 32 tokens 784 / 768, 64 tokens 917 / 901.
+constexpr int kDeepRoutes = 128;
+constexpr int kXVecs = 7, kGVecs = 8;           // vectors of eight values that a LOCAL thread holds
+constexpr int kQuantThreads = 256;
 
 struct FewDev {
     const uint4 *x;            // bf16 [T, H]
@@ -65,11 +70,11 @@ struct FewDev {
     const float *scale1, *scale2;
     __nv_bfloat16 *out;
     float *g;                  // [T*K, Nh]
-    float *gmax;               // [T*K, Nh / 8] largest |g| of 8 channels
     const int8_t *q;           // codes of the rows (not LOCAL): [T, H] or [T*K, Nh]
     const float *qs;           // and their scales
     int32_t *status;
     int T, K, R, E, Z, C, H, Nh, mask_kind;
+    Divisor by_k, by_units, by_stages1, by_stages2;   // K, Nh / 8, stages of H and of Nh
 };
 
 // What a CTA knows of the routes, in shared memory.
@@ -81,33 +86,82 @@ struct Routes {
     uint16_t blk_first[kMaxRoutes];
     uint8_t blk_n[kMaxRoutes];
     uint32_t count[kMaxExperts];
-    uint32_t part[kWarps];
+    uint32_t part[32];
     int32_t blocks, rows, bad;
 };
 
-__device__ void find_routes(const FewDev &p, Routes &r) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e < p.E; e += kThreads) r.count[e] = 0;
-    if (tid == 0) r.bad = 0;
+// Before the inputs may be read.
+template <int kThreads>
+__device__ __forceinline__ void clear_routes(const FewDev &p, Routes &r) {
+    if (p.R > 32)
+        for (int e = threadIdx.x; e < p.E; e += kThreads) r.count[e] = 0;
+    if (threadIdx.x == 0) r.bad = 0;
     __syncthreads();
+}
+
+__device__ __forceinline__ int route_code(const FewDev &p, int i) {
+    const int e = p.ids[i];
+    bool on = true;
+    if (p.mask_kind == 1) on = p.mask[p.by_k(i)] != 0;
+    if (p.mask_kind == 2) on = p.mask[i] != 0;
+    if (!on) return -1;
+    if (e >= 0 && e < p.E) return e;
+    if (e >= p.E && e < p.E + p.Z) return -2;
+    if (e >= p.E + p.Z && e < p.E + p.Z + p.C) return -3;
+    return -4;
+}
+
+// Up to 32 routes: one warp's votes, no counts per expert.
+__device__ __forceinline__ void find_routes_warp(const FewDev &p, Routes &r) {
+    const int lane = threadIdx.x & 31;
+    const int code = lane < p.R ? route_code(p, lane) : -1;
+    if (lane < p.R) r.code[lane] = code == -4 ? -1 : code;
+    if (code == -4) r.bad = 1;
+    const uint32_t same = __match_any_sync(kFull, code);
+    const int head = __ffs(same) - 1, n = __popc(same), nb = (n + kRows - 1) / kRows;
+    const bool heads = code >= 0 && head == lane;
+    const uint32_t own = heads ? (uint32_t)(n << 16 | nb) : 0u;
+    uint32_t sum = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(kFull, sum, d);
+        if (lane >= d) sum += v;
+    }
+    const int first = (int)((sum - own) >> 16), b0 = (int)((sum - own) & 0xffffu);
+    if (heads)
+        for (int b = 0; b < nb; ++b) {
+            r.blk_e[b0 + b] = (uint16_t)code;
+            r.blk_first[b0 + b] = (uint16_t)(first + b * kRows);
+            r.blk_n[b0 + b] = (uint8_t)min(kRows, n - b * kRows);
+        }
+    const int at = __shfl_sync(kFull, first, head) + __popc(same & lanemask_lt());
+    if (code >= 0) {
+        r.list[at] = (uint16_t)lane;
+        r.place[lane] = (uint16_t)at;
+    }
+    if (lane == 31) {
+        r.rows = (int)(sum >> 16);
+        r.blocks = (int)(sum & 0xffffu);
+    }
+}
+
+template <int kThreads>
+__device__ __forceinline__ void find_routes(const FewDev &p, Routes &r) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.R <= 32) {
+        if (warp == 0) find_routes_warp(p, r);
+        __syncthreads();
+        return;
+    }
     constexpr int kOwn = (kMaxRoutes + kThreads - 1) / kThreads;
     uint32_t pos[kOwn];
 #pragma unroll
     for (int o = 0; o < kOwn; ++o) {
         const int i = o * kThreads + tid;
         if (i >= p.R) break;
-        bool on = true;
-        if (p.mask_kind == 1) on = p.mask[i / p.K] != 0;
-        if (p.mask_kind == 2) on = p.mask[i] != 0;
-        const int e = p.ids[i];
-        int code = -1;
-        if (on) {
-            if (e >= 0 && e < p.E) code = e;
-            else if (e >= p.E && e < p.E + p.Z) code = -2;
-            else if (e >= p.E + p.Z && e < p.E + p.Z + p.C) code = -3;
-            else r.bad = 1;
-        }
-        r.code[i] = code;
+        const int code = route_code(p, i);
+        if (code == -4) r.bad = 1;
+        r.code[i] = code == -4 ? -1 : code;
         if (code >= 0) pos[o] = atomicAdd(&r.count[code], 1u);
     }
     __syncthreads();
@@ -126,7 +180,7 @@ __device__ void find_routes(const FewDev &p, Routes &r) {
     __syncthreads();
     uint32_t at = sum - own;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
+    for (int w = 0; w < kThreads / 32; ++w)
         if (w < warp) at += r.part[w];
     for (int e = e0; e < e1; ++e) {
         const int n = (int)r.count[e], first = (int)(at >> 16), b0 = (int)(at & 0xffffu);
@@ -213,44 +267,56 @@ __host__ __device__ inline int padded(int k) { return (k + kDepth - 1) / kDepth 
 // ---------------------------------------------------------------- h = q1 . W1, g = silu(h_a) h_b
 // Unit u of block u / (Nh / 8): SiLU channels 8 j .. 8 j + 7 and their
 // multipliers (16 rows of the packed W1, two runs of eight).
-template <bool LOCAL>
-__global__ void __launch_bounds__(kThreads, 512 / kThreads)
+template <bool LOCAL, int D>
+__global__ void __launch_bounds__(Cfg<LOCAL>::kThreads, LOCAL ? 2 : 1)
 k_few_gate_up(FewDev p) {
-    constexpr int kD = LOCAL ? kDepthLocal : kDepthRing;
-    constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : kRowBytes);
+    using C = Cfg<LOCAL, D>;
+    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kBatchUnits = kUnits<LOCAL>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Routes r;
     __shared__ int32_t acc[2][kBatchUnits][kRows][kChannels];
-    __shared__ uint32_t amax[kMaxRoutes];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint8_t *codes = smem + (size_t)kWarps * kD * kBytes;
+    __shared__ uint32_t amax[kWarps];
+    const int tid = threadIdx.x, warp = tid >> 5;
+    uint8_t *codes = smem + C::kRing;
     const int H = p.H, KS = (H + kDepth - 1) / kDepth, pitch = KS * kDepth, NU = p.Nh / 8;
     const Lane l;
 
     for (int i = tid; i < 2 * kBatchUnits * kRows * kChannels; i += kThreads) (&acc[0][0][0][0])[i] = 0;
-    if (LOCAL) {
+    if (LOCAL)
         for (int i = tid; i < p.T; i += kThreads) amax[i] = 0;
-        pdl_wait();
-    }
+    clear_routes<kThreads>(p, r);
     // with LOCAL unset, the kernel before this one has waited for the inputs
-    find_routes(p, r);
+    // LOCAL: a token's row is shared by `group` warps, this one's part starts at vector x0
+    const int H8 = H / 8, group = kWarps / min(p.T, kWarps), xt = warp / group;
+    const int x0 = (warp - xt * group) * 32 + (tid & 31);
+    uint4 xv[LOCAL ? kXVecs : 1];
+    if (LOCAL) {
+        pdl_wait();
+        if (xt < p.T)
+#pragma unroll
+            for (int u = 0; u < kXVecs; ++u)
+                if (x0 + 32 * group * u < H8) xv[u] = p.x[xt * H8 + x0 + 32 * group * u];
+    }
+    find_routes<kThreads>(p, r);
     const int64_t units = (int64_t)r.blocks * NU;
     const int u_begin = (int)(units * blockIdx.x / gridDim.x), u_end = (int)(units * (blockIdx.x + 1) / gridDim.x);
 
     // this warp's share of a batch of units: first unit, its first stage, stages
     auto share = [&](int first, int &unit, int &ks, int &n) {
         const int total = min(kBatchUnits, u_end - first) * KS;
-        const int a = total * warp / kWarps, b = total * (warp + 1) / kWarps;
-        unit = first + a / KS;
-        ks = a % KS;
+        const int a = total * warp / kWarps, b = total * (warp + 1) / kWarps, q = p.by_stages1(a);
+        unit = first + q;
+        ks = a - q * KS;
         n = b - a;
     };
     // the stages to fetch, batch by batch
+    const uint64_t once = l2_policy_evict_first();
+    auto copy_weights = [&](uint32_t dst, const void *src, bool in) { copy16_once(dst, src, in, once); };
     int f_batch = u_begin, f_unit = 0, f_ks = 0, f_left = 0;
     const uint8_t *f_src = nullptr;                      // the lane's bytes of the next stage
     const int8_t *f_row[2] = {nullptr, nullptr};         // and of the rows, where they are
     auto enter = [&]() {
-        const int blk = f_unit / NU, j = (f_unit - blk * NU) * 8;
+        const int blk = p.by_units(f_unit), j = (f_unit - blk * NU) * 8;
         const int64_t prow = (int64_t)r.blk_e[blk] * (2 * p.Nh) + (j >> 6) * 128 + ((j >> 4) & 3) * 32 + (j & 15);
         f_src = p.w1 + (prow + l.cr) * H + f_ks * kDepth + l.cu * 16;
         if (!LOCAL) {
@@ -259,7 +325,7 @@ k_few_gate_up(FewDev p) {
                 const int row = 4 * i + l.cr;
                 f_row[i] = nullptr;
                 if (row < r.blk_n[blk])
-                    f_row[i] = p.q + (int64_t)(r.list[r.blk_first[blk] + row] / p.K) * H + f_ks * kDepth + l.cu * 16;
+                    f_row[i] = p.q + (int64_t)p.by_k(r.list[r.blk_first[blk] + row]) * H + f_ks * kDepth + l.cu * 16;
             }
         }
     };
@@ -275,10 +341,10 @@ k_few_gate_up(FewDev p) {
             enter();
         }
         const bool in = f_ks * kDepth + l.cu * 16 < H;
-        copy16(slot + l.to0, f_src, in);
-        copy16(slot + l.to1, f_src + (int64_t)4 * H, in);
-        copy16(slot + l.to0 + 8 * kDepth, f_src + (int64_t)16 * H, in);
-        copy16(slot + l.to1 + 8 * kDepth, f_src + (int64_t)20 * H, in);
+        copy_weights(slot + l.to0, f_src, in);
+        copy_weights(slot + l.to1, f_src + (int64_t)4 * H, in);
+        copy_weights(slot + l.to0 + 8 * kDepth, f_src + (int64_t)16 * H, in);
+        copy_weights(slot + l.to1 + 8 * kDepth, f_src + (int64_t)20 * H, in);
         f_src += kDepth;
         if (!LOCAL) {
             if (f_row[0]) {
@@ -297,35 +363,37 @@ k_few_gate_up(FewDev p) {
             if (f_left > 0) enter();
         }
     };
-    Walk<kD, kBytes, LOCAL> walk(smem_u32(smem) + (uint32_t)(warp * kD * kBytes));
+    Walk<C::kD, C::kBytes, LOCAL> walk(smem_u32(smem) + (uint32_t)(warp * C::kD * C::kBytes));
     if (LOCAL) {
         walk.first(fetch);
         // the tokens' codes, in every CTA
-        const int H8 = H / 8;
-        for (int i = tid; i < p.T * H8; i += kThreads) {
-            const int t = i / H8;
-            float v[8];
-            unpack8(p.x[i], v);
-            const uint32_t m = __float_as_uint(max8(v, 0.0f));
-            const uint32_t act = __activemask();
-            if (__match_any_sync(act, t) == act) {
-                const uint32_t w = __reduce_max_sync(act, m);
-                if (lane == __ffs(act) - 1) atomicMax(&amax[t], w);
-            } else {
-                atomicMax(&amax[t], m);
-            }
+        if (xt < p.T) {
+            float m = 0.0f;
+#pragma unroll
+            for (int u = 0; u < kXVecs; ++u)
+                if (x0 + 32 * group * u < H8) {
+                    float v[8];
+                    unpack8(xv[u], v);
+                    m = max8(v, m);
+                }
+            const uint32_t w = __reduce_max_sync(kFull, __float_as_uint(m));
+            if ((tid & 31) == 0) atomicMax(&amax[xt], w);
         }
         __syncthreads();
-        for (int i = tid; i < p.T * (pitch / 8); i += kThreads) {
-            const int t = i / (pitch / 8), c = i % (pitch / 8);
-            uint2 q = make_uint2(0, 0);
-            if (c < H8) {
-                float v[8];
-                unpack8(p.x[(int64_t)t * H8 + c], v);
-                const float s = __fdiv_rn(__uint_as_float(amax[t]), 127.0f);
-                q = codes8(v, s, __frcp_rn(s));
-            }
-            put_codes(codes, t, pitch, c, q);
+        if (xt < p.T) {
+            const float s = __fdiv_rn(__uint_as_float(amax[xt]), 127.0f), rs = __frcp_rn(s);
+#pragma unroll
+            for (int u = 0; u < kXVecs; ++u)
+                if (x0 + 32 * group * u < H8) {
+                    float v[8];
+                    unpack8(xv[u], v);
+                    put_codes(codes, xt, pitch, x0 + 32 * group * u, codes8(v, s, rs));
+                }
+        }
+        if (H % kDepth) {   // zeros behind the rows' ends
+            const int pad = pitch / 8 - H8;
+            for (int i = tid; i < p.T * pad; i += kThreads)
+                put_codes(codes, i / pad, pitch, H8 + i % pad, make_uint2(0, 0));
         }
         __syncthreads();
     } else {
@@ -342,7 +410,7 @@ k_few_gate_up(FewDev p) {
         int eblk = 0, ech = 0;
         float sa = 0.0f, sb = 0.0f;
         if (eu < nu) {
-            eblk = (first + eu) / NU;
+            eblk = p.by_units(first + eu);
             ech = ((first + eu) - eblk * NU) * 8 + ej;
             const float *sc = p.scale1 + (int64_t)r.blk_e[eblk] * (2 * p.Nh) + ech;
             sa = __ldg(sc);
@@ -351,11 +419,11 @@ k_few_gate_up(FewDev p) {
         int unit, ks, n;
         share(first, unit, ks, n);
         while (n > 0) {
-            const int blk = unit / NU, m = min(n, KS - ks);
+            const int blk = p.by_units(unit), m = min(n, KS - ks);
             int32_t (*a)[kChannels] = acc[buf][unit - first];
             auto row = [&](int i) -> uint32_t {
                 if (!LOCAL) return kWeightBytes + i * kDepth + l.of_row(i);
-                const int t = r.list[r.blk_first[blk] + i] / p.K;
+                const int t = p.by_k(r.list[r.blk_first[blk] + i]);
                 return smem_u32(codes) + (uint32_t)(t * pitch + ks * kDepth) + l.of_row(t);
             };
             auto add = [&](int i, int c, int32_t v) { atomicAdd(&a[i][c], v); };
@@ -368,22 +436,14 @@ k_few_gate_up(FewDev p) {
         if (eu < nu) {
             const int nr = r.blk_n[eblk];
             for (int row = er; row < nr; row += kUnitThreads / 8) {
-                const int route = r.list[r.blk_first[eblk] + row], t = route / p.K;
+                const int route = r.list[r.blk_first[eblk] + row], t = p.by_k(route);
                 int32_t *a = acc[buf][eu][row];
                 const float s1 = LOCAL ? __fdiv_rn(__uint_as_float(amax[t]), 127.0f) : p.qs[t];
                 const float ha = __fmul_rn(__fmul_rn(__int2float_rn(a[ej]), sa), s1);
                 const float hb = __fmul_rn(__fmul_rn(__int2float_rn(a[ej + 8]), sb), s1);
                 a[ej] = 0;
                 a[ej + 8] = 0;
-                const float v = __fmul_rn(tc::silu_f32(ha), hb);
-                p.g[(int64_t)route * p.Nh + ech] = v;
-                if (LOCAL) {
-                    float mx = fmaxf(0.0f, fabsf(v));
-                    const uint32_t eight = 0xffu << (lane & 24);   // the lanes of this unit and row
-#pragma unroll
-                    for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(eight, mx, o));
-                    if (ej == 0) p.gmax[(int64_t)route * NU + (ech >> 3)] = mx;
-                }
+                p.g[(int64_t)route * p.Nh + ech] = __fmul_rn(tc::silu_f32(ha), hb);
             }
         }
     }
@@ -391,27 +451,33 @@ k_few_gate_up(FewDev p) {
 }
 
 // ---------------------------------------------------------------- y = q2 . W2, out
-template <bool LOCAL>
-__global__ void __launch_bounds__(kThreads, 512 / kThreads)
+template <bool LOCAL, int D>
+__global__ void __launch_bounds__(Cfg<LOCAL>::kThreads, LOCAL ? 2 : 1)
 k_few_down(FewDev p) {
-    constexpr int kD = LOCAL ? kDepthLocal2 : kDepthRing;
-    constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : kRowBytes);
+    using C = Cfg<LOCAL, D>;
+    constexpr int kThreads = C::kThreads, kWarps = C::kWarps;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Routes r;
-    __shared__ float s2[kMaxRoutes];      // by place in the list
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float scale[kMaxRoutes];      // of g, by place in the list
+    __shared__ float probs[kMaxRoutes];
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int Nh = p.Nh, KS = (Nh + kDepth - 1) / kDepth, pitch = KS * kDepth;
     const Lane l;
-    uint8_t *codes = smem + (size_t)kWarps * kD * kBytes;
+    uint8_t *codes = smem + C::kRing;
     int32_t *acc = reinterpret_cast<int32_t *>(codes + (LOCAL ? (size_t)p.R * pitch : 0));   // [2][R][16]
 
     for (int i = tid; i < 2 * p.R * kChannels; i += kThreads) acc[i] = 0;
-    // ids, mask and weights were there before the kernel before this one began
-    find_routes(p, r);
+    clear_routes<kThreads>(p, r);
+    // ids, mask, weights and probs were there before the kernel before this one began
+    for (int i = tid; i < p.R; i += kThreads) probs[i] = p.probs[i];
+    find_routes<kThreads>(p, r);
     const int per_batch = r.blocks * KS;      // stages of 16 channels
     const int mine_a = per_batch * warp / kWarps, mine_n = per_batch * (warp + 1) / kWarps - mine_a;
+    const int mine_blk = p.by_stages2(mine_a), mine_ks = mine_a - mine_blk * KS;
     const int batches = p.H / kChannels;
 
+    const uint64_t once = l2_policy_evict_first();
+    auto copy_weights = [&](uint32_t dst, const void *src, bool in) { copy16_once(dst, src, in, once); };
     int f_batch = blockIdx.x, f_blk = 0, f_ks = 0, f_left = 0;
     const uint8_t *f_src = nullptr;
     const int8_t *f_row[2] = {nullptr, nullptr};
@@ -429,8 +495,8 @@ k_few_down(FewDev p) {
     };
     auto begin = [&]() {
         f_left = mine_n;
-        f_blk = mine_a / KS;
-        f_ks = mine_a % KS;
+        f_blk = mine_blk;
+        f_ks = mine_ks;
         if (f_left > 0) enter();
     };
     if (f_batch < batches) begin();
@@ -441,10 +507,10 @@ k_few_down(FewDev p) {
             begin();
         }
         const bool in = f_ks * kDepth + l.cu * 16 < Nh;
-        copy16(slot + l.to0, f_src, in);
-        copy16(slot + l.to1, f_src + (int64_t)4 * Nh, in);
-        copy16(slot + l.to0 + 8 * kDepth, f_src + (int64_t)8 * Nh, in);
-        copy16(slot + l.to1 + 8 * kDepth, f_src + (int64_t)12 * Nh, in);
+        copy_weights(slot + l.to0, f_src, in);
+        copy_weights(slot + l.to1, f_src + (int64_t)4 * Nh, in);
+        copy_weights(slot + l.to0 + 8 * kDepth, f_src + (int64_t)8 * Nh, in);
+        copy_weights(slot + l.to1 + 8 * kDepth, f_src + (int64_t)12 * Nh, in);
         f_src += kDepth;
         if (!LOCAL) {
             if (f_row[0]) {
@@ -463,43 +529,72 @@ k_few_down(FewDev p) {
             if (f_left > 0) enter();
         }
     };
-    Walk<kD, kBytes, LOCAL> walk(smem_u32(smem) + (uint32_t)(warp * kD * kBytes));
+    Walk<C::kD, C::kBytes, LOCAL> walk(smem_u32(smem) + (uint32_t)(warp * C::kD * C::kBytes));
     if (LOCAL) {
         walk.first(fetch);
         pdl_wait();
-        // the routes' codes: a row to a warp, or part of one where there are fewer
-        const int parts = r.rows > 0 ? max(1, kWarps / r.rows) : 1, n8 = Nh / 8;
-        for (int it = warp; it < r.rows * parts; it += kWarps) {
-            const int at = it / parts, part = it - at * parts;
-            const int route = r.list[at];
-            const float *gm = p.gmax + (int64_t)route * n8;
+        // the routes' codes, a row to a warp
+        const int n8 = Nh / 8;
+        for (int at = warp; at < r.rows; at += kWarps) {
+            const float4 *src = reinterpret_cast<const float4 *>(p.g + (int64_t)r.list[at] * Nh);
+            const int lane = tid & 31;
+            float4 v[kGVecs][2];
             float m = 0.0f;
-            for (int i = lane; i < n8; i += 32) m = fmaxf(m, __ldcg(gm + i));
+            for (int i0 = 0; i0 < n8; i0 += 32 * kGVecs) {
+#pragma unroll
+                for (int u = 0; u < kGVecs; ++u) {
+                    const int i = i0 + 32 * u + lane;
+                    v[u][0] = v[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i < n8) {
+                        v[u][0] = __ldcg(src + 2 * i);
+                        v[u][1] = __ldcg(src + 2 * i + 1);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kGVecs; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        m = fmaxf(fmaxf(m, fmaxf(fabsf(v[u][h].x), fabsf(v[u][h].y))),
+                                  fmaxf(fabsf(v[u][h].z), fabsf(v[u][h].w)));
+            }
             m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
             const float s = __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
-            if (lane == 0 && part == 0) s2[at] = s;
-            const float4 *src = reinterpret_cast<const float4 *>(p.g + (int64_t)route * Nh);
-            for (int i = part * 32 + lane; i < pitch / 8; i += 32 * parts) {
-                uint2 q = make_uint2(0, 0);
-                if (i < n8) {
-                    const float4 a = __ldcg(src + 2 * i), b = __ldcg(src + 2 * i + 1);
-                    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                    q = codes8(v, s, rs);
-                }
-                put_codes(codes, at, pitch, i, q);
+            if (lane == 0) scale[at] = s;
+            // the last vectors are still in registers: all of a row of up to 2048
+            const int last = (n8 - 1) / (32 * kGVecs) * (32 * kGVecs);
+#pragma unroll
+            for (int u = 0; u < kGVecs; ++u) {
+                const int i = last + 32 * u + lane;
+                const float f[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w,
+                                    v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
+                if (i < n8) put_codes(codes, at, pitch, i, codes8(f, s, rs));
+            }
+            for (int i = lane; i < last; i += 32) {
+                const float4 a = __ldcg(src + 2 * i), b = __ldcg(src + 2 * i + 1);
+                const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                put_codes(codes, at, pitch, i, codes8(f, s, rs));
             }
         }
     } else {
         pdl_wait();
         walk.first(fetch);
-        for (int i = tid; i < r.rows; i += kThreads) s2[i] = __ldcg(p.qs + r.list[i]);
+        for (int i = tid; i < r.rows; i += kThreads) scale[i] = __ldcg(p.qs + r.list[i]);
     }
     __syncthreads();
 
+    // what place `at` of the list multiplies its sums with
+    auto scale2_of = [&](int i, int batch) {
+        return __ldg(p.scale2 + (int64_t)r.code[r.list[i / kChannels]] * p.H + batch * kChannels + i % kChannels);
+    };
     int buf = 0;
+    const int outs = p.T * kChannels, sums = r.rows * kChannels;
     for (int batch = blockIdx.x; batch < batches; batch += gridDim.x, buf ^= 1) {
         int32_t *a = acc + (size_t)buf * p.R * kChannels;
-        int blk = mine_a / KS, ks = mine_a % KS, n = mine_n;
+        const float sc = tid < sums ? scale2_of(tid, batch) : 0.0f;   // on its way meanwhile
+        const float shared = p.shared && tid < outs
+                                 ? __bfloat162float(p.shared[(int64_t)(tid / kChannels) * p.H + batch * kChannels + tid % kChannels])
+                                 : 0.0f;
+        int blk = mine_blk, ks = mine_ks, n = mine_n;
         while (n > 0) {
             const int base = r.blk_first[blk], m = min(n, KS - ks);
             auto row = [&](int i) -> uint32_t {
@@ -513,27 +608,34 @@ k_few_down(FewDev p) {
             ++blk;
         }
         __syncthreads();
-        for (int i = tid; i < p.T * kChannels; i += kThreads) {
-            const int t = i / kChannels, c = i % kChannels, col = batch * kChannels + c;
-            const int64_t o = (int64_t)t * p.H + col;
+        // p * y of every route in the place of its sum, then the sum over a token's
+        // routes in slot order from +0, as the combine kernel forms it
+#pragma unroll 1
+        for (int i = tid; i < sums; i += kThreads) {
+            const int at = i / kChannels;
+            const float w2s = i == tid ? sc : scale2_of(i, batch);
+            const float y = __bfloat162float(
+                __float2bfloat16_rn(__fmul_rn(__fmul_rn(__int2float_rn(a[i]), w2s), scale[at])));
+            a[i] = __float_as_int(__fmul_rn(probs[r.list[at]], y));
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int i = tid; i < outs; i += kThreads) {
+            const int t = i / kChannels, c = i % kChannels;
+            const int64_t o = (int64_t)t * p.H + batch * kChannels + c;
             float v = 0.0f;
-            for (int k = 0; k < p.K; ++k) {
-                const int route = t * p.K + k, code = r.code[route];
-                if (code == -1) continue;
-                float y = 0.0f;
+            for (int route = t * p.K; route < (t + 1) * p.K; ++route) {
+                const int code = r.code[route];
                 if (code >= 0) {
-                    const int at = r.place[route];
-                    int32_t *s = a + at * kChannels + c;
-                    const float sc = __ldg(p.scale2 + (int64_t)code * p.H + col);
-                    y = __bfloat162float(
-                        __float2bfloat16_rn(__fmul_rn(__fmul_rn(__int2float_rn(*s), sc), s2[at])));
+                    int32_t *s = a + r.place[route] * kChannels + c;
+                    v = __fadd_rn(v, __int_as_float(*s));
                     *s = 0;
-                } else if (code == -3) {
-                    y = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.x)[o]);
+                } else if (code != -1) {
+                    const float x = code == -3 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p.x)[o]) : 0.0f;
+                    v = __fadd_rn(v, __fmul_rn(probs[route], x));
                 }
-                v = __fadd_rn(v, __fmul_rn(__ldg(p.probs + route), y));
             }
-            if (p.shared) v = __fadd_rn(v, __bfloat162float(p.shared[o]));
+            if (p.shared) v = __fadd_rn(v, i == tid ? shared : __bfloat162float(p.shared[o]));
             p.out[o] = __float2bfloat16_rn(v);
         }
     }
@@ -542,9 +644,9 @@ k_few_down(FewDev p) {
 // ---------------------------------------------------------------- codes of rows, once for all CTAs
 // bf16 or fp32 rows -> int8 codes and scales, a CTA a row.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kQuantThreads)
 k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, float *__restrict__ s_out) {
-    __shared__ float part[kWarps];
+    __shared__ float part[kQuantThreads / 32];
     pdl_wait();
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
@@ -560,7 +662,7 @@ k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, fl
         }
     };
     float m = 0.0f;
-    for (int i = tid; i < n8; i += kThreads) {
+    for (int i = tid; i < n8; i += kQuantThreads) {
         float v[8];
         load(i, v);
         m = max8(v, m);
@@ -569,9 +671,9 @@ k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, fl
     if ((tid & 31) == 0) part[tid >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, part[w]);
+    for (int w = 0; w < kQuantThreads / 32; ++w) m = fmaxf(m, part[w]);
     const float s = __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
-    for (int i = tid; i < n8; i += kThreads) {
+    for (int i = tid; i < n8; i += kQuantThreads) {
         float v[8];
         load(i, v);
         reinterpret_cast<uint2 *>(q + row * n)[i] = codes8(v, s, rs);
@@ -584,18 +686,46 @@ k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, fl
 moe_status launch_quant_rows_i8(const void *src, bool bf16, int64_t rows, int64_t n, int8_t *q,
                                 float *scales, cudaStream_t stream) {
     if (bf16) {
-        MOE_LAUNCH("quant_rows_i8", k_quant_rows_i8<__nv_bfloat16>, (unsigned)rows, kThreads, 0, stream,
+        MOE_LAUNCH("quant_rows_i8", k_quant_rows_i8<__nv_bfloat16>, (unsigned)rows, kQuantThreads, 0, stream,
                    static_cast<const __nv_bfloat16 *>(src), n, q, scales);
     } else {
-        MOE_LAUNCH("quant_rows_i8", k_quant_rows_i8<float>, (unsigned)rows, kThreads, 0, stream,
+        MOE_LAUNCH("quant_rows_i8", k_quant_rows_i8<float>, (unsigned)rows, kQuantThreads, 0, stream,
                    static_cast<const float *>(src), n, q, scales);
     }
     return MOE_OK;
 }
 
-// The codes that each kernel's CTAs would hold themselves.
+// Whether each kernel's CTAs hold all codes themselves.  Measured (us, one against
+// the other):
 static bool few_tokens_local(int64_t T, int64_t K, int64_t H, int64_t Nh) {
-    return T * padded((int)H) <= (int64_t)kLocalBytes && T * K * padded((int)Nh) <= (int64_t)kLocalBytes;
+    constexpr int kWarps = Cfg<true>::kWarps;
+    return T <= kWarps && (H / 8 + 31) / 32 <= kXVecs * (kWarps / T) && T * K * Nh <= 16384;
+}
+
+// extra1, extra2: shared memory of the two kernels beside their rings.
+template <bool LOCAL, int D>
+static moe_status launch_both(FewDev p, unsigned grid1, unsigned grid2, size_t extra1, size_t extra2,
+                              const FewTokensArgs &a, cudaStream_t stream) {
+    using C = Cfg<LOCAL, D>;
+    auto up = k_few_gate_up<LOCAL, D>;
+    auto down = k_few_down<LOCAL, D>;
+    if (!set_smem_limit((const void *)up, C::kRing + extra1) ||
+        !set_smem_limit((const void *)down, C::kRing + extra2))
+        return MOE_ERR_CUDA;
+    if (!LOCAL) {
+        MOE_TRY(launch_quant_rows_i8(a.x, true, p.T, p.H, a.q, a.qs, stream));
+        p.q = a.q;
+        p.qs = a.qs;
+    }
+    MOE_LAUNCH("few_gate_up", up, grid1, C::kThreads, C::kRing + extra1, stream, p);
+    if (!LOCAL) {
+        int8_t *q2 = a.q + align_up((size_t)p.T * p.H, kAlign);
+        MOE_TRY(launch_quant_rows_i8(a.g, false, p.R, p.Nh, q2, a.qs + p.T, stream));
+        p.q = q2;
+        p.qs = a.qs + p.T;
+    }
+    MOE_LAUNCH("few_down", down, grid2, C::kThreads, C::kRing + extra2, stream, p);
+    return MOE_OK;
 }
 
 moe_status launch_layer_few_tokens(const moe_shape &s, const FewTokensArgs &a, cudaStream_t stream) {
@@ -612,7 +742,6 @@ moe_status launch_layer_few_tokens(const moe_shape &s, const FewTokensArgs &a, c
     p.scale2 = a.scale2;
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.g = a.g;
-    p.gmax = a.gmax;
     p.q = nullptr;
     p.qs = nullptr;
     p.status = a.status;
@@ -625,34 +754,19 @@ moe_status launch_layer_few_tokens(const moe_shape &s, const FewTokensArgs &a, c
     p.H = (int)H;
     p.Nh = (int)Nh;
     p.mask_kind = s.mask_kind;
+    p.by_k = Divisor((uint32_t)K);
+    p.by_units = Divisor((uint32_t)(Nh / 8));
+    p.by_stages1 = Divisor((uint32_t)(padded((int)H) / kDepth));
+    p.by_stages2 = Divisor((uint32_t)(padded((int)Nh) / kDepth));
     const unsigned sms = (unsigned)num_sms();
     const unsigned grid1 = (unsigned)std::min<int64_t>(sms, R * (Nh / 8));
     const unsigned grid2 = (unsigned)std::min<int64_t>(sms, H / kChannels);
     const size_t acc2 = (size_t)2 * R * kChannels * sizeof(int32_t);
-    if (few_tokens_local(T, K, H, Nh)) {
-        const size_t smem1 = (size_t)kWarps * kDepthLocal * kWeightBytes + (size_t)T * padded((int)H);
-        const size_t smem2 = (size_t)kWarps * kDepthLocal2 * kWeightBytes + (size_t)R * padded((int)Nh) + acc2;
-        if (!set_smem_limit((const void *)k_few_gate_up<true>, smem1) ||
-            !set_smem_limit((const void *)k_few_down<true>, smem2))
-            return MOE_ERR_CUDA;
-        MOE_LAUNCH("few_gate_up", k_few_gate_up<true>, grid1, kThreads, smem1, stream, p);
-        MOE_LAUNCH("few_down", k_few_down<true>, grid2, kThreads, smem2, stream, p);
-        return MOE_OK;
-    }
-    const size_t ring = (size_t)kWarps * kDepthRing * (kWeightBytes + kRowBytes);
-    if (!set_smem_limit((const void *)k_few_gate_up<false>, ring) ||
-        !set_smem_limit((const void *)k_few_down<false>, ring + acc2))
-        return MOE_ERR_CUDA;
-    MOE_TRY(launch_quant_rows_i8(a.x, true, T, H, a.q, a.qs, stream));
-    p.q = a.q;
-    p.qs = a.qs;
-    MOE_LAUNCH("few_gate_up", k_few_gate_up<false>, grid1, kThreads, ring, stream, p);
-    int8_t *q2 = a.q + align_up((size_t)(T * H), kAlign);
-    MOE_TRY(launch_quant_rows_i8(a.g, false, R, Nh, q2, a.qs + T, stream));
-    p.q = q2;
-    p.qs = a.qs + T;
-    MOE_LAUNCH("few_down", k_few_down<false>, grid2, kThreads, ring + acc2, stream, p);
-    return MOE_OK;
+    if (few_tokens_local(T, K, H, Nh))
+        return launch_both<true, 5>(p, grid1, grid2, (size_t)T * padded((int)H),
+                                    (size_t)R * padded((int)Nh) + acc2, a, stream);
+    return R <= kDeepRoutes ? launch_both<false, 5>(p, grid1, grid2, 0, acc2, a, stream)
+                            : launch_both<false, 4>(p, grid1, grid2, 0, acc2, a, stream);
 }
 
 }  // namespace moe

@@ -22,11 +22,6 @@
 namespace moe {
 namespace si8 {
 
-#ifndef MOE_W
-#define MOE_W 16
-#endif
-constexpr int kWarps = MOE_W;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kChannels = 16;                      // output channels of a stage
 constexpr int kDepth = 128;                        // its share of the inner dimension
 constexpr int kWeightBytes = kChannels * kDepth;
@@ -38,6 +33,14 @@ constexpr int kExactStages = 1024 / kDepth;        // stages that an fp32 sum ho
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(on ? 16u : 0u)
+                 : "memory");
+}
+// The same for bytes that are read once: they leave L2 before anything else does, so
+// that a call's stream of weights does not push out what every call needs again (the
+// kernels' instructions, scales, the next call's inputs).
+__device__ __forceinline__ void copy16_once(uint32_t dst, const void *src, bool on, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+                 "r"(on ? 16u : 0u), "l"(policy)
                  : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -144,45 +147,34 @@ struct Sums {
 // The same products for NR <= 4 rows with dp4a, on the integer pipe (64 lanes a
 // clock of an SM): 16 instructions a row and stage, against the 104 that the widening
 // and the mma take whatever the rows (even at about five).  Lane (g, t) adds
-// bytes [32 t, 32 t + 32) of channels g and g + 8; join() adds the four lanes.
-// row[n]: the lane's first 16 bytes of row n at this stage.
+// bytes [32 t, 32 t + 32) of channels g and g + 8.
 template <int NR>
-struct Dots {
-    int32_t acc[2][NR];
-
-    __device__ __forceinline__ void clear() {
+__device__ __forceinline__ void dot_stage(int32_t (&acc)[NR][2], uint32_t at, const uint32_t (&row)[NR]) {
 #pragma unroll
-        for (int n = 0; n < NR; ++n) acc[0][n] = acc[1][n] = 0;
-    }
-    __device__ __forceinline__ void add_stage(uint32_t at, const uint32_t (&row)[NR]) {
+    for (int h = 0; h < 2; ++h) {
+        const uint4 wa = lds16(at ^ (h << 4)), wb = lds16((at ^ (h << 4)) + 8 * kDepth);
+        const uint32_t a[4] = {wa.x ^ 0x80808080u, wa.y ^ 0x80808080u, wa.z ^ 0x80808080u,
+                               wa.w ^ 0x80808080u};
+        const uint32_t b[4] = {wb.x ^ 0x80808080u, wb.y ^ 0x80808080u, wb.z ^ 0x80808080u,
+                               wb.w ^ 0x80808080u};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint4 wa = lds16(at ^ (h << 4)), wb = lds16((at ^ (h << 4)) + 8 * kDepth);
-            const uint32_t a[4] = {wa.x ^ 0x80808080u, wa.y ^ 0x80808080u, wa.z ^ 0x80808080u,
-                                   wa.w ^ 0x80808080u};
-            const uint32_t b[4] = {wb.x ^ 0x80808080u, wb.y ^ 0x80808080u, wb.z ^ 0x80808080u,
-                                   wb.w ^ 0x80808080u};
+        for (int n = 0; n < NR; ++n) {
+            const uint4 x = lds16(row[n] ^ (h << 4));
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                const uint4 x = lds16(row[n] ^ (h << 4));
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[0][n] = __dp4a((int)a[i], (int)xs[i], acc[0][n]);
-                    acc[1][n] = __dp4a((int)b[i], (int)xs[i], acc[1][n]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                acc[n][0] = __dp4a((int)a[i], (int)xs[i], acc[n][0]);
+                acc[n][1] = __dp4a((int)b[i], (int)xs[i], acc[n][1]);
             }
         }
     }
-    __device__ __forceinline__ void join() {
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                acc[c][n] += __shfl_xor_sync(0xffffffffu, acc[c][n], 1);
-                acc[c][n] += __shfl_xor_sync(0xffffffffu, acc[c][n], 2);
-            }
-    }
+}
+
+// Quotients by a divisor that is the same all over a launch, a * d < 2^32.
+struct Divisor {
+    uint32_t d, m;
+    __host__ explicit Divisor(uint32_t by = 1) : d(by), m(by > 1 ? (uint32_t)(0x100000000ull / by) + 1 : 0) {}
+    __device__ __forceinline__ int operator()(int a) const { return m ? (int)__umulhi((uint32_t)a, m) : a; }
 };
 
 // What the lanes of a warp need to fetch and find their parts of a stage.
@@ -234,11 +226,13 @@ struct Walk {
     }
     template <int NR, typename Fetch, typename Row, typename Add>
     __device__ __forceinline__ void dots(const Lane &l, int stages, Fetch &fetch, Row &row, Add &add) {
-        Dots<NR> d;
-        d.clear();
+        int32_t acc[NR][2];
         uint32_t r[NR];
 #pragma unroll
-        for (int n = 0; n < NR; ++n) r[n] = row(n);
+        for (int n = 0; n < NR; ++n) {
+            acc[n][0] = acc[n][1] = 0;
+            r[n] = row(n);
+        }
 #pragma unroll 1
         for (int i = 0; i < stages; ++i) {
             const uint32_t st = next(fetch);
@@ -248,19 +242,25 @@ struct Walk {
                 at[n] = LOCAL ? r[n] : st + r[n];
                 if (LOCAL) r[n] += kDepth;
             }
-            d.add_stage(st + l.from, at);
+            dot_stage<NR>(acc, st + l.from, at);
         }
-        d.join();
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
-            if (n == l.t) {
-                add(n, l.g, d.acc[0][n]);
-                add(n, l.g + 8, d.acc[1][n]);
+        for (int n = 0; n < NR; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                acc[n][c] += __shfl_xor_sync(0xffffffffu, acc[n][c], 1);
+                acc[n][c] += __shfl_xor_sync(0xffffffffu, acc[n][c], 2);
             }
+            if (n == l.t) {
+                add(n, l.g, acc[n][0]);
+                add(n, l.g + 8, acc[n][1]);
+            }
+        }
     }
     // `stages` stages of one unit with nr rows.  row(n): the lane's first bytes of
     // row n (LOCAL: at the first stage; else in the slot); add(n, c, v) takes the
     // sum of row n and channel c (0 .. 15), from one lane each.
+    // (One loop that branches on nr inside measured 4 to 8 % slower.)
     template <typename Fetch, typename Row, typename Add>
     __device__ __forceinline__ void run(const Lane &l, int stages, int nr, Fetch &fetch, Row &row, Add &add) {
         if (nr == 1) {
