@@ -41,6 +41,8 @@ EXPORTED = [
     "moe_grouped_gemm_fp8_workspace_size", "moe_grouped_gemm_fp8",
     "moe_grouped_ffn_fp8_workspace_size", "moe_grouped_ffn_fp8",
     "moe_layer_few_tokens_workspace_size", "moe_layer_few_tokens",
+    "moe_int8_packed_bytes", "moe_pack_int8",
+    "moe_grouped_gemm_int8_workspace_size", "moe_grouped_gemm_int8",
 ]
 
 
@@ -76,7 +78,7 @@ class MoeGateDesc(ctypes.Structure):
 
 GATE_SCORES = {"softmax": 0, "sigmoid": 1}
 GATE_GROUP_SCORES = {"max": 0, "top2": 1}
-DTYPE_F32, DTYPE_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_I8 = 0, 1, 2
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
 
@@ -129,6 +131,11 @@ def lib():
         "moe_grouped_ffn_fp8": [SP, P, P, P, P, P, P, P, P, P, P, SZ, P],
         "moe_layer_few_tokens_workspace_size": [SP, ctypes.POINTER(SZ)],
         "moe_layer_few_tokens": [SP, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
+        "moe_int8_packed_bytes": [I64, I64, I64, ctypes.c_int, ctypes.POINTER(SZ)],
+        "moe_pack_int8": [I64, I64, I64, ctypes.c_int, P, P, P],
+        "moe_grouped_gemm_int8_workspace_size": [I64, I64, I64, I64, ctypes.POINTER(SZ)],
+        "moe_grouped_gemm_int8": [I64, I64, I64, I64, P, P, ctypes.c_int, P, P, P, P, P,
+                                  ctypes.c_int, ctypes.c_int, P, SZ, P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -532,6 +539,65 @@ def grouped_gemm_s32(expert_offsets, A, W, ws=None, C=None, stream=None, path="a
     _call("moe_grouped_gemm_s32", rows, E, N, Kd, _ptr(expert_offsets), _ptr(A), _ptr(W), _ptr(C),
           FFN_PATHS[path], _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(stream))
     return C, ws
+
+
+def int8_packed_bytes(E, N, Kd, path="auto") -> int:
+    n = ctypes.c_size_t()
+    _call("moe_int8_packed_bytes", E, N, Kd, FFN_PATHS[path], ctypes.byref(n))
+    return n.value
+
+
+def pack_int8(w, path="auto", stream=None):
+    """moe_pack_int8: int8 w [E, N, Kd] -> (owner, packed) for
+    :func:`grouped_gemm_int8` with the same path."""
+    E, N, Kd = w.shape
+    dev = w.get_device()
+    _check(w, torch.int8, (E, N, Kd), "w", dev)
+    owner, packed = _alloc_ws(int8_packed_bytes(E, N, Kd, path), w.device)
+    _call("moe_pack_int8", E, N, Kd, FFN_PATHS[path], w.data_ptr(), packed.data_ptr(),
+          _raw_stream(stream, dev))
+    return owner, packed
+
+
+def grouped_gemm_int8(expert_offsets, a, w_packed, w_scales, a_scales=None, bias=None, ws=None,
+                      out=None, out_dtype=torch.bfloat16, stream=None, path="auto"):
+    """moe_grouped_gemm_int8: rows of group e times w[e]^T in 8-bit integers.  a:
+    int8 [rows, Kd] with a_scales fp32 [rows], or bf16 [rows, Kd], quantised per
+    row in the call; w_packed from :func:`pack_int8` with the same path; w_scales
+    (and bias) fp32 [E, N].  Returns (out [rows, N], workspace); `out`'s dtype (or
+    out_dtype) is bfloat16 or float32."""
+    rows, Kd = a.shape
+    E, N = w_scales.shape
+    dev = a.get_device()
+    if a.dtype is torch.bfloat16:
+        if a_scales is not None:
+            raise ValueError("a_scales: bf16 rows are quantised in the call")
+        a_dtype = DTYPE_BF16
+    else:
+        if a_scales is None:
+            raise ValueError("a_scales: int8 rows need their scales")
+        a_dtype = DTYPE_I8
+        _check(a_scales, torch.float32, (rows,), "a_scales", dev)
+    _check(a, torch.bfloat16 if a_dtype == DTYPE_BF16 else torch.int8, (rows, Kd), "a", dev)
+    _check(w_scales, torch.float32, (E, N), "w_scales", dev)
+    _check(bias, torch.float32, (E, N), "bias", dev)
+    _check(expert_offsets, torch.int32, (E + 1,), "expert_offsets", dev)
+    _check(w_packed, torch.uint8, (int8_packed_bytes(E, N, Kd, path),), "w_packed", dev)
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=a.device)
+    if out.dtype not in _DTYPES:
+        raise TypeError(f"out: dtype {out.dtype}, expected float32 or bfloat16")
+    _check(out, out.dtype, (rows, N), "out", dev)
+    if ws is None:
+        n = ctypes.c_size_t()
+        _call("moe_grouped_gemm_int8_workspace_size", rows, E, N, Kd, ctypes.byref(n))
+        _, ws = _alloc_ws(n.value, a.device)
+    if ws.get_device() != dev:
+        _check_device(ws, "ws", dev)
+    _call("moe_grouped_gemm_int8", rows, E, N, Kd, expert_offsets.data_ptr(), a.data_ptr(), a_dtype,
+          _addr(a_scales), w_packed.data_ptr(), w_scales.data_ptr(), _addr(bias), out.data_ptr(),
+          _DTYPES[out.dtype], FFN_PATHS[path], ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    return out, ws
 
 
 # ----------------------------------------------------------------- fp8 expert path

@@ -2,6 +2,8 @@
 // (include/moe_gb300.h): argument checks, workspace layout and the order of kernels.
 #include "common.cuh"
 
+#include <algorithm>
+
 namespace moe {
 namespace {
 
@@ -43,6 +45,66 @@ moe_status check_few(const moe_shape *shape) {
     if (shape->ffn_path != MOE_FFN_PATH_SMALL && shape->ffn_path != MOE_FFN_PATH_AUTO)
         return MOE_FAIL(MOE_ERR_PARAM_INVALID);
     return MOE_OK;
+}
+
+// ---------------------------------------------------------------- product with token and channel scales
+bool valid_path(int path) { return path >= MOE_FFN_PATH_AUTO && path <= MOE_FFN_PATH_LARGE_PAIR; }
+bool has_images(int path) { return path != MOE_FFN_PATH_SMALL; }
+bool has_bytes(int path) { return path == MOE_FFN_PATH_SMALL || path == MOE_FFN_PATH_AUTO; }
+size_t image_bytes(int64_t E, int64_t N, int64_t Kd) { return align_up((size_t)E * N * Kd * 2, kAlign); }
+
+moe_status check_int8(int64_t E, int64_t N, int64_t Kd) {
+    if (E < 1 || E > kMaxExperts || N < 8 || N % 8 != 0 || N > (1 << 20) || Kd < 16 || Kd % 16 != 0 ||
+        Kd > 131072)
+        return MOE_FAIL(MOE_ERR_SHAPE);
+    return MOE_OK;
+}
+
+// How a call multiplies.
+enum class How { Stream, Tiles, Large };
+#ifndef MOE_STREAM_ROWS
+#define MOE_STREAM_ROWS 32
+#endif
+#ifndef MOE_TILE_ROWS
+#define MOE_TILE_ROWS 128
+#endif
+How how(int path, int64_t rows, int64_t E) {
+    if (path == MOE_FFN_PATH_LARGE || path == MOE_FFN_PATH_LARGE_PAIR) return How::Large;
+    if (rows <= MOE_STREAM_ROWS * E) return How::Stream;
+    return path == MOE_FFN_PATH_SMALL || rows <= MOE_TILE_ROWS * E ? How::Tiles : How::Large;
+}
+
+// CTAs that share a tile's inner dimension where the tiles are too few for the GPU.
+constexpr int kMaxSplits = 8;
+struct Split {
+    int64_t tiles;
+    int splits;
+};
+Split split_of(int64_t rows, int64_t E, int64_t N, int64_t Kd) {
+    const int64_t tb = rows > 32 * E ? 128 : 64;
+    Split s;
+    s.tiles = (rows / tb + std::min(E, rows)) * ((N + 127) / 128);   // at most
+    const int64_t likely = std::max<int64_t>(1, (rows + tb - 1) / tb) * ((N + 127) / 128);
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)num_sms() / std::max<int64_t>(1, likely),
+                                                           Kd / 512, kMaxSplits}));
+    return s;
+}
+
+struct Int8Layout {
+    size_t status, sched, rows, scales, arrived, partial, total;
+};
+Int8Layout int8_layout(int64_t rows, int64_t E, int64_t N, int64_t Kd, const Split &sp) {
+    Int8Layout L;
+    Carve c;
+    const int64_t tb = rows > 32 * E ? 128 : 64;
+    L.status = c.take(4);
+    L.sched = c.take((size_t)(E + 1) * sizeof(int32_t));
+    L.rows = c.take((size_t)rows * Kd * 2);
+    L.scales = c.take((size_t)rows * sizeof(float));
+    L.arrived = c.take(sp.splits > 1 ? (size_t)sp.tiles * 8 * sizeof(uint32_t) : 0);
+    L.partial = c.take(sp.splits > 1 ? (size_t)sp.tiles * sp.splits * tb * 128 * sizeof(int32_t) : 0);
+    L.total = c.off;
+    return L;
 }
 
 }  // namespace
@@ -98,6 +160,119 @@ moe_status moe_layer_few_tokens(const moe_shape *shape, const void *x, const int
     a.qs = at<float>(workspace, L.qs);
     a.status = at<int32_t>(workspace, L.status);
     return launch_layer_few_tokens(s, a, stream);
+}
+
+moe_status moe_int8_packed_bytes(int64_t E, int64_t N, int64_t Kd, int path, size_t *bytes) {
+    if (!bytes) return MOE_FAIL(MOE_ERR_NULLPTR);
+    MOE_TRY(check_int8(E, N, Kd));
+    if (!valid_path(path)) return MOE_FAIL(MOE_ERR_PARAM_INVALID);
+    *bytes = (has_images(path) ? image_bytes(E, N, Kd) : 0) + (has_bytes(path) ? (size_t)E * N * Kd : 0);
+    return MOE_OK;
+}
+
+moe_status moe_pack_int8(int64_t E, int64_t N, int64_t Kd, int path, const int8_t *w, void *w_packed,
+                         cudaStream_t stream) {
+    MOE_TRY(check_int8(E, N, Kd));
+    if (!valid_path(path)) return MOE_FAIL(MOE_ERR_PARAM_INVALID);
+    if (!w || !w_packed) return MOE_FAIL(MOE_ERR_NULLPTR);
+    if (!aligned(w, 16) || !aligned(w_packed, kAlign)) return MOE_FAIL(MOE_ERR_ALIGNMENT);
+    if (has_images(path)) MOE_TRY(launch_i8_to_f16(w, w_packed, E * N * Kd, stream));
+    if (has_bytes(path))
+        MOE_TRY(launch_bias_i8(w, static_cast<uint8_t *>(w_packed) + (has_images(path) ? image_bytes(E, N, Kd) : 0),
+                               E * N * Kd, stream));
+    return MOE_OK;
+}
+
+moe_status moe_grouped_gemm_int8_workspace_size(int64_t rows, int64_t E, int64_t N, int64_t Kd,
+                                                size_t *bytes) {
+    if (!bytes) return MOE_FAIL(MOE_ERR_NULLPTR);
+    MOE_TRY(check_int8(E, N, Kd));
+    if (rows < 0 || rows > INT32_MAX || rows * Kd >= (int64_t)1 << 40) return MOE_FAIL(MOE_ERR_SHAPE);
+    *bytes = int8_layout(rows, E, N, Kd, split_of(rows, E, N, Kd)).total;
+    return MOE_OK;
+}
+
+moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
+                                 const int32_t *expert_offsets, const void *A, int a_dtype,
+                                 const float *a_scales, const void *w_packed,
+                                 const float *w_scales, const float *bias, void *C, int out_dtype,
+                                 int path, void *workspace, size_t workspace_bytes,
+                                 cudaStream_t stream) {
+    size_t need = 0;
+    MOE_TRY(moe_grouped_gemm_int8_workspace_size(rows, E, N, Kd, &need));
+    if ((a_dtype != MOE_DTYPE_BF16 && a_dtype != MOE_DTYPE_I8) ||
+        (out_dtype != MOE_DTYPE_F32 && out_dtype != MOE_DTYPE_BF16) || !valid_path(path))
+        return MOE_FAIL(MOE_ERR_PARAM_INVALID);
+    const bool bf16 = a_dtype == MOE_DTYPE_BF16, empty = rows == 0;
+    if (bf16 && a_scales) return MOE_FAIL(MOE_ERR_PARAM_INVALID);
+    if (!expert_offsets || !w_packed || !w_scales || !workspace) return MOE_FAIL(MOE_ERR_NULLPTR);
+    if (!empty && (!A || !C || (!bf16 && !a_scales))) return MOE_FAIL(MOE_ERR_NULLPTR);
+    // fp32 rows of C are stored 32 bytes at a time, the scales read 16
+    if (!aligned(A, 16) || !aligned(C, out_dtype == MOE_DTYPE_F32 ? 32 : 16) || !aligned(a_scales, 4) ||
+        !aligned(w_scales, 16) || !aligned(bias, 16) || !aligned(expert_offsets, 4) ||
+        !aligned(w_packed, kAlign) || !aligned(workspace, kAlign))
+        return MOE_FAIL(MOE_ERR_ALIGNMENT);
+    if (workspace_bytes < need) return MOE_FAIL(MOE_ERR_WORKSPACE);
+    if (empty) return MOE_OK;
+    const Split sp = split_of(rows, E, N, Kd);
+    const Int8Layout L = int8_layout(rows, E, N, Kd, sp);
+    int32_t *status = at<int32_t>(workspace, L.status);
+    const How way = how(path, rows, E);
+    const uint8_t *bytes = static_cast<const uint8_t *>(w_packed) + (has_images(path) ? image_bytes(E, N, Kd) : 0);
+    if (way == How::Stream) {
+        Int8FewArgs f{};
+        f.rows = A;
+        f.rows_bf16 = bf16;
+        f.row_scales = a_scales;
+        f.offsets = expert_offsets;
+        f.cap_rows = rows;
+        f.E = E;
+        f.N = N;
+        f.Kd = Kd;
+        f.w = bytes;
+        f.w_scales = w_scales;
+        f.bias = bias;
+        f.c = C;
+        f.out_bf16 = out_dtype == MOE_DTYPE_BF16;
+        f.status = status;
+        if (bf16 && !int8_few_local(rows, E, Kd)) {
+            MOE_TRY(launch_quant_rows_i8(A, true, rows, Kd, at<int8_t>(workspace, L.rows),
+                                         at<float>(workspace, L.scales), stream));
+            f.rows = at<void>(workspace, L.rows);
+            f.row_scales = at<float>(workspace, L.scales);
+            f.rows_bf16 = false;
+        }
+        return launch_int8_few(f, stream);
+    }
+    const bool split = way == How::Tiles && sp.splits > 1;
+    MOE_TRY(launch_rows_to_f16(A, bf16, a_scales, expert_offsets, E, rows, Kd, at<void>(workspace, L.rows),
+                               at<float>(workspace, L.scales), status, at<uint32_t>(workspace, L.arrived),
+                               split ? sp.tiles * 8 : 0, stream));
+    GemmArgs g{};
+    g.a_img = at<void>(workspace, L.rows);
+    g.cap_rows = rows;
+    g.b_img = way == How::Large ? w_packed : bytes;
+    g.E = E;
+    g.Nout = N;
+    g.Kd = Kd;
+    g.offsets = expert_offsets;
+    g.sched = at<int32_t>(workspace, L.sched);
+    g.y = C;
+    g.y_f32 = out_dtype == MOE_DTYPE_F32;
+    g.scale2 = w_scales;
+    g.s2 = at<float>(workspace, L.scales);
+    g.bias = bias;
+    g.status = status;
+    if (way == How::Tiles) {
+        g.splits = split ? sp.splits : 1;
+        g.partial = at<int32_t>(workspace, L.partial);
+        g.arrived = at<uint32_t>(workspace, L.arrived);
+        return launch_grouped_gemm_small(Epi::Linear, g, stream);
+    }
+    const bool pair = path != MOE_FFN_PATH_LARGE && linear_pairs_fit();
+    // the one-SM kernel takes its schedule from memory (which clears the status word again)
+    if (!pair) MOE_TRY(launch_sched(expert_offsets, E, at<int32_t>(workspace, L.sched), status, stream));
+    return launch_grouped_gemm(Epi::Linear, g, stream, pair);
 }
 
 }  // extern "C"

@@ -295,7 +295,7 @@ moe_status launch_pack_w1_i8(const int8_t *w1, void *w1p, int64_t E, int64_t N, 
 moe_status launch_bias_i8(const int8_t *src, void *dst, int64_t n, cudaStream_t stream);
 
 // Grouped GEMM on fp16 images of int8 operands (tcgen05, TMEM accumulators).
-enum class Epi { S32 = 0, SwiGLU = 1, DequantBF16 = 2 };
+enum class Epi { S32 = 0, SwiGLU = 1, DequantBF16 = 2, Linear = 3 };
 struct GemmArgs {
     const void *a_img;        // fp16 [cap_rows, Kd]
     int64_t cap_rows;
@@ -312,11 +312,21 @@ struct GemmArgs {
     const float *scale2;      // [E, Nout]
     const float *s2;          // [cap_rows]
     int32_t *status;
+    // Linear: y = (acc * scale2[e, n]) * s2[row] + bias[e, n], bf16 or fp32
+    const float *bias;        // [E, Nout] or NULL
+    bool y_f32;
+    // the int8-weight GEMM on a grid too small for the GPU: `splits` CTAs share a
+    // tile's inner dimension (Linear only)
+    int splits;               // 0 or 1: none
+    int32_t *partial;         // [tiles, splits, tile] sums
+    uint32_t *arrived;        // [tiles, 8], cleared before the call
 };
 // pair: 256-row tiles on clusters of two CTAs (falls back to one-SM tiles when
 // no cluster of that kernel fits).
 moe_status launch_grouped_gemm(Epi epi, const GemmArgs &a, cudaStream_t stream,
                                bool pair = false);
+// Whether the Linear epilogue's pair kernel runs here; it needs no `sched`.
+bool linear_pairs_fit();
 // The same GEMM for few rows per expert: the weights stream as biased bytes
 // (b_img, w + 128; W1 in launch_pack_w1_i8's row order), are widened on chip
 // into tensor memory and are the MMA's M side; the expert's rows are its N
@@ -343,6 +353,28 @@ struct FewTokensArgs {
     float *qs;                 // [T + T*K]
     int32_t *status;
 };
+// Product with few rows a group, the weights (biased bytes, [E, N, Kd]) streamed
+// per warp.  rows: bf16 [cap_rows, Kd] to be quantised (only where int8_few_local()),
+// or int8 with scales.
+struct Int8FewArgs {
+    const void *rows;
+    bool rows_bf16;
+    const float *row_scales;
+    const int32_t *offsets;    // [E+1]; rows >= cap_rows are never stored
+    int64_t cap_rows, E, N, Kd;
+    const void *w;
+    const float *w_scales, *bias;   // [E, N]; bias may be NULL
+    void *c;                   // [cap_rows, N]
+    bool out_bf16;
+    int32_t *status;           // cleared
+};
+bool int8_few_local(int64_t rows, int64_t E, int64_t Kd);
+moe_status launch_int8_few(const Int8FewArgs &a, cudaStream_t stream);
+// bf16 rows quantised, or int8 rows as they are -> fp16 images and scales; clears
+// the status word and `clear` (n_clear words).
+moe_status launch_rows_to_f16(const void *rows, bool bf16, const float *scales, const int32_t *offsets,
+                              int64_t E, int64_t cap_rows, int64_t Kd, void *img, float *img_scales,
+                              int32_t *status, uint32_t *clear, int64_t n_clear, cudaStream_t stream);
 moe_status launch_layer_few_tokens(const moe_shape &s, const FewTokensArgs &a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- fp8 expert path

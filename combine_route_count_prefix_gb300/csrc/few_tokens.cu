@@ -427,7 +427,7 @@ k_few_gate_up(FewDev p) {
                 return smem_u32(codes) + (uint32_t)(t * pitch + ks * kDepth) + l.of_row(t);
             };
             auto add = [&](int i, int c, int32_t v) { atomicAdd(&a[i][c], v); };
-            walk.run(l, m, r.blk_n[blk], fetch, row, add);
+            walk.template run<1>(l, m, r.blk_n[blk], fetch, row, add);
             n -= m;
             ks = 0;
             ++unit;
@@ -602,7 +602,7 @@ k_few_down(FewDev p) {
                 return smem_u32(codes) + (uint32_t)((base + i) * pitch + ks * kDepth) + l.of_row(base + i);
             };
             auto add = [&](int i, int c, int32_t v) { atomicAdd(&a[(base + i) * kChannels + c], v); };
-            walk.run(l, m, r.blk_n[blk], fetch, row, add);
+            walk.template run<1>(l, m, r.blk_n[blk], fetch, row, add);
             n -= m;
             ks = 0;
             ++blk;

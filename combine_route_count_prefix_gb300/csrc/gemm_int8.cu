@@ -1,0 +1,384 @@
+// gemm_int8.cu -- int8 products with one scale per row and one per output
+// channel: the kernel for few rows a group, and the rows' images for the tile
+// kernels.
+//
+//   C[r, n] = (float(sum_k q[r, k] * W[e, n, k]) * w_scale[e, n]) * row_scale[r] + bias[e, n]
+//
+// k_int8_few streams the weights (stream_i8.cuh): its CTAs share out the (group,
+// 8 NB rows, 16 channels) units evenly in the weights' order, its warps a batch of
+// units.  Reading the weights bounds it up to about 8 rows a group, and beyond that the
+// widening of the rows and the mma.
+// Rows come with the weights through the rings, or, LOCAL, are quantised from
+// bf16 by every CTA into its own memory (a few rows of one group).
+#include "common.cuh"
+#include "quant.cuh"
+#include "stream_i8.cuh"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+using namespace si8;
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr size_t kLocalBytes = 64 * 1024;
+
+struct Int8FewDev {
+    const uint4 *x;            // bf16 rows (LOCAL)
+    const int8_t *q;           // codes
+    const float *qs;
+    const int32_t *offsets;
+    const uint8_t *w;
+    const float *w_scales, *bias;
+    void *c;
+    int32_t *status;
+    int64_t cap_rows;
+    int E, N, Kd, out_bf16;
+    Divisor by_units, by_stages;
+};
+
+template <bool LOCAL, int NB>
+struct Cfg {
+    static constexpr int kWarps = NB == 1 ? 12 : 8;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kD = NB == 1 ? 5 : 4;
+    static constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : NB * kRowBytes);
+    static constexpr int kRing = kWarps * kD * kBytes;
+    static constexpr int kUnits = NB == 1 ? 16 : 4;      // between two block barriers
+    static constexpr int kMaxRows = NB * kRows;
+};
+
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ float max8(const float (&f)[8], float m) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+    return m;
+}
+
+template <bool LOCAL, int NB>
+__global__ void __launch_bounds__(Cfg<LOCAL, NB>::kThreads, 1)
+k_int8_few(Int8FewDev p) {
+    using C = Cfg<LOCAL, NB>;
+    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kUnits = C::kUnits, kMaxRows = C::kMaxRows;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int32_t acc[2][kUnits][kMaxRows][kChannels];
+    __shared__ int32_t s_off[kMaxExperts + 1], s_blk[kMaxExperts + 1];
+    __shared__ uint32_t amax[kRows];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t *codes = smem + C::kRing;
+    const int Kd = p.Kd, KS = (Kd + kDepth - 1) / kDepth, pitch = KS * kDepth, NU = (p.N + kChannels - 1) / kChannels;
+    const Lane l;
+
+    for (int i = tid; i < 2 * kUnits * kMaxRows * kChannels; i += kThreads) (&acc[0][0][0][0])[i] = 0;
+    if (LOCAL && tid < kRows) amax[tid] = 0;
+    pdl_wait();
+    if (blockIdx.x == 0 && tid == 0) *p.status = 0;
+    for (int i = tid; i <= p.E; i += kThreads) s_off[i] = (int)min((int64_t)p.offsets[i], p.cap_rows);
+    __syncthreads();
+    if (warp == 0) {   // s_blk[e]: row blocks of the groups before e
+        int carry = 0;
+        for (int base = 0; base < p.E; base += 32) {
+            const int e = base + lane;
+            const int c = e < p.E ? (s_off[e + 1] - s_off[e] + kMaxRows - 1) / kMaxRows : 0;
+            int x = c;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(kFull, x, d);
+                if (lane >= d) x += y;
+            }
+            if (e < p.E) s_blk[e] = carry + x - c;
+            carry += __shfl_sync(kFull, x, 31);
+        }
+        if (lane == 0) s_blk[p.E] = carry;
+    }
+    __syncthreads();
+    const int64_t units = (int64_t)s_blk[p.E] * NU;
+    const int64_t u_begin = units * blockIdx.x / gridDim.x, u_end = units * (blockIdx.x + 1) / gridDim.x;
+
+    // unit -> group, first row, rows, first channel
+    struct At {
+        int e, row0, rows, ch;
+    };
+    auto find = [&](int64_t unit) {
+        At a;
+        const int blk = units * NU <= UINT32_MAX ? p.by_units((int)unit) : (int)(unit / NU);
+        int lo = 0, hi = p.E - 1;
+        while (lo < hi) {   // last group whose first block is <= blk
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_blk[mid] <= blk) lo = mid; else hi = mid - 1;
+        }
+        a.e = lo;
+        a.row0 = s_off[lo] + (blk - s_blk[lo]) * kMaxRows;
+        a.rows = min(kMaxRows, s_off[lo + 1] - a.row0);
+        a.ch = (int)(unit - (int64_t)blk * NU) * kChannels;
+        return a;
+    };
+    auto share = [&](int64_t first, int64_t &unit, int &ks, int &n) {
+        const int total = (int)min((int64_t)kUnits, u_end - first) * KS;
+        const int a = total * warp / kWarps, b = total * (warp + 1) / kWarps, q = p.by_stages(a);
+        unit = first + q;
+        ks = a - q * KS;
+        n = b - a;
+    };
+    const uint64_t once = l2_policy_evict_first();
+    int64_t f_batch = u_begin, f_unit = 0;
+    int f_ks = 0, f_left = 0, f_rows = 0, f_ch = 0;
+    const uint8_t *f_src = nullptr;
+    const int8_t *f_row = nullptr;
+    auto enter = [&]() {
+        const At a = find(f_unit);
+        f_ch = a.ch;
+        f_src = p.w + ((int64_t)a.e * p.N + a.ch + l.cr) * Kd + f_ks * kDepth + l.cu * 16;
+        if (!LOCAL) {
+            f_rows = a.rows;
+            f_row = p.q + (int64_t)(a.row0 + l.cr) * Kd + f_ks * kDepth + l.cu * 16;
+        }
+    };
+    if (u_begin < u_end) share(u_begin, f_unit, f_ks, f_left);
+    if (f_left > 0) enter();
+    auto fetch = [&](uint32_t slot) {
+        if (f_left == 0) {
+            while (f_left == 0 && f_batch + kUnits < u_end) {
+                f_batch += kUnits;
+                share(f_batch, f_unit, f_ks, f_left);
+            }
+            if (f_left == 0) return;
+            enter();
+        }
+        const bool in = f_ks * kDepth + l.cu * 16 < Kd;
+        const bool in8 = in && f_ch + 8 < p.N;    // N is a multiple of 8
+        copy16_once(slot + l.to0, f_src, in, once);
+        copy16_once(slot + l.to1, f_src + (int64_t)4 * Kd, in, once);
+        copy16_once(slot + l.to0 + 8 * kDepth, f_src + (int64_t)8 * Kd, in8, once);
+        copy16_once(slot + l.to1 + 8 * kDepth, f_src + (int64_t)12 * Kd, in8, once);
+        f_src += kDepth;
+        if (!LOCAL) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                if (n * kRows + l.cr < f_rows)
+                    copy16(slot + l.to0 + kWeightBytes + n * kRowBytes, f_row + (int64_t)(n * kRows) * Kd, in);
+                if (n * kRows + 4 + l.cr < f_rows)
+                    copy16(slot + l.to1 + kWeightBytes + n * kRowBytes, f_row + (int64_t)(n * kRows + 4) * Kd, in);
+            }
+            f_row += kDepth;
+        }
+        --f_left;
+        if (++f_ks == KS) {
+            f_ks = 0;
+            ++f_unit;
+            if (f_left > 0) enter();
+        }
+    };
+    Walk<C::kD, C::kBytes, LOCAL> walk(smem_u32(smem) + (uint32_t)(warp * C::kD * C::kBytes));
+    walk.first(fetch);
+    if (LOCAL) {
+        // one group of at most kRows rows: its codes, in every CTA, kWarps / rows warps a row
+        const int rows = s_off[1] - s_off[0], k8 = Kd / 8, group = rows > 0 ? kWarps / rows : 1, t = warp / group;
+        const int first = (warp - t * group) * 32 + lane;
+        const uint4 *src = p.x + (int64_t)(s_off[0] + t) * k8;
+        if (t < rows) {
+            float m = 0.0f;
+#pragma unroll 4
+            for (int i = first; i < k8; i += 32 * group) {
+                float v[8];
+                unpack8(src[i], v);
+                m = max8(v, m);
+            }
+            const uint32_t w = __reduce_max_sync(kFull, __float_as_uint(m));
+            if (lane == 0) atomicMax(&amax[t], w);
+        }
+        __syncthreads();
+        if (t < rows) {
+            const float s = __fdiv_rn(__uint_as_float(amax[t]), 127.0f), rs = __frcp_rn(s);
+#pragma unroll 1
+            for (int i = first; i < pitch / 8; i += 32 * group) {
+                uint2 q = make_uint2(0, 0);
+                if (i < k8) {
+                    float v[8], c[8];
+                    unpack8(src[i], v);
+                    quant_codes<8>(v, s, rs, c);
+                    q = make_uint2(pack_i8x4(c[0], c[1], c[2], c[3]), pack_i8x4(c[4], c[5], c[6], c[7]));
+                }
+                *reinterpret_cast<uint2 *>(codes + (size_t)t * pitch + (i >> 4) * kDepth +
+                                           unit_at(t, (i >> 1) & 7) + (i & 1) * 8) = q;
+            }
+        }
+        __syncthreads();
+    }
+
+    int buf = 0;
+    for (int64_t first = u_begin; first < u_end; first += kUnits, buf ^= 1) {
+        const int nu = (int)min((int64_t)kUnits, u_end - first);
+        int64_t unit;
+        int ks, n;
+        share(first, unit, ks, n);
+        while (n > 0) {
+            const At at = find(unit);
+            const int m = min(n, KS - ks);
+            int32_t (*a)[kChannels] = acc[buf][unit - first];
+            auto row = [&](int i) -> uint32_t {
+                if (!LOCAL) return kWeightBytes + i * kDepth + l.of_row(i);
+                return smem_u32(codes) + (uint32_t)(i * pitch + ks * kDepth) + l.of_row(i);
+            };
+            auto add = [&](int i, int c, int32_t v) { atomicAdd(&a[i][c], v); };
+            walk.template run<NB>(l, m, at.rows, fetch, row, add);
+            n -= m;
+            ks = 0;
+            ++unit;
+        }
+        __syncthreads();
+        constexpr int kEach = kThreads / kChannels;     // units x rows that are written at once
+#pragma unroll 1
+        for (int i = tid / kChannels; i < nu * kMaxRows; i += kEach) {
+            const At at = find(first + i / kMaxRows);
+            const int row = i % kMaxRows, ch = at.ch + tid % kChannels;
+            if (row >= at.rows) continue;
+            int32_t *a = &acc[buf][i / kMaxRows][row][tid % kChannels];
+            const int32_t sum = *a;
+            *a = 0;
+            if (ch >= p.N) continue;
+            const int64_t r = at.row0 + row, wn = (int64_t)at.e * p.N + ch;
+            const float s = LOCAL ? __fdiv_rn(__uint_as_float(amax[row]), 127.0f) : __ldg(p.qs + r);
+            float v = __fmul_rn(__fmul_rn(__int2float_rn(sum), __ldg(p.w_scales + wn)), s);
+            if (p.bias) v = __fadd_rn(v, __ldg(p.bias + wn));
+            if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.c)[r * p.N + ch] = __float2bfloat16_rn(v);
+            else static_cast<float *>(p.c)[r * p.N + ch] = v;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- rows for the tile kernels
+// A CTA a row: fp16 images of int8 codes, and their scale.
+constexpr int kImgThreads = 256;
+template <bool BF16>
+__global__ void __launch_bounds__(kImgThreads)
+k_rows_to_f16(const void *__restrict__ rows, const float *__restrict__ scales,
+              const int32_t *__restrict__ offsets, int64_t E, int64_t cap_rows, int64_t Kd,
+              uint4 *__restrict__ img, float *__restrict__ img_scales, int32_t *__restrict__ status,
+              uint32_t *__restrict__ clear, int64_t n_clear) {
+    __shared__ float part[kImgThreads / 32];
+    const int tid = threadIdx.x;
+    pdl_wait();
+    if (blockIdx.x == 0 && tid == 0) *status = 0;
+    for (int64_t i = (int64_t)blockIdx.x * kImgThreads + tid; i < n_clear; i += (int64_t)gridDim.x * kImgThreads)
+        clear[i] = 0;
+    const int64_t R = min((int64_t)offsets[E], cap_rows);
+    const int k8 = (int)(Kd / 8);
+    constexpr int kOwn = 4;      // vectors that stay in registers: rows of up to 8192
+    for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
+        uint4 *out = img + r * k8;
+        if constexpr (BF16) {
+            const uint4 *src = static_cast<const uint4 *>(rows) + r * k8;
+            uint4 raw[kOwn];
+            float m = 0.0f;
+#pragma unroll
+            for (int u = 0; u < kOwn; ++u) {
+                const int i = u * kImgThreads + tid;
+                raw[u] = i < k8 ? __ldcs(src + i) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < kOwn; ++u) {
+                float v[8];
+                unpack8(raw[u], v);
+                m = max8(v, m);
+            }
+            for (int i = kOwn * kImgThreads + tid; i < k8; i += kImgThreads) {
+                float v[8];
+                unpack8(src[i], v);
+                m = max8(v, m);
+            }
+            m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
+            __syncthreads();      // the row before has read part
+            if ((tid & 31) == 0) part[tid >> 5] = m;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kImgThreads / 32; ++w) m = fmaxf(m, part[w]);
+            const float s = __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
+            auto put = [&](int i, const uint4 &x) {
+                float v[8], c[8];
+                unpack8(x, v);
+                quant_codes<8>(v, s, rs, c);
+                out[i] = make_uint4(pack_half2(c[0], c[1]), pack_half2(c[2], c[3]), pack_half2(c[4], c[5]),
+                                    pack_half2(c[6], c[7]));
+            };
+#pragma unroll
+            for (int u = 0; u < kOwn; ++u)
+                if (u * kImgThreads + tid < k8) put(u * kImgThreads + tid, raw[u]);
+            for (int i = kOwn * kImgThreads + tid; i < k8; i += kImgThreads) put(i, src[i]);
+            if (tid == 0) img_scales[r] = s;
+        } else {
+            const uint2 *src = static_cast<const uint2 *>(rows) + r * k8;
+            for (int i = tid; i < k8; i += kImgThreads) {
+                const uint2 b = __ldcs(src + i);
+                const uint32_t lo = b.x ^ 0x80808080u, hi = b.y ^ 0x80808080u;
+                out[i] = make_uint4(widen_lo(lo), widen_hi(lo), widen_lo(hi), widen_hi(hi));
+            }
+            if (tid == 0) img_scales[r] = scales[r];
+        }
+    }
+}
+
+template <bool LOCAL, int NB>
+moe_status launch(const Int8FewDev &p, size_t extra, cudaStream_t stream) {
+    using C = Cfg<LOCAL, NB>;
+    auto kernel = k_int8_few<LOCAL, NB>;
+    if (!set_smem_limit((const void *)kernel, C::kRing + extra)) return MOE_ERR_CUDA;
+    const int64_t units = p.cap_rows * ((p.N + kChannels - 1) / kChannels);
+    const unsigned grid = (unsigned)std::min<int64_t>(num_sms(), units);
+    MOE_LAUNCH("int8_few", kernel, grid, C::kThreads, C::kRing + extra, stream, p);
+    return MOE_OK;
+}
+
+int64_t padded(int64_t k) { return (k + kDepth - 1) / kDepth * kDepth; }
+
+}  // namespace
+
+bool int8_few_local(int64_t rows, int64_t E, int64_t Kd) {
+    return E == 1 && rows <= kRows && rows * padded(Kd) <= (int64_t)kLocalBytes;
+}
+
+moe_status launch_int8_few(const Int8FewArgs &a, cudaStream_t stream) {
+    Int8FewDev p;
+    p.x = static_cast<const uint4 *>(a.rows);
+    p.q = static_cast<const int8_t *>(a.rows);
+    p.qs = a.row_scales;
+    p.offsets = a.offsets;
+    p.w = static_cast<const uint8_t *>(a.w);
+    p.w_scales = a.w_scales;
+    p.bias = a.bias;
+    p.c = a.c;
+    p.status = a.status;
+    p.cap_rows = a.cap_rows;
+    p.E = (int)a.E;
+    p.N = (int)a.N;
+    p.Kd = (int)a.Kd;
+    p.out_bf16 = a.out_bf16;
+    p.by_units = Divisor((uint32_t)((a.N + kChannels - 1) / kChannels));
+    p.by_stages = Divisor((uint32_t)(padded(a.Kd) / kDepth));
+    if (a.rows_bf16) return launch<true, 1>(p, (size_t)(a.cap_rows * padded(a.Kd)), stream);
+    return a.cap_rows <= kRows * a.E ? launch<false, 1>(p, 0, stream) : launch<false, 4>(p, 0, stream);
+}
+
+moe_status launch_rows_to_f16(const void *rows, bool bf16, const float *scales, const int32_t *offsets,
+                              int64_t E, int64_t cap_rows, int64_t Kd, void *img, float *img_scales,
+                              int32_t *status, uint32_t *clear, int64_t n_clear, cudaStream_t stream) {
+    const unsigned grid = (unsigned)std::min<int64_t>(cap_rows, (int64_t)num_sms() * 8);
+    if (bf16) {
+        MOE_LAUNCH("rows_to_f16", k_rows_to_f16<true>, grid, kImgThreads, 0, stream, rows, scales, offsets, E,
+                   cap_rows, Kd, static_cast<uint4 *>(img), img_scales, status, clear, n_clear);
+    } else {
+        MOE_LAUNCH("rows_to_f16", k_rows_to_f16<false>, grid, kImgThreads, 0, stream, rows, scales, offsets, E,
+                   cap_rows, Kd, static_cast<uint4 *>(img), img_scales, status, clear, n_clear);
+    }
+    return MOE_OK;
+}
+
+}  // namespace moe

@@ -117,16 +117,35 @@ struct SmallDev {
     const float *scale2;
     const float *s2;
     int32_t *status;
+    // Linear
+    const float *bias;
+    float *y32;
+    int splits;
+    int32_t *partial;
+    uint32_t *arrived;
 };
 
+// kb0, kb1: the k-blocks of this CTA (all of them unless the tile is split);
+// index: the tile's number.
 struct Tile {
-    int e, row0, rows, wb;
+    int e, row0, rows, wb, kb0, kb1, split;
+    int64_t index;
 };
 
 template <int TB>
-__device__ __forceinline__ Tile decode_tile(int64_t tile, int n_wblocks, int E,
+__device__ __forceinline__ Tile decode_tile(int64_t tile, int splits, int num_kb, int n_wblocks, int E,
                                             const int32_t *s_sched, const int32_t *s_off) {
     Tile t;
+    t.split = 0;
+    t.kb0 = 0;
+    t.kb1 = num_kb;
+    if (splits > 1) {
+        t.split = (int)(tile % splits);
+        tile /= splits;
+        t.kb0 = num_kb * t.split / splits;
+        t.kb1 = num_kb * (t.split + 1) / splits;
+    }
+    t.index = tile;
     const int mblk = (int)(tile / n_wblocks);
     t.wb = (int)(tile % n_wblocks);
     int lo = 0, hi = E - 1;
@@ -181,6 +200,22 @@ __device__ __forceinline__ void epilogue_small(const SmallDev &p, const Tile &t,
             const float m = __shfl_down_sync(0xffffffffu, h, 16);
             if (gate) p.g[row * Nh + j] = __fmul_rn(silu_f32(h), m);
         }
+    } else if (EPI == (int)Epi::Linear) {
+        const bool in = ch < p.Nout;
+        const float sc = in ? __ldg(p.scale2 + (int64_t)t.e * p.Nout + ch) : 0.0f;
+        const float bias = in && p.bias ? __ldg(p.bias + (int64_t)t.e * p.Nout + ch) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i) {
+            if (c0 + i >= t.rows) break;
+            const int64_t row = (int64_t)t.row0 + c0 + i;
+            if (row >= p.cap_rows) break;
+            float v = __fmul_rn(__fmul_rn(__int2float_rn(acc[i]), sc), __ldg(p.s2 + row));
+            if (p.bias) v = __fadd_rn(v, bias);
+            if (in) {
+                if (p.y32) p.y32[row * p.Nout + ch] = v;
+                else p.y[row * p.Nout + ch] = __float2bfloat16_rn(v);
+            }
+        }
     } else {
         const float sc = ch < p.Nout ? __ldg(p.scale2 + (int64_t)t.e * p.Nout + ch) : 0.0f;
 #pragma unroll
@@ -194,6 +229,35 @@ __device__ __forceinline__ void epilogue_small(const SmallDev &p, const Tile &t,
     }
 }
 
+// Where several CTAs share a tile's inner dimension: each epilogue warp leaves its
+// sums, and the last of the same warps of the tile's CTAs adds the others' to its own
+// (integers: in any order the same).  True for that one.
+template <int TB, int EPI_COLS>
+__device__ __forceinline__ bool join_splits(const SmallDev &p, const Tile &t, int ew, int q, int lane,
+                                            int c0, int32_t (&acc)[EPI_COLS]) {
+    // [tile][split][row][channel]
+    const int64_t size = (int64_t)TB * BW;
+    int32_t *mine = p.partial + (t.index * p.splits + t.split) * size + (int64_t)c0 * BW + q * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < EPI_COLS; ++i)
+        if (c0 + i < t.rows) __stcg(mine + (int64_t)i * BW, acc[i]);
+    __threadfence();
+    __syncwarp();
+    uint32_t before = 0;
+    if (lane == 0) before = atomicAdd(p.arrived + t.index * EPI_WARPS + ew, 1u);
+    before = __shfl_sync(0xffffffffu, before, 0);
+    if (before != (uint32_t)p.splits - 1) return false;
+    __threadfence();
+    for (int s = 0; s < p.splits; ++s) {
+        if (s == t.split) continue;
+        const int32_t *other = p.partial + (t.index * p.splits + s) * size + (int64_t)c0 * BW + q * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < EPI_COLS; ++i)
+            if (c0 + i < t.rows) acc[i] += __ldcg(other + (int64_t)i * BW);
+    }
+    return true;
+}
+
 // ---------------------------------------------------------------- the kernel
 template <int EPI, int TB_>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -203,6 +267,7 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
     constexpr int TB = Cfg::TB, NBUF = Cfg::NBUF, CHUNK_KB = Cfg::CHUNK_KB;
     constexpr int B_HALF_BYTES = Cfg::B_HALF_BYTES, B_BYTES = Cfg::B_BYTES;
     constexpr int EPI_COLS = Cfg::EPI_COLS;
+    constexpr bool kSplits = EPI == (int)Epi::Linear;
     constexpr size_t RING_BYTES = Cfg::RING_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -275,8 +340,8 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int64_t total_tiles = (int64_t)s_sched[p.E] * p.n_wblocks;
-    const int num_chunks = (p.num_kb + CHUNK_KB - 1) / CHUNK_KB;
+    const int64_t total_tiles = (int64_t)s_sched[p.E] * p.n_wblocks * (kSplits ? p.splits : 1);
+    const int all_chunks = (p.num_kb + CHUNK_KB - 1) / CHUNK_KB;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -288,8 +353,8 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
             for (int s = 0; s < S8; ++s) issued_phase[s] = -1;
             bool ok = true;
             for (int64_t tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-                const Tile t = decode_tile<TB>(tile, p.n_wblocks, p.E, s_sched, s_off);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                const Tile t = decode_tile<TB>(tile, kSplits ? p.splits : 1, p.num_kb, p.n_wblocks, p.E, s_sched, s_off);
+                for (int kb = kSplits ? t.kb0 : 0, kb1 = kSplits ? t.kb1 : p.num_kb; kb < kb1; ++kb) {
                     if (!wait_bounded(&w8_empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     mbar_arrive_expect_tx(&w8_full[stage], W8_BYTES);
                     tma_load_3d(ring8 + (size_t)stage * W8_BYTES, &tmW, &w8_full[stage], kb * BK,
@@ -312,8 +377,8 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
             for (int s = 0; s < SA; ++s) issued_phase[s] = -1;
             bool ok = true;
             for (int64_t tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-                const Tile t = decode_tile<TB>(tile, p.n_wblocks, p.E, s_sched, s_off);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                const Tile t = decode_tile<TB>(tile, kSplits ? p.splits : 1, p.num_kb, p.n_wblocks, p.E, s_sched, s_off);
+                for (int kb = kSplits ? t.kb0 : 0, kb1 = kSplits ? t.kb1 : p.num_kb; kb < kb1; ++kb) {
                     if (!wait_bounded(&ab_empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     mbar_arrive_expect_tx(&ab_full[stage], (uint32_t)B_BYTES);
                     uint8_t *dst = ringB + (size_t)stage * B_BYTES;
@@ -337,7 +402,8 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
         uint32_t ph8 = 0, pha = 0;
         bool ok = true;
         for (int64_t tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-            for (int kb = 0; kb < p.num_kb; ++kb) {
+            const Tile t = decode_tile<TB>(tile, kSplits ? p.splits : 1, p.num_kb, p.n_wblocks, p.E, s_sched, s_off);
+            for (int kb = kSplits ? t.kb0 : 0, kb1 = kSplits ? t.kb1 : p.num_kb; kb < kb1; ++kb) {
                 const bool w = wait_bounded(&w8_full[s8], ph8, abort_flag, p.status) &&
                                wait_bounded(&ab_empty[sa], pha ^ 1u, abort_flag, p.status);
                 if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
@@ -384,14 +450,14 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
             uint32_t acc_phase = 0;
             bool ok = true;
             for (int64_t tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-                const Tile t = decode_tile<TB>(tile, p.n_wblocks, p.E, s_sched, s_off);
+                const Tile t = decode_tile<TB>(tile, kSplits ? p.splits : 1, p.num_kb, p.n_wblocks, p.E, s_sched, s_off);
                 const int n16 = ((t.rows + 15) / 16) * 16;
                 const uint32_t idesc = idesc_f16(BW, n16);
-                for (int kb0 = 0; ok && kb0 < p.num_kb; kb0 += CHUNK_KB) {
+                for (int kb0 = kSplits ? t.kb0 : 0, end = kSplits ? t.kb1 : p.num_kb; ok && kb0 < end; kb0 += CHUNK_KB) {
                     if (!wait_bounded(&acc_empty[accb], acc_phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t d_tmem = tmem_base + (uint32_t)(is * ACC_COLS + accb * TB);
-                    const int kb1 = min(kb0 + CHUNK_KB, p.num_kb);
+                    const int kb1 = min(kb0 + CHUNK_KB, end);
                     for (int kb = kb0; kb < kb1; ++kb) {
                         if (!wait_bounded(&ab_full[stage], phase, abort_flag, p.status)) {
                             ok = false;
@@ -426,12 +492,13 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
         // buffer and the sums fit the registers together
         constexpr int LDW = EPI_COLS > 32 ? 16 : 32;
         for (int64_t tile = blockIdx.x; tile < total_tiles; tile += gridDim.x) {
-            const Tile t = decode_tile<TB>(tile, p.n_wblocks, p.E, s_sched, s_off);
+            const Tile t = decode_tile<TB>(tile, kSplits ? p.splits : 1, p.num_kb, p.n_wblocks, p.E, s_sched, s_off);
             const int nj = (t.rows - c0 + LDW - 1) / LDW;   // column groups holding rows (may be <= 0)
             int32_t acc[EPI_COLS];
 #pragma unroll
             for (int i = 0; i < EPI_COLS; ++i) acc[i] = 0;
             bool ok = true;
+            const int num_chunks = kSplits ? (t.kb1 - t.kb0 + CHUNK_KB - 1) / CHUNK_KB : all_chunks;
             for (int c = 0; c < num_chunks; ++c) {
                 const bool w = wait_bounded(&acc_full[accb], acc_phase, abort_flag, p.status);
                 if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
@@ -461,6 +528,9 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
                 if (++accb == NBUF) { accb = 0; acc_phase ^= 1u; }
             }
             if (!ok) break;
+            if (kSplits && p.splits > 1 && nj > 0 &&
+                !join_splits<TB, EPI_COLS>(p, t, warp - EPI_WARP0, q, lane, c0, acc))
+                continue;
             if (nj > 0) epilogue_small<EPI, EPI_COLS>(p, t, q, lane, c0, acc);
         }
     }
@@ -476,7 +546,8 @@ moe_status launch_small_tb(const CUtensorMap &mr, const CUtensorMap &mw, const S
                            cudaStream_t stream) {   // mr: boxes of TB rows
     constexpr size_t smem = SmallCfg<TB>::SMEM_BYTES;
     if (!set_smem_limit((const void *)k_gemm_small<EPI, TB>, smem)) return MOE_ERR_CUDA;
-    const char *names[3] = {"gemm_s32_small", "gemm1_swiglu_small", "gemm2_dequant_small"};
+    const char *names[4] = {"gemm_s32_small", "gemm1_swiglu_small", "gemm2_dequant_small",
+                            "gemm_linear_small"};
     MOE_LAUNCH(names[EPI], (k_gemm_small<EPI, TB>), num_sms(), THREADS, smem, stream, mr, mw, d);
     return MOE_OK;
 }
@@ -526,11 +597,17 @@ moe_status launch_grouped_gemm_small(Epi epi, const GemmArgs &a, cudaStream_t st
     d.scale2 = a.scale2;
     d.s2 = a.s2;
     d.status = a.status;
+    d.bias = a.bias;
+    d.y32 = a.y_f32 ? static_cast<float *>(a.y) : nullptr;
+    d.splits = a.splits > 1 ? a.splits : 1;
+    d.partial = a.partial;
+    d.arrived = a.arrived;
     switch (epi) {
         case Epi::S32: return launch_small_epi<(int)Epi::S32>(mr, mw, d, wide, stream);
         case Epi::SwiGLU: return launch_small_epi<(int)Epi::SwiGLU>(mr, mw, d, wide, stream);
         case Epi::DequantBF16:
             return launch_small_epi<(int)Epi::DequantBF16>(mr, mw, d, wide, stream);
+        case Epi::Linear: return launch_small_epi<(int)Epi::Linear>(mr, mw, d, wide, stream);
     }
     return MOE_ERR_PARAM_INVALID;
 }

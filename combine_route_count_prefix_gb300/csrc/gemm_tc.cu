@@ -109,6 +109,8 @@ struct GemmDev {
     const float *s2;
     int32_t *status;
     int y_vec32;        // y rows start on 32-byte boundaries: 32-byte stores
+    const float *bias;  // Linear
+    float *y32;         // Linear with fp32 output
 };
 
 // One 32-byte store (eight 32-bit words) to a 32-byte aligned global address.
@@ -187,6 +189,40 @@ __device__ __forceinline__ void epilogue_store(const GemmDev &p, const Tile &t, 
                 o[u] = __fmul_rn(silu_f32(ha), hb);
             }
             dst[i] = make_float4(o[0], o[1], o[2], o[3]);
+        }
+    } else if (EPI == (int)Epi::Linear) {
+        const int c0 = t.nb * BN + hf * 128;
+        const float s2 = p.s2[row];
+        const float *sc = p.scale2 + (int64_t)t.e * p.Nout + c0;
+        const float *bs = p.bias ? p.bias + (int64_t)t.e * p.Nout + c0 : nullptr;
+        const int64_t o = (int64_t)row * p.Nout + c0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (c0 + 8 * i >= p.Nout) break;
+            const float4 sa = __ldg(reinterpret_cast<const float4 *>(sc) + 2 * i);
+            const float4 sb = __ldg(reinterpret_cast<const float4 *>(sc) + 2 * i + 1);
+            float v[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = __fmul_rn(__fmul_rn(__int2float_rn(acc[8 * i + u]), v[u]), s2);
+            if (bs) {
+                const float4 ba = __ldg(reinterpret_cast<const float4 *>(bs) + 2 * i);
+                const float4 bb = __ldg(reinterpret_cast<const float4 *>(bs) + 2 * i + 1);
+                const float b[8] = {ba.x, ba.y, ba.z, ba.w, bb.x, bb.y, bb.z, bb.w};
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] = __fadd_rn(v[u], b[u]);
+            }
+            if (p.y32) {   // rows of N % 8 == 0 floats: 32-byte boundaries
+                st_global_v8(p.y32 + o + 8 * i, __float_as_uint(v[0]), __float_as_uint(v[1]),
+                             __float_as_uint(v[2]), __float_as_uint(v[3]), __float_as_uint(v[4]),
+                             __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    w[u] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[2 * u])) |
+                           ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[2 * u + 1])) << 16);
+                *reinterpret_cast<uint4 *>(p.y + o + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
         }
     } else {
         const int c0 = t.nb * BN + hf * 128;
@@ -640,7 +676,7 @@ template <int EPI>
 moe_status launch_epi(const CUtensorMap &ma, const CUtensorMap &mb, const GemmDev &d,
                       cudaStream_t stream) {
     if (!set_smem_limit((const void *)k_grouped_gemm<EPI>, SMEM_BYTES)) return MOE_ERR_CUDA;
-    const char *names[3] = {"gemm_s32", "gemm1_swiglu", "gemm2_dequant"};
+    const char *names[4] = {"gemm_s32", "gemm1_swiglu", "gemm2_dequant", "gemm_linear"};
     MOE_LAUNCH(names[EPI], k_grouped_gemm<EPI>, num_sms(), THREADS, SMEM_BYTES, stream, ma, mb, d);
     return MOE_OK;
 }
@@ -678,7 +714,8 @@ int pair_clusters() {
 template <int EPI>
 moe_status launch_epi_pair(const CUtensorMap &ma, const CUtensorMap &mb, const GemmDev &d,
                            int clusters, cudaStream_t stream) {
-    const char *names[3] = {"gemm_s32_pair", "gemm1_swiglu_pair", "gemm2_dequant_pair"};
+    const char *names[4] = {"gemm_s32_pair", "gemm1_swiglu_pair", "gemm2_dequant_pair",
+                            "gemm_linear_pair"};
     MOE_LAUNCH_CLUSTER(names[EPI], k_grouped_gemm_pair<EPI>, 2 * clusters, THREADS, P_SMEM_BYTES,
                        stream, 2u, ma, mb, d);
     return MOE_OK;
@@ -702,6 +739,8 @@ GemmDev gemm_dev(const GemmArgs &a) {
     d.s2 = a.s2;
     d.status = a.status;
     // 32-byte stores need every y row to start on a 32-byte boundary
+    d.bias = a.bias;
+    d.y32 = a.y_f32 ? static_cast<float *>(a.y) : nullptr;
     d.y_vec32 = a.y != nullptr && ((uintptr_t)a.y % 32) == 0 && ((a.Nout * 2) % 32) == 0;
     return d;
 }
@@ -752,12 +791,15 @@ moe_status launch_pair_or_single(const GemmArgs &a, cudaStream_t stream, bool pa
     return launch_epi<EPI>(ma, mb, d, stream);
 }
 
+bool linear_pairs_fit() { return pair_clusters<(int)Epi::Linear>() > 0; }
+
 moe_status launch_grouped_gemm(Epi epi, const GemmArgs &a, cudaStream_t stream, bool pair) {
     if (a.cap_rows <= 0 || a.E <= 0) return MOE_OK;
     switch (epi) {
         case Epi::S32: return launch_pair_or_single<(int)Epi::S32>(a, stream, pair);
         case Epi::SwiGLU: return launch_pair_or_single<(int)Epi::SwiGLU>(a, stream, pair);
         case Epi::DequantBF16: return launch_pair_or_single<(int)Epi::DequantBF16>(a, stream, pair);
+        case Epi::Linear: return launch_pair_or_single<(int)Epi::Linear>(a, stream, pair);
     }
     return MOE_ERR_PARAM_INVALID;
 }

@@ -257,11 +257,42 @@ struct Walk {
             }
         }
     }
-    // `stages` stages of one unit with nr rows.  row(n): the lane's first bytes of
-    // row n (LOCAL: at the first stage; else in the slot); add(n, c, v) takes the
-    // sum of row n and channel c (0 .. 15), from one lane each.
+    template <int NB, typename Fetch, typename Row, typename Add>
+    __device__ __forceinline__ void blocks(const Lane &l, int stages, int nr, Fetch &fetch, Row &row, Add &add) {
+        Sums<NB> s;
+        s.clear();
+        uint32_t r[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {   // lanes of rows that are not there read the last
+            const int i = kRows * n + l.g;
+            r[n] = row(i < nr ? i : nr - 1);
+        }
+#pragma unroll 1
+        for (int i = 0; i < stages; ++i) {
+            const uint32_t st = next(fetch);
+            uint32_t at[NB];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                at[n] = LOCAL ? r[n] : st + r[n];
+                if (LOCAL) r[n] += kDepth;
+            }
+            s.add_stage(st + l.from, at);
+            if (i % kExactStages == kExactStages - 1) s.flush();
+        }
+        s.flush();
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r0 = kRows * n + 2 * l.t + (i & 1);
+                if (r0 < nr) add(r0, l.g + (i >> 1) * 8, s.total[n][i]);
+            }
+    }
+    // `stages` stages of one unit with nr <= 8 NB rows.  row(n): the lane's first
+    // bytes of row n (LOCAL: at the first stage; else in the slot); add(n, c, v) takes
+    // the sum of row n and channel c (0 .. 15), from one lane each.
     // (One loop that branches on nr inside measured 4 to 8 % slower.)
-    template <typename Fetch, typename Row, typename Add>
+    template <int NB, typename Fetch, typename Row, typename Add>
     __device__ __forceinline__ void run(const Lane &l, int stages, int nr, Fetch &fetch, Row &row, Add &add) {
         if (nr == 1) {
             dots<1>(l, stages, fetch, row, add);
@@ -271,24 +302,12 @@ struct Walk {
             dots<3>(l, stages, fetch, row, add);
         } else if (nr == 4) {
             dots<4>(l, stages, fetch, row, add);
+        } else if (NB == 1 || nr <= kRows) {
+            blocks<1>(l, stages, nr, fetch, row, add);
+        } else if (NB == 2 || nr <= 2 * kRows) {
+            blocks<2>(l, stages, nr, fetch, row, add);
         } else {
-            Sums<1> s;
-            s.clear();
-            uint32_t r = row(l.g < nr ? l.g : 0);   // lanes of rows that are not there read the first
-#pragma unroll 1
-            for (int i = 0; i < stages; ++i) {
-                const uint32_t st = next(fetch);
-                const uint32_t at[1] = {LOCAL ? r : st + r};
-                if (LOCAL) r += kDepth;
-                s.add_stage(st + l.from, at);
-                if (i % kExactStages == kExactStages - 1) s.flush();
-            }
-            s.flush();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = 2 * l.t + (i & 1);
-                if (n < nr) add(n, l.g + (i >> 1) * 8, s.total[0][i]);
-            }
+            blocks<NB>(l, stages, nr, fetch, row, add);
         }
     }
 };

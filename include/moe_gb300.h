@@ -395,6 +395,7 @@ moe_status moe_dispatch_noalloc(const moe_shape *shape, const void *x, const int
 /* Element types of the calls below that take more than one. */
 #define MOE_DTYPE_F32  0
 #define MOE_DTYPE_BF16 1
+#define MOE_DTYPE_I8   2
 
 /* Residual addition and root-mean-square norm.  Per token, in fp32:
  *   h = x + residual (h = x when residual is NULL)
@@ -485,6 +486,37 @@ moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
                                 const float *a_scales, const void *W, const float *w_scales,
                                 void *C, int out_dtype, int path, void *workspace,
                                 size_t workspace_bytes, cudaStream_t stream);
+
+/* Grouped product in 8-bit integers with one scale per row and one per output
+ * channel: what a model with int8 weights multiplies around the experts (E = 1 is
+ * a dense projection).  For the rows r of group e, [expert_offsets[e],
+ * expert_offsets[e+1]):
+ *   C[r, n] = (float(sum_k q[r, k] * W[e, n, k]) * w_scales[e, n]) * s[r] + bias[e, n]
+ * The sum is exact; each other operation is one rounded fp32 operation, and a
+ * bf16 output is rounded once more.
+ * A               int8 [rows, Kd] (MOE_DTYPE_I8) with a_scales fp32 [rows]: q and s;
+ *                 or bf16 [rows, Kd] (MOE_DTYPE_BF16) with a_scales NULL: each row is
+ *                 quantised in the call, s = max|a| / 127, q = rint(a / s), as
+ *                 moe_dispatch_quant does
+ * w_packed        from moe_pack_int8 with the same E, N, Kd and path
+ * w_scales        fp32 [E, N]; bias fp32 [E, N] or NULL
+ * C               [rows, N] in out_dtype (MOE_DTYPE_F32 or MOE_DTYPE_BF16); rows
+ *                 >= expert_offsets[E] untouched
+ * N % 8 == 0, N <= 1048576, Kd % 16 == 0, 16 <= Kd <= 131072, rows * Kd < 2^40.
+ * path: MOE_FFN_PATH_* as in moe_shape.  moe_pack_int8 writes w int8 [E, N, Kd] as
+ * fp16 images (LARGE, LARGE_PAIR; 2 bytes a weight), as biased bytes (SMALL; 1
+ * byte) or both (AUTO; 3 bytes, the call picks by its rows). */
+moe_status moe_int8_packed_bytes(int64_t E, int64_t N, int64_t Kd, int path, size_t *bytes);
+moe_status moe_pack_int8(int64_t E, int64_t N, int64_t Kd, int path, const int8_t *w,
+                         void *w_packed, cudaStream_t stream);
+moe_status moe_grouped_gemm_int8_workspace_size(int64_t rows, int64_t E, int64_t N, int64_t Kd,
+                                                size_t *bytes);
+moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
+                                 const int32_t *expert_offsets, const void *A, int a_dtype,
+                                 const float *a_scales, const void *w_packed,
+                                 const float *w_scales, const float *bias, void *C, int out_dtype,
+                                 int path, void *workspace, size_t workspace_bytes,
+                                 cudaStream_t stream);
 
 /* The experts' FFN on block-scaled e4m3 tokens and weights.  For a row of
  * expert e, with moe_grouped_gemm_fp8's products:

@@ -1,0 +1,159 @@
+"""moe_grouped_gemm_int8: bit for bit its definition (an exact integer sum and
+single fp32 operations), and within derived bounds of 64 bits, on every kernel."""
+import pytest
+import torch
+
+from gpu_util import load_binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def B():
+    return load_binding()
+
+
+def make(rows, E, N, Kd, a="int8", bias=False, counts=None, seed=0, extreme=False):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+
+    def rand(*s):
+        return torch.rand(*s, generator=g, device=DEV)
+
+    def int8(*s):
+        w = torch.randint(-128, 128, s, generator=g, dtype=torch.int8, device=DEV)
+        if extreme:
+            w = torch.where(rand(*s) < 0.95, torch.full_like(w, -128), torch.full_like(w, 127))
+        return w
+
+    if counts is None:
+        pick = torch.randint(0, E, (rows,), generator=g, device=DEV)
+        counts = torch.bincount(pick, minlength=E).tolist()
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[1:] = torch.tensor(counts).cumsum(0)
+    d = dict(off=off.to(DEV), w=int8(E, N, Kd), ws=1e-4 + 9e-4 * rand(E, N),
+             bias=torch.randn(E, N, generator=g, device=DEV) if bias else None)
+    if a == "int8":
+        d["a"], d["as_"] = int8(rows, Kd), 0.01 + 0.02 * rand(rows)
+    else:
+        d["a"], d["as_"] = torch.randn(rows, Kd, generator=g, device=DEV).bfloat16(), None
+    return d
+
+
+def codes(d):
+    if d["as_"] is not None:
+        return d["a"].double(), d["as_"]
+    x = d["a"].float()
+    s = x.abs().amax(1) / torch.full((), 127.0, device=DEV)
+    q = torch.where(s[:, None] > 0, torch.round(x / torch.where(s > 0, s, 1.0)[:, None]), 0.0)
+    return q.clamp(-127, 127).double(), s
+
+
+def reference(d, dtype):
+    """The definition in the precision it is defined in, and in 64 bits."""
+    q, s = codes(d)
+    off = d["off"].tolist()
+    R = off[-1]
+    out = torch.empty(R, d["w"].shape[1], device=DEV)
+    out64 = out.double()
+    for e, (lo, hi) in enumerate(zip(off, off[1:])):
+        acc = q[lo:hi] @ d["w"][e].double().T                    # exact: below 2^53
+        v = (acc.float() * d["ws"][e]) * s[lo:hi, None]
+        v64 = acc * d["ws"][e].double() * s[lo:hi, None].double()
+        if d["bias"] is not None:
+            v, v64 = v + d["bias"][e], v64 + d["bias"][e].double()
+        out[lo:hi], out64[lo:hi] = v, v64
+    return out.to(dtype), out64
+
+
+def check(B, d, path, dtype, **kw):
+    _, packed = B.pack_int8(d["w"], path=path)
+    rows, N = d["a"].shape[0], d["w"].shape[1]
+    out = torch.full((rows, N), 7.0, dtype=dtype, device=DEV)
+    got, ws = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], bias=d["bias"],
+                                  out=out, path=path, **kw)
+    torch.cuda.synchronize()
+    assert B.read_device_status(ws) == 0
+    ref, ref64 = reference(d, dtype)
+    R = ref.shape[0]
+    assert torch.equal(got[:R], ref)
+    assert bool((got[R:] == 7.0).all())
+    # three roundings of the product and one of the sum with the bias, then bf16's
+    prod = (ref64 if d["bias"] is None else ref64 - torch.repeat_interleave(
+        d["bias"], torch.diff(d["off"]).long(), 0).double()).abs()
+    tol = prod * 3.01 * 2.0 ** -24 + ref64.abs() * 1.01 * 2.0 ** -24
+    if dtype is torch.bfloat16:
+        tol = tol * (1 + 2.0 ** -8) + ref64.abs() * 2.0 ** -8
+    assert bool(((got[:R].double() - ref64).abs() <= tol + 1e-30).all())
+
+
+@pytest.mark.parametrize("path", ["auto", "small", "large", "large_pair"])
+@pytest.mark.parametrize("kw", [
+    dict(rows=1, E=1, N=8, Kd=16),
+    dict(rows=1, E=1, N=4096, Kd=7168, a="bf16"),
+    dict(rows=2, E=1, N=1000, Kd=1456, a="bf16", bias=True),
+    dict(rows=5, E=1, N=264, Kd=4112, a="bf16"),
+    dict(rows=8, E=1, N=520, Kd=8192, a="bf16"),
+    dict(rows=9, E=1, N=520, Kd=8208, a="bf16"),
+    dict(rows=7, E=1, N=72, Kd=144),
+    dict(rows=17, E=1, N=1040, Kd=2048, bias=True),
+    dict(rows=31, E=2, N=136, Kd=272, a="bf16"),
+    dict(rows=33, E=1, N=4096, Kd=1024),
+    dict(rows=64, E=1, N=7168, Kd=2048),
+    dict(rows=100, E=3, N=392, Kd=5008, a="bf16", bias=True),
+    dict(rows=130, E=1, N=256, Kd=16384, a="bf16"),
+    dict(rows=300, E=40, N=136, Kd=400),
+    dict(rows=257, E=1, N=1000, Kd=1456, bias=True),
+    dict(rows=600, E=3, N=4104, Kd=528, a="bf16"),
+], ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_definition(B, path, kw):
+    for dtype in (torch.bfloat16, torch.float32):
+        check(B, make(**kw), path, dtype)
+
+
+@pytest.mark.parametrize("counts", [[0, 0, 0], [0, 5, 0], [1, 0, 9], [33, 2, 0], [0, 0, 140]], ids=str)
+@pytest.mark.parametrize("path", ["auto", "small", "large", "large_pair"])
+def test_empty_groups_and_rows_behind_the_last(B, path, counts):
+    for a in ("int8", "bf16"):
+        check(B, make(sum(counts) + 3, 3, 200, 336, a=a, counts=counts, bias=True), path, torch.float32)
+
+
+@pytest.mark.parametrize("path", ["small", "large", "large_pair"])
+@pytest.mark.parametrize("rows", [1, 4, 6, 12, 30, 64, 128])
+def test_sums_are_exact(B, path, rows):
+    """Nearly every product is (-128) * (-128): sums of 1024 of them are just
+    under 2^24, the whole ones far beyond it."""
+    check(B, make(rows, 1, 136, 8192, extreme=True), path, torch.float32)
+
+
+def test_zero_rows_and_special_values(B):
+    d = make(6, 1, 64, 128, a="bf16")
+    d["a"][1] = 0.0
+    d["a"][2] = 0.0
+    d["a"][2, 5] = 3e38
+    d["a"][3] *= 1e-38
+    for path in ("small", "large_pair"):
+        check(B, d, path, torch.float32)
+
+
+def test_no_rows(B):
+    d = make(0, 2, 64, 128)
+    _, packed = B.pack_int8(d["w"])
+    out, _ = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"])
+    assert out.shape == (0, 64)
+
+
+def test_split_tiles_many_times(B):
+    """The CTAs that share a tile's inner dimension meet at a counter that every
+    call clears: the same bits whatever the workspace held."""
+    d = make(64, 1, 1024, 4096)
+    _, packed = B.pack_int8(d["w"], path="small")
+    ref, ws = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], path="small")
+    want, _ = reference(d, torch.bfloat16)
+    assert torch.equal(ref, want)
+    for fill in (0, 1, 0xff):
+        ws.fill_(fill)
+        for _ in range(20):
+            got, _ = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], ws=ws,
+                                         path="small")
+        assert torch.equal(got, want)
