@@ -60,49 +60,65 @@ moe_status check_int8(int64_t E, int64_t N, int64_t Kd) {
     return MOE_OK;
 }
 
-// How a call multiplies.
-enum class How { Stream, Tiles, Large };
-#ifndef MOE_STREAM_ROWS
-#define MOE_STREAM_ROWS 32
-#endif
-#ifndef MOE_TILE_ROWS
-#define MOE_TILE_ROWS 128
-#endif
-How how(int path, int64_t rows, int64_t E) {
-    if (path == MOE_FFN_PATH_LARGE || path == MOE_FFN_PATH_LARGE_PAIR) return How::Large;
-    if (rows <= MOE_STREAM_ROWS * E) return How::Stream;
-    return path == MOE_FFN_PATH_SMALL || rows <= MOE_TILE_ROWS * E ? How::Tiles : How::Large;
-}
-
 // CTAs that share a tile's inner dimension where the tiles are too few for the GPU.
 constexpr int kMaxSplits = 8;
 struct Split {
-    int64_t tiles;
+    int64_t tiles;             // at most
+    int64_t likely;            // with the rows spread evenly
     int splits;
+    size_t words() const { return splits > 1 ? (size_t)tiles * 8 : 0; }
 };
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 Split split_of(int64_t rows, int64_t E, int64_t N, int64_t Kd) {
-    const int64_t tb = rows > 32 * E ? 128 : 64;
+    const int64_t tb = small_tile_rows(rows, E), cols = ceil_div(N, 128), groups = std::max<int64_t>(1, std::min(E, rows));
     Split s;
-    s.tiles = (rows / tb + std::min(E, rows)) * ((N + 127) / 128);   // at most
-    const int64_t likely = std::max<int64_t>(1, (rows + tb - 1) / tb) * ((N + 127) / 128);
-    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(int64_t)num_sms() / std::max<int64_t>(1, likely),
-                                                           Kd / 512, kMaxSplits}));
+    s.tiles = (rows / tb + groups) * cols;
+    s.likely = groups * ceil_div(ceil_div(rows, groups), tb) * cols;
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({num_sms() / std::max<int64_t>(1, s.likely), Kd / 512, kMaxSplits}));
     return s;
 }
 
+// How a call multiplies, measured (us, bf16 rows of one group):
+//   N x Kd          rows     stream  tiles  large
+//   4096 x 7168       16       13.3   15.4   44.9
+//                     24       17.5   14.9   43.7
+//                    256       92.2   27.3   47.4
+//                   1024      334     68.5   53.6
+//   7168 x 2048       32       11.6   12.4   20.8
+//                     64       18.7   12.7   21.9
+//                    512      118     25.3   23.4
+//   1536 x 2048      128       11.7   12.6   20.6
+//                    256       18.6   13.5   21.0
+// The stream's time is that of its weights up to 8 rows a group; beyond, it grows with
+// the products, and the tiles overtake it at about 4.8e8 of them, where their 4 us
+// more of preparation are won back.  Tiles and large tiles go by an estimate: the
+// waves of tiles x blocks of K x the time a block takes (0.55 us of 128 channels x 128
+// rows on one SM, 0.74 us of 256 x 256 on a pair, under the power cap).
+enum class How { Stream, Tiles, Large };
+How how(int path, int64_t rows, int64_t E, int64_t N, int64_t Kd, const Split &sp) {
+    if (path == MOE_FFN_PATH_LARGE || path == MOE_FFN_PATH_LARGE_PAIR) return How::Large;
+    if (rows <= 8 * E || (double)rows * (double)N * (double)Kd <= 4.8e8) return How::Stream;
+    if (path == MOE_FFN_PATH_SMALL) return How::Tiles;
+    const int64_t groups = std::min(E, rows), per = ceil_div(rows, groups);
+    const double kb = (double)ceil_div(Kd, 128);
+    const double tiles = 8.0 + (double)ceil_div(sp.likely * sp.splits, num_sms()) * kb / sp.splits * 0.55;
+    const double large = 9.0 + (double)ceil_div(groups * ceil_div(per, 256) * ceil_div(N, 256), num_sms() / 2) * kb * 0.74;
+    return tiles <= large ? How::Tiles : How::Large;
+}
+
 struct Int8Layout {
-    size_t status, sched, rows, scales, arrived, partial, total;
+    size_t status, sched, rows, scales, sums, total;
+    size_t clear;              // words behind `sums` that a split call has cleared: sums, arrivals
 };
 Int8Layout int8_layout(int64_t rows, int64_t E, int64_t N, int64_t Kd, const Split &sp) {
     Int8Layout L;
     Carve c;
-    const int64_t tb = rows > 32 * E ? 128 : 64;
     L.status = c.take(4);
     L.sched = c.take((size_t)(E + 1) * sizeof(int32_t));
     L.rows = c.take((size_t)rows * Kd * 2);
     L.scales = c.take((size_t)rows * sizeof(float));
-    L.arrived = c.take(sp.splits > 1 ? (size_t)sp.tiles * 8 * sizeof(uint32_t) : 0);
-    L.partial = c.take(sp.splits > 1 ? (size_t)sp.tiles * sp.splits * tb * 128 * sizeof(int32_t) : 0);
+    L.clear = sp.splits > 1 ? (size_t)rows * ((N + 127) / 128 * 128) + sp.words() : 0;
+    L.sums = c.take(L.clear * sizeof(uint32_t));
     L.total = c.off;
     return L;
 }
@@ -217,7 +233,7 @@ moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
     const Split sp = split_of(rows, E, N, Kd);
     const Int8Layout L = int8_layout(rows, E, N, Kd, sp);
     int32_t *status = at<int32_t>(workspace, L.status);
-    const How way = how(path, rows, E);
+    const How way = how(path, rows, E, N, Kd, sp);
     const uint8_t *bytes = static_cast<const uint8_t *>(w_packed) + (has_images(path) ? image_bytes(E, N, Kd) : 0);
     if (way == How::Stream) {
         Int8FewArgs f{};
@@ -241,13 +257,14 @@ moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
             f.rows = at<void>(workspace, L.rows);
             f.row_scales = at<float>(workspace, L.scales);
             f.rows_bf16 = false;
+            f.early = true;
         }
         return launch_int8_few(f, stream);
     }
     const bool split = way == How::Tiles && sp.splits > 1;
     MOE_TRY(launch_rows_to_f16(A, bf16, a_scales, expert_offsets, E, rows, Kd, at<void>(workspace, L.rows),
-                               at<float>(workspace, L.scales), status, at<uint32_t>(workspace, L.arrived),
-                               split ? sp.tiles * 8 : 0, stream));
+                               at<float>(workspace, L.scales), status, at<uint32_t>(workspace, L.sums),
+                               split ? (int64_t)L.clear : 0, stream));
     GemmArgs g{};
     g.a_img = at<void>(workspace, L.rows);
     g.cap_rows = rows;
@@ -265,8 +282,8 @@ moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
     g.status = status;
     if (way == How::Tiles) {
         g.splits = split ? sp.splits : 1;
-        g.partial = at<int32_t>(workspace, L.partial);
-        g.arrived = at<uint32_t>(workspace, L.arrived);
+        g.partial = at<int32_t>(workspace, L.sums);
+        g.arrived = at<uint32_t>(workspace, L.sums) + (L.clear - sp.words());
         return launch_grouped_gemm_small(Epi::Linear, g, stream);
     }
     const bool pair = path != MOE_FFN_PATH_LARGE && linear_pairs_fit();

@@ -318,8 +318,8 @@ struct GemmArgs {
     // the int8-weight GEMM on a grid too small for the GPU: `splits` CTAs share a
     // tile's inner dimension (Linear only)
     int splits;               // 0 or 1: none
-    int32_t *partial;         // [tiles, splits, tile] sums
-    uint32_t *arrived;        // [tiles, 8], cleared before the call
+    int32_t *partial;         // [cap_rows, Nout rounded up to 128] sums, cleared before the call
+    uint32_t *arrived;        // [tiles, 8], cleared too
 };
 // pair: 256-row tiles on clusters of two CTAs (falls back to one-SM tiles when
 // no cluster of that kernel fits).
@@ -332,6 +332,7 @@ bool linear_pairs_fit();
 // into tensor memory and are the MMA's M side; the expert's rows are its N
 // side, only as many as present.  Kd % 16 == 0 (and Nout % 128 == 0 for the
 // SwiGLU epilogue).
+int small_tile_rows(int64_t rows, int64_t E);   // Linear: 64 or 128
 moe_status launch_grouped_gemm_small(Epi epi, const GemmArgs &a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- a few tokens
@@ -367,6 +368,8 @@ struct Int8FewArgs {
     void *c;                   // [cap_rows, N]
     bool out_bf16;
     int32_t *status;           // cleared
+    bool early;                // not the call's first kernel: offsets, weights and their scales
+                               // were final before the kernel before this one began
 };
 bool int8_few_local(int64_t rows, int64_t E, int64_t Kd);
 moe_status launch_int8_few(const Int8FewArgs &a, cudaStream_t stream);

@@ -312,60 +312,64 @@ k_few_gate_up(FewDev p) {
     // the stages to fetch, batch by batch
     const uint64_t once = l2_policy_evict_first();
     auto copy_weights = [&](uint32_t dst, const void *src, bool in) { copy16_once(dst, src, in, once); };
-    int f_batch = u_begin, f_unit = 0, f_ks = 0, f_left = 0;
-    const uint8_t *f_src = nullptr;                      // the lane's bytes of the next stage
-    const int8_t *f_row[2] = {nullptr, nullptr};         // and of the rows, where they are
+    struct Next {
+        int batch, unit, ks, left;
+        const uint8_t *src;          // the lane's bytes of the next stage
+        const int8_t *row[2];        // and of the rows, where they are
+    } f = {u_begin, 0, 0, 0, nullptr, {nullptr, nullptr}};
     auto enter = [&]() {
-        const int blk = p.by_units(f_unit), j = (f_unit - blk * NU) * 8;
+        const int blk = p.by_units(f.unit), j = (f.unit - blk * NU) * 8;
         const int64_t prow = (int64_t)r.blk_e[blk] * (2 * p.Nh) + (j >> 6) * 128 + ((j >> 4) & 3) * 32 + (j & 15);
-        f_src = p.w1 + (prow + l.cr) * H + f_ks * kDepth + l.cu * 16;
+        f.src = p.w1 + (prow + l.cr) * H + f.ks * kDepth + l.cu * 16;
         if (!LOCAL) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = 4 * i + l.cr;
-                f_row[i] = nullptr;
+                f.row[i] = nullptr;
                 if (row < r.blk_n[blk])
-                    f_row[i] = p.q + (int64_t)p.by_k(r.list[r.blk_first[blk] + row]) * H + f_ks * kDepth + l.cu * 16;
+                    f.row[i] = p.q + (int64_t)p.by_k(r.list[r.blk_first[blk] + row]) * H + f.ks * kDepth + l.cu * 16;
             }
         }
     };
-    if (u_begin < u_end) share(u_begin, f_unit, f_ks, f_left);
-    if (f_left > 0) enter();
-    auto fetch = [&](uint32_t slot) {
-        if (f_left == 0) {
-            while (f_left == 0 && f_batch + kBatchUnits < u_end) {
-                f_batch += kBatchUnits;
-                share(f_batch, f_unit, f_ks, f_left);
+    if (u_begin < u_end) share(u_begin, f.unit, f.ks, f.left);
+    if (f.left > 0) enter();
+    auto fetch = [&](uint32_t slot, bool weights, bool rows) {
+        if (f.left == 0) {
+            while (f.left == 0 && f.batch + kBatchUnits < u_end) {
+                f.batch += kBatchUnits;
+                share(f.batch, f.unit, f.ks, f.left);
             }
-            if (f_left == 0) return;
+            if (f.left == 0) return;
             enter();
         }
-        const bool in = f_ks * kDepth + l.cu * 16 < H;
-        copy_weights(slot + l.to0, f_src, in);
-        copy_weights(slot + l.to1, f_src + (int64_t)4 * H, in);
-        copy_weights(slot + l.to0 + 8 * kDepth, f_src + (int64_t)16 * H, in);
-        copy_weights(slot + l.to1 + 8 * kDepth, f_src + (int64_t)20 * H, in);
-        f_src += kDepth;
-        if (!LOCAL) {
-            if (f_row[0]) {
-                copy16(slot + l.to0 + kWeightBytes, f_row[0], in);
-                f_row[0] += kDepth;
+        const bool in = f.ks * kDepth + l.cu * 16 < H;
+        if (weights) {
+            copy_weights(slot + l.to0, f.src, in);
+            copy_weights(slot + l.to1, f.src + (int64_t)4 * H, in);
+            copy_weights(slot + l.to0 + 8 * kDepth, f.src + (int64_t)16 * H, in);
+            copy_weights(slot + l.to1 + 8 * kDepth, f.src + (int64_t)20 * H, in);
+        }
+        f.src += kDepth;
+        if (!LOCAL && rows) {
+            if (f.row[0]) {
+                copy16(slot + l.to0 + kWeightBytes, f.row[0], in);
+                f.row[0] += kDepth;
             }
-            if (f_row[1]) {
-                copy16(slot + l.to1 + kWeightBytes, f_row[1], in);
-                f_row[1] += kDepth;
+            if (f.row[1]) {
+                copy16(slot + l.to1 + kWeightBytes, f.row[1], in);
+                f.row[1] += kDepth;
             }
         }
-        --f_left;
-        if (++f_ks == KS) {
-            f_ks = 0;
-            ++f_unit;
-            if (f_left > 0) enter();
+        --f.left;
+        if (++f.ks == KS) {
+            f.ks = 0;
+            ++f.unit;
+            if (f.left > 0) enter();
         }
     };
     Walk<C::kD, C::kBytes, LOCAL> walk(smem_u32(smem) + (uint32_t)(warp * C::kD * C::kBytes));
     if (LOCAL) {
-        walk.first(fetch);
+        walk.first(fetch, true, true);
         // the tokens' codes, in every CTA
         if (xt < p.T) {
             float m = 0.0f;
@@ -397,8 +401,12 @@ k_few_gate_up(FewDev p) {
         }
         __syncthreads();
     } else {
+        // the weights before the wait, the rows that the kernel before this one makes after it
+        const Next start = f;
+        walk.first(fetch, true, false);
+        f = start;
         pdl_wait();
-        walk.first(fetch);
+        walk.first(fetch, false, true);
     }
 
     int buf = 0;
@@ -478,60 +486,64 @@ k_few_down(FewDev p) {
 
     const uint64_t once = l2_policy_evict_first();
     auto copy_weights = [&](uint32_t dst, const void *src, bool in) { copy16_once(dst, src, in, once); };
-    int f_batch = blockIdx.x, f_blk = 0, f_ks = 0, f_left = 0;
-    const uint8_t *f_src = nullptr;
-    const int8_t *f_row[2] = {nullptr, nullptr};
+    struct Next {
+        int batch, blk, ks, left;
+        const uint8_t *src;
+        const int8_t *row[2];
+    } f = {(int)blockIdx.x, 0, 0, 0, nullptr, {nullptr, nullptr}};
     auto enter = [&]() {
-        f_src = p.w2 + ((int64_t)r.blk_e[f_blk] * p.H + f_batch * kChannels + l.cr) * Nh + f_ks * kDepth + l.cu * 16;
+        f.src = p.w2 + ((int64_t)r.blk_e[f.blk] * p.H + f.batch * kChannels + l.cr) * Nh + f.ks * kDepth + l.cu * 16;
         if (!LOCAL) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = 4 * i + l.cr;
-                f_row[i] = nullptr;
-                if (row < r.blk_n[f_blk])
-                    f_row[i] = p.q + (int64_t)r.list[r.blk_first[f_blk] + row] * Nh + f_ks * kDepth + l.cu * 16;
+                f.row[i] = nullptr;
+                if (row < r.blk_n[f.blk])
+                    f.row[i] = p.q + (int64_t)r.list[r.blk_first[f.blk] + row] * Nh + f.ks * kDepth + l.cu * 16;
             }
         }
     };
     auto begin = [&]() {
-        f_left = mine_n;
-        f_blk = mine_blk;
-        f_ks = mine_ks;
-        if (f_left > 0) enter();
+        f.left = mine_n;
+        f.blk = mine_blk;
+        f.ks = mine_ks;
+        if (f.left > 0) enter();
     };
-    if (f_batch < batches) begin();
-    auto fetch = [&](uint32_t slot) {
-        if (f_left == 0) {
-            if (mine_n == 0 || f_batch + (int)gridDim.x >= batches) return;
-            f_batch += gridDim.x;
+    if (f.batch < batches) begin();
+    auto fetch = [&](uint32_t slot, bool weights, bool rows) {
+        if (f.left == 0) {
+            if (mine_n == 0 || f.batch + (int)gridDim.x >= batches) return;
+            f.batch += gridDim.x;
             begin();
         }
-        const bool in = f_ks * kDepth + l.cu * 16 < Nh;
-        copy_weights(slot + l.to0, f_src, in);
-        copy_weights(slot + l.to1, f_src + (int64_t)4 * Nh, in);
-        copy_weights(slot + l.to0 + 8 * kDepth, f_src + (int64_t)8 * Nh, in);
-        copy_weights(slot + l.to1 + 8 * kDepth, f_src + (int64_t)12 * Nh, in);
-        f_src += kDepth;
-        if (!LOCAL) {
-            if (f_row[0]) {
-                copy16(slot + l.to0 + kWeightBytes, f_row[0], in);
-                f_row[0] += kDepth;
+        const bool in = f.ks * kDepth + l.cu * 16 < Nh;
+        if (weights) {
+            copy_weights(slot + l.to0, f.src, in);
+            copy_weights(slot + l.to1, f.src + (int64_t)4 * Nh, in);
+            copy_weights(slot + l.to0 + 8 * kDepth, f.src + (int64_t)8 * Nh, in);
+            copy_weights(slot + l.to1 + 8 * kDepth, f.src + (int64_t)12 * Nh, in);
+        }
+        f.src += kDepth;
+        if (!LOCAL && rows) {
+            if (f.row[0]) {
+                copy16(slot + l.to0 + kWeightBytes, f.row[0], in);
+                f.row[0] += kDepth;
             }
-            if (f_row[1]) {
-                copy16(slot + l.to1 + kWeightBytes, f_row[1], in);
-                f_row[1] += kDepth;
+            if (f.row[1]) {
+                copy16(slot + l.to1 + kWeightBytes, f.row[1], in);
+                f.row[1] += kDepth;
             }
         }
-        --f_left;
-        if (++f_ks == KS) {
-            f_ks = 0;
-            ++f_blk;
-            if (f_left > 0) enter();
+        --f.left;
+        if (++f.ks == KS) {
+            f.ks = 0;
+            ++f.blk;
+            if (f.left > 0) enter();
         }
     };
     Walk<C::kD, C::kBytes, LOCAL> walk(smem_u32(smem) + (uint32_t)(warp * C::kD * C::kBytes));
     if (LOCAL) {
-        walk.first(fetch);
+        walk.first(fetch, true, true);
         pdl_wait();
         // the routes' codes, a row to a warp
         const int n8 = Nh / 8;
@@ -576,8 +588,12 @@ k_few_down(FewDev p) {
             }
         }
     } else {
+        // the weights before the wait, the rows that the kernel before this one makes after it
+        const Next start = f;
+        walk.first(fetch, true, false);
+        f = start;
         pdl_wait();
-        walk.first(fetch);
+        walk.first(fetch, false, true);
         for (int i = tid; i < r.rows; i += kThreads) scale[i] = __ldcg(p.qs + r.list[i]);
     }
     __syncthreads();

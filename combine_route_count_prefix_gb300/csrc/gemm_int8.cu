@@ -22,7 +22,7 @@ namespace {
 using namespace si8;
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr size_t kLocalBytes = 64 * 1024;
+constexpr int kXVecs = 5;        // vectors of eight values of a row that a LOCAL thread holds
 
 struct Int8FewDev {
     const uint4 *x;            // bf16 rows (LOCAL)
@@ -34,18 +34,18 @@ struct Int8FewDev {
     void *c;
     int32_t *status;
     int64_t cap_rows;
-    int E, N, Kd, out_bf16;
+    int E, N, Kd, out_bf16, early;
     Divisor by_units, by_stages;
 };
 
 template <bool LOCAL, int NB>
 struct Cfg {
-    static constexpr int kWarps = NB == 1 ? 12 : 8;
+    static constexpr int kWarps = NB == 1 ? 12 : NB == 2 ? 12 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kD = NB == 1 ? 5 : 4;
     static constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : NB * kRowBytes);
     static constexpr int kRing = kWarps * kD * kBytes;
-    static constexpr int kUnits = NB == 1 ? 16 : 4;      // between two block barriers
+    static constexpr int kUnits = NB == 1 ? 16 : NB == 2 ? 8 : 4;      // between two block barriers
     static constexpr int kMaxRows = NB * kRows;
 };
 
@@ -79,8 +79,18 @@ k_int8_few(Int8FewDev p) {
 
     for (int i = tid; i < 2 * kUnits * kMaxRows * kChannels; i += kThreads) (&acc[0][0][0][0])[i] = 0;
     if (LOCAL && tid < kRows) amax[tid] = 0;
-    pdl_wait();
-    if (blockIdx.x == 0 && tid == 0) *p.status = 0;
+    // early: the kernel before this one (the rows' codes) has waited for everything else
+    if (!p.early) pdl_wait();
+    // LOCAL: one group of a few rows, each shared by `group` warps; this one's part of
+    // row xt starts at vector x0
+    const int k8 = Kd / 8, group = kWarps / (int)min(p.cap_rows, (int64_t)kWarps), xt = warp / group;
+    const int x0 = (warp - xt * group) * 32 + lane;
+    uint4 xv[LOCAL ? kXVecs : 1];
+    if (LOCAL && xt < p.cap_rows) {
+#pragma unroll
+        for (int u = 0; u < kXVecs; ++u)
+            if (x0 + 32 * group * u < k8) xv[u] = p.x[(int64_t)xt * k8 + x0 + 32 * group * u];
+    }
     for (int i = tid; i <= p.E; i += kThreads) s_off[i] = (int)min((int64_t)p.offsets[i], p.cap_rows);
     __syncthreads();
     if (warp == 0) {   // s_blk[e]: row blocks of the groups before e
@@ -129,87 +139,102 @@ k_int8_few(Int8FewDev p) {
         n = b - a;
     };
     const uint64_t once = l2_policy_evict_first();
-    int64_t f_batch = u_begin, f_unit = 0;
-    int f_ks = 0, f_left = 0, f_rows = 0, f_ch = 0;
-    const uint8_t *f_src = nullptr;
-    const int8_t *f_row = nullptr;
+    struct Next {
+        int64_t batch, unit;
+        int ks, left, rows, ch;
+        const uint8_t *src;          // the lane's bytes of the next stage
+        const int8_t *row;           // and of the rows
+    } f = {u_begin, 0, 0, 0, 0, 0, nullptr, nullptr};
     auto enter = [&]() {
-        const At a = find(f_unit);
-        f_ch = a.ch;
-        f_src = p.w + ((int64_t)a.e * p.N + a.ch + l.cr) * Kd + f_ks * kDepth + l.cu * 16;
+        const At a = find(f.unit);
+        f.ch = a.ch;
+        f.src = p.w + ((int64_t)a.e * p.N + a.ch + l.cr) * Kd + f.ks * kDepth + l.cu * 16;
         if (!LOCAL) {
-            f_rows = a.rows;
-            f_row = p.q + (int64_t)(a.row0 + l.cr) * Kd + f_ks * kDepth + l.cu * 16;
+            f.rows = a.rows;
+            f.row = p.q + (int64_t)(a.row0 + l.cr) * Kd + f.ks * kDepth + l.cu * 16;
         }
     };
-    if (u_begin < u_end) share(u_begin, f_unit, f_ks, f_left);
-    if (f_left > 0) enter();
-    auto fetch = [&](uint32_t slot) {
-        if (f_left == 0) {
-            while (f_left == 0 && f_batch + kUnits < u_end) {
-                f_batch += kUnits;
-                share(f_batch, f_unit, f_ks, f_left);
+    if (u_begin < u_end) share(u_begin, f.unit, f.ks, f.left);
+    if (f.left > 0) enter();
+    auto fetch = [&](uint32_t slot, bool weights, bool rows) {
+        if (f.left == 0) {
+            while (f.left == 0 && f.batch + kUnits < u_end) {
+                f.batch += kUnits;
+                share(f.batch, f.unit, f.ks, f.left);
             }
-            if (f_left == 0) return;
+            if (f.left == 0) return;
             enter();
         }
-        const bool in = f_ks * kDepth + l.cu * 16 < Kd;
-        const bool in8 = in && f_ch + 8 < p.N;    // N is a multiple of 8
-        copy16_once(slot + l.to0, f_src, in, once);
-        copy16_once(slot + l.to1, f_src + (int64_t)4 * Kd, in, once);
-        copy16_once(slot + l.to0 + 8 * kDepth, f_src + (int64_t)8 * Kd, in8, once);
-        copy16_once(slot + l.to1 + 8 * kDepth, f_src + (int64_t)12 * Kd, in8, once);
-        f_src += kDepth;
-        if (!LOCAL) {
+        const bool in = f.ks * kDepth + l.cu * 16 < Kd;
+        const bool in8 = in && f.ch + 8 < p.N;    // N is a multiple of 8
+        if (weights) {
+            copy16_once(slot + l.to0, f.src, in, once);
+            copy16_once(slot + l.to1, f.src + (int64_t)4 * Kd, in, once);
+            copy16_once(slot + l.to0 + 8 * kDepth, f.src + (int64_t)8 * Kd, in8, once);
+            copy16_once(slot + l.to1 + 8 * kDepth, f.src + (int64_t)12 * Kd, in8, once);
+        }
+        f.src += kDepth;
+        if (!LOCAL && rows) {
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                if (n * kRows + l.cr < f_rows)
-                    copy16(slot + l.to0 + kWeightBytes + n * kRowBytes, f_row + (int64_t)(n * kRows) * Kd, in);
-                if (n * kRows + 4 + l.cr < f_rows)
-                    copy16(slot + l.to1 + kWeightBytes + n * kRowBytes, f_row + (int64_t)(n * kRows + 4) * Kd, in);
+                if (n * kRows + l.cr < f.rows)
+                    copy16(slot + l.to0 + kWeightBytes + n * kRowBytes, f.row + (int64_t)(n * kRows) * Kd, in);
+                if (n * kRows + 4 + l.cr < f.rows)
+                    copy16(slot + l.to1 + kWeightBytes + n * kRowBytes, f.row + (int64_t)(n * kRows + 4) * Kd, in);
             }
-            f_row += kDepth;
         }
-        --f_left;
-        if (++f_ks == KS) {
-            f_ks = 0;
-            ++f_unit;
-            if (f_left > 0) enter();
+        if (!LOCAL) f.row += kDepth;
+        --f.left;
+        if (++f.ks == KS) {
+            f.ks = 0;
+            ++f.unit;
+            if (f.left > 0) enter();
         }
     };
     Walk<C::kD, C::kBytes, LOCAL> walk(smem_u32(smem) + (uint32_t)(warp * C::kD * C::kBytes));
-    walk.first(fetch);
+    if (!p.early) {
+        walk.first(fetch, true, true);
+    } else {
+        // the weights before the wait, the rows after it
+        const Next start = f;
+        walk.first(fetch, true, false);
+        f = start;
+        pdl_wait();
+        walk.first(fetch, false, true);
+    }
+    if (blockIdx.x == 0 && tid == 0) *p.status = 0;
     if (LOCAL) {
-        // one group of at most kRows rows: its codes, in every CTA, kWarps / rows warps a row
-        const int rows = s_off[1] - s_off[0], k8 = Kd / 8, group = rows > 0 ? kWarps / rows : 1, t = warp / group;
-        const int first = (warp - t * group) * 32 + lane;
-        const uint4 *src = p.x + (int64_t)(s_off[0] + t) * k8;
-        if (t < rows) {
+        // the rows' codes, in every CTA
+        if (xt < p.cap_rows) {
             float m = 0.0f;
-#pragma unroll 4
-            for (int i = first; i < k8; i += 32 * group) {
-                float v[8];
-                unpack8(src[i], v);
-                m = max8(v, m);
-            }
+#pragma unroll
+            for (int u = 0; u < kXVecs; ++u)
+                if (x0 + 32 * group * u < k8) {
+                    float v[8];
+                    unpack8(xv[u], v);
+                    m = max8(v, m);
+                }
             const uint32_t w = __reduce_max_sync(kFull, __float_as_uint(m));
-            if (lane == 0) atomicMax(&amax[t], w);
+            if (lane == 0) atomicMax(&amax[xt], w);
         }
         __syncthreads();
-        if (t < rows) {
-            const float s = __fdiv_rn(__uint_as_float(amax[t]), 127.0f), rs = __frcp_rn(s);
-#pragma unroll 1
-            for (int i = first; i < pitch / 8; i += 32 * group) {
-                uint2 q = make_uint2(0, 0);
+        if (xt < p.cap_rows) {
+            const float s = __fdiv_rn(__uint_as_float(amax[xt]), 127.0f), rs = __frcp_rn(s);
+            auto put = [&](int i, uint2 q) {
+                *reinterpret_cast<uint2 *>(codes + (size_t)xt * pitch + (i >> 4) * kDepth +
+                                           unit_at(xt, (i >> 1) & 7) + (i & 1) * 8) = q;
+            };
+#pragma unroll
+            for (int u = 0; u < kXVecs; ++u) {
+                const int i = x0 + 32 * group * u;
                 if (i < k8) {
                     float v[8], c[8];
-                    unpack8(src[i], v);
+                    unpack8(xv[u], v);
                     quant_codes<8>(v, s, rs, c);
-                    q = make_uint2(pack_i8x4(c[0], c[1], c[2], c[3]), pack_i8x4(c[4], c[5], c[6], c[7]));
+                    put(i, make_uint2(pack_i8x4(c[0], c[1], c[2], c[3]), pack_i8x4(c[4], c[5], c[6], c[7])));
                 }
-                *reinterpret_cast<uint2 *>(codes + (size_t)t * pitch + (i >> 4) * kDepth +
-                                           unit_at(t, (i >> 1) & 7) + (i & 1) * 8) = q;
             }
+            for (int i = k8 + x0; i < pitch / 8; i += 32 * group) put(i, make_uint2(0, 0));
         }
         __syncthreads();
     }
@@ -342,7 +367,8 @@ int64_t padded(int64_t k) { return (k + kDepth - 1) / kDepth * kDepth; }
 }  // namespace
 
 bool int8_few_local(int64_t rows, int64_t E, int64_t Kd) {
-    return E == 1 && rows <= kRows && rows * padded(Kd) <= (int64_t)kLocalBytes;
+    constexpr int kWarps = Cfg<true, 1>::kWarps;
+    return E == 1 && rows <= kRows && Kd / 8 <= kXVecs * 32 * (kWarps / rows);
 }
 
 moe_status launch_int8_few(const Int8FewArgs &a, cudaStream_t stream) {
@@ -361,16 +387,20 @@ moe_status launch_int8_few(const Int8FewArgs &a, cudaStream_t stream) {
     p.N = (int)a.N;
     p.Kd = (int)a.Kd;
     p.out_bf16 = a.out_bf16;
+    p.early = a.early;
     p.by_units = Divisor((uint32_t)((a.N + kChannels - 1) / kChannels));
     p.by_stages = Divisor((uint32_t)(padded(a.Kd) / kDepth));
     if (a.rows_bf16) return launch<true, 1>(p, (size_t)(a.cap_rows * padded(a.Kd)), stream);
-    return a.cap_rows <= kRows * a.E ? launch<false, 1>(p, 0, stream) : launch<false, 4>(p, 0, stream);
+    if (a.cap_rows <= kRows * a.E) return launch<false, 1>(p, 0, stream);
+    return a.cap_rows <= 2 * kRows * a.E ? launch<false, 2>(p, 0, stream) : launch<false, 4>(p, 0, stream);
 }
 
 moe_status launch_rows_to_f16(const void *rows, bool bf16, const float *scales, const int32_t *offsets,
                               int64_t E, int64_t cap_rows, int64_t Kd, void *img, float *img_scales,
                               int32_t *status, uint32_t *clear, int64_t n_clear, cudaStream_t stream) {
-    const unsigned grid = (unsigned)std::min<int64_t>(cap_rows, (int64_t)num_sms() * 8);
+    // (the CTAs without a row help to clear)
+    const int64_t clearers = std::min<int64_t>(num_sms() * 2, (n_clear + 2047) / 2048);
+    const unsigned grid = (unsigned)std::min<int64_t>(std::max(cap_rows, clearers), (int64_t)num_sms() * 8);
     if (bf16) {
         MOE_LAUNCH("rows_to_f16", k_rows_to_f16<true>, grid, kImgThreads, 0, stream, rows, scales, offsets, E,
                    cap_rows, Kd, static_cast<uint4 *>(img), img_scales, status, clear, n_clear);

@@ -204,16 +204,21 @@ __device__ __forceinline__ void epilogue_small(const SmallDev &p, const Tile &t,
         const bool in = ch < p.Nout;
         const float sc = in ? __ldg(p.scale2 + (int64_t)t.e * p.Nout + ch) : 0.0f;
         const float bias = in && p.bias ? __ldg(p.bias + (int64_t)t.e * p.Nout + ch) : 0.0f;
+        const int n = (int)min((int64_t)(t.rows - c0), p.cap_rows - t.row0 - c0);
+        int64_t o = ((int64_t)t.row0 + c0) * p.Nout + ch;
 #pragma unroll
-        for (int i = 0; i < EPI_COLS; ++i) {
-            if (c0 + i >= t.rows) break;
-            const int64_t row = (int64_t)t.row0 + c0 + i;
-            if (row >= p.cap_rows) break;
-            float v = __fmul_rn(__fmul_rn(__int2float_rn(acc[i]), sc), __ldg(p.s2 + row));
-            if (p.bias) v = __fadd_rn(v, bias);
-            if (in) {
-                if (p.y32) p.y32[row * p.Nout + ch] = v;
-                else p.y[row * p.Nout + ch] = __float2bfloat16_rn(v);
+        for (int h = 0; h < EPI_COLS / 32; ++h) {
+            // one load for the scales of 32 rows
+            const float s_lane = 32 * h + lane < n ? __ldg(p.s2 + t.row0 + c0 + 32 * h + lane) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i, o += p.Nout) {
+                const float s2 = __shfl_sync(0xffffffffu, s_lane, i);
+                float v = __fmul_rn(__fmul_rn(__int2float_rn(acc[32 * h + i]), sc), s2);
+                if (p.bias) v = __fadd_rn(v, bias);
+                if (in && 32 * h + i < n) {
+                    if (p.y32) p.y32[o] = v;
+                    else p.y[o] = __float2bfloat16_rn(v);
+                }
             }
         }
     } else {
@@ -229,18 +234,23 @@ __device__ __forceinline__ void epilogue_small(const SmallDev &p, const Tile &t,
     }
 }
 
-// Where several CTAs share a tile's inner dimension: each epilogue warp leaves its
-// sums, and the last of the same warps of the tile's CTAs adds the others' to its own
-// (integers: in any order the same).  True for that one.
+// Where several CTAs share a tile's inner dimension, each epilogue warp adds its
+// sums to the call's (cleared before it; integers, so in any order the same),
+// and the last of the same warps of the tile's CTAs takes the whole sums.  True for
+// that one.  (Left apart and added by the last, the parts cost it 64 waits for L2 each:
+// 64 rows, 1536 x 2048 in eight parts took 46 us.)
 template <int TB, int EPI_COLS>
 __device__ __forceinline__ bool join_splits(const SmallDev &p, const Tile &t, int ew, int q, int lane,
                                             int c0, int32_t (&acc)[EPI_COLS]) {
-    // [tile][split][row][channel]
-    const int64_t size = (int64_t)TB * BW;
-    int32_t *mine = p.partial + (t.index * p.splits + t.split) * size + (int64_t)c0 * BW + q * 32 + lane;
+    const int64_t pitch = (int64_t)p.n_wblocks * BW;
+    int32_t *sum = p.partial + ((int64_t)t.row0 + c0) * pitch + t.wb * BW + q * 32 + lane;
+    const int n = (int)min((int64_t)(t.rows - c0), p.cap_rows - t.row0 - c0);
+    int32_t *at = sum;
 #pragma unroll
-    for (int i = 0; i < EPI_COLS; ++i)
-        if (c0 + i < t.rows) __stcg(mine + (int64_t)i * BW, acc[i]);
+    for (int i = 0; i < EPI_COLS; ++i, at += pitch) {
+        asm volatile("" : "+l"(at));   // one address after another, not all of them in registers
+        if (i < n) asm volatile("red.global.add.s32 [%0], %1;" ::"l"(at), "r"(acc[i]) : "memory");
+    }
     __threadfence();
     __syncwarp();
     uint32_t before = 0;
@@ -248,12 +258,12 @@ __device__ __forceinline__ bool join_splits(const SmallDev &p, const Tile &t, in
     before = __shfl_sync(0xffffffffu, before, 0);
     if (before != (uint32_t)p.splits - 1) return false;
     __threadfence();
-    for (int s = 0; s < p.splits; ++s) {
-        if (s == t.split) continue;
-        const int32_t *other = p.partial + (t.index * p.splits + s) * size + (int64_t)c0 * BW + q * 32 + lane;
+    at = sum;
 #pragma unroll
-        for (int i = 0; i < EPI_COLS; ++i)
-            if (c0 + i < t.rows) acc[i] += __ldcg(other + (int64_t)i * BW);
+    for (int j = 0; j < EPI_COLS; j += 16) {   // 16 loads at once, no more registers
+#pragma unroll
+        for (int i = j; i < j + 16; ++i, at += pitch) acc[i] = i < n ? __ldcg(at) : 0;
+        asm volatile("" : "+l"(at)::"memory");
     }
     return true;
 }
@@ -312,7 +322,11 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmRows) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmW) : "memory");
     }
-    pdl_wait();   // everything below may read what earlier kernels wrote
+    // Linear: the kernel before this one (the rows' images) has waited for everything
+    // else, so that only its own rows, scales and cleared sums are waited for, by those
+    // who read them; the weights are on their way meanwhile.
+    constexpr bool kEarly = EPI == (int)Epi::Linear;
+    if (!kEarly) pdl_wait();   // everything below may read what earlier kernels wrote
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x) s_off[i] = p.offsets[i];
     __syncthreads();
     if (warp == 0) {
@@ -370,6 +384,7 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
     } else if (warp == 2) {
         if (lane == 0) {
             // ------------------------------------------------ row producer
+            if (kEarly) pdl_wait();
             int stage = 0;
             uint32_t phase = 0;
             int issued_phase[SA];
@@ -484,6 +499,7 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
         }
     } else if (warp >= EPI_WARP0) {
         // ---------------------------------------------------- epilogue warps
+        if (kEarly) pdl_wait();
         const int q = warp & 3;
         const int c0 = ((warp - EPI_WARP0) >> 2) * EPI_COLS;   // first tile row of this warp
         int accb = 0;
@@ -561,13 +577,18 @@ moe_status launch_small_epi(const CUtensorMap &mr, const CUtensorMap &mw, const 
 
 }  // namespace
 
+// The Linear product's rows a tile: one group's rows are known, those of several
+// spread.
+int small_tile_rows(int64_t rows, int64_t E) { return rows > (E == 1 ? 64 : kNarrowTileMaxRowsPerExpert * E) ? 128 : 64; }
+
 moe_status launch_grouped_gemm_small(Epi epi, const GemmArgs &a, cudaStream_t stream) {
     if (a.cap_rows <= 0 || a.E <= 0) return MOE_OK;
     if (a.Kd % 16 != 0) return MOE_ERR_SHAPE;   // byte rows must be 16-byte strided for TMA
     if (epi == Epi::SwiGLU && a.Nout % 128 != 0) return MOE_ERR_SHAPE;
     // the row capacity bounds the rows present: 64-row tiles while it averages
     // at most 32 rows per expert, else 128-row tiles
-    const bool wide = a.cap_rows > kNarrowTileMaxRowsPerExpert * a.E;
+    const bool wide = epi == Epi::Linear ? small_tile_rows(a.cap_rows, a.E) > 64
+                                         : a.cap_rows > kNarrowTileMaxRowsPerExpert * a.E;
     CUtensorMap mr, mw;
     const uint64_t rdims[2] = {(uint64_t)a.Kd, (uint64_t)a.cap_rows};
     const uint64_t rstr[1] = {(uint64_t)a.Kd * 2};

@@ -506,7 +506,10 @@ k_grouped_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmA) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
     }
-    pdl_wait();   // everything below may read what earlier kernels wrote
+    // Linear: the kernel before this one (the rows' images) has waited for everything
+    // else; only those who read its rows and scales wait for it
+    constexpr bool kEarly = EPI == (int)Epi::Linear;
+    if (!kEarly) pdl_wait();   // everything below may read what earlier kernels wrote
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x) s_off[i] = p.offsets[i];
     __syncthreads();
     if (warp == 0) {
@@ -542,6 +545,7 @@ k_grouped_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     if (warp == 0) {
         if (lane == 0) {
             // ------------------------------------------------ TMA producer (both CTAs)
+            if (kEarly) pdl_wait();
             const uint32_t full0 = cluster_addr(full, 0);   // CTA 0's full[0]
             int stage = 0;
             uint32_t phase = 0;
@@ -618,6 +622,7 @@ k_grouped_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         }
     } else {
         // ---------------------------------------------------- epilogue warps (both CTAs)
+        if (kEarly) pdl_wait();
         const int q = warp & 3;
         const int hf = (warp - 2) >> 2;
         const int rloc = q * 32 + lane;

@@ -198,7 +198,7 @@ struct Lane {
 };
 
 // One warp's way through its stages.  The ring holds kD; stage i + kD - 1 is
-// fetched (fetch(slot)) once every lane has read stage i - 1, into its slot.
+// fetched once every lane has read stage i - 1, into its slot.
 // LOCAL: the rows' codes lie elsewhere in shared memory, stage after stage;
 // else they come with the weights, behind them in the slot.
 template <int kD, int kBytes, bool LOCAL>
@@ -206,19 +206,20 @@ struct Walk {
     uint32_t base, cur, prev;
     __device__ __forceinline__ explicit Walk(uint32_t b)
         : base(b), cur(b), prev(b + (uint32_t)((kD - 1) * kBytes)) {}
+    // The first kD - 1 stages.  fetch(slot, weights, rows) copies one or both and steps on.
     template <typename Fetch>
-    __device__ __forceinline__ void first(Fetch &fetch) {
+    __device__ __forceinline__ void first(Fetch &fetch, bool weights, bool rows) {
 #pragma unroll 1
         for (int i = 0; i < kD - 1; ++i) {
-            fetch(base + (uint32_t)(i * kBytes));
-            copy_commit();
+            fetch(base + (uint32_t)(i * kBytes), weights, rows);
+            if (rows) copy_commit();   // weights copied before belong to the first group then
         }
     }
     template <typename Fetch>
     __device__ __forceinline__ uint32_t next(Fetch &fetch) {
         copy_wait<kD - 2>();
         __syncwarp();
-        fetch(prev);
+        fetch(prev, true, true);
         copy_commit();
         prev = cur;
         cur = cur + kBytes == base + kD * kBytes ? base : cur + kBytes;
