@@ -43,6 +43,7 @@ EXPORTED = [
     "moe_layer_few_tokens_workspace_size", "moe_layer_few_tokens",
     "moe_int8_packed_bytes", "moe_pack_int8",
     "moe_grouped_gemm_int8_workspace_size", "moe_grouped_gemm_int8",
+    "moe_block_norm",
 ]
 
 
@@ -76,6 +77,15 @@ class MoeGateDesc(ctypes.Structure):
                 ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+class MoeBlockNormDesc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("gate_rows", ctypes.c_int64), ("gate_stride", ctypes.c_int64),
+                ("weight_dtype", ctypes.c_int32), ("gate_act", ctypes.c_int32),
+                ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+GATE_ACTS = {"none": 0, "sigmoid": 1}
 GATE_SCORES = {"softmax": 0, "sigmoid": 1}
 GATE_GROUP_SCORES = {"max": 0, "top2": 1}
 DTYPE_F32, DTYPE_BF16, DTYPE_I8 = 0, 1, 2
@@ -123,6 +133,7 @@ def lib():
         "moe_grouped_ffn_q": [SP, P, P, P, P, P, P, P, P, P, SZ, P],
         "moe_wait_selftest": [P, SZ, ctypes.c_uint64, P],
         "moe_add_rms_norm": [I64, I64, P, P, P, ctypes.c_int, ctypes.c_float, P, P, P, P, P],
+        "moe_block_norm": [ctypes.POINTER(MoeBlockNormDesc), P, P, P, P, P, P, P, P, P, P],
         "moe_gate": [ctypes.POINTER(MoeGateDesc), P, P, P, P, P, P, P],
         "moe_grouped_gemm_fp8_workspace_size": [I64, I64, I64, I64, ctypes.POINTER(SZ)],
         "moe_grouped_gemm_fp8": [I64, I64, I64, I64, P, P, P, P, P, P, ctypes.c_int, ctypes.c_int,
@@ -640,6 +651,65 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, out=None, with_y=True, with
     _call("moe_add_rms_norm", T, H, x.data_ptr(), _addr(residual), weight.data_ptr(),
           _DTYPES[weight.dtype], eps, _addr(out.get("residual_out")), _addr(out.get("y")),
           _addr(out.get("q")), _addr(out.get("scales")), _raw_stream(stream, dev))
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _block_norm_desc(T, H, gate_rows, gate_stride, dtype, act, residual_scale, branch_scale, eps):
+    return MoeBlockNormDesc(T, H, gate_rows, gate_stride, _DTYPES[dtype], GATE_ACTS[act],
+                            residual_scale, branch_scale, eps, 0)
+
+
+def block_norm(x, residual, weight=None, post_weight=None, gate=None, gate_act="none",
+               residual_scale=1.0, branch_scale=1.0, eps=1e-6, out=None, with_y=True, with_q=True,
+               stream=None):
+    """moe_block_norm: norm of a block's output x (post_weight), its gate [G, H]
+    (G divides the tokens; rows may be strided), scaled residual addition, and the
+    next block's norm (weight) with block-scaled e4m3 codes.  Returns a dict with
+    residual_out, y (bf16) and q, scales (e4m3 [T, H], fp32 [T, ceil(H/128)]).  Given
+    `out`, a dict of residual_out and some of these, exactly those are computed;
+    residual_out may be the residual itself and y may be x itself.  Without a
+    weight only residual_out is."""
+    T, H = x.shape
+    dev = x.get_device()
+    w = weight if weight is not None else post_weight
+    dtype = torch.bfloat16 if w is None else w.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"weight: dtype {dtype}, expected float32 or bfloat16")
+    _check(x, torch.bfloat16, (T, H), "x", dev)
+    _check(residual, torch.bfloat16, (T, H), "residual", dev)
+    _check(weight, dtype, (H,), "weight", dev)
+    _check(post_weight, dtype, (H,), "post_weight", dev)
+    rows = stride = 0
+    if gate is not None:
+        rows = gate.shape[0]
+        if gate.dtype is not torch.bfloat16:
+            raise TypeError(f"gate: dtype {gate.dtype}, expected torch.bfloat16")
+        if gate.dim() != 2 or gate.shape[1] != H or gate.stride(1) != 1 or (rows == 0) != (T == 0):
+            raise ValueError(f"gate: shape {tuple(gate.shape)}, expected [rows, {H}] with contiguous rows")
+        if gate.get_device() != dev:
+            _check_device(gate, "gate", dev)
+        stride = gate.stride(0) if rows > 1 else H
+        if T == 0:
+            rows = stride = 0
+            gate, gate_act = None, "none"
+    if out is None:
+        out = dict(residual_out=torch.empty_like(x))
+        if with_y and weight is not None:
+            out["y"] = torch.empty_like(x)
+        if with_q and weight is not None:
+            out["q"] = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=x.device)
+            out["scales"] = torch.empty((T, _blocks(H)), dtype=torch.float32, device=x.device)
+    else:
+        _check(out["residual_out"], torch.bfloat16, (T, H), "residual_out", dev)
+        _check(out.get("y"), torch.bfloat16, (T, H), "y", dev)
+        _check(out.get("q"), torch.float8_e4m3fn, (T, H), "q", dev)
+        _check(out.get("scales"), torch.float32, (T, _blocks(H)), "scales", dev)
+    desc = _block_norm_desc(T, H, rows, stride, dtype, gate_act, float(residual_scale),
+                            float(branch_scale), float(eps))
+    _call("moe_block_norm", desc, x.data_ptr(), residual.data_ptr(), _addr(post_weight), _addr(gate),
+          _addr(weight), out["residual_out"].data_ptr(), _addr(out.get("y")), _addr(out.get("q")),
+          _addr(out.get("scales")), _raw_stream(stream, dev))
     return out
 
 

@@ -1,0 +1,265 @@
+// block_norm.cu -- the boundary between two blocks: norm of a block's output, its
+// gate, the scaled residual addition, and the next block's norm.
+//
+//   a = x * rsqrt(sum(x^2) / H + eps) * post_weight          (x without one)
+//   h = residual_scale * residual + branch_scale * act(gate) * a
+//   v = h * rsqrt(sum(h^2) / H + eps) * weight
+// h to bf16, v to bf16 and / or block-scaled e4m3.
+//
+// Memory bounds it: every input is read once and every output written once (11
+// bytes an element with a gate per token and all outputs).  Persistent CTAs walk the
+// tokens; a token's rows of x, residual and gate come by bulk copies into a
+// shared-memory ring, the next tokens' on their way meanwhile, and stay in
+// registers from there to the stores, through both sums.  Thread i holds the
+// 16-byte vectors i, i + threads, ... (eight channels each); a block of 128 channels
+// is 16 neighbouring vectors, half a warp: its maximum is four shuffles.
+#include "common.cuh"
+#include "fp8.cuh"
+#include "norm.cuh"
+#include "ptx.cuh"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+constexpr int kMaxStages = 3;
+
+struct BlockNormDev {
+    const uint4 *x, *residual, *gate;
+    const void *post, *weight;
+    uint4 *residual_out, *y;
+    uint2 *q;
+    float *scales;
+    int64_t T, gate_tokens, gate_stride8;   // tokens that share a gate row; vectors from one to the next
+    int H8, nb, stages, gate_act;
+    float eps, inv_h, residual_scale, branch_scale;
+};
+
+template <bool W_BF16>
+__device__ __forceinline__ void load_weight(const void *w, int i, float (&f)[8]) {
+    if (W_BF16) {
+        unpack8(__ldg(static_cast<const uint4 *>(w) + i), f);
+    } else {
+        const float4 a = __ldg(static_cast<const float4 *>(w) + 2 * i), b = __ldg(static_cast<const float4 *>(w) + 2 * i + 1);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+}
+
+// 1 / (1 + exp(-g)), the hardware's exponential and reciprocal (each within two
+// units in the last place, the argument rounded once): relative error about
+// 1e-7 (2 + |g|), beside bf16 gates that stand for 4e-3 of themselves.
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
+template <int V, bool W_BF16>
+__global__ void __launch_bounds__(kNormMaxThreads)
+k_block_norm(BlockNormDev p) {
+    extern __shared__ __align__(128) uint8_t smem[];   // [stages][x, residual, gate][H]
+    __shared__ __align__(16) float part[2][kNormMaxThreads / 32];
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ volatile int abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, nt = blockDim.x;
+    const uint32_t row_bytes = (uint32_t)p.H8 * 16u;
+    const bool gate_rows = p.gate && p.gate_tokens < p.T;   // else one row for all, read from L1
+    const uint32_t in_bytes = (gate_rows ? 3u : 2u) * row_bytes;
+    if (tid == 0) {
+        for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+        abort_flag = 0;
+        for (int w = nt >> 5; w < kNormMaxThreads / 32; ++w) part[0][w] = part[1][w] = 0.0f;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    pdl_wait();
+    auto load = [&](int64_t t, int s) {
+        uint8_t *dst = smem + (size_t)s * in_bytes;
+        mbar_arrive_expect_tx(&full[s], in_bytes);
+        bulk_load(dst, p.x + t * p.H8, row_bytes, &full[s]);
+        bulk_load(dst + row_bytes, p.residual + t * p.H8, row_bytes, &full[s]);
+        if (gate_rows) bulk_load(dst + 2 * row_bytes, p.gate + t / p.gate_tokens * p.gate_stride8, row_bytes, &full[s]);
+    };
+    if (tid == 0)
+        for (int s = 0; s < p.stages; ++s)
+            if (blockIdx.x + (int64_t)s * gridDim.x < p.T) load(blockIdx.x + (int64_t)s * gridDim.x, s);
+
+    int s = 0, turn = 0;
+    uint32_t phase = 0;
+    bool failed = false;
+    // rsqrt(sum(v^2) / H + eps) over the row; where squares pass fp32's range (|v|
+    // above about 1e17) the same with v * 2^-80, beside which eps is nothing.  An infinite
+    // or NaN v leaves it at 0 or NaN, as the formula does.
+    auto inverse_rms = [&](float (&v)[V][8], bool fail) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) ss = fmaf(v[u][c], v[u][c], ss);
+        ss = block_sum(ss, part[turn], fail, failed);
+        turn ^= 1;
+        if (ss <= kF32Max || failed) return __frsqrt_rn(fmaf(ss, p.inv_h, p.eps));
+        ss = 0.0f;
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                v[u][c] *= 0x1p-80f;
+                ss = fmaf(v[u][c], v[u][c], ss);
+            }
+        ss = block_sum(ss, part[turn], false, failed);
+        turn ^= 1;
+        return __frsqrt_rn(ss * p.inv_h);
+    };
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const bool ok = wait_bounded(&full[s], phase, &abort_flag, nullptr);
+        const uint4 *sx = reinterpret_cast<const uint4 *>(smem + (size_t)s * in_bytes);
+        float h[V][8];
+        uint4 res[V], gt[V];
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const int i = u * nt + tid;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) h[u][c] = 0.0f;
+            res[u] = gt[u] = make_uint4(0, 0, 0, 0);
+            if (i < p.H8) {
+                unpack8(sx[i], h[u]);
+                res[u] = sx[p.H8 + i];
+                if (p.gate) gt[u] = gate_rows ? sx[2 * p.H8 + i] : __ldg(p.gate + i);
+            }
+        }
+        float r = 1.0f;
+        if (p.post) {
+            r = inverse_rms(h, !ok);
+            if (failed) break;
+        }
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const int i = u * nt + tid;
+            if (i < p.H8) {
+                float f[8];
+                if (p.post) {
+                    load_weight<W_BF16>(p.post, i, f);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) h[u][c] *= r * f[c];
+                }
+                if (p.gate) {
+                    unpack8(gt[u], f);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) h[u][c] *= p.gate_act ? sigmoid(f[c]) : f[c];
+                }
+                unpack8(res[u], f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) h[u][c] = fmaf(p.branch_scale, h[u][c], p.residual_scale * f[c]);
+                if (ok) p.residual_out[t * p.H8 + i] = pack8(h[u]);
+            }
+        }
+        r = inverse_rms(h, !ok);
+        if (failed) break;
+        // everyone has read the stage: the token `stages` ahead may land in it
+        if (tid == 0 && t + (int64_t)p.stages * gridDim.x < p.T) load(t + (int64_t)p.stages * gridDim.x, s);
+        if (++s == p.stages) { s = 0; phase ^= 1u; }
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const int i = u * nt + tid;
+            const bool in = i < p.H8;
+            float amax = 0.0f;
+            if (in && p.weight) {
+                float w[8];
+                load_weight<W_BF16>(p.weight, i, w);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    h[u][c] *= w[c];
+                    amax = fmaxf(amax, fabsf(h[u][c]));
+                }
+                if (p.y) {
+                    float v[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[c] = h[u][c] * r;
+                    p.y[t * p.H8 + i] = pack8(v);
+                }
+            }
+            if (p.q) {
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+                if (in) {
+                    // v = r * (h w), and r is the same all over the block: the codes
+                    // are (h w) * 448 / max|h w|, one rounding fewer, unless the floor
+                    // or the range of h w says otherwise
+                    const float a = fmaxf(amax * r, kAmaxFloor);
+                    const float sc = a * (1.0f / kE4m3Max);
+                    const float inv = amax >= kAmaxFloor && amax * r >= kAmaxFloor
+                                          ? inverse_scale(amax) : inverse_scale(a) * r;
+                    p.q[t * p.H8 + i] =
+                        make_uint2(e4m3x4(h[u][0] * inv, h[u][1] * inv, h[u][2] * inv, h[u][3] * inv),
+                                   e4m3x4(h[u][4] * inv, h[u][5] * inv, h[u][6] * inv, h[u][7] * inv));
+                    if ((lane & 15) == 0) p.scales[t * p.nb + (i >> 4)] = sc;
+                }
+            }
+        }
+    }
+    if (failed) {   // copies still in flight get time to land before the block's memory goes
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 100000ull) __nanosleep(2000);
+    }
+}
+
+template <int V, bool W_BF16>
+moe_status launch(BlockNormDev p, cudaStream_t stream) {
+    auto kernel = k_block_norm<V, W_BF16>;
+    const bool gate_rows = p.gate && p.gate_tokens < p.T;
+    const size_t stage = (size_t)(gate_rows ? 3 : 2) * p.H8 * 16;
+    const size_t room = 224 * 1024;
+    p.stages = kMaxStages * stage <= room ? kMaxStages : 2;     // 16384 channels with gate rows: 96 KB each
+    const size_t smem = p.stages * stage;
+    if (!set_smem_limit((const void *)kernel, smem)) return MOE_ERR_CUDA;
+    const int threads = ((p.H8 + V - 1) / V + 31) / 32 * 32;
+    // as many blocks as fit beside each other on every SM
+    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(room / (smem + 1024), 2048 / 3 * 2 / threads));
+    const int64_t cap = num_sms() * per_sm;
+    const unsigned grid = (unsigned)(p.T < cap ? p.T : cap);
+    MOE_LAUNCH("block_norm", kernel, grid, threads, smem, stream, p);
+    return MOE_OK;
+}
+
+template <int V>
+moe_status launch_v(const BlockNormDev &p, bool w_bf16, cudaStream_t stream) {
+    return w_bf16 ? launch<V, true>(p, stream) : launch<V, false>(p, stream);
+}
+
+}  // namespace
+
+moe_status launch_block_norm(const moe_block_norm_desc &d, const void *x, const void *residual,
+                             const void *post_weight, const void *gate, const void *weight,
+                             void *residual_out, void *y, void *q, float *scales, cudaStream_t stream) {
+    BlockNormDev p;
+    p.x = static_cast<const uint4 *>(x);
+    p.residual = static_cast<const uint4 *>(residual);
+    p.gate = static_cast<const uint4 *>(gate);
+    p.post = post_weight;
+    p.weight = weight;
+    p.residual_out = static_cast<uint4 *>(residual_out);
+    p.y = static_cast<uint4 *>(y);
+    p.q = static_cast<uint2 *>(q);
+    p.scales = scales;
+    p.T = d.num_tokens;
+    p.gate_tokens = gate ? d.num_tokens / d.gate_rows : 0;
+    p.gate_stride8 = d.gate_stride / 8;
+    p.H8 = (int)(d.hidden / 8);
+    p.nb = (int)((d.hidden + kFp8Block - 1) / kFp8Block);
+    p.gate_act = d.gate_act;
+    p.eps = d.eps;
+    p.inv_h = 1.0f / (float)d.hidden;
+    p.residual_scale = d.residual_scale;
+    p.branch_scale = d.branch_scale;
+    const bool w_bf16 = d.weight_dtype == MOE_DTYPE_BF16;
+    // vectors a thread: few enough for registers, many enough for at most 512 threads
+    if (p.H8 <= 256) return launch_v<1>(p, w_bf16, stream);
+    if (p.H8 <= 1024) return launch_v<2>(p, w_bf16, stream);
+    return launch_v<4>(p, w_bf16, stream);
+}
+
+}  // namespace moe

@@ -112,6 +112,38 @@ moe_status moe_add_rms_norm(int64_t num_tokens, int64_t hidden, const void *x,
                                stream);
 }
 
+moe_status moe_block_norm(const moe_block_norm_desc *desc, const void *x, const void *residual,
+                          const void *post_weight, const void *gate, const void *weight,
+                          void *residual_out, void *y, void *q, float *scales,
+                          cudaStream_t stream) {
+    if (!desc) return MOE_FAIL(MOE_ERR_NULLPTR);
+    const moe_block_norm_desc &d = *desc;
+    const int64_t T = d.num_tokens, H = d.hidden;
+    if (T < 0 || T > INT32_MAX || H < 8 || H % 8 != 0 || H > 16384) return MOE_FAIL(MOE_ERR_SHAPE);
+    if ((d.weight_dtype != MOE_DTYPE_F32 && d.weight_dtype != MOE_DTYPE_BF16) ||
+        (d.gate_act != MOE_GATE_ACT_NONE && d.gate_act != MOE_GATE_ACT_SIGMOID) || d.reserved != 0)
+        return MOE_FAIL(MOE_ERR_PARAM_INVALID);
+    if (!(d.eps >= 1e-30f) || !std::isfinite(d.eps) || !std::isfinite(d.residual_scale) ||
+        !std::isfinite(d.branch_scale))
+        return MOE_FAIL(MOE_ERR_PARAM_INVALID);
+    if (d.gate_rows < 0 || d.gate_stride < 0 || (d.gate_rows == 0) != (d.gate_stride == 0) ||
+        (d.gate_rows > 0 && (T % d.gate_rows != 0 || d.gate_rows > std::max<int64_t>(T, 1) ||
+                             d.gate_stride < H || d.gate_stride % 8 != 0 || d.gate_stride > INT32_MAX)))
+        return MOE_FAIL(MOE_ERR_SHAPE);
+    if (d.gate_rows == 0 && (gate || d.gate_act != MOE_GATE_ACT_NONE)) return MOE_FAIL(MOE_ERR_PARAM_INVALID);
+    if (!weight && (y || q)) return MOE_FAIL(MOE_ERR_NULLPTR);
+    if (T > 0) {
+        if (!x || !residual || !residual_out || (d.gate_rows > 0 && !gate)) return MOE_FAIL(MOE_ERR_NULLPTR);
+        if ((q == nullptr) != (scales == nullptr)) return MOE_FAIL(MOE_ERR_NULLPTR);
+    }
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(post_weight, 16) || !aligned(gate, 16) ||
+        !aligned(weight, 16) || !aligned(residual_out, 16) || !aligned(y, 16) || !aligned(q, 16) ||
+        !aligned(scales, 4))
+        return MOE_FAIL(MOE_ERR_ALIGNMENT);
+    if (T == 0) return MOE_OK;
+    return launch_block_norm(d, x, residual, post_weight, gate, weight, residual_out, y, q, scales, stream);
+}
+
 moe_status moe_gate(const moe_gate_desc *desc, const void *logits, const float *bias,
                     const uint8_t *x_active_mask, int32_t *expert_ids, float *expert_scales,
                     uint8_t *route_mask, cudaStream_t stream) {

@@ -388,6 +388,11 @@ moe_status launch_add_rms_norm(int64_t T, int64_t H, const void *x, const void *
                                const void *weight, bool w_bf16, float eps, void *residual_out,
                                void *y, void *q, float *scales, cudaStream_t stream);
 
+moe_status launch_block_norm(const moe_block_norm_desc &d, const void *x, const void *residual,
+                             const void *post_weight, const void *gate, const void *weight,
+                             void *residual_out, void *y, void *q, float *scales,
+                             cudaStream_t stream);
+
 // Grouped product of block-scaled e4m3 operands.
 struct Fp8GemmArgs {
     const void *a;             // e4m3 [cap_rows, Kd]

@@ -13,6 +13,7 @@
 // neighbouring vectors, half a warp: its maximum is four shuffles.
 #include "common.cuh"
 #include "fp8.cuh"
+#include "norm.cuh"
 #include "ptx.cuh"
 
 #include <algorithm>
@@ -20,9 +21,6 @@
 namespace moe {
 namespace {
 
-constexpr uint32_t kFull = 0xffffffffu;
-constexpr float kF32Max = 3.402823466e38f;
-constexpr int kNormMaxThreads = 512;
 constexpr int kStages = 3;
 
 struct NormDev {
@@ -35,41 +33,6 @@ struct NormDev {
     int H8, nb;
     float eps, inv_h;
 };
-
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
-}
-
-// Sum over the CTA, the same in every thread.  `fail` from any thread makes
-// `failed` true in all.  Every thread's earlier shared-memory reads are done
-// when it returns.
-__device__ __forceinline__ float block_sum(float v, float *part, bool fail, bool &failed) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    failed = __syncthreads_or(fail);
-    // places of warps that the block does not have hold 0
-    const float4 *p4 = reinterpret_cast<const float4 *>(part);
-    float4 a = p4[0];
-#pragma unroll
-    for (int w = 1; w < kNormMaxThreads / 128; ++w) {
-        const float4 b = p4[w];
-        a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-    }
-    return (a.x + a.y) + (a.z + a.w);
-}
 
 template <int V, bool W_BF16, bool RES>
 __global__ void __launch_bounds__(kNormMaxThreads)

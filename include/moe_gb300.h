@@ -416,6 +416,47 @@ moe_status moe_add_rms_norm(int64_t num_tokens, int64_t hidden, const void *x,
                             void *residual_out, void *y, void *q, float *scales,
                             cudaStream_t stream);
 
+/* The boundary between two blocks: norm of a block's output, its gate, the scaled
+ * residual addition, and the next block's norm.  Per token t, in fp32:
+ *   a = x * rsqrt(sum(x^2) / hidden + eps) * post_weight   (a = x when it is NULL)
+ *   h = residual_scale * residual + branch_scale * act(gate[t / (T / gate_rows)]) * a
+ *       (the gate is 1 when it is NULL)
+ *   v = h * rsqrt(sum(h^2) / hidden + eps) * weight
+ * residual_out = bf16(h); y = bf16(v); q, scales = v quantised as above.  All
+ * are computed from the fp32 values, so each output is rounded once.
+ * x, residual     bf16 [T, H]; H % 8 == 0, 8 <= H <= 16384
+ * post_weight     [H] in weight_dtype, or NULL
+ * gate            bf16 [gate_rows, H], rows gate_stride elements apart, or NULL: one
+ *                 row for all tokens, one a token, or one for each T / gate_rows
+ *                 consecutive tokens.  MOE_GATE_ACT_SIGMOID: 1 / (1 + exp(-gate)),
+ *                 exponential and quotient within a few units in the last place.
+ * weight          [H] in weight_dtype; may be NULL when y and q are
+ * residual_out    bf16 [T, H]; may be the residual buffer itself, else overlaps no
+ *                 input
+ * y               bf16 [T, H] or NULL (may be x itself)
+ * q, scales       e4m3 [T, H] and fp32 [T, ceil(H / 128)], or both NULL
+ * eps >= 1e-30 and finite; the two factors finite.  h * weight is formed before the
+ * factor rsqrt(...) joins it: it, and x times its own factor and the post weight, have
+ * to be within fp32's range. */
+#define MOE_GATE_ACT_NONE    0
+#define MOE_GATE_ACT_SIGMOID 1
+typedef struct moe_block_norm_desc {
+    int64_t num_tokens;      /* T >= 0 */
+    int64_t hidden;          /* H */
+    int64_t gate_rows;       /* divides T, >= 1, where there is a gate; else 0 */
+    int64_t gate_stride;     /* elements, >= H and a multiple of 8, where there is a gate; else 0 */
+    int32_t weight_dtype;    /* MOE_DTYPE_F32 or MOE_DTYPE_BF16, of both weights */
+    int32_t gate_act;        /* MOE_GATE_ACT_* */
+    float residual_scale;
+    float branch_scale;
+    float eps;
+    int32_t reserved;        /* must be 0 */
+} moe_block_norm_desc;
+moe_status moe_block_norm(const moe_block_norm_desc *desc, const void *x, const void *residual,
+                          const void *post_weight, const void *gate, const void *weight,
+                          void *residual_out, void *y, void *q, float *scales,
+                          cudaStream_t stream);
+
 /* Router.  Scores of E experts from a token's logits, choice of K of them, and
  * their weights; what moe_dispatch and moe_combine take as expert_ids and
  * expert_scales.  Per token, in fp32:
