@@ -213,13 +213,16 @@ moe_status launch(BlockNormDev p, cudaStream_t stream) {
     const bool gate_rows = p.gate && p.gate_tokens < p.T;
     const size_t stage = (size_t)(gate_rows ? 3 : 2) * p.H8 * 16;
     const size_t room = 224 * 1024;
-    p.stages = kMaxStages * stage <= room ? kMaxStages : 2;     // 16384 channels with gate rows: 96 KB each
+    const int threads = ((p.H8 + V - 1) / V + 31) / 32 * 32;
+    // as many CTAs as registers (64 a thread, 128 with four vectors) and rings let stand beside each
+    // other on an SM, with three stages where two CTAs fit so, else two: 16384 x 7168
+    // with gates, one CTA of three stages 291 us, two of two 204 us
+    const int64_t by_regs = std::max<int64_t>(1, (V > 2 ? 512 : 1024) / threads);
+    auto beside = [&](int stages) { return std::min<int64_t>(by_regs, room / (stages * stage + 1024)); };
+    p.stages = beside(kMaxStages) >= std::min<int64_t>(2, by_regs) ? kMaxStages : 2;
     const size_t smem = p.stages * stage;
     if (!set_smem_limit((const void *)kernel, smem)) return MOE_ERR_CUDA;
-    const int threads = ((p.H8 + V - 1) / V + 31) / 32 * 32;
-    // as many blocks as fit beside each other on every SM
-    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(room / (smem + 1024), 2048 / 3 * 2 / threads));
-    const int64_t cap = num_sms() * per_sm;
+    const int64_t cap = num_sms() * std::max<int64_t>(1, beside(p.stages));
     const unsigned grid = (unsigned)(p.T < cap ? p.T : cap);
     MOE_LAUNCH("block_norm", kernel, grid, threads, smem, stream, p);
     return MOE_OK;
@@ -256,8 +259,11 @@ moe_status launch_block_norm(const moe_block_norm_desc &d, const void *x, const 
     p.residual_scale = d.residual_scale;
     p.branch_scale = d.branch_scale;
     const bool w_bf16 = d.weight_dtype == MOE_DTYPE_BF16;
-    // vectors a thread: few enough for registers, many enough for at most 512 threads
-    if (p.H8 <= 256) return launch_v<1>(p, w_bf16, stream);
+    // Vectors a thread: few enough for registers, many enough for at most 512 threads.
+    // Two rather than one also for short rows, whose CTAs are many then (16384 x 2048: 63
+    // against 69 us), unless one token a CTA is all there is (1023 x 1000: 4.0 against 3.6 us).
+    const int64_t threads1 = (p.H8 + 31) / 32 * 32;
+    if (p.H8 <= 256 && p.T <= num_sms() * (1024 / threads1)) return launch_v<1>(p, w_bf16, stream);
     if (p.H8 <= 1024) return launch_v<2>(p, w_bf16, stream);
     return launch_v<4>(p, w_bf16, stream);
 }
