@@ -184,3 +184,65 @@ def test_crowded_experts_many_times(B):
         d = make(B, T=33 + seed, H=384, E=40, K=1 + seed % 4, N=256, ids=str(seed), seed=seed)
         got, _, ref, _ = both(B, d)
         assert torch.equal(got.view(torch.int16), ref.view(torch.int16)), seed
+
+
+def test_stores_stay_in_bounds(B):
+    """Output and workspace between guard bytes, on both ways through the kernels."""
+    for kw in (dict(T=1, H=272, E=5, K=3, N=256), dict(T=37, H=2000, E=9, K=4, N=768, mask=2, shared=True)):
+        d = make(B, **kw)
+        _, _, ref, _ = both(B, d)
+        T, H = kw["T"], kw["H"]
+        whole = torch.full(((T + 32) * H,), 0x5A5A, dtype=torch.int16, device=DEV)
+        out = whole[16 * H:(16 + T) * H].view(torch.bfloat16).view(T, H)
+        need = B.layer_few_tokens_workspace_size(d["shape"])
+        owner = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+        at = (-owner.data_ptr()) % 1024 + 1024
+        B.layer_few_tokens(d["shape"], d["x"], d["ids"], d["probs"], d["p1"], d["s1"], d["p2"], d["s2"],
+                           mask=d["mask"], shared=d["shared"], ws=owner[at:at + need], out=out)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
+        assert bool((whole[:16 * H] == 0x5A5A).all()) and bool((whole[(16 + T) * H:] == 0x5A5A).all())
+        assert bool((owner[:at] == 0xA5).all()) and bool((owner[at + need:] == 0xA5).all())
+
+
+def test_nan_and_infinity_stay_in_their_tokens(B):
+    for T, K, N in ((4, 2, 256), (40, 4, 2816)):
+        d = make(B, T=T, H=512, E=6, K=K, N=N)
+        clean, _, _, _ = both(B, d)
+        d["x"][1, 7] = float("nan")
+        d["x"][3, 9] = float("inf")
+        d["probs"][2, 0] = float("nan")
+        got, _, ref, _ = both(B, d)
+        rest = [t for t in range(T) if t not in (1, 2, 3)]
+        assert torch.equal(got[rest].view(torch.int16), clean[rest].view(torch.int16))
+        assert bool(torch.isnan(got[2]).all())
+        same = torch.isnan(got) & torch.isnan(ref) | (got == ref)
+        assert bool(same.all())
+
+
+def test_output_in_the_shared_buffer(B):
+    for T in (1, 20):
+        d = make(B, T=T, H=1024, E=6, K=3, N=512, shared=True)
+        _, _, ref, _ = both(B, d)
+        out, _ = B.layer_few_tokens(d["shape"], d["x"], d["ids"], d["probs"], d["p1"], d["s1"], d["p2"],
+                                    d["s2"], shared=d["shared"], out=d["shared"])
+        assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
+
+
+def test_weights_past_32_bits(B):
+    """Experts whose weights begin beyond 2^32 bytes of the packed buffer."""
+    E, H, N = 200, 7168, 4096
+    g = torch.Generator(device=DEV).manual_seed(9)
+    s1 = 1e-3 + 9e-3 * torch.rand(E, N, generator=g, device=DEV)
+    s2 = 1e-3 + 9e-3 * torch.rand(E, H, generator=g, device=DEV)
+    w1 = torch.randint(-127, 128, (E, N, H), generator=g, dtype=torch.int8, device=DEV)
+    w2 = torch.randint(-127, 128, (E, H, N // 2), generator=g, dtype=torch.int8, device=DEV)
+    for T in (1, 3):
+        shape = B.make_shape(T, 1, H, E, 4, N, ffn_path="small")
+        (o1, p1), (o2, p2) = B.pack_weights(shape, w1, w2)
+        x = torch.randn(T, H, generator=g, device=DEV).bfloat16()
+        ids = (E - 1 - torch.arange(4 * T, device=DEV).view(T, 4)).int()
+        probs = torch.full((T, 4), 0.25, device=DEV)
+        ref, _ = B.layer(shape, x, ids, probs, p1, s1, p2, s2)
+        got, _ = B.layer_few_tokens(shape, x, ids, probs, p1, s1, p2, s2)
+        assert torch.equal(got.view(torch.int16), ref.view(torch.int16))

@@ -157,3 +157,44 @@ def test_split_tiles_many_times(B):
             got, _ = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], ws=ws,
                                          path="small")
         assert torch.equal(got, want)
+
+
+def test_stores_stay_in_bounds(B):
+    """Output and workspace between guard bytes, on every kernel."""
+    for rows, N, Kd, path in ((3, 200, 336, "small"), (20, 200, 336, "small"), (130, 1000, 5008, "small"),
+                              (300, 1000, 528, "large_pair"), (300, 1000, 528, "large")):
+        for dtype in (torch.float32, torch.bfloat16):
+            d = make(rows, 1, N, Kd)
+            _, packed = B.pack_int8(d["w"], path=path)
+            ref, ws = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], path=path,
+                                          out_dtype=dtype)
+            size = torch.finfo(dtype).bits // 8
+            whole = torch.full(((rows + 32) * N * size,), 0x5A, dtype=torch.uint8, device=DEV)
+            out = whole[16 * N * size:(16 + rows) * N * size].view(dtype).view(rows, N)
+            need = ws.numel()
+            owner = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+            at = (-owner.data_ptr()) % 1024 + 1024
+            B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], path=path, out=out,
+                                ws=owner[at:at + need])
+            torch.cuda.synchronize()
+            assert torch.equal(out, ref)
+            assert bool((whole[:16 * N * size] == 0x5A).all()) and bool((whole[(16 + rows) * N * size:] == 0x5A).all())
+            assert bool((owner[:at] == 0xA5).all()) and bool((owner[at + need:] == 0xA5).all())
+
+
+def test_weights_past_32_bits(B):
+    """Groups whose weights begin beyond 2^32 bytes, on every kernel."""
+    E, N, Kd = 40, 8192, 16384
+    w = torch.randint(-127, 128, (E, N, Kd), dtype=torch.int8, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    ws = 1e-4 + 9e-4 * torch.rand(E, N, generator=g, device=DEV)
+    for rows, path in ((3, "small"), (400, "small"), (300, "large_pair"), (300, "large")):
+        _, packed = B.pack_int8(w, path=path)
+        off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+        off[E] = rows                              # all rows in the last group
+        a = torch.randint(-127, 128, (rows, Kd), generator=g, dtype=torch.int8, device=DEV)
+        s = 0.01 + 0.02 * torch.rand(rows, generator=g, device=DEV)
+        got, _ = B.grouped_gemm_int8(off, a, packed, ws, a_scales=s, path=path, out_dtype=torch.float32)
+        acc = a.double() @ w[E - 1].double().T
+        assert torch.equal(got, (acc.float() * ws[E - 1]) * s[:, None])
+        del packed
