@@ -250,11 +250,6 @@ __device__ __forceinline__ float max8(const float (&f)[8], float m) {
     for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
     return m;
 }
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s, float rs) {
-    float c[8];
-    quant_codes<8>(v, s, rs, c);
-    return make_uint2(pack_i8x4(c[0], c[1], c[2], c[3]), pack_i8x4(c[4], c[5], c[6], c[7]));
-}
 // Eight codes at column 8 i of row r of a CTA's own codes (rows of `pitch`
 // bytes, in 128-byte pieces swizzled as a stage's rows are).
 __device__ __forceinline__ void put_codes(uint8_t *codes, int r, int pitch, int i, uint2 v) {
@@ -298,8 +293,11 @@ k_few_gate_up(FewDev p) {
                 if (x0 + 32 * group * u < H8) xv[u] = p.x[xt * H8 + x0 + 32 * group * u];
     }
     find_routes<kThreads>(p, r);
-    const int64_t units = (int64_t)r.blocks * NU;
-    const int u_begin = (int)(units * blockIdx.x / gridDim.x), u_end = (int)(units * (blockIdx.x + 1) / gridDim.x);
+    // this CTA's units are blockIdx.x, blockIdx.x + gridDim.x, ...: every CTA meets every expert, the
+    // crowded ones, whose rows take more arithmetic, too
+    const int units = r.blocks * NU, u_end = (units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int u_begin = 0;
+    auto unit_of = [&](int i) { return (int)blockIdx.x + i * (int)gridDim.x; };
 
     // this warp's share of a batch of units: first unit, its first stage, stages
     auto share = [&](int first, int &unit, int &ks, int &n) {
@@ -318,7 +316,7 @@ k_few_gate_up(FewDev p) {
         const int8_t *row[2];        // and of the rows, where they are
     } f = {u_begin, 0, 0, 0, nullptr, {nullptr, nullptr}};
     auto enter = [&]() {
-        const int blk = p.by_units(f.unit), j = (f.unit - blk * NU) * 8;
+        const int unit = unit_of(f.unit), blk = p.by_units(unit), j = (unit - blk * NU) * 8;
         const int64_t prow = (int64_t)r.blk_e[blk] * (2 * p.Nh) + (j >> 6) * 128 + ((j >> 4) & 3) * 32 + (j & 15);
         f.src = p.w1 + (prow + l.cr) * H + f.ks * kDepth + l.cu * 16;
         if (!LOCAL) {
@@ -386,13 +384,18 @@ k_few_gate_up(FewDev p) {
         __syncthreads();
         if (xt < p.T) {
             const float s = __fdiv_rn(__uint_as_float(amax[xt]), 127.0f), rs = __frcp_rn(s);
-#pragma unroll
-            for (int u = 0; u < kXVecs; ++u)
-                if (x0 + 32 * group * u < H8) {
-                    float v[8];
-                    unpack8(xv[u], v);
-                    put_codes(codes, xt, pitch, x0 + 32 * group * u, codes8(v, s, rs));
-                }
+            // from L1 again, two vectors at a time: short code, whose lines come from L2
+#pragma unroll 1
+            for (int i = x0; i < H8; i += 64 * group) {
+                const int j = i + 32 * group;
+                const uint4 a = p.x[xt * H8 + i], b = p.x[xt * H8 + (j < H8 ? j : i)];
+                float v[8];
+                unpack8(a, v);
+                put_codes(codes, xt, pitch, i, quant8(v, s, rs));
+                unpack8(b, v);
+                const uint2 q = quant8(v, s, rs);
+                if (j < H8) put_codes(codes, xt, pitch, j, q);
+            }
         }
         if (H % kDepth) {   // zeros behind the rows' ends
             const int pad = pitch / 8 - H8;
@@ -418,8 +421,9 @@ k_few_gate_up(FewDev p) {
         int eblk = 0, ech = 0;
         float sa = 0.0f, sb = 0.0f;
         if (eu < nu) {
-            eblk = p.by_units(first + eu);
-            ech = ((first + eu) - eblk * NU) * 8 + ej;
+            const int unit = unit_of(first + eu);
+            eblk = p.by_units(unit);
+            ech = (unit - eblk * NU) * 8 + ej;
             const float *sc = p.scale1 + (int64_t)r.blk_e[eblk] * (2 * p.Nh) + ech;
             sa = __ldg(sc);
             sb = __ldg(sc + p.Nh);
@@ -427,7 +431,7 @@ k_few_gate_up(FewDev p) {
         int unit, ks, n;
         share(first, unit, ks, n);
         while (n > 0) {
-            const int blk = p.by_units(unit), m = min(n, KS - ks);
+            const int blk = p.by_units(unit_of(unit)), m = min(n, KS - ks);
             int32_t (*a)[kChannels] = acc[buf][unit - first];
             auto row = [&](int i) -> uint32_t {
                 if (!LOCAL) return kWeightBytes + i * kDepth + l.of_row(i);
@@ -558,8 +562,8 @@ k_few_down(FewDev p) {
                     const int i = i0 + 32 * u + lane;
                     v[u][0] = v[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (i < n8) {
-                        v[u][0] = __ldcg(src + 2 * i);
-                        v[u][1] = __ldcg(src + 2 * i + 1);
+                        v[u][0] = src[2 * i];
+                        v[u][1] = src[2 * i + 1];
                     }
                 }
 #pragma unroll
@@ -572,19 +576,15 @@ k_few_down(FewDev p) {
             m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
             const float s = __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
             if (lane == 0) scale[at] = s;
-            // the last vectors are still in registers: all of a row of up to 2048
-            const int last = (n8 - 1) / (32 * kGVecs) * (32 * kGVecs);
-#pragma unroll
-            for (int u = 0; u < kGVecs; ++u) {
-                const int i = last + 32 * u + lane;
-                const float f[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w,
-                                    v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
-                if (i < n8) put_codes(codes, at, pitch, i, codes8(f, s, rs));
-            }
-            for (int i = lane; i < last; i += 32) {
-                const float4 a = __ldcg(src + 2 * i), b = __ldcg(src + 2 * i + 1);
+#pragma unroll 1
+            for (int i = lane; i < n8; i += 64) {
+                const int j = i + 32 < n8 ? i + 32 : i;
+                const float4 a = src[2 * i], b = src[2 * i + 1], c = src[2 * j], d = src[2 * j + 1];
                 const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                put_codes(codes, at, pitch, i, codes8(f, s, rs));
+                const float h[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+                const uint2 q0 = quant8(f, s, rs), q1 = quant8(h, s, rs);
+                put_codes(codes, at, pitch, i, q0);
+                if (j != i) put_codes(codes, at, pitch, j, q1);
             }
         }
     } else {
@@ -692,7 +692,7 @@ k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, fl
     for (int i = tid; i < n8; i += kQuantThreads) {
         float v[8];
         load(i, v);
-        reinterpret_cast<uint2 *>(q + row * n)[i] = codes8(v, s, rs);
+        reinterpret_cast<uint2 *>(q + row * n)[i] = quant8(v, s, rs);
     }
     if (tid == 0) s_out[row] = s;
 }

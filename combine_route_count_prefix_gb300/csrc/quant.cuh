@@ -66,4 +66,31 @@ __device__ __forceinline__ void quant_codes(const float (&v)[n], float s, float 
     }
 }
 
+// The same codes of eight values as their bytes (v[0] in the low byte of x).  In
+// few instructions: adding 1.5 * 2^23 rounds the quotient, and leaves the code's byte
+// in the sum; the rare values near a tie, and non-finite ones, take the division in a
+// function of their own.  A kernel that quantises once is as long as its code, which
+// comes from memory line by line.
+static __device__ __noinline__ uint2 quant8_divided(float4 a, float4 b, float s) {
+    float q[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(rintf(__fdiv_rn(q[i], s)), -127.0f), 127.0f);
+    return make_uint2(pack_i8x4(q[0], q[1], q[2], q[3]), pack_i8x4(q[4], q[5], q[6], q[7]));
+}
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], float s, float rs) {
+    if (s == 0.0f) return make_uint2(0, 0);
+    const float kMagic = 12582912.0f;
+    uint32_t u[8];
+    bool slow = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = __fmul_rn(v[i], rs), m = __fadd_rn(x, kMagic);
+        slow = slow || !(fabsf(__fsub_rn(x, __fsub_rn(m, kMagic))) <= kTieGuard);
+        u[i] = __float_as_uint(m);
+    }
+    if (slow) return quant8_divided(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), s);
+    return make_uint2(__byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410));
+}
+
 }  // namespace moe
