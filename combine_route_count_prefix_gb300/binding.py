@@ -676,8 +676,6 @@ def block_norm(x, residual, weight=None, post_weight=None, gate=None, gate_act="
     dtype = torch.bfloat16 if w is None else w.dtype
     if dtype not in _DTYPES:
         raise TypeError(f"weight: dtype {dtype}, expected float32 or bfloat16")
-    _check(x, torch.bfloat16, (T, H), "x", dev)
-    _check(residual, torch.bfloat16, (T, H), "residual", dev)
     _check(weight, dtype, (H,), "weight", dev)
     _check(post_weight, dtype, (H,), "post_weight", dev)
     rows = stride = 0
@@ -692,7 +690,7 @@ def block_norm(x, residual, weight=None, post_weight=None, gate=None, gate_act="
         stride = gate.stride(0) if rows > 1 else H
         if T == 0:
             rows = stride = 0
-            gate, gate_act = None, "none"
+            gate = None
     if out is None:
         out = dict(residual_out=torch.empty_like(x))
         if with_y and weight is not None:
@@ -701,14 +699,17 @@ def block_norm(x, residual, weight=None, post_weight=None, gate=None, gate_act="
             out["q"] = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=x.device)
             out["scales"] = torch.empty((T, _blocks(H)), dtype=torch.float32, device=x.device)
     else:
-        _check(out["residual_out"], torch.bfloat16, (T, H), "residual_out", dev)
-        _check(out.get("y"), torch.bfloat16, (T, H), "y", dev)
         _check(out.get("q"), torch.float8_e4m3fn, (T, H), "q", dev)
         _check(out.get("scales"), torch.float32, (T, _blocks(H)), "scales", dev)
+    shape, y = x.shape, out.get("y")
+    for name, v in (("x", x), ("residual", residual), ("residual_out", out["residual_out"]), ("y", y)):
+        if v is not None and (v.dtype is not torch.bfloat16 or v.shape != shape or
+                              not v.is_contiguous() or v.get_device() != dev):
+            _check(v, torch.bfloat16, shape, name, dev)
     desc = _block_norm_desc(T, H, rows, stride, dtype, gate_act, float(residual_scale),
                             float(branch_scale), float(eps))
     _call("moe_block_norm", desc, x.data_ptr(), residual.data_ptr(), _addr(post_weight), _addr(gate),
-          _addr(weight), out["residual_out"].data_ptr(), _addr(out.get("y")), _addr(out.get("q")),
+          _addr(weight), out["residual_out"].data_ptr(), _addr(y), _addr(out.get("q")),
           _addr(out.get("scales")), _raw_stream(stream, dev))
     return out
 

@@ -130,7 +130,7 @@ moe_status moe_block_norm(const moe_block_norm_desc *desc, const void *x, const 
         (d.gate_rows > 0 && (T % d.gate_rows != 0 || d.gate_rows > std::max<int64_t>(T, 1) ||
                              d.gate_stride < H || d.gate_stride % 8 != 0 || d.gate_stride > INT32_MAX)))
         return MOE_FAIL(MOE_ERR_SHAPE);
-    if (d.gate_rows == 0 && (gate || d.gate_act != MOE_GATE_ACT_NONE)) return MOE_FAIL(MOE_ERR_PARAM_INVALID);
+    if (d.gate_rows == 0 && gate) return MOE_FAIL(MOE_ERR_PARAM_INVALID);
     if (!weight && (y || q)) return MOE_FAIL(MOE_ERR_NULLPTR);
     if (T > 0) {
         if (!x || !residual || !residual_out || (d.gate_rows > 0 && !gate)) return MOE_FAIL(MOE_ERR_NULLPTR);

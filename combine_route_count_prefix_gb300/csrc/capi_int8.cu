@@ -252,7 +252,7 @@ moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
         f.out_bf16 = out_dtype == MOE_DTYPE_BF16;
         f.status = status;
         if (bf16 && !int8_few_local(rows, E, Kd)) {
-            MOE_TRY(launch_quant_rows_i8(A, true, rows, Kd, at<int8_t>(workspace, L.rows),
+            MOE_TRY(launch_quant_rows_i8(A, true, true, rows, Kd, at<int8_t>(workspace, L.rows),
                                          at<float>(workspace, L.scales), stream));
             f.rows = at<void>(workspace, L.rows);
             f.row_scales = at<float>(workspace, L.scales);

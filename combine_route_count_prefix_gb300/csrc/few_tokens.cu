@@ -658,8 +658,9 @@ k_few_down(FewDev p) {
 }
 
 // ---------------------------------------------------------------- codes of rows, once for all CTAs
-// bf16 or fp32 rows -> int8 codes and scales, a CTA a row.
-template <typename T>
+// bf16 or fp32 rows -> int8 codes and scales, a CTA a row.  A NaN stays out of its
+// row's maximum, as in the layer's other kernels, or (NAN_SCALE) makes the scale NaN.
+template <typename T, bool NAN_SCALE>
 __global__ void __launch_bounds__(kQuantThreads)
 k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, float *__restrict__ s_out) {
     __shared__ float part[kQuantThreads / 32];
@@ -681,13 +682,20 @@ k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, fl
     for (int i = tid; i < n8; i += kQuantThreads) {
         float v[8];
         load(i, v);
-        m = max8(v, m);
+        if (NAN_SCALE) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(v[c]) & 0x7fffffffu));
+        } else {
+            m = max8(v, m);
+        }
     }
     m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
     if ((tid & 31) == 0) part[tid >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kQuantThreads / 32; ++w) m = fmaxf(m, part[w]);
+    for (int w = 0; w < kQuantThreads / 32; ++w)
+        m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(part[w])));
     const float s = __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
     for (int i = tid; i < n8; i += kQuantThreads) {
         float v[8];
@@ -699,13 +707,17 @@ k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, fl
 
 }  // namespace
 
-moe_status launch_quant_rows_i8(const void *src, bool bf16, int64_t rows, int64_t n, int8_t *q,
-                                float *scales, cudaStream_t stream) {
-    if (bf16) {
-        MOE_LAUNCH("quant_rows_i8", k_quant_rows_i8<__nv_bfloat16>, (unsigned)rows, kQuantThreads, 0, stream,
-                   static_cast<const __nv_bfloat16 *>(src), n, q, scales);
+moe_status launch_quant_rows_i8(const void *src, bool bf16, bool nan_scale, int64_t rows, int64_t n,
+                                int8_t *q, float *scales, cudaStream_t stream) {
+    const auto *b = static_cast<const __nv_bfloat16 *>(src);
+    if (bf16 && nan_scale) {
+        MOE_LAUNCH("quant_rows_i8", (k_quant_rows_i8<__nv_bfloat16, true>), (unsigned)rows, kQuantThreads, 0,
+                   stream, b, n, q, scales);
+    } else if (bf16) {
+        MOE_LAUNCH("quant_rows_i8", (k_quant_rows_i8<__nv_bfloat16, false>), (unsigned)rows, kQuantThreads, 0,
+                   stream, b, n, q, scales);
     } else {
-        MOE_LAUNCH("quant_rows_i8", k_quant_rows_i8<float>, (unsigned)rows, kQuantThreads, 0, stream,
+        MOE_LAUNCH("quant_rows_i8", (k_quant_rows_i8<float, false>), (unsigned)rows, kQuantThreads, 0, stream,
                    static_cast<const float *>(src), n, q, scales);
     }
     return MOE_OK;
@@ -729,14 +741,14 @@ static moe_status launch_both(FewDev p, unsigned grid1, unsigned grid2, size_t e
         !set_smem_limit((const void *)down, C::kRing + extra2))
         return MOE_ERR_CUDA;
     if (!LOCAL) {
-        MOE_TRY(launch_quant_rows_i8(a.x, true, p.T, p.H, a.q, a.qs, stream));
+        MOE_TRY(launch_quant_rows_i8(a.x, true, false, p.T, p.H, a.q, a.qs, stream));
         p.q = a.q;
         p.qs = a.qs;
     }
     MOE_LAUNCH("few_gate_up", up, grid1, C::kThreads, C::kRing + extra1, stream, p);
     if (!LOCAL) {
         int8_t *q2 = a.q + align_up((size_t)p.T * p.H, kAlign);
-        MOE_TRY(launch_quant_rows_i8(a.g, false, p.R, p.Nh, q2, a.qs + p.T, stream));
+        MOE_TRY(launch_quant_rows_i8(a.g, false, false, p.R, p.Nh, q2, a.qs + p.T, stream));
         p.q = q2;
         p.qs = a.qs + p.T;
     }

@@ -57,9 +57,11 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
         f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ float max8(const float (&f)[8], float m) {
+// The largest magnitude as bits; a NaN counts above all, so that it makes its row's
+// scale, and with it the row's outputs, NaN.
+__device__ __forceinline__ uint32_t max8(const float (&f)[8], uint32_t m) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
     return m;
 }
 
@@ -206,7 +208,7 @@ k_int8_few(Int8FewDev p) {
     if (LOCAL) {
         // the rows' codes, in every CTA
         if (xt < p.cap_rows) {
-            float m = 0.0f;
+            uint32_t m = 0;
 #pragma unroll
             for (int u = 0; u < kXVecs; ++u)
                 if (x0 + 32 * group * u < k8) {
@@ -214,7 +216,7 @@ k_int8_few(Int8FewDev p) {
                     unpack8(xv[u], v);
                     m = max8(v, m);
                 }
-            const uint32_t w = __reduce_max_sync(kFull, __float_as_uint(m));
+            const uint32_t w = __reduce_max_sync(kFull, m);
             if (lane == 0) atomicMax(&amax[xt], w);
         }
         __syncthreads();
@@ -247,7 +249,8 @@ k_int8_few(Int8FewDev p) {
             int32_t (*a)[kChannels] = acc[buf][unit - first];
             auto row = [&](int i) -> uint32_t {
                 if (!LOCAL) return kWeightBytes + i * kDepth + l.of_row(i);
-                return smem_u32(codes) + (uint32_t)(i * pitch + ks * kDepth) + l.of_row(i);
+                const int r = at.row0 + i;      // LOCAL rows are those of the whole call
+                return smem_u32(codes) + (uint32_t)(r * pitch + ks * kDepth) + l.of_row(r);
             };
             auto add = [&](int i, int c, int32_t v) { atomicAdd(&a[i][c], v); };
             walk.template run<NB>(l, m, at.rows, fetch, row, add);
@@ -267,7 +270,7 @@ k_int8_few(Int8FewDev p) {
             *a = 0;
             if (ch >= p.N) continue;
             const int64_t r = at.row0 + row, wn = (int64_t)at.e * p.N + ch;
-            const float s = LOCAL ? __fdiv_rn(__uint_as_float(amax[row]), 127.0f) : __ldg(p.qs + r);
+            const float s = LOCAL ? __fdiv_rn(__uint_as_float(amax[r]), 127.0f) : __ldg(p.qs + r);
             float v = __fmul_rn(__fmul_rn(__int2float_rn(sum), __ldg(p.w_scales + wn)), s);
             if (p.bias) v = __fadd_rn(v, __ldg(p.bias + wn));
             if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.c)[r * p.N + ch] = __float2bfloat16_rn(v);
@@ -285,7 +288,7 @@ k_rows_to_f16(const void *__restrict__ rows, const float *__restrict__ scales,
               const int32_t *__restrict__ offsets, int64_t E, int64_t cap_rows, int64_t Kd,
               uint4 *__restrict__ img, float *__restrict__ img_scales, int32_t *__restrict__ status,
               uint32_t *__restrict__ clear, int64_t n_clear) {
-    __shared__ float part[kImgThreads / 32];
+    __shared__ uint32_t part[kImgThreads / 32];
     const int tid = threadIdx.x;
     pdl_wait();
     if (blockIdx.x == 0 && tid == 0) *status = 0;
@@ -299,7 +302,7 @@ k_rows_to_f16(const void *__restrict__ rows, const float *__restrict__ scales,
         if constexpr (BF16) {
             const uint4 *src = static_cast<const uint4 *>(rows) + r * k8;
             uint4 raw[kOwn];
-            float m = 0.0f;
+            uint32_t m = 0;
 #pragma unroll
             for (int u = 0; u < kOwn; ++u) {
                 const int i = u * kImgThreads + tid;
@@ -316,13 +319,13 @@ k_rows_to_f16(const void *__restrict__ rows, const float *__restrict__ scales,
                 unpack8(src[i], v);
                 m = max8(v, m);
             }
-            m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
+            m = __reduce_max_sync(kFull, m);
             __syncthreads();      // the row before has read part
             if ((tid & 31) == 0) part[tid >> 5] = m;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < kImgThreads / 32; ++w) m = fmaxf(m, part[w]);
-            const float s = __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
+            for (int w = 0; w < kImgThreads / 32; ++w) m = max(m, part[w]);
+            const float s = __fdiv_rn(__uint_as_float(m), 127.0f), rs = __frcp_rn(s);
             auto put = [&](int i, const uint4 &x) {
                 float v[8], c[8];
                 unpack8(x, v);

@@ -420,7 +420,7 @@ moe_status moe_add_rms_norm(int64_t num_tokens, int64_t hidden, const void *x,
  * residual addition, and the next block's norm.  Per token t, in fp32:
  *   a = x * rsqrt(sum(x^2) / hidden + eps) * post_weight   (a = x when it is NULL)
  *   h = residual_scale * residual + branch_scale * act(gate[t / (T / gate_rows)]) * a
- *       (the gate is 1 when it is NULL)
+ *       (without a gate 1, whatever act)
  *   v = h * rsqrt(sum(h^2) / hidden + eps) * weight
  * residual_out = bf16(h); y = bf16(v); q, scales = v quantised as above.  All
  * are computed from the fp32 values, so each output is rounded once.
@@ -537,8 +537,9 @@ moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
  * bf16 output is rounded once more.
  * A               int8 [rows, Kd] (MOE_DTYPE_I8) with a_scales fp32 [rows]: q and s;
  *                 or bf16 [rows, Kd] (MOE_DTYPE_BF16) with a_scales NULL: each row is
- *                 quantised in the call, s = max|a| / 127, q = rint(a / s), as
- *                 moe_dispatch_quant does
+ *                 quantised in the call, s = max|a| / 127, q = clamp(rint(a / s), -127,
+ *                 127), q = 0 where s = 0, in fp32 with IEEE rounding; a NaN makes its
+ *                 row's s and outputs NaN
  * w_packed        from moe_pack_int8 with the same E, N, Kd and path
  * w_scales        fp32 [E, N]; bias fp32 [E, N] or NULL
  * C               [rows, N] in out_dtype (MOE_DTYPE_F32 or MOE_DTYPE_BF16); rows

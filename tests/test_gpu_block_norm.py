@@ -99,7 +99,7 @@ RS, BS = float(np.float32(0.9)), float(np.float32(0.4))
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("T,H,gates,act", [
     (1, 8, 0, "none"), (1, 7168, 1, "none"), (2, 128, 2, "sigmoid"), (3, 136, 1, "sigmoid"),
-    (6, 1000, 3, "none"), (4, 2048, 4, "none"), (7, 2056, 0, "none"), (3, 4104, 1, "none"),
+    (6, 1000, 3, "none"), (4, 2048, 4, "none"), (7, 2056, 0, "none"), (7, 2056, 0, "sigmoid"), (3, 4104, 1, "none"),
     (4, 8192, 2, "sigmoid"), (3, 8200, 3, "none"), (2, 16384, 2, "sigmoid"), (500, 16376, 500, "none"),
     (700, 512, 7, "none"), (2600, 264, 2600, "sigmoid"), (2000, 7168, 1, "sigmoid")])
 def test_values(B, T, H, gates, act, post, dtype):

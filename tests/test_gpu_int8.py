@@ -198,3 +198,88 @@ def test_weights_past_32_bits(B):
         acc = a.double() @ w[E - 1].double().T
         assert torch.equal(got, (acc.float() * ws[E - 1]) * s[:, None])
         del packed
+
+
+@pytest.mark.parametrize("path", ["small", "large", "large_pair"])
+def test_nan_makes_its_row_nan(B, path):
+    for rows in (2, 8, 20, 300):
+        d = make(rows, 1, 264, 528, a="bf16")
+        _, packed = B.pack_int8(d["w"], path=path)
+        clean, _ = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], path=path)
+        d["a"][rows // 2, 100] = float("nan")
+        got, _ = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], path=path)
+        rest = [r for r in range(rows) if r != rows // 2]
+        assert bool(torch.isnan(got[rows // 2]).all())
+        assert torch.equal(got[rest], clean[rest])
+
+
+@pytest.mark.parametrize("path", ["small", "large", "large_pair"])
+def test_first_group_begins_behind_the_first_row(B, path):
+    """Rows before expert_offsets[0] belong to no group: not read, not written."""
+    for rows, a in ((5, "bf16"), (5, "int8"), (30, "bf16"), (300, "int8")):
+        d = make(rows, 1, 200, 336, a=a)
+        want, _ = reference(d, torch.float32)
+        d["off"][0] = 2
+        _, packed = B.pack_int8(d["w"], path=path)
+        out = torch.full((rows, 200), 7.0, device=DEV)
+        B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], out=out, path=path)
+        assert torch.equal(out[2:], want[2:])
+        assert bool((out[:2] == 7.0).all())
+
+
+# Products large enough for the tile kernel of the small path, with and without a
+# split inner dimension, at widths and depths that end inside a tile.
+TILES = [dict(rows=130, E=1, N=1000, Kd=5008, bias=True), dict(rows=64, E=1, N=520, Kd=16400, a="bf16"),
+         dict(rows=65, E=1, N=1032, Kd=8208), dict(rows=200, E=3, N=1000, Kd=2512, bias=True),
+         dict(rows=500, E=40, N=392, Kd=2608, a="bf16"), dict(rows=17, E=1, N=8200, Kd=4000),
+         dict(rows=300, E=3, N=264, Kd=7168, counts=[0, 290, 7], a="bf16")]
+
+
+@pytest.mark.parametrize("kw", TILES, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
+def test_tiles(B, kw):
+    assert kw["rows"] * kw["N"] * kw["Kd"] > 4.8e8 and kw["rows"] > 8 * kw["E"]
+    for path in ("small", "auto"):
+        for dtype in (torch.bfloat16, torch.float32):
+            check(B, make(**kw), path, dtype)
+
+
+def test_tiles_sums_are_exact(B):
+    for rows in (64, 128):
+        check(B, make(rows, 1, 1024, 8192, extreme=True), "small", torch.float32)
+
+
+def test_split_tiles_clear_their_counters(B):
+    """The CTAs that share a tile's inner dimension meet at counters and sums that
+    every call clears: the same bits whatever the workspace held."""
+    d = make(64, 1, 1024, 8192)
+    _, packed = B.pack_int8(d["w"], path="small")
+    ref, ws = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], path="small")
+    want, _ = reference(d, torch.bfloat16)
+    assert torch.equal(ref, want)
+    for fill in (0, 1, 0xff):
+        ws.fill_(fill)
+        for _ in range(20):
+            got, _ = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], ws=ws,
+                                         path="small")
+        assert torch.equal(got, want)
+
+
+def test_tiles_store_in_bounds_and_keep_nan(B):
+    for rows, N, Kd in ((130, 1000, 5008), (64, 1032, 8208)):
+        d = make(rows, 1, N, Kd, a="bf16")
+        _, packed = B.pack_int8(d["w"], path="small")
+        ref, ws = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], path="small")
+        whole = torch.full(((rows + 32) * N,), 0x5A5A, dtype=torch.int16, device=DEV)
+        out = whole[16 * N:(16 + rows) * N].view(torch.bfloat16).view(rows, N)
+        need = ws.numel()
+        owner = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+        at = (-owner.data_ptr()) % 1024 + 1024
+        B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], path="small", out=out, ws=owner[at:at + need])
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+        assert bool((whole[:16 * N] == 0x5A5A).all()) and bool((whole[(16 + rows) * N:] == 0x5A5A).all())
+        assert bool((owner[:at] == 0xA5).all()) and bool((owner[at + need:] == 0xA5).all())
+        d["a"][7, 3] = float("nan")
+        got, _ = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], path="small")
+        rest = [r for r in range(rows) if r != 7]
+        assert bool(torch.isnan(got[7]).all()) and torch.equal(got[rest], ref[rest])

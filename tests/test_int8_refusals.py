@@ -131,7 +131,7 @@ G = dict(gate=A, gate_rows=2, gate_stride=128)
     (dict(num_tokens=-1), SHAPE), (dict(num_tokens=1 << 31), SHAPE), (dict(weight_dtype=2), PARAM),
     (dict(gate_act=2), PARAM), (dict(reserved=1), PARAM), (dict(eps=0.0), PARAM),
     (dict(eps=float("inf")), PARAM), (dict(residual_scale=float("nan")), PARAM),
-    (dict(branch_scale=float("inf")), PARAM), (dict(gate=A), PARAM), (dict(gate_act=1), PARAM),
+    (dict(branch_scale=float("inf")), PARAM), (dict(gate=A), PARAM),
     (dict(G, gate=None), NULLPTR), (dict(G, gate_rows=3), SHAPE), (dict(G, gate_rows=8), SHAPE),
     (dict(G, gate_rows=-1), SHAPE), (dict(G, gate_stride=64), SHAPE), (dict(G, gate_stride=132), SHAPE),
     (dict(G, gate_stride=0), SHAPE), (dict(gate_stride=128), SHAPE),
