@@ -384,18 +384,13 @@ k_few_gate_up(FewDev p) {
         __syncthreads();
         if (xt < p.T) {
             const float s = __fdiv_rn(__uint_as_float(amax[xt]), 127.0f), rs = __frcp_rn(s);
-            // from L1 again, two vectors at a time: short code, whose lines come from L2
-#pragma unroll 1
-            for (int i = x0; i < H8; i += 64 * group) {
-                const int j = i + 32 * group;
-                const uint4 a = p.x[xt * H8 + i], b = p.x[xt * H8 + (j < H8 ? j : i)];
-                float v[8];
-                unpack8(a, v);
-                put_codes(codes, xt, pitch, i, quant8(v, s, rs));
-                unpack8(b, v);
-                const uint2 q = quant8(v, s, rs);
-                if (j < H8) put_codes(codes, xt, pitch, j, q);
-            }
+#pragma unroll
+            for (int u = 0; u < kXVecs; ++u)
+                if (x0 + 32 * group * u < H8) {
+                    float v[8];
+                    unpack8(xv[u], v);
+                    put_codes(codes, xt, pitch, x0 + 32 * group * u, quant8(v, s, rs));
+                }
         }
         if (H % kDepth) {   // zeros behind the rows' ends
             const int pad = pitch / 8 - H8;
@@ -678,17 +673,32 @@ k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, fl
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         }
     };
-    float m = 0.0f;
-    for (int i = tid; i < n8; i += kQuantThreads) {
+    auto add = [&](const float (&v)[8], float m) {
+        if (!NAN_SCALE) return max8(v, m);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(v[c]) & 0x7fffffffu));
+        return m;
+    };
+    // the row's first kOwn * kQuantThreads vectors (up to 8192 values) stay in registers
+    constexpr int kOwn = 4;
+    float own[kOwn][8], m = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u) {
+        const int i = u * kQuantThreads + tid;
+        if (i < n8) {
+            load(i, own[u]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) own[u][c] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u) m = add(own[u], m);
+    for (int i = kOwn * kQuantThreads + tid; i < n8; i += kQuantThreads) {
         float v[8];
         load(i, v);
-        if (NAN_SCALE) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(v[c]) & 0x7fffffffu));
-        } else {
-            m = max8(v, m);
-        }
+        m = add(v, m);
     }
     m = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
     if ((tid & 31) == 0) part[tid >> 5] = m;
@@ -697,10 +707,16 @@ k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, fl
     for (int w = 0; w < kQuantThreads / 32; ++w)
         m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(part[w])));
     const float s = __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
-    for (int i = tid; i < n8; i += kQuantThreads) {
+    uint2 *out = reinterpret_cast<uint2 *>(q + row * n);
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u) {
+        const int i = u * kQuantThreads + tid;
+        if (i < n8) out[i] = quant8(own[u], s, rs);
+    }
+    for (int i = kOwn * kQuantThreads + tid; i < n8; i += kQuantThreads) {
         float v[8];
         load(i, v);
-        reinterpret_cast<uint2 *>(q + row * n)[i] = quant8(v, s, rs);
+        out[i] = quant8(v, s, rs);
     }
     if (tid == 0) s_out[row] = s;
 }

@@ -226,11 +226,14 @@ k_int8_few(Int8FewDev p) {
                 *reinterpret_cast<uint2 *>(codes + (size_t)xt * pitch + (i >> 4) * kDepth +
                                            unit_at(xt, (i >> 1) & 7) + (i & 1) * 8) = q;
             };
-#pragma unroll 1
-            for (int i = x0; i < k8; i += 32 * group) {   // from L1 again: short code
-                float v[8];
-                unpack8(p.x[(int64_t)xt * k8 + i], v);
-                put(i, quant8(v, s, rs));
+#pragma unroll
+            for (int u = 0; u < kXVecs; ++u) {
+                const int i = x0 + 32 * group * u;
+                if (i < k8) {
+                    float v[8];
+                    unpack8(xv[u], v);
+                    put(i, quant8(v, s, rs));
+                }
             }
             for (int i = k8 + x0; i < pitch / 8; i += 32 * group) put(i, make_uint2(0, 0));
         }
