@@ -89,21 +89,22 @@ Split split_of(int64_t rows, int64_t E, int64_t N, int64_t Kd) {
 //                    512      118     25.3   23.4
 //   1536 x 2048      128       11.7   12.6   20.6
 //                    256       18.6   13.5   21.0
-// The stream's time is that of its weights up to 8 rows a group; beyond, it grows with
-// the products, and the tiles overtake it at about 4.8e8 of them, where their 4 us
-// more of preparation are won back.  Tiles and large tiles go by an estimate: the
-// waves of tiles x blocks of K x the time a block takes (0.55 us of 128 channels x 128
-// rows on one SM, 0.74 us of 256 x 256 on a pair, under the power cap).
+// The stream's time is that of its weights up to 8 rows a group.  Beyond, the ways go
+// by estimates (us): of the stream by its outputs and products, of the tile kernels by
+// the waves of tiles x blocks of K x the time a block takes (0.55 us of 128 channels x
+// 128 rows on one SM, 0.74 us of 256 x 256 on a pair, under the power cap), each with what
+// it takes at least.
 enum class How { Stream, Tiles, Large };
 How how(int path, int64_t rows, int64_t E, int64_t N, int64_t Kd, const Split &sp) {
     if (path == MOE_FFN_PATH_LARGE || path == MOE_FFN_PATH_LARGE_PAIR) return How::Large;
-    if (rows <= 8 * E || (double)rows * (double)N * (double)Kd <= 4.8e8) return How::Stream;
-    if (path == MOE_FFN_PATH_SMALL) return How::Tiles;
+    if (rows <= 8 * E) return How::Stream;
     const int64_t groups = std::min(E, rows), per = ceil_div(rows, groups);
-    const double kb = (double)ceil_div(Kd, 128);
-    const double tiles = 8.0 + (double)ceil_div(sp.likely * sp.splits, num_sms()) * kb / sp.splits * 0.55;
-    const double large = 9.0 + (double)ceil_div(groups * ceil_div(per, 256) * ceil_div(N, 256), num_sms() / 2) * kb * 0.74;
-    return tiles <= large ? How::Tiles : How::Large;
+    const double kb = (double)ceil_div(Kd, 128), outputs = (double)rows * (double)N;
+    const double stream = 4.0 + 13e-6 * outputs + 16e-9 * outputs * (double)Kd;
+    const double tiles = 9.0 + (double)ceil_div(sp.likely * sp.splits, num_sms()) * kb / sp.splits * 0.55;
+    const double large = 10.0 + (double)ceil_div(groups * ceil_div(per, 256) * ceil_div(N, 256), num_sms() / 2) * kb * 0.74;
+    if (stream <= tiles && (path == MOE_FFN_PATH_SMALL || stream <= large)) return How::Stream;
+    return path == MOE_FFN_PATH_SMALL || tiles <= large ? How::Tiles : How::Large;
 }
 
 struct Int8Layout {

@@ -2,7 +2,7 @@
 //
 // out[t] = bf16(sum_k p[t,k] * y(t,k) + shared[t]) with the stages of the
 // layer's other kernels, in the same arithmetic, so that the outputs are the
-// same bit for bit:
+// same bit for bit (y's rounding to bf16 among them):
 //   q1, s1 = quantised x[t];  h = (float(q1 . W1[e]) * scale1) * s1
 //   g = silu(h_a) * h_b;      q2, s2 = quantised g
 //   y = bf16((float(q2 . W2[e]) * scale2) * s2)
@@ -12,19 +12,33 @@
 // Reading the chosen experts' weights bounds it (stream_i8.cuh), and for one
 // token of small experts the steps between the reads.  So there are two
 // kernels, and neither an expert-major copy of the rows nor a routing kernel:
-//   k_few_gate_up  quantises the tokens in every CTA (a few KB from L2) and
-//                  multiplies; its CTAs share out the (expert, 8 rows, 8 + 8
-//                  channels) units evenly, in the weights' order.  The integer sums are exact,
-//                  so warps and stages may be added in any order.
+//   k_few_gate_up  deals the (expert, 8 rows, 8 + 8 channels) units to its CTAs in
+//                  turn, so that every CTA meets the crowded experts too (dealt in
+//                  runs, 32 tokens took 780 us, in turn 755); the warps share out the
+//                  stages of a batch of units.  The integer sums are exact, so they may be
+//                  added in any order.
 //   k_few_down     is launched while the first runs and fetches its first
 //                  weights meanwhile; a CTA owns 16 output channels for every
 //                  expert and route, so the weighted sum needs no other CTA.
-//                  It quantises g itself, from row maxima that the first kernel left.
-// Every CTA finds the experts' rows from expert_ids by itself (at most 512
-// routes: five block barriers).
-// Where the quantised rows do not fit shared memory beside the rings (kLocalBytes), a small
-// kernel before each product quantises them once, and the codes travel through the rings
-// with the weights.
+// Every CTA finds the experts' rows from expert_ids by itself: up to 32 routes by
+// one warp's votes, up to 512 by counts and sums.
+// With one or two tokens the CTAs also quantise by themselves (LOCAL): the tokens
+// from registers that are loaded before the routes are known, g a row to a warp.
+// Otherwise a small kernel before each product quantises the rows once, and the codes
+// travel through the rings with the weights.
+//
+// Measured, 128 experts, top-8, in a graph (us, moe_layer's small-batch path, the
+// weights at the HBM rate), slower and faster boxes 5 % apart:
+//   tokens            1    2    4    8   16   32   64
+//   H 7168, N 4096   62  110  200  343  540  754  880
+//     moe_layer     146  175  259  418  638  843  946
+//     weights        52  101  189  335  535  725  817
+//   H 2048, N 1536   13   20   31   47   71   96  116
+//     moe_layer      38   47   58   76  101  125  139
+//     weights         6   11   20   36   57   78   88
+// Time goes by what a kernel executes once, too: its instructions come from L2 line by
+// line, so the parts outside the loops are kept short (scales loaded for 16 slots in
+// straight code cost 4 us a batch of the second kernel).
 #include "common.cuh"
 #include "quant.cuh"
 #include "stream_i8.cuh"
@@ -40,23 +54,30 @@ using namespace si8;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxRoutes = MOE_FEW_TOKENS_MAX_ROUTES;
 
-// LOCAL: every CTA quantises what it multiplies, from registers.  Eight warps
-// and rings of 80 KB, so that a CTA of either kernel fits an SM beside one of the other.
-// Else the codes come through the rings.
-template <bool LOCAL, int D = 5>
+// LOCAL: every CTA quantises what it multiplies.  Eight warps and rings of 80 KB, so
+// that a CTA of either kernel fits an SM beside one of the other.  Else the codes
+// come through the rings, of twelve warps: 8 tokens of 7168 x 4096 took 584 us with 8
+// warps of four stages, 407 with 16 of three (each before other changes), 8, 12 and 16
+// warps of equal bytes then 356, 347 and 356.
+// Rows of an expert that share a reading of its weights: 8 NB.
+template <bool LOCAL, int D = 5, int NB = 1>
 struct Cfg {
     static constexpr int kWarps = LOCAL ? 8 : 12;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kD = D;                                 // stages of a warp's ring
-    static constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : kRowBytes);
+    static constexpr int kBytes = kWeightBytes + (LOCAL ? 0 : NB * kRowBytes);
     static constexpr int kRing = kWarps * kD * kBytes;
+    static constexpr int kBlock = NB * kRows;
+    static constexpr int kUnits = LOCAL || NB > 1 ? 8 : 16;     // of the first kernel, between two block barriers
 };
-template <bool LOCAL>
-constexpr int kUnits = LOCAL ? 8 : 16;          // of the first kernel, between two block barriers
 // Routes up to which the rings are five stages deep, else four (the sums of more
 // routes also need the room).  7168 x 4096, top-8, 128 experts (us, five against four): 2
 // tokens 112 / 115, 8 tokens 347 / 355, 16 tokens 566 / 568, 32 tokens 784 / 768, 64 tokens 917 / 901.
 constexpr int kDeepRoutes = 128;
+// Routes an expert, on average, above which 16 rows share a reading of its weights instead of
+// 8 (H 2048, N 1536, us, 16 against 8: 8 an expert 29.6 / 30.7, 16 an expert 69.3 / 77.9, 4 an
+// expert 23.8 either way; H 3280, N 1792, 14 an expert 38.9 / 46.3).
+constexpr int kCrowded = 4;
 constexpr int kXVecs = 7, kGVecs = 8;           // vectors of eight values that a LOCAL thread holds
 constexpr int kQuantThreads = 256;
 
@@ -82,7 +103,7 @@ struct Routes {
     int32_t code[kMaxRoutes];      // expert, -1 none, -2 zero expert, -3 copy expert
     uint16_t list[kMaxRoutes];     // the routes of each expert, expert after expert
     uint16_t place[kMaxRoutes];    // a route's place in that list
-    uint16_t blk_e[kMaxRoutes];    // blocks of up to 8 routes of one expert
+    uint16_t blk_e[kMaxRoutes];    // blocks of up to kBlock routes of one expert
     uint16_t blk_first[kMaxRoutes];
     uint8_t blk_n[kMaxRoutes];
     uint32_t count[kMaxExperts];
@@ -112,13 +133,14 @@ __device__ __forceinline__ int route_code(const FewDev &p, int i) {
 }
 
 // Up to 32 routes: one warp's votes, no counts per expert.
+template <int kBlock>
 __device__ __forceinline__ void find_routes_warp(const FewDev &p, Routes &r) {
     const int lane = threadIdx.x & 31;
     const int code = lane < p.R ? route_code(p, lane) : -1;
     if (lane < p.R) r.code[lane] = code == -4 ? -1 : code;
     if (code == -4) r.bad = 1;
     const uint32_t same = __match_any_sync(kFull, code);
-    const int head = __ffs(same) - 1, n = __popc(same), nb = (n + kRows - 1) / kRows;
+    const int head = __ffs(same) - 1, n = __popc(same), nb = (n + kBlock - 1) / kBlock;
     const bool heads = code >= 0 && head == lane;
     const uint32_t own = heads ? (uint32_t)(n << 16 | nb) : 0u;
     uint32_t sum = own;
@@ -131,8 +153,8 @@ __device__ __forceinline__ void find_routes_warp(const FewDev &p, Routes &r) {
     if (heads)
         for (int b = 0; b < nb; ++b) {
             r.blk_e[b0 + b] = (uint16_t)code;
-            r.blk_first[b0 + b] = (uint16_t)(first + b * kRows);
-            r.blk_n[b0 + b] = (uint8_t)min(kRows, n - b * kRows);
+            r.blk_first[b0 + b] = (uint16_t)(first + b * kBlock);
+            r.blk_n[b0 + b] = (uint8_t)min(kBlock, n - b * kBlock);
         }
     const int at = __shfl_sync(kFull, first, head) + __popc(same & lanemask_lt());
     if (code >= 0) {
@@ -145,11 +167,11 @@ __device__ __forceinline__ void find_routes_warp(const FewDev &p, Routes &r) {
     }
 }
 
-template <int kThreads>
+template <int kThreads, int kBlock>
 __device__ __forceinline__ void find_routes(const FewDev &p, Routes &r) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (p.R <= 32) {
-        if (warp == 0) find_routes_warp(p, r);
+        if (warp == 0) find_routes_warp<kBlock>(p, r);
         __syncthreads();
         return;
     }
@@ -169,7 +191,7 @@ __device__ __forceinline__ void find_routes(const FewDev &p, Routes &r) {
     const int per = (p.E + kThreads - 1) / kThreads;
     const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
     uint32_t own = 0;
-    for (int e = e0; e < e1; ++e) own += (r.count[e] << 16) | ((r.count[e] + kRows - 1) / kRows);
+    for (int e = e0; e < e1; ++e) own += (r.count[e] << 16) | ((r.count[e] + kBlock - 1) / kBlock);
     uint32_t sum = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -184,11 +206,11 @@ __device__ __forceinline__ void find_routes(const FewDev &p, Routes &r) {
         if (w < warp) at += r.part[w];
     for (int e = e0; e < e1; ++e) {
         const int n = (int)r.count[e], first = (int)(at >> 16), b0 = (int)(at & 0xffffu);
-        const int nb = (n + kRows - 1) / kRows;
+        const int nb = (n + kBlock - 1) / kBlock;
         for (int b = 0; b < nb; ++b) {
             r.blk_e[b0 + b] = (uint16_t)e;
-            r.blk_first[b0 + b] = (uint16_t)(first + b * kRows);
-            r.blk_n[b0 + b] = (uint8_t)min(kRows, n - b * kRows);
+            r.blk_first[b0 + b] = (uint16_t)(first + b * kBlock);
+            r.blk_n[b0 + b] = (uint8_t)min(kBlock, n - b * kBlock);
         }
         r.count[e] = (uint32_t)(first | n << 16);
         at += ((uint32_t)n << 16) | (uint32_t)nb;
@@ -206,7 +228,7 @@ __device__ __forceinline__ void find_routes(const FewDev &p, Routes &r) {
         const int code = r.code[i];
         if (code >= 0) {
             pos[o] += r.count[code] & 0xffffu;
-            several |= (r.count[code] >> 16) > kRows;
+            several |= (r.count[code] >> 16) > kBlock;
             r.list[pos[o]] = (uint16_t)i;
             r.place[i] = (uint16_t)pos[o];
         }
@@ -262,21 +284,21 @@ __host__ __device__ inline int padded(int k) { return (k + kDepth - 1) / kDepth 
 // ---------------------------------------------------------------- h = q1 . W1, g = silu(h_a) h_b
 // Unit u of block u / (Nh / 8): SiLU channels 8 j .. 8 j + 7 and their
 // multipliers (16 rows of the packed W1, two runs of eight).
-template <bool LOCAL, int D>
+template <bool LOCAL, int D, int NB>
 __global__ void __launch_bounds__(Cfg<LOCAL>::kThreads, LOCAL ? 2 : 1)
 k_few_gate_up(FewDev p) {
-    using C = Cfg<LOCAL, D>;
-    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kBatchUnits = kUnits<LOCAL>;
+    using C = Cfg<LOCAL, D, NB>;
+    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kBatchUnits = C::kUnits;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Routes r;
-    __shared__ int32_t acc[2][kBatchUnits][kRows][kChannels];
+    __shared__ int32_t acc[2][kBatchUnits][C::kBlock][kChannels];
     __shared__ uint32_t amax[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5;
     uint8_t *codes = smem + C::kRing;
     const int H = p.H, KS = (H + kDepth - 1) / kDepth, pitch = KS * kDepth, NU = p.Nh / 8;
     const Lane l;
 
-    for (int i = tid; i < 2 * kBatchUnits * kRows * kChannels; i += kThreads) (&acc[0][0][0][0])[i] = 0;
+    for (int i = tid; i < 2 * kBatchUnits * C::kBlock * kChannels; i += kThreads) (&acc[0][0][0][0])[i] = 0;
     if (LOCAL)
         for (int i = tid; i < p.T; i += kThreads) amax[i] = 0;
     clear_routes<kThreads>(p, r);
@@ -292,7 +314,7 @@ k_few_gate_up(FewDev p) {
             for (int u = 0; u < kXVecs; ++u)
                 if (x0 + 32 * group * u < H8) xv[u] = p.x[xt * H8 + x0 + 32 * group * u];
     }
-    find_routes<kThreads>(p, r);
+    find_routes<kThreads, C::kBlock>(p, r);
     // this CTA's units are blockIdx.x, blockIdx.x + gridDim.x, ...: every CTA meets every expert, the
     // crowded ones, whose rows take more arithmetic, too
     const int units = r.blocks * NU, u_end = (units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
@@ -313,15 +335,15 @@ k_few_gate_up(FewDev p) {
     struct Next {
         int batch, unit, ks, left;
         const uint8_t *src;          // the lane's bytes of the next stage
-        const int8_t *row[2];        // and of the rows, where they are
-    } f = {u_begin, 0, 0, 0, nullptr, {nullptr, nullptr}};
+        const int8_t *row[2 * NB];   // and of the rows, where they are
+    } f = {u_begin, 0, 0, 0, nullptr, {}};
     auto enter = [&]() {
         const int unit = unit_of(f.unit), blk = p.by_units(unit), j = (unit - blk * NU) * 8;
         const int64_t prow = (int64_t)r.blk_e[blk] * (2 * p.Nh) + (j >> 6) * 128 + ((j >> 4) & 3) * 32 + (j & 15);
         f.src = p.w1 + (prow + l.cr) * H + f.ks * kDepth + l.cu * 16;
         if (!LOCAL) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 2 * NB; ++i) {
                 const int row = 4 * i + l.cr;
                 f.row[i] = nullptr;
                 if (row < r.blk_n[blk])
@@ -349,14 +371,12 @@ k_few_gate_up(FewDev p) {
         }
         f.src += kDepth;
         if (!LOCAL && rows) {
-            if (f.row[0]) {
-                copy16(slot + l.to0 + kWeightBytes, f.row[0], in);
-                f.row[0] += kDepth;
-            }
-            if (f.row[1]) {
-                copy16(slot + l.to1 + kWeightBytes, f.row[1], in);
-                f.row[1] += kDepth;
-            }
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i)
+                if (f.row[i]) {
+                    copy16(slot + (i & 1 ? l.to1 : l.to0) + kWeightBytes + (i >> 1) * kRowBytes, f.row[i], in);
+                    f.row[i] += kDepth;
+                }
         }
         --f.left;
         if (++f.ks == KS) {
@@ -434,7 +454,7 @@ k_few_gate_up(FewDev p) {
                 return smem_u32(codes) + (uint32_t)(t * pitch + ks * kDepth) + l.of_row(t);
             };
             auto add = [&](int i, int c, int32_t v) { atomicAdd(&a[i][c], v); };
-            walk.template run<1>(l, m, r.blk_n[blk], fetch, row, add);
+            walk.template run<NB>(l, m, r.blk_n[blk], fetch, row, add);
             n -= m;
             ks = 0;
             ++unit;
@@ -458,10 +478,10 @@ k_few_gate_up(FewDev p) {
 }
 
 // ---------------------------------------------------------------- y = q2 . W2, out
-template <bool LOCAL, int D>
+template <bool LOCAL, int D, int NB>
 __global__ void __launch_bounds__(Cfg<LOCAL>::kThreads, LOCAL ? 2 : 1)
 k_few_down(FewDev p) {
-    using C = Cfg<LOCAL, D>;
+    using C = Cfg<LOCAL, D, NB>;
     constexpr int kThreads = C::kThreads, kWarps = C::kWarps;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Routes r;
@@ -477,7 +497,7 @@ k_few_down(FewDev p) {
     clear_routes<kThreads>(p, r);
     // ids, mask, weights and probs were there before the kernel before this one began
     for (int i = tid; i < p.R; i += kThreads) probs[i] = p.probs[i];
-    find_routes<kThreads>(p, r);
+    find_routes<kThreads, C::kBlock>(p, r);
     const int per_batch = r.blocks * KS;      // stages of 16 channels
     const int mine_a = per_batch * warp / kWarps, mine_n = per_batch * (warp + 1) / kWarps - mine_a;
     const int mine_blk = p.by_stages2(mine_a), mine_ks = mine_a - mine_blk * KS;
@@ -488,13 +508,13 @@ k_few_down(FewDev p) {
     struct Next {
         int batch, blk, ks, left;
         const uint8_t *src;
-        const int8_t *row[2];
-    } f = {(int)blockIdx.x, 0, 0, 0, nullptr, {nullptr, nullptr}};
+        const int8_t *row[2 * NB];
+    } f = {(int)blockIdx.x, 0, 0, 0, nullptr, {}};
     auto enter = [&]() {
         f.src = p.w2 + ((int64_t)r.blk_e[f.blk] * p.H + f.batch * kChannels + l.cr) * Nh + f.ks * kDepth + l.cu * 16;
         if (!LOCAL) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 2 * NB; ++i) {
                 const int row = 4 * i + l.cr;
                 f.row[i] = nullptr;
                 if (row < r.blk_n[f.blk])
@@ -524,14 +544,12 @@ k_few_down(FewDev p) {
         }
         f.src += kDepth;
         if (!LOCAL && rows) {
-            if (f.row[0]) {
-                copy16(slot + l.to0 + kWeightBytes, f.row[0], in);
-                f.row[0] += kDepth;
-            }
-            if (f.row[1]) {
-                copy16(slot + l.to1 + kWeightBytes, f.row[1], in);
-                f.row[1] += kDepth;
-            }
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i)
+                if (f.row[i]) {
+                    copy16(slot + (i & 1 ? l.to1 : l.to0) + kWeightBytes + (i >> 1) * kRowBytes, f.row[i], in);
+                    f.row[i] += kDepth;
+                }
         }
         --f.left;
         if (++f.ks == KS) {
@@ -613,7 +631,7 @@ k_few_down(FewDev p) {
                 return smem_u32(codes) + (uint32_t)((base + i) * pitch + ks * kDepth) + l.of_row(base + i);
             };
             auto add = [&](int i, int c, int32_t v) { atomicAdd(&a[(base + i) * kChannels + c], v); };
-            walk.template run<1>(l, m, r.blk_n[blk], fetch, row, add);
+            walk.template run<NB>(l, m, r.blk_n[blk], fetch, row, add);
             n -= m;
             ks = 0;
             ++blk;
@@ -674,11 +692,14 @@ k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, fl
         }
     };
     auto add = [&](const float (&v)[8], float m) {
-        if (!NAN_SCALE) return max8(v, m);
+        if constexpr (NAN_SCALE) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(v[c]) & 0x7fffffffu));
-        return m;
+            for (int c = 0; c < 8; ++c)
+                m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(v[c]) & 0x7fffffffu));
+            return m;
+        } else {
+            return max8(v, m);
+        }
     };
     // the row's first kOwn * kQuantThreads vectors (up to 8192 values) stay in registers
     constexpr int kOwn = 4;
@@ -739,20 +760,22 @@ moe_status launch_quant_rows_i8(const void *src, bool bf16, bool nan_scale, int6
     return MOE_OK;
 }
 
-// Whether each kernel's CTAs hold all codes themselves.  Measured (us, one against
-// the other):
+// Whether each kernel's CTAs quantise for themselves: a row's part fits a warp's
+// registers, and g is at most 16384 values.  Measured (us, so against with the two kernels
+// before the products): 1 token, H 2048, N 1536 13.1 / 15.3; H 7168, N 4096 62.3 / 62.0; 2
+// tokens, H 2048, N 1536 20.4 / 20.7.
 static bool few_tokens_local(int64_t T, int64_t K, int64_t H, int64_t Nh) {
     constexpr int kWarps = Cfg<true>::kWarps;
     return T <= kWarps && (H / 8 + 31) / 32 <= kXVecs * (kWarps / T) && T * K * Nh <= 16384;
 }
 
 // extra1, extra2: shared memory of the two kernels beside their rings.
-template <bool LOCAL, int D>
+template <bool LOCAL, int D, int NB>
 static moe_status launch_both(FewDev p, unsigned grid1, unsigned grid2, size_t extra1, size_t extra2,
                               const FewTokensArgs &a, cudaStream_t stream) {
-    using C = Cfg<LOCAL, D>;
-    auto up = k_few_gate_up<LOCAL, D>;
-    auto down = k_few_down<LOCAL, D>;
+    using C = Cfg<LOCAL, D, NB>;
+    auto up = k_few_gate_up<LOCAL, D, NB>;
+    auto down = k_few_down<LOCAL, D, NB>;
     if (!set_smem_limit((const void *)up, C::kRing + extra1) ||
         !set_smem_limit((const void *)down, C::kRing + extra2))
         return MOE_ERR_CUDA;
@@ -807,10 +830,11 @@ moe_status launch_layer_few_tokens(const moe_shape &s, const FewTokensArgs &a, c
     const unsigned grid2 = (unsigned)std::min<int64_t>(sms, H / kChannels);
     const size_t acc2 = (size_t)2 * R * kChannels * sizeof(int32_t);
     if (few_tokens_local(T, K, H, Nh))
-        return launch_both<true, 5>(p, grid1, grid2, (size_t)T * padded((int)H),
-                                    (size_t)R * padded((int)Nh) + acc2, a, stream);
-    return R <= kDeepRoutes ? launch_both<false, 5>(p, grid1, grid2, 0, acc2, a, stream)
-                            : launch_both<false, 4>(p, grid1, grid2, 0, acc2, a, stream);
+        return launch_both<true, 5, 1>(p, grid1, grid2, (size_t)T * padded((int)H),
+                                       (size_t)R * padded((int)Nh) + acc2, a, stream);
+    if (R > kCrowded * s.num_experts) return launch_both<false, 3, 2>(p, grid1, grid2, 0, acc2, a, stream);
+    return R <= kDeepRoutes ? launch_both<false, 5, 1>(p, grid1, grid2, 0, acc2, a, stream)
+                            : launch_both<false, 4, 1>(p, grid1, grid2, 0, acc2, a, stream);
 }
 
 }  // namespace moe

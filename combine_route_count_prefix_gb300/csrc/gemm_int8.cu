@@ -7,9 +7,12 @@
 // k_int8_few streams the weights (stream_i8.cuh): its CTAs share out the (group,
 // 8 NB rows, 16 channels) units evenly in the weights' order, its warps a batch of
 // units.  Reading the weights bounds it up to about 8 rows a group, and beyond that the
-// widening of the rows and the mma.
+// widening of the rows and the mma (products) and the rows' stores.
 // Rows come with the weights through the rings, or, LOCAL, are quantised from
-// bf16 by every CTA into its own memory (a few rows of one group).
+// bf16 by every CTA into its own memory (one or two rows of one group; more take a
+// kernel before: 4096 x 7168, 8 rows, 22 us in every CTA, 10.5 with it).
+// One bf16 row (us, of which the weights at the HBM rate): 4096 x 7168 7.7 (4.3), 7168 x
+// 2048 5.5 (2.2), 1536 x 2048 4.7 (0.5); 16 rows 12.5, 8.5, 6.4.
 #include "common.cuh"
 #include "quant.cuh"
 #include "stream_i8.cuh"

@@ -12,8 +12,10 @@
 // tensor memory to fill and drain), whose fp32 sums are exact below 2^24, that is
 // for 1024 products.
 // 16 channels x 8 rows x 128 take 4 + 2 shared loads, 96 integer and half
-// instructions for the widening and 8 mma per warp: about a third of the issue
-// slots at the rate the stages arrive at from HBM.
+// instructions for the widening and 8 mma per warp; one row takes 32 with dp4a. With
+// the copies and the loop a stage of one row is 114 instructions of a warp, a quarter
+// of the issue slots at the rate the stages arrive at from HBM.  A copy of 1 GB in
+// this shape runs at 6.5 TB/s with about 96 KB in flight on an SM.
 #pragma once
 #include <stdint.h>
 
