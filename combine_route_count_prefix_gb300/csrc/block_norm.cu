@@ -13,6 +13,10 @@
 // registers from there to the stores, through both sums.  Thread i holds the
 // 16-byte vectors i, i + threads, ... (eight channels each); a block of 128 channels
 // is 16 neighbouring vectors, half a warp: its maximum is four shuffles.
+// 16384 tokens of 7168 channels, a gate per token, all outputs: 204 us, 6.3 TB/s, 0.94
+// of a plain copy's rate; without gate and outer norm 172 us, 6.1 TB/s; one
+// token 3.3 us in a graph, the latency of two sums over the row.  Rows of a few KB are
+// bounded by the sums' barriers instead (16384 x 2048 63 us, 4.8 TB/s).
 #include "common.cuh"
 #include "fp8.cuh"
 #include "norm.cuh"
@@ -57,7 +61,7 @@ __device__ __forceinline__ float sigmoid(float g) {
     return r;
 }
 
-template <int V, bool W_BF16>
+template <int V, bool W_BF16, bool KEEP>
 __global__ void __launch_bounds__(kNormMaxThreads)
 k_block_norm(BlockNormDev p) {
     extern __shared__ __align__(128) uint8_t smem[];   // [stages][x, residual, gate][H]
@@ -87,6 +91,18 @@ k_block_norm(BlockNormDev p) {
         for (int s = 0; s < p.stages; ++s)
             if (blockIdx.x + (int64_t)s * gridDim.x < p.T) load(blockIdx.x + (int64_t)s * gridDim.x, s);
 
+    // KEEP: the weights come into registers before the first wait (a token alone would wait for L2 twice)
+    uint4 kept[KEEP ? 2 : 1][V];
+    if (KEEP) {
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const int i = u * nt + tid;
+            if (i < p.H8) {
+                if (p.post) kept[0][u] = __ldg(static_cast<const uint4 *>(p.post) + i);
+                if (p.weight) kept[KEEP ? 1 : 0][u] = __ldg(static_cast<const uint4 *>(p.weight) + i);
+            }
+        }
+    }
     int s = 0, turn = 0;
     uint32_t phase = 0;
     bool failed = false;
@@ -142,7 +158,8 @@ k_block_norm(BlockNormDev p) {
             if (i < p.H8) {
                 float f[8];
                 if (p.post) {
-                    load_weight<W_BF16>(p.post, i, f);
+                    if (KEEP) unpack8(kept[0][u], f);
+                    else load_weight<W_BF16>(p.post, i, f);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) h[u][c] *= r * f[c];
                 }
@@ -169,7 +186,8 @@ k_block_norm(BlockNormDev p) {
             float amax = 0.0f;
             if (in && p.weight) {
                 float w[8];
-                load_weight<W_BF16>(p.weight, i, w);
+                if (KEEP) unpack8(kept[KEEP ? 1 : 0][u], w);
+                else load_weight<W_BF16>(p.weight, i, w);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     h[u][c] *= w[c];
@@ -207,9 +225,9 @@ k_block_norm(BlockNormDev p) {
     }
 }
 
-template <int V, bool W_BF16>
+template <int V, bool W_BF16, bool KEEP>
 moe_status launch(BlockNormDev p, cudaStream_t stream) {
-    auto kernel = k_block_norm<V, W_BF16>;
+    auto kernel = k_block_norm<V, W_BF16, KEEP>;
     const bool gate_rows = p.gate && p.gate_tokens < p.T;
     const size_t stage = (size_t)(gate_rows ? 3 : 2) * p.H8 * 16;
     const size_t room = 224 * 1024;
@@ -230,7 +248,12 @@ moe_status launch(BlockNormDev p, cudaStream_t stream) {
 
 template <int V>
 moe_status launch_v(const BlockNormDev &p, bool w_bf16, cudaStream_t stream) {
-    return w_bf16 ? launch<V, true>(p, stream) : launch<V, false>(p, stream);
+    if constexpr (V <= 2) {
+        // a token a CTA: 128 x 7168 with gates 4.46 -> 3.78 us; for many tokens the registers cost
+        // CTAs (16384 x 7168, one gate, 195 -> 209 us)
+        if (w_bf16 && p.T <= num_sms()) return launch<V, true, true>(p, stream);
+    }
+    return w_bf16 ? launch<V, true, false>(p, stream) : launch<V, false, false>(p, stream);
 }
 
 }  // namespace
