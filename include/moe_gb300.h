@@ -278,14 +278,16 @@ moe_status moe_layer(const moe_shape *shape, const void *x, const int32_t *exper
                      void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* The whole layer for a few tokens: moe_layer's arguments and, for finite
- * inputs and scales, its results bit for bit, in two kernels (four where the
- * quantised rows of all tokens or routes pass 64 KB) and without its
- * workspace's row images.  For the steps of a decoding batch, where the time is
- * that of reading the chosen experts' weights.
+ * inputs and scales, its results bit for bit, in two kernels (four with more
+ * than a token or two) and without its workspace's row images.  For the steps of a
+ * decoding batch, where the time is that of reading the chosen experts' weights;
+ * with more than about 16 routes an expert moe_layer is faster.
  *   - T * K <= MOE_FEW_TOKENS_MAX_ROUTES; more return MOE_ERR_SHAPE.
  *   - shape->ffn_path SMALL or AUTO, and weights that moe_pack_weights packed
  *     with it (the packed bytes are read); the others return
  *     MOE_ERR_PARAM_INVALID.
+ *   - A token with NaN or infinities makes its own output NaN, infinite or
+ *     arbitrary, and no other's.
  *   - x_out may be the shared_expert_x buffer itself, and overlaps no other
  *     argument. */
 #define MOE_FEW_TOKENS_MAX_ROUTES 512
