@@ -53,9 +53,10 @@ bool has_images(int path) { return path != MOE_FFN_PATH_SMALL; }
 bool has_bytes(int path) { return path == MOE_FFN_PATH_SMALL || path == MOE_FFN_PATH_AUTO; }
 size_t image_bytes(int64_t E, int64_t N, int64_t Kd) { return align_up((size_t)E * N * Kd * 2, kAlign); }
 
+constexpr int64_t kMaxDepth = 131056;     // products of 2^14 at most: sums below 2^31
 moe_status check_int8(int64_t E, int64_t N, int64_t Kd) {
     if (E < 1 || E > kMaxExperts || N < 8 || N % 8 != 0 || N > (1 << 20) || Kd < 16 || Kd % 16 != 0 ||
-        Kd > 131072)
+        Kd > kMaxDepth)
         return MOE_FAIL(MOE_ERR_SHAPE);
     return MOE_OK;
 }
@@ -108,14 +109,13 @@ How how(int path, int64_t rows, int64_t E, int64_t N, int64_t Kd, const Split &s
 }
 
 struct Int8Layout {
-    size_t status, sched, rows, scales, sums, total;
+    size_t status, rows, scales, sums, total;
     size_t clear;              // words behind `sums` that a split call has cleared: sums, arrivals
 };
-Int8Layout int8_layout(int64_t rows, int64_t E, int64_t N, int64_t Kd, const Split &sp) {
+Int8Layout int8_layout(int64_t rows, int64_t N, int64_t Kd, const Split &sp) {
     Int8Layout L;
     Carve c;
     L.status = c.take(4);
-    L.sched = c.take((size_t)(E + 1) * sizeof(int32_t));
     L.rows = c.take((size_t)rows * Kd * 2);
     L.scales = c.take((size_t)rows * sizeof(float));
     L.clear = sp.splits > 1 ? (size_t)rows * ((N + 127) / 128 * 128) + sp.words() : 0;
@@ -205,7 +205,7 @@ moe_status moe_grouped_gemm_int8_workspace_size(int64_t rows, int64_t E, int64_t
     if (!bytes) return MOE_FAIL(MOE_ERR_NULLPTR);
     MOE_TRY(check_int8(E, N, Kd));
     if (rows < 0 || rows > INT32_MAX || rows * Kd >= (int64_t)1 << 40) return MOE_FAIL(MOE_ERR_SHAPE);
-    *bytes = int8_layout(rows, E, N, Kd, split_of(rows, E, N, Kd)).total;
+    *bytes = int8_layout(rows, N, Kd, split_of(rows, E, N, Kd)).total;
     return MOE_OK;
 }
 
@@ -232,7 +232,7 @@ moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
     if (workspace_bytes < need) return MOE_FAIL(MOE_ERR_WORKSPACE);
     if (empty) return MOE_OK;
     const Split sp = split_of(rows, E, N, Kd);
-    const Int8Layout L = int8_layout(rows, E, N, Kd, sp);
+    const Int8Layout L = int8_layout(rows, N, Kd, sp);
     int32_t *status = at<int32_t>(workspace, L.status);
     const How way = how(path, rows, E, N, Kd, sp);
     const uint8_t *bytes = static_cast<const uint8_t *>(w_packed) + (has_images(path) ? image_bytes(E, N, Kd) : 0);
@@ -274,7 +274,6 @@ moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
     g.Nout = N;
     g.Kd = Kd;
     g.offsets = expert_offsets;
-    g.sched = at<int32_t>(workspace, L.sched);
     g.y = C;
     g.y_f32 = out_dtype == MOE_DTYPE_F32;
     g.scale2 = w_scales;
@@ -287,10 +286,7 @@ moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
         g.arrived = at<uint32_t>(workspace, L.sums) + (L.clear - sp.words());
         return launch_grouped_gemm_small(Epi::Linear, g, stream);
     }
-    const bool pair = path != MOE_FFN_PATH_LARGE && linear_pairs_fit();
-    // the one-SM kernel takes its schedule from memory (which clears the status word again)
-    if (!pair) MOE_TRY(launch_sched(expert_offsets, E, at<int32_t>(workspace, L.sched), status, stream));
-    return launch_grouped_gemm(Epi::Linear, g, stream, pair);
+    return launch_grouped_gemm(Epi::Linear, g, stream, path != MOE_FFN_PATH_LARGE);
 }
 
 }  // extern "C"

@@ -325,8 +325,6 @@ struct GemmArgs {
 // no cluster of that kernel fits).
 moe_status launch_grouped_gemm(Epi epi, const GemmArgs &a, cudaStream_t stream,
                                bool pair = false);
-// Whether the Linear epilogue's pair kernel runs here; it needs no `sched`.
-bool linear_pairs_fit();
 // The same GEMM for few rows per expert: the weights stream as biased bytes
 // (b_img, w + 128; W1 in launch_pack_w1_i8's row order), are widened on chip
 // into tensor memory and are the MMA's M side; the expert's rows are its N

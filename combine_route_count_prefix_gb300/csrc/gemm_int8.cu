@@ -14,6 +14,7 @@
 // One bf16 row (us, of which the weights at the HBM rate): 4096 x 7168 7.7 (4.3), 7168 x
 // 2048 5.5 (2.2), 1536 x 2048 4.7 (0.5); 16 rows 12.5, 8.5, 6.4.
 #include "common.cuh"
+#include "groups.cuh"
 #include "quant.cuh"
 #include "stream_i8.cuh"
 
@@ -96,23 +97,11 @@ k_int8_few(Int8FewDev p) {
         for (int u = 0; u < kXVecs; ++u)
             if (x0 + 32 * group * u < k8) xv[u] = p.x[(int64_t)xt * k8 + x0 + 32 * group * u];
     }
-    for (int i = tid; i <= p.E; i += kThreads) s_off[i] = (int)min((int64_t)p.offsets[i], p.cap_rows);
+    for (int i = tid; i <= p.E; i += kThreads) s_off[i] = p.offsets[i];
     __syncthreads();
-    if (warp == 0) {   // s_blk[e]: row blocks of the groups before e
-        int carry = 0;
-        for (int base = 0; base < p.E; base += 32) {
-            const int e = base + lane;
-            const int c = e < p.E ? (s_off[e + 1] - s_off[e] + kMaxRows - 1) / kMaxRows : 0;
-            int x = c;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(kFull, x, d);
-                if (lane >= d) x += y;
-            }
-            if (e < p.E) s_blk[e] = carry + x - c;
-            carry += __shfl_sync(kFull, x, 31);
-        }
-        if (lane == 0) s_blk[p.E] = carry;
+    if (warp == 0) {
+        bound_offsets(s_off, p.E, p.cap_rows);
+        count_blocks(s_off, s_blk, p.E, kMaxRows);
     }
     __syncthreads();
     const int64_t units = (int64_t)s_blk[p.E] * NU;

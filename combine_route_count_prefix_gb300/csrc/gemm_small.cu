@@ -50,6 +50,7 @@
 //             products per row, still exact) to halve the drains.
 // Every wait is bounded (about two seconds) and sets MOE_DEV_TIMEOUT.
 #include "common.cuh"
+#include "groups.cuh"
 #include "tcgen05.cuh"
 
 #include <cudaTypedefs.h>
@@ -330,6 +331,7 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x) s_off[i] = p.offsets[i];
     __syncthreads();
     if (warp == 0) {
+        if (EPI == (int)Epi::Linear) bound_offsets(s_off, p.E, p.cap_rows);
         // s_sched[e] = TB-row blocks of the experts before e (warp scan)
         int carry = 0;
         for (int base = 0; base < p.E; base += 32) {

@@ -32,6 +32,7 @@
 // Every wait is bounded: after about two seconds a wait gives up, sets
 // MOE_DEV_TIMEOUT in the status word and the CTA drains and exits.
 #include "common.cuh"
+#include "groups.cuh"
 #include "tcgen05.cuh"
 
 #include <cuda.h>
@@ -302,9 +303,18 @@ k_grouped_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmB) : "memory");
     }
     pdl_wait();   // everything below may read what earlier kernels wrote
+    // Linear makes its schedule from the offsets; the others find it made
+    constexpr bool kOwnSched = EPI == (int)Epi::Linear;
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x) {
-        s_sched[i] = p.sched[i];
+        if (!kOwnSched) s_sched[i] = p.sched[i];
         s_off[i] = p.offsets[i];
+    }
+    if (kOwnSched) {
+        __syncthreads();
+        if (warp == 0) {
+            bound_offsets(s_off, p.E, p.cap_rows);
+            count_blocks(s_off, s_sched, p.E, BM);
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, TMEM_COLS);
@@ -513,6 +523,7 @@ k_grouped_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x) s_off[i] = p.offsets[i];
     __syncthreads();
     if (warp == 0) {
+        if (EPI == (int)Epi::Linear) bound_offsets(s_off, p.E, p.cap_rows);
         // s_psched[e] = 256-row blocks of the experts before e (warp scan)
         int carry = 0;
         for (int base = 0; base < p.E; base += 32) {
@@ -795,8 +806,6 @@ moe_status launch_pair_or_single(const GemmArgs &a, cudaStream_t stream, bool pa
     if (clusters > 0) return launch_epi_pair<EPI>(ma, mb, d, clusters, stream);
     return launch_epi<EPI>(ma, mb, d, stream);
 }
-
-bool linear_pairs_fit() { return pair_clusters<(int)Epi::Linear>() > 0; }
 
 moe_status launch_grouped_gemm(Epi epi, const GemmArgs &a, cudaStream_t stream, bool pair) {
     if (a.cap_rows <= 0 || a.E <= 0) return MOE_OK;

@@ -546,7 +546,11 @@ moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
  * w_scales        fp32 [E, N]; bias fp32 [E, N] or NULL
  * C               [rows, N] in out_dtype (MOE_DTYPE_F32 or MOE_DTYPE_BF16); rows
  *                 >= expert_offsets[E] untouched
- * N % 8 == 0, N <= 1048576, Kd % 16 == 0, 16 <= Kd <= 131072, rows * Kd < 2^40.
+ * expert_offsets  int32 [E+1], ascending and at most rows; others count as the
+ *                 nearest that are, the last one before all (no call reaches behind
+ *                 its arrays for them)
+ * N % 8 == 0, N <= 1048576, Kd % 16 == 0, 16 <= Kd <= 131056 (any int8 codes' sum
+ * fits 32 bits), rows * Kd < 2^40.
  * path: MOE_FFN_PATH_* as in moe_shape.  moe_pack_int8 writes w int8 [E, N, Kd] as
  * fp16 images (LARGE, LARGE_PAIR; 2 bytes a weight), as biased bytes (SMALL; 1
  * byte) or both (AUTO; 3 bytes, the call picks by its rows). */

@@ -227,6 +227,43 @@ def test_first_group_begins_behind_the_first_row(B, path):
         assert bool((out[:2] == 7.0).all())
 
 
+@pytest.mark.parametrize("path", ["small", "large", "large_pair"])
+def test_offsets_that_are_not_ascending(B, path):
+    """Groups end at the last offset, and begin where the ones before them end, whatever is given."""
+    for rows, N, Kd, a in ((30, 200, 336, "int8"), (130, 1000, 5008, "int8"), (130, 1000, 5008, "bf16")):
+        d = make(rows, 40, N, Kd, a=a)
+        _, packed = B.pack_int8(d["w"], path=path)
+        up = d["off"].cpu()
+        for bad in (up + torch.arange(41) * 1000, up - 1000, up.flip(0), torch.where(torch.arange(41) % 2 == 0, up, rows - up),
+                    torch.where(torch.arange(41) < 40, torch.full_like(up, 2 ** 31 - 1), torch.full_like(up, rows - 3)),
+                    torch.where(torch.arange(41) < 40, torch.full_like(up, -2 ** 31), torch.full_like(up, 2 ** 31 - 1))):
+            last = int(bad[-1].clamp(0, rows))
+            meant = bad.clamp(0, last).cummax(0).values
+            out = [torch.full((rows, N), 7.0, device=DEV) for _ in range(2)]
+            for off, o in zip((bad, meant), out):
+                _, ws = B.grouped_gemm_int8(off.to(DEV, torch.int32), d["a"], packed, d["ws"], a_scales=d["as_"], out=o,
+                                            path=path)
+                assert B.read_device_status(ws) == 0
+            assert torch.equal(*out)
+            assert bool((out[0][last:] == 7.0).all()) and bool((out[0][:int(meant[0])] == 7.0).all())
+
+
+@pytest.mark.parametrize("path", ["small", "large", "large_pair"])
+@pytest.mark.parametrize("rows", [2, 6, 20])
+def test_deepest_sums_fit_32_bits(B, path, rows):
+    Kd = 131056
+    w = torch.full((1, 8, Kd), -128, dtype=torch.int8, device=DEV)
+    w[0, 1] = 127
+    a = torch.full((rows, Kd), -128, dtype=torch.int8, device=DEV)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    one = torch.ones(1, 8, device=DEV)
+    out, _ = B.grouped_gemm_int8(off, a, B.pack_int8(w, path=path)[1], one, a_scales=torch.ones(rows, device=DEV),
+                                 out_dtype=torch.float32, path=path)
+    want = torch.full((rows, 8), float(Kd * 16384), device=DEV)      # fp32 rounds it once, as the definition does
+    want[:, 1] = -float(Kd * 128 * 127)
+    assert torch.equal(out, want)
+
+
 # Products large enough for the tile kernel of the small path, with and without a
 # split inner dimension, at widths and depths that end inside a tile.
 TILES = [dict(rows=130, E=1, N=1000, Kd=5008, bias=True), dict(rows=64, E=1, N=520, Kd=16400, a="bf16"),
