@@ -61,65 +61,55 @@ moe_status check_int8(int64_t E, int64_t N, int64_t Kd) {
     return MOE_OK;
 }
 
-// CTAs that share a tile's inner dimension where the tiles are too few for the GPU.
-constexpr int kMaxSplits = 8;
-struct Split {
-    int64_t tiles;             // at most
-    int64_t likely;            // with the rows spread evenly
-    int splits;
-    size_t words() const { return splits > 1 ? (size_t)tiles * 8 : 0; }
-};
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-Split split_of(int64_t rows, int64_t E, int64_t N, int64_t Kd) {
-    const int64_t tb = small_tile_rows(rows, E), cols = ceil_div(N, 128), groups = std::max<int64_t>(1, std::min(E, rows));
-    Split s;
-    s.tiles = (rows / tb + groups) * cols;
-    s.likely = groups * ceil_div(ceil_div(rows, groups), tb) * cols;
-    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({num_sms() / std::max<int64_t>(1, s.likely), Kd / 512, kMaxSplits}));
-    return s;
-}
 
-// How a call multiplies, measured (us, bf16 rows of one group):
-//   N x Kd          rows     stream  tiles  large
-//   4096 x 7168       16       13.3   15.4   44.9
-//                     24       17.5   14.9   43.7
-//                    256       92.2   27.3   47.4
-//                   1024      334     68.5   53.6
-//   7168 x 2048       32       11.6   12.4   20.8
-//                     64       18.7   12.7   21.9
-//                    512      118     25.3   23.4
-//   1536 x 2048      128       11.7   12.6   20.6
-//                    256       18.6   13.5   21.0
-// The stream's time is that of its weights up to 8 rows a group.  Beyond, the ways go
-// by estimates (us): of the stream by its outputs and products, of the tile kernels by
-// the waves of tiles x blocks of K x the time a block takes (0.55 us of 128 channels x
-// 128 rows on one SM, 0.74 us of 256 x 256 on a pair, under the power cap), each with what
-// it takes at least.
+// How a call multiplies, measured (us, bf16 rows, in brackets int8):
+//   N x Kd, one group, rows      stream         tiles          large
+//     4096 x 7168       16     12.4 (10.8)    13.3 (12.2)
+//                       32     17.1 (15.4)    15.0 (12.8)
+//                       64     28.8 (26.5)    16.3 (13.9)
+//                      256     90.7           26.0           47.0
+//                      512                    32.6           49.5
+//                     1024                    59.0           53.3
+//     7168 x 2048       16      8.5  (7.1)    10.8  (9.2)
+//                       32     11.8 (10.3)    10.9  (9.8)
+//                       64     18.9 (17.3)    11.8 (10.6)
+//                      512                    21.4           23.5
+//     1536 x 2048       32      7.7  (5.6)     8.2  (7.3)
+//                     1024                    15.0           23.6
+//   32 groups, 2048 x 2048, rows a group
+//                        4     26.4           32.0           62.8
+//                       16     45.4           33.7           65.2
+//                      200                    72.6           88.5
+//   64 groups, 2048 x 1024
+//                        4     37.3           31.7
+//                       64                    45.8           90.1
+// So the ways go by estimates (us): of the stream by its readings of the weights, for 8, 16 or
+// 32 rows each, of the tiles by int8_tiles_plan, of the SM-pair tiles by their waves and blocks
+// of K (0.74 us of 256 x 256 on a pair, under the power cap) and their images of the weights.
 enum class How { Stream, Tiles, Large };
-How how(int path, int64_t rows, int64_t E, int64_t N, int64_t Kd, const Split &sp) {
+How how(int path, int64_t rows, int64_t E, int64_t N, int64_t Kd, const Int8TilesPlan &plan) {
     if (path == MOE_FFN_PATH_LARGE || path == MOE_FFN_PATH_LARGE_PAIR) return How::Large;
-    if (rows <= 8 * E) return How::Stream;
     const int64_t groups = std::min(E, rows), per = ceil_div(rows, groups);
-    const double kb = (double)ceil_div(Kd, 128), outputs = (double)rows * (double)N;
-    const double stream = 4.0 + 13e-6 * outputs + 16e-9 * outputs * (double)Kd;
-    const double tiles = 9.0 + (double)ceil_div(sp.likely * sp.splits, num_sms()) * kb / sp.splits * 0.55;
-    const double large = 10.0 + (double)ceil_div(groups * ceil_div(per, 256) * ceil_div(N, 256), num_sms() / 2) * kb * 0.74;
-    if (stream <= tiles && (path == MOE_FFN_PATH_SMALL || stream <= large)) return How::Stream;
-    return path == MOE_FFN_PATH_SMALL || tiles <= large ? How::Tiles : How::Large;
+    const double w = (double)(groups * N), k = (double)Kd;
+    const double stream = rows <= 8 * E    ? 4.0 + w * (0.155e-6 * k + 1.0e-4)
+                          : rows <= 16 * E ? 4.0 + w * (0.25e-6 * k + 1.5e-4)
+                                           : 5.0 + w * (double)ceil_div(per, 32) * (0.38e-6 * k + 2.0e-4);
+    const int64_t waves = ceil_div(groups * ceil_div(per, 256) * ceil_div(N, 256), num_sms() / 2);
+    const double large = 10.0 + (double)waves * (2.0 + (double)ceil_div(Kd, 128) * 0.74) + (double)(E * N) * k * 0.24e-6;
+    if (stream <= plan.us && (path == MOE_FFN_PATH_SMALL || stream <= large)) return How::Stream;
+    return path == MOE_FFN_PATH_SMALL || plan.us <= large ? How::Tiles : How::Large;
 }
 
 struct Int8Layout {
-    size_t status, rows, scales, sums, total;
-    size_t clear;              // words behind `sums` that a split call has cleared: sums, arrivals
+    size_t status, rows, scales, total;
 };
-Int8Layout int8_layout(int64_t rows, int64_t N, int64_t Kd, const Split &sp) {
+Int8Layout int8_layout(int64_t rows, int64_t Kd) {
     Int8Layout L;
     Carve c;
     L.status = c.take(4);
-    L.rows = c.take((size_t)rows * Kd * 2);
+    L.rows = c.take((size_t)rows * Kd * 2);      // codes or fp16 images
     L.scales = c.take((size_t)rows * sizeof(float));
-    L.clear = sp.splits > 1 ? (size_t)rows * ((N + 127) / 128 * 128) + sp.words() : 0;
-    L.sums = c.take(L.clear * sizeof(uint32_t));
     L.total = c.off;
     return L;
 }
@@ -205,7 +195,7 @@ moe_status moe_grouped_gemm_int8_workspace_size(int64_t rows, int64_t E, int64_t
     if (!bytes) return MOE_FAIL(MOE_ERR_NULLPTR);
     MOE_TRY(check_int8(E, N, Kd));
     if (rows < 0 || rows > INT32_MAX || rows * Kd >= (int64_t)1 << 40) return MOE_FAIL(MOE_ERR_SHAPE);
-    *bytes = int8_layout(rows, N, Kd, split_of(rows, E, N, Kd)).total;
+    *bytes = int8_layout(rows, Kd).total;
     return MOE_OK;
 }
 
@@ -231,10 +221,10 @@ moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
         return MOE_FAIL(MOE_ERR_ALIGNMENT);
     if (workspace_bytes < need) return MOE_FAIL(MOE_ERR_WORKSPACE);
     if (empty) return MOE_OK;
-    const Split sp = split_of(rows, E, N, Kd);
-    const Int8Layout L = int8_layout(rows, N, Kd, sp);
+    const Int8Layout L = int8_layout(rows, Kd);
+    const Int8TilesPlan plan = int8_tiles_plan(rows, !bf16, E, N, Kd);
     int32_t *status = at<int32_t>(workspace, L.status);
-    const How way = how(path, rows, E, N, Kd, sp);
+    const How way = how(path, rows, E, N, Kd, plan);
     const uint8_t *bytes = static_cast<const uint8_t *>(w_packed) + (has_images(path) ? image_bytes(E, N, Kd) : 0);
     if (way == How::Stream) {
         Int8FewArgs f{};
@@ -262,10 +252,28 @@ moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
         }
         return launch_int8_few(f, stream);
     }
-    const bool split = way == How::Tiles && sp.splits > 1;
-    MOE_TRY(launch_rows_to_f16(A, bf16, a_scales, expert_offsets, E, rows, Kd, at<void>(workspace, L.rows),
-                               at<float>(workspace, L.scales), status, at<uint32_t>(workspace, L.sums),
-                               split ? (int64_t)L.clear : 0, stream));
+    const bool images = way == How::Large || !plan.bytes;
+    if (images)
+        MOE_TRY(launch_rows_to_f16(A, bf16, a_scales, expert_offsets, E, rows, Kd, at<void>(workspace, L.rows),
+                                   at<float>(workspace, L.scales), status, stream));
+    if (way == How::Tiles && !plan.whole) {
+        Int8TilesArgs t{};
+        t.rows = images ? at<void>(workspace, L.rows) : A;
+        t.row_scales = images ? at<float>(workspace, L.scales) : a_scales;
+        t.offsets = expert_offsets;
+        t.cap_rows = rows;
+        t.E = E;
+        t.N = N;
+        t.Kd = Kd;
+        t.w = bytes;
+        t.w_scales = w_scales;
+        t.bias = bias;
+        t.c = C;
+        t.out_bf16 = out_dtype == MOE_DTYPE_BF16;
+        t.status = status;
+        t.early = images;
+        return launch_int8_tiles(t, plan, stream);
+    }
     GemmArgs g{};
     g.a_img = at<void>(workspace, L.rows);
     g.cap_rows = rows;
@@ -280,12 +288,8 @@ moe_status moe_grouped_gemm_int8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
     g.s2 = at<float>(workspace, L.scales);
     g.bias = bias;
     g.status = status;
-    if (way == How::Tiles) {
-        g.splits = split ? sp.splits : 1;
-        g.partial = at<int32_t>(workspace, L.sums);
-        g.arrived = at<uint32_t>(workspace, L.sums) + (L.clear - sp.words());
-        return launch_grouped_gemm_small(Epi::Linear, g, stream);
-    }
+    g.wide = plan.wide;
+    if (way == How::Tiles) return launch_grouped_gemm_small(Epi::Linear, g, stream);
     return launch_grouped_gemm(Epi::Linear, g, stream, path != MOE_FFN_PATH_LARGE);
 }
 

@@ -315,11 +315,7 @@ struct GemmArgs {
     // Linear: y = (acc * scale2[e, n]) * s2[row] + bias[e, n], bf16 or fp32
     const float *bias;        // [E, Nout] or NULL
     bool y_f32;
-    // the int8-weight GEMM on a grid too small for the GPU: `splits` CTAs share a
-    // tile's inner dimension (Linear only)
-    int splits;               // 0 or 1: none
-    int32_t *partial;         // [cap_rows, Nout rounded up to 128] sums, cleared before the call
-    uint32_t *arrived;        // [tiles, 8], cleared too
+    bool wide;                // the small-batch kernel's tiles have 128 rows, not 64 (Linear only)
 };
 // pair: 256-row tiles on clusters of two CTAs (falls back to one-SM tiles when
 // no cluster of that kernel fits).
@@ -330,7 +326,6 @@ moe_status launch_grouped_gemm(Epi epi, const GemmArgs &a, cudaStream_t stream,
 // into tensor memory and are the MMA's M side; the expert's rows are its N
 // side, only as many as present.  Kd % 16 == 0 (and Nout % 128 == 0 for the
 // SwiGLU epilogue).
-int small_tile_rows(int64_t rows, int64_t E);   // Linear: 64 or 128
 moe_status launch_grouped_gemm_small(Epi epi, const GemmArgs &a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- a few tokens
@@ -372,11 +367,33 @@ struct Int8FewArgs {
 };
 bool int8_few_local(int64_t rows, int64_t E, int64_t Kd);
 moe_status launch_int8_few(const Int8FewArgs &a, cudaStream_t stream);
+// The same product of more rows a group, on tiles.
+struct Int8TilesArgs {
+    const void *rows;          // [cap_rows, Kd]: int8 (plan.bytes), or fp16 images
+    const float *row_scales;
+    const int32_t *offsets;
+    int64_t cap_rows, E, N, Kd;
+    const void *w;             // biased bytes
+    const float *w_scales, *bias;
+    void *c;
+    bool out_bf16;
+    int32_t *status;           // cleared (with images: the kernel that makes them does)
+    bool early;                // as above
+};
+struct Int8TilesPlan {
+    bool wide;                 // tiles of 128 rows, else 64
+    bool whole;                // launch_grouped_gemm_small instead, with images
+    bool bytes;                // takes the rows as int8
+    int splits;                // CTAs that share a tile's inner dimension
+    double us;                 // estimate
+};
+Int8TilesPlan int8_tiles_plan(int64_t rows, bool bytes, int64_t E, int64_t N, int64_t Kd);
+moe_status launch_int8_tiles(const Int8TilesArgs &a, const Int8TilesPlan &plan, cudaStream_t stream);
 // bf16 rows quantised, or int8 rows as they are -> fp16 images and scales; clears
-// the status word and `clear` (n_clear words).
+// the status word.
 moe_status launch_rows_to_f16(const void *rows, bool bf16, const float *scales, const int32_t *offsets,
                               int64_t E, int64_t cap_rows, int64_t Kd, void *img, float *img_scales,
-                              int32_t *status, uint32_t *clear, int64_t n_clear, cudaStream_t stream);
+                              int32_t *status, cudaStream_t stream);
 moe_status launch_layer_few_tokens(const moe_shape &s, const FewTokensArgs &a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- fp8 expert path

@@ -281,14 +281,11 @@ template <bool BF16>
 __global__ void __launch_bounds__(kImgThreads)
 k_rows_to_f16(const void *__restrict__ rows, const float *__restrict__ scales,
               const int32_t *__restrict__ offsets, int64_t E, int64_t cap_rows, int64_t Kd,
-              uint4 *__restrict__ img, float *__restrict__ img_scales, int32_t *__restrict__ status,
-              uint32_t *__restrict__ clear, int64_t n_clear) {
+              uint4 *__restrict__ img, float *__restrict__ img_scales, int32_t *__restrict__ status) {
     __shared__ uint32_t part[kImgThreads / 32];
     const int tid = threadIdx.x;
     pdl_wait();
     if (blockIdx.x == 0 && tid == 0) *status = 0;
-    for (int64_t i = (int64_t)blockIdx.x * kImgThreads + tid; i < n_clear; i += (int64_t)gridDim.x * kImgThreads)
-        clear[i] = 0;
     const int64_t R = min((int64_t)offsets[E], cap_rows);
     const int k8 = (int)(Kd / 8);
     constexpr int kOwn = 4;      // vectors that stay in registers: rows of up to 8192
@@ -391,16 +388,14 @@ moe_status launch_int8_few(const Int8FewArgs &a, cudaStream_t stream) {
 
 moe_status launch_rows_to_f16(const void *rows, bool bf16, const float *scales, const int32_t *offsets,
                               int64_t E, int64_t cap_rows, int64_t Kd, void *img, float *img_scales,
-                              int32_t *status, uint32_t *clear, int64_t n_clear, cudaStream_t stream) {
-    // (the CTAs without a row help to clear)
-    const int64_t clearers = std::min<int64_t>(num_sms() * 2, (n_clear + 2047) / 2048);
-    const unsigned grid = (unsigned)std::min<int64_t>(std::max(cap_rows, clearers), (int64_t)num_sms() * 8);
+                              int32_t *status, cudaStream_t stream) {
+    const unsigned grid = (unsigned)std::min<int64_t>(cap_rows, (int64_t)num_sms() * 8);
     if (bf16) {
         MOE_LAUNCH("rows_to_f16", k_rows_to_f16<true>, grid, kImgThreads, 0, stream, rows, scales, offsets, E,
-                   cap_rows, Kd, static_cast<uint4 *>(img), img_scales, status, clear, n_clear);
+                   cap_rows, Kd, static_cast<uint4 *>(img), img_scales, status);
     } else {
         MOE_LAUNCH("rows_to_f16", k_rows_to_f16<false>, grid, kImgThreads, 0, stream, rows, scales, offsets, E,
-                   cap_rows, Kd, static_cast<uint4 *>(img), img_scales, status, clear, n_clear);
+                   cap_rows, Kd, static_cast<uint4 *>(img), img_scales, status);
     }
     return MOE_OK;
 }

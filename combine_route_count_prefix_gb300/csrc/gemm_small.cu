@@ -18,10 +18,11 @@
 // Kernel shape (one persistent CTA per SM, 16 warps):
 //   warp 0       weight producer: one biased-int8 TMA tile (128 rows x 128,
 //                128-byte swizzle) per k-block into a 4-stage ring
-//   warps 1, 3   MMA issuers: one thread spends ~130 cycles issuing each
-//                tcgen05.mma whatever its N, and two threads issue at twice
-//                the rate, so the 8 MMAs (K = 16) of a 128-deep k-block are
-//                split: issuer i takes K [64 i, 64 i + 64) into its own 128
+//   warps 1, 3   MMA issuers, one elected lane each (the rest of the warp comes
+//                along, so that the compiler sees uniform operands; a branch on the
+//                lane instead cost ~130 cycles an MMA; 1 token of 7168 x 4096,
+//                top-8, 146.0 -> 141.5 us, 64 tokens 951 -> 937).  The 8 MMAs (K = 16) of
+//                a 128-deep k-block are split: issuer i takes K [64 i, 64 i + 64) into its own 128
 //                accumulator columns (the sums are exact integers, so how they
 //                are split and added does not matter); warp 1 also owns TMEM
 //                (512 columns: the issuers' 256 accumulator columns and four
@@ -118,35 +119,18 @@ struct SmallDev {
     const float *scale2;
     const float *s2;
     int32_t *status;
-    // Linear
-    const float *bias;
-    float *y32;
-    int splits;
-    int32_t *partial;
-    uint32_t *arrived;
+    const float *bias;   // Linear
+    float *y32;          // Linear with fp32 output
 };
 
-// kb0, kb1: the k-blocks of this CTA (all of them unless the tile is split);
-// index: the tile's number.
 struct Tile {
-    int e, row0, rows, wb, kb0, kb1, split;
-    int64_t index;
+    int e, row0, rows, wb;
 };
 
 template <int TB>
-__device__ __forceinline__ Tile decode_tile(int64_t tile, int splits, int num_kb, int n_wblocks, int E,
+__device__ __forceinline__ Tile decode_tile(int64_t tile, int n_wblocks, int E,
                                             const int32_t *s_sched, const int32_t *s_off) {
     Tile t;
-    t.split = 0;
-    t.kb0 = 0;
-    t.kb1 = num_kb;
-    if (splits > 1) {
-        t.split = (int)(tile % splits);
-        tile /= splits;
-        t.kb0 = num_kb * t.split / splits;
-        t.kb1 = num_kb * (t.split + 1) / splits;
-    }
-    t.index = tile;
     const int mblk = (int)(tile / n_wblocks);
     t.wb = (int)(tile % n_wblocks);
     int lo = 0, hi = E - 1;
@@ -235,40 +219,6 @@ __device__ __forceinline__ void epilogue_small(const SmallDev &p, const Tile &t,
     }
 }
 
-// Where several CTAs share a tile's inner dimension, each epilogue warp adds its
-// sums to the call's (cleared before it; integers, so in any order the same),
-// and the last of the same warps of the tile's CTAs takes the whole sums.  True for
-// that one.  (Left apart and added by the last, the parts cost it 64 waits for L2 each:
-// 64 rows, 1536 x 2048 in eight parts took 46 us.)
-template <int TB, int EPI_COLS>
-__device__ __forceinline__ bool join_splits(const SmallDev &p, const Tile &t, int ew, int q, int lane,
-                                            int c0, int32_t (&acc)[EPI_COLS]) {
-    const int64_t pitch = (int64_t)p.n_wblocks * BW;
-    int32_t *sum = p.partial + ((int64_t)t.row0 + c0) * pitch + t.wb * BW + q * 32 + lane;
-    const int n = (int)min((int64_t)(t.rows - c0), p.cap_rows - t.row0 - c0);
-    int32_t *at = sum;
-#pragma unroll
-    for (int i = 0; i < EPI_COLS; ++i, at += pitch) {
-        asm volatile("" : "+l"(at));   // one address after another, not all of them in registers
-        if (i < n) asm volatile("red.global.add.s32 [%0], %1;" ::"l"(at), "r"(acc[i]) : "memory");
-    }
-    __threadfence();
-    __syncwarp();
-    uint32_t before = 0;
-    if (lane == 0) before = atomicAdd(p.arrived + t.index * EPI_WARPS + ew, 1u);
-    before = __shfl_sync(0xffffffffu, before, 0);
-    if (before != (uint32_t)p.splits - 1) return false;
-    __threadfence();
-    at = sum;
-#pragma unroll
-    for (int j = 0; j < EPI_COLS; j += 16) {   // 16 loads at once, no more registers
-#pragma unroll
-        for (int i = j; i < j + 16; ++i, at += pitch) acc[i] = i < n ? __ldcg(at) : 0;
-        asm volatile("" : "+l"(at)::"memory");
-    }
-    return true;
-}
-
 // ---------------------------------------------------------------- the kernel
 template <int EPI, int TB_>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -278,7 +228,6 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
     constexpr int TB = Cfg::TB, NBUF = Cfg::NBUF, CHUNK_KB = Cfg::CHUNK_KB;
     constexpr int B_HALF_BYTES = Cfg::B_HALF_BYTES, B_BYTES = Cfg::B_BYTES;
     constexpr int EPI_COLS = Cfg::EPI_COLS;
-    constexpr bool kSplits = EPI == (int)Epi::Linear;
     constexpr size_t RING_BYTES = Cfg::RING_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -324,8 +273,8 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tmW) : "memory");
     }
     // Linear: the kernel before this one (the rows' images) has waited for everything
-    // else, so that only its own rows, scales and cleared sums are waited for, by those
-    // who read them; the weights are on their way meanwhile.
+    // else, so that only its rows and scales are waited for, by those who read them; the
+    // weights are on their way meanwhile.
     constexpr bool kEarly = EPI == (int)Epi::Linear;
     if (!kEarly) pdl_wait();   // everything below may read what earlier kernels wrote
     for (int i = threadIdx.x; i <= p.E; i += blockDim.x) s_off[i] = p.offsets[i];
@@ -356,8 +305,8 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int64_t total_tiles = (int64_t)s_sched[p.E] * p.n_wblocks * (kSplits ? p.splits : 1);
-    const int all_chunks = (p.num_kb + CHUNK_KB - 1) / CHUNK_KB;
+    const int64_t total_tiles = (int64_t)s_sched[p.E] * p.n_wblocks;
+    const int num_chunks = (p.num_kb + CHUNK_KB - 1) / CHUNK_KB;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -369,8 +318,8 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
             for (int s = 0; s < S8; ++s) issued_phase[s] = -1;
             bool ok = true;
             for (int64_t tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-                const Tile t = decode_tile<TB>(tile, kSplits ? p.splits : 1, p.num_kb, p.n_wblocks, p.E, s_sched, s_off);
-                for (int kb = kSplits ? t.kb0 : 0, kb1 = kSplits ? t.kb1 : p.num_kb; kb < kb1; ++kb) {
+                const Tile t = decode_tile<TB>(tile, p.n_wblocks, p.E, s_sched, s_off);
+                for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!wait_bounded(&w8_empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     mbar_arrive_expect_tx(&w8_full[stage], W8_BYTES);
                     tma_load_3d(ring8 + (size_t)stage * W8_BYTES, &tmW, &w8_full[stage], kb * BK,
@@ -394,8 +343,8 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
             for (int s = 0; s < SA; ++s) issued_phase[s] = -1;
             bool ok = true;
             for (int64_t tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-                const Tile t = decode_tile<TB>(tile, kSplits ? p.splits : 1, p.num_kb, p.n_wblocks, p.E, s_sched, s_off);
-                for (int kb = kSplits ? t.kb0 : 0, kb1 = kSplits ? t.kb1 : p.num_kb; kb < kb1; ++kb) {
+                const Tile t = decode_tile<TB>(tile, p.n_wblocks, p.E, s_sched, s_off);
+                for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!wait_bounded(&ab_empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
                     mbar_arrive_expect_tx(&ab_full[stage], (uint32_t)B_BYTES);
                     uint8_t *dst = ringB + (size_t)stage * B_BYTES;
@@ -419,8 +368,7 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
         uint32_t ph8 = 0, pha = 0;
         bool ok = true;
         for (int64_t tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-            const Tile t = decode_tile<TB>(tile, kSplits ? p.splits : 1, p.num_kb, p.n_wblocks, p.E, s_sched, s_off);
-            for (int kb = kSplits ? t.kb0 : 0, kb1 = kSplits ? t.kb1 : p.num_kb; kb < kb1; ++kb) {
+            for (int kb = 0; kb < p.num_kb; ++kb) {
                 const bool w = wait_bounded(&w8_full[s8], ph8, abort_flag, p.status) &&
                                wait_bounded(&ab_empty[sa], pha ^ 1u, abort_flag, p.status);
                 if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
@@ -458,47 +406,50 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
             }
         }
     } else if (warp == 1 || warp == 3) {
-        if (lane == 0) {
-            // ------------------------------------------------ MMA issuers
-            const int is = warp >> 1;   // 0 or 1: K [64 is, 64 is + 64) of every k-block
-            int stage = 0;
-            uint32_t phase = 0;
-            int accb = 0;
-            uint32_t acc_phase = 0;
-            bool ok = true;
-            for (int64_t tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
-                const Tile t = decode_tile<TB>(tile, kSplits ? p.splits : 1, p.num_kb, p.n_wblocks, p.E, s_sched, s_off);
-                const int n16 = ((t.rows + 15) / 16) * 16;
-                const uint32_t idesc = idesc_f16(BW, n16);
-                for (int kb0 = kSplits ? t.kb0 : 0, end = kSplits ? t.kb1 : p.num_kb; ok && kb0 < end; kb0 += CHUNK_KB) {
-                    if (!wait_bounded(&acc_empty[accb], acc_phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+        // ---------------------------------------------------- MMA issuers
+        const int is = __shfl_sync(0xffffffffu, warp >> 1, 0);   // 0 or 1: K [64 is, 64 is + 64) of every k-block
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
+        int stage = 0;
+        uint32_t phase = 0;
+        int accb = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int64_t tile = blockIdx.x; ok && tile < total_tiles; tile += gridDim.x) {
+            const Tile t = decode_tile<TB>(tile, p.n_wblocks, p.E, s_sched, s_off);
+            const int n16 = ((t.rows + 15) / 16) * 16;
+            const uint32_t idesc = __shfl_sync(0xffffffffu, idesc_f16(BW, n16), 0);
+            for (int kb0 = 0; ok && kb0 < p.num_kb; kb0 += CHUNK_KB) {
+                ok = __all_sync(0xffffffffu, wait_bounded(&acc_empty[accb], acc_phase ^ 1u, abort_flag, p.status));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tm + (uint32_t)(is * ACC_COLS + accb * TB);
+                const int kb1 = min(kb0 + CHUNK_KB, p.num_kb);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = __all_sync(0xffffffffu, wait_bounded(&ab_full[stage], phase, abort_flag, p.status));
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + (uint32_t)(is * ACC_COLS + accb * TB);
-                    const int kb1 = min(kb0 + CHUNK_KB, end);
-                    for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!wait_bounded(&ab_full[stage], phase, abort_flag, p.status)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t a_tmem = tmem_base + A_COL0 + (uint32_t)stage * A_STAGE_COLS;
-                        const uint32_t b_addr = smem_u32(ringB + (size_t)stage * B_BYTES);
+                    const uint32_t a_tmem = tm + A_COL0 + (uint32_t)stage * A_STAGE_COLS;
+                    const uint32_t b_addr = smem_u32(ringB + (size_t)stage * B_BYTES);
+                    if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)   // K = 16: 8 TMEM columns, 32 bytes of a row
                             mma_f16_ta(d_tmem, a_tmem + 32 * is + 8 * k,
                                        desc_sw128(b_addr + is * B_HALF_BYTES + 32 * k), idesc,
                                        (kb > kb0 || k > 0) ? 1u : 0u);
                         mma_commit(&ab_empty[stage]);
-                        if (++stage == SA) { stage = 0; phase ^= 1u; }
                     }
-                    if (!ok) break;
-                    mma_commit(&acc_full[accb]);
-                    if (++accb == NBUF) { accb = 0; acc_phase ^= 1u; }
+                    __syncwarp();
+                    if (++stage == SA) { stage = 0; phase ^= 1u; }
                 }
+                if (!ok) break;
+                if (elect_one()) mma_commit(&acc_full[accb]);
+                __syncwarp();
+                if (++accb == NBUF) { accb = 0; acc_phase ^= 1u; }
             }
-            mma_commit(drain);
-            wait_bounded(drain, 0, abort_flag, p.status, false);
         }
+        if (elect_one()) mma_commit(drain);
+        __syncwarp();
+        wait_bounded(drain, 0, abort_flag, p.status, false);
     } else if (warp >= EPI_WARP0) {
         // ---------------------------------------------------- epilogue warps
         if (kEarly) pdl_wait();
@@ -510,13 +461,12 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
         // buffer and the sums fit the registers together
         constexpr int LDW = EPI_COLS > 32 ? 16 : 32;
         for (int64_t tile = blockIdx.x; tile < total_tiles; tile += gridDim.x) {
-            const Tile t = decode_tile<TB>(tile, kSplits ? p.splits : 1, p.num_kb, p.n_wblocks, p.E, s_sched, s_off);
+            const Tile t = decode_tile<TB>(tile, p.n_wblocks, p.E, s_sched, s_off);
             const int nj = (t.rows - c0 + LDW - 1) / LDW;   // column groups holding rows (may be <= 0)
             int32_t acc[EPI_COLS];
 #pragma unroll
             for (int i = 0; i < EPI_COLS; ++i) acc[i] = 0;
             bool ok = true;
-            const int num_chunks = kSplits ? (t.kb1 - t.kb0 + CHUNK_KB - 1) / CHUNK_KB : all_chunks;
             for (int c = 0; c < num_chunks; ++c) {
                 const bool w = wait_bounded(&acc_full[accb], acc_phase, abort_flag, p.status);
                 if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
@@ -546,9 +496,6 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
                 if (++accb == NBUF) { accb = 0; acc_phase ^= 1u; }
             }
             if (!ok) break;
-            if (kSplits && p.splits > 1 && nj > 0 &&
-                !join_splits<TB, EPI_COLS>(p, t, warp - EPI_WARP0, q, lane, c0, acc))
-                continue;
             if (nj > 0) epilogue_small<EPI, EPI_COLS>(p, t, q, lane, c0, acc);
         }
     }
@@ -579,18 +526,13 @@ moe_status launch_small_epi(const CUtensorMap &mr, const CUtensorMap &mw, const 
 
 }  // namespace
 
-// The Linear product's rows a tile: one group's rows are known, those of several
-// spread.
-int small_tile_rows(int64_t rows, int64_t E) { return rows > (E == 1 ? 64 : kNarrowTileMaxRowsPerExpert * E) ? 128 : 64; }
-
 moe_status launch_grouped_gemm_small(Epi epi, const GemmArgs &a, cudaStream_t stream) {
     if (a.cap_rows <= 0 || a.E <= 0) return MOE_OK;
     if (a.Kd % 16 != 0) return MOE_ERR_SHAPE;   // byte rows must be 16-byte strided for TMA
     if (epi == Epi::SwiGLU && a.Nout % 128 != 0) return MOE_ERR_SHAPE;
     // the row capacity bounds the rows present: 64-row tiles while it averages
     // at most 32 rows per expert, else 128-row tiles
-    const bool wide = epi == Epi::Linear ? small_tile_rows(a.cap_rows, a.E) > 64
-                                         : a.cap_rows > kNarrowTileMaxRowsPerExpert * a.E;
+    const bool wide = epi == Epi::Linear ? a.wide : a.cap_rows > kNarrowTileMaxRowsPerExpert * a.E;
     CUtensorMap mr, mw;
     const uint64_t rdims[2] = {(uint64_t)a.Kd, (uint64_t)a.cap_rows};
     const uint64_t rstr[1] = {(uint64_t)a.Kd * 2};
@@ -622,9 +564,6 @@ moe_status launch_grouped_gemm_small(Epi epi, const GemmArgs &a, cudaStream_t st
     d.status = a.status;
     d.bias = a.bias;
     d.y32 = a.y_f32 ? static_cast<float *>(a.y) : nullptr;
-    d.splits = a.splits > 1 ? a.splits : 1;
-    d.partial = a.partial;
-    d.arrived = a.arrived;
     switch (epi) {
         case Epi::S32: return launch_small_epi<(int)Epi::S32>(mr, mw, d, wide, stream);
         case Epi::SwiGLU: return launch_small_epi<(int)Epi::SwiGLU>(mr, mw, d, wide, stream);

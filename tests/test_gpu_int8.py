@@ -280,14 +280,62 @@ def test_tiles(B, kw):
             check(B, make(**kw), path, dtype)
 
 
+# Each kernel for tiles, on whole and on split inner dimensions, with more tiles than the GPU
+# takes at once (groups much larger than the others), and rows that end anywhere in a tile.
+KERNELS = [dict(rows=60, E=3, N=5000, Kd=400), dict(rows=37, E=1, N=1000, Kd=7184), dict(rows=64, E=1, N=4104, Kd=2064),
+           dict(rows=50, E=1, N=7168, Kd=2048), dict(rows=1000, E=40, N=520, Kd=528), dict(rows=2400, E=40, N=520, Kd=272),
+           dict(rows=127, E=1, N=1024, Kd=8192), dict(rows=250, E=1, N=3080, Kd=4112), dict(rows=129, E=1, N=264, Kd=2048),
+           dict(rows=512, E=16, N=128, Kd=4096, counts=[0, 301, 1, 2] + [17] * 12),
+           dict(rows=320, E=10, N=1920, Kd=336, counts=[211, 65, 1] + [6] * 7),
+           dict(rows=1536, E=16, N=256, Kd=4096, counts=[129, 1, 900] + [33] * 13)]
+
+
+@pytest.mark.parametrize("kw", KERNELS, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items() if k != "counts"))
+def test_tile_kernels(B, kw):
+    for a in ("int8", "bf16"):
+        for bias, dtype in ((False, torch.bfloat16), (True, torch.float32)):
+            check(B, make(a=a, bias=bias, **kw), "small", dtype)
+
+
+def test_split_tiles_in_graphs_and_on_two_streams(B):
+    """Calls whose CTAs share tiles, one after another in a graph and at once on two streams."""
+    sets = []
+    for i in range(2):
+        d = make(64, 1, 1024, 8192, seed=i)
+        sets.append((d, B.pack_int8(d["w"])[1], reference(d, torch.bfloat16)[0], torch.cuda.Stream(),
+                     [torch.empty(64, 1024, dtype=torch.bfloat16, device=DEV) for _ in range(12)]))
+    torch.cuda.synchronize()
+    graphs = []
+    for d, packed, want, stream, outs in sets:
+        with torch.cuda.stream(stream):
+            _, ws = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], out=outs[0])
+        stream.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            for o in outs:
+                B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], out=o, ws=ws)
+        graphs.append((g, ws))
+    for _ in range(5):
+        for _, _, _, _, outs in sets:
+            for o in outs:
+                o.fill_(7.0)
+        torch.cuda.synchronize()
+        for (g, _), (_, _, _, stream, _) in zip(graphs, sets):
+            with torch.cuda.stream(stream):
+                g.replay()
+        torch.cuda.synchronize()
+        for d, packed, want, _, outs in sets:
+            assert all(torch.equal(o, want) for o in outs)
+    assert all(B.read_device_status(ws) == 0 for _, ws in graphs)
+
+
 def test_tiles_sums_are_exact(B):
     for rows in (64, 128):
         check(B, make(rows, 1, 1024, 8192, extreme=True), "small", torch.float32)
 
 
 def test_split_tiles_clear_their_counters(B):
-    """The CTAs that share a tile's inner dimension meet at counters and sums that
-    every call clears: the same bits whatever the workspace held."""
+    """CTAs that share a tile's inner dimension: the same bits whatever the workspace held."""
     d = make(64, 1, 1024, 8192)
     _, packed = B.pack_int8(d["w"], path="small")
     ref, ws = B.grouped_gemm_int8(d["off"], d["a"], packed, d["ws"], a_scales=d["as_"], path="small")
