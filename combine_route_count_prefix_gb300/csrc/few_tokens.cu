@@ -31,10 +31,10 @@
 // weights at the HBM rate), slower and faster boxes 5 % apart:
 //   tokens            1    2    4    8   16   32   64
 //   H 7168, N 4096   62  110  200  343  540  754  880
-//     moe_layer     146  175  259  418  638  843  946
+//     moe_layer     143  171  250  404  622  838  934
 //     weights        52  101  189  335  535  725  817
 //   H 2048, N 1536   13   20   31   47   71   96  116
-//     moe_layer      38   47   58   76  101  125  139
+//     moe_layer      37   46   56   75   97  123  136
 //     weights         6   11   20   36   57   78   88
 // Time goes by what a kernel executes once, too: its instructions come from L2 line by
 // line, so the parts outside the loops are kept short (scales loaded for 16 slots in

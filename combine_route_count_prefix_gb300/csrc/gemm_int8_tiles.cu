@@ -8,17 +8,20 @@
 // side, fp32 sums of at most 1024 products are exact, totals are int32.  What a call of
 // this size waits for is not the products, though, but the steps before and behind them (64
 // int8 rows of 7168 x 2048, 10.6 us, of which the weights' 2.2: start and offsets 0.9, first
-// blocks 2.2, 8 blocks of K 2.6, last sums 0.7, exchange 0.9, stores 1, end and next start 1.5),
+// blocks 2.2, 8 blocks of K 2.6, last sums 0.7, exchange 1.1, stores 1.2, end and next start 1.9),
 // so here
 //   - int8 rows in tiles of 64 come as they are, and the warps that widen a block of weights
 //     widen its rows, into the swizzled layout the MMA reads: no kernel makes images of
-//     them first (64 rows of 7168 x 2048 12.2 -> 10.6 us).  For tiles of 128 that took
-//     longer: every CTA widens them again, and shared memory carries each row three times;
+//     them first (64 rows of 7168 x 2048 12.2 -> 10.6 us).  For tiles of 128 it saved nothing
+//     (4096 x 7168 19.0 / 18.8, 1536 x 2048 12.3 / 12.1): every CTA widens the rows again, and
+//     shared memory carries each of them three times;
 //   - three sets of four warps widen a block each, in turn, so that the way from a block's
 //     arrival to its MMAs (half a microsecond) is not the time a block takes;
 //   - where the tiles are fewer than SMs, a cluster of up to eight CTAs shares a tile's inner
 //     dimension.  Its CTAs swap their parts through distributed shared memory with stores
-//     that the receiver's barrier counts (plain stores, a fence and an arrival took 1 us longer),
+//     that the receiver's barrier counts (against plain stores, a fence and an arrival,
+//     4096 x 7168, 64 rows 14.8 -> 14.5 us; against sums added in L2, 128 rows of 1536 x 2048
+//     13.0 -> 11.4),
 //     four rows in turn to each, so the exchange, the scaling and the stores are shared out,
 //     and nothing has to be cleared before the call.
 //
