@@ -552,6 +552,7 @@ def grouped_gemm_s32(expert_offsets, A, W, ws=None, C=None, stream=None, path="a
     return C, ws
 
 
+@functools.lru_cache(maxsize=256)
 def int8_packed_bytes(E, N, Kd, path="auto") -> int:
     n = ctypes.c_size_t()
     _call("moe_int8_packed_bytes", E, N, Kd, FFN_PATHS[path], ctypes.byref(n))
