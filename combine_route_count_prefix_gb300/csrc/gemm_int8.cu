@@ -11,8 +11,8 @@
 // Rows come with the weights through the rings, or, LOCAL, are quantised from
 // bf16 by every CTA into its own memory (one or two rows of one group; more take a
 // kernel before: 4096 x 7168, 8 rows, 22 us in every CTA, 10.5 with it).
-// One bf16 row (us, of which the weights at the HBM rate): 4096 x 7168 7.7 (4.3), 7168 x
-// 2048 5.5 (2.2), 1536 x 2048 4.7 (0.5); 16 rows 12.5, 8.5, 6.4.
+// One bf16 row (us, of which the weights at the HBM rate): 4096 x 7168 7.0 (4.3), 7168 x
+// 2048 4.8 (2.2), 1536 x 2048 4.0 (0.5); one int8 row 6.8, 4.6, 3.0; 16 bf16 rows 12.0, 8.0, 5.9.
 #include "common.cuh"
 #include "groups.cuh"
 #include "quant.cuh"
@@ -97,14 +97,28 @@ k_int8_few(Int8FewDev p) {
         for (int u = 0; u < kXVecs; ++u)
             if (x0 + 32 * group * u < k8) xv[u] = p.x[(int64_t)xt * k8 + x0 + 32 * group * u];
     }
-    for (int i = tid; i <= p.E; i += kThreads) s_off[i] = p.offsets[i];
-    __syncthreads();
-    if (warp == 0) {
-        bound_offsets(s_off, p.E, p.cap_rows);
-        count_blocks(s_off, s_blk, p.E, kMaxRows);
+    // One group of at most one block of rows: no search, and LOCAL fetches weights before the offsets are
+    // here (one row of 4096 x 7168 8.1 -> 7.0 us, of 1536 x 2048 4.9 -> 4.0).  They are asked for first:
+    // behind the weights they take a microsecond more.
+    const bool one = LOCAL || (p.E == 1 && p.cap_rows <= kMaxRows);
+    const int one_first = one ? p.offsets[0] : 0, one_last = one ? p.offsets[1] : 0;
+    int one_row0 = 0, one_rows = 0;
+    auto see_offsets = [&]() {
+        const int last = (int)max((int64_t)0, min((int64_t)one_last, p.cap_rows));
+        one_row0 = min(max(one_first, 0), last);
+        one_rows = last - one_row0;
+    };
+    if (one && !LOCAL) see_offsets();
+    if (!one) {
+        for (int i = tid; i <= p.E; i += kThreads) s_off[i] = p.offsets[i];
+        __syncthreads();
+        if (warp == 0) {
+            bound_offsets(s_off, p.E, p.cap_rows);
+            count_blocks(s_off, s_blk, p.E, kMaxRows);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    const int64_t units = (int64_t)s_blk[p.E] * NU;
+    const int64_t units = one ? NU : (int64_t)s_blk[p.E] * NU;
     const int64_t u_begin = units * blockIdx.x / gridDim.x, u_end = units * (blockIdx.x + 1) / gridDim.x;
 
     // unit -> group, first row, rows, first channel
@@ -113,6 +127,13 @@ k_int8_few(Int8FewDev p) {
     };
     auto find = [&](int64_t unit) {
         At a;
+        if (one) {
+            a.e = 0;
+            a.row0 = one_row0;
+            a.rows = one_rows;
+            a.ch = (int)unit * kChannels;
+            return a;
+        }
         const int blk = units * NU <= UINT32_MAX ? p.by_units((int)unit) : (int)(unit / NU);
         int lo = 0, hi = p.E - 1;
         while (lo < hi) {   // last group whose first block is <= blk
@@ -197,6 +218,13 @@ k_int8_few(Int8FewDev p) {
         walk.first(fetch, false, true);
     }
     if (blockIdx.x == 0 && tid == 0) *p.status = 0;
+    if (LOCAL) see_offsets();
+    if (one && one_rows == 0) {   // the same for all threads
+        copy_commit();
+        copy_wait<0>();
+        return;
+    }
+    if (one) __syncthreads();   // acc and amax are cleared
     if (LOCAL) {
         // the rows' codes, in every CTA
         if (xt < p.cap_rows) {
