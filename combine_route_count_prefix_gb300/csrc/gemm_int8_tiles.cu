@@ -7,8 +7,8 @@
 // channels), widened from bytes to fp16 straight into tensor memory, the rows the N
 // side, fp32 sums of at most 1024 products are exact, totals are int32.  What a call of
 // this size waits for is not the products, though, but the steps before and behind them (64
-// int8 rows of 7168 x 2048, 10.6 us, of which the weights' 2.2: start and offsets 0.9, first
-// blocks 2.2, 8 blocks of K 2.6, last sums 0.7, exchange 1.1, stores 1.2, end and next start 1.9),
+// int8 rows of 7168 x 2048, 10.3 us, of which the weights' 2.2: start, offsets and first
+// blocks 2.8, 8 blocks of K 2.6, last sums 0.7, exchange 1.1, stores 1.2, end and next start 1.9),
 // so here
 //   - int8 rows in tiles of 64 come as they are, and the warps that widen a block of weights
 //     widen its rows, into the swizzled layout the MMA reads: no kernel makes images of
@@ -237,8 +237,11 @@ k_int8_tiles(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
     const int64_t first = blockIdx.x / splits, step = gridDim.x / splits;
     const int kb0 = p.num_kb * rank / splits, kb1 = p.num_kb * (rank + 1) / splits;   // this CTA's k-blocks
     // With one group the first tile's weights need no offsets (int8, 17 rows of 4096 x 7168
-    // 12.7 -> 12.2 us, 32 of 7168 x 2048 9.9 -> 9.5, with the cluster that need not end together, below).
+    // 12.7 -> 11.9 us, 32 of 7168 x 2048 9.9 -> 9.4, with the cluster that need not end together, below).
+    // The offsets are asked for first: behind the weights they would come later.
     const int ahead = p.E == 1 ? min(S8, kb1 - kb0) : 0;
+    int32_t off = 0;
+    if (warp == 0 && lane <= p.E) off = p.offsets[lane];
     if (threadIdx.x == 0)
         for (int s = 0; s < ahead; ++s) {
             mbar_arrive_expect_tx(&w8_full[s], W8_BYTES);
@@ -246,7 +249,8 @@ k_int8_tiles(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
         }
     __syncwarp();
     if (warp == 0) {
-        for (int i = lane; i <= p.E; i += 32) s_off[i] = p.offsets[i];
+        if (lane <= p.E) s_off[lane] = off;
+        for (int i = lane + 32; i <= p.E; i += 32) s_off[i] = p.offsets[i];
         __syncwarp();
         bound_offsets(s_off, p.E, p.cap_rows);
         count_blocks(s_off, s_blk, p.E, TB);
