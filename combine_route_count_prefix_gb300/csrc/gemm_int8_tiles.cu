@@ -78,7 +78,10 @@ struct Cfg {
     static constexpr int S8 = TB == 64 ? 4 : 3;         // weight stages
     static constexpr int SR = 4;                        // stages of rows as bytes
     static constexpr int kAhead = SA - 1;               // k-blocks widened before a chunk's sums are taken
-    static_assert(SA >= kSets && S8 >= kSets && SR >= kSets, "a set's next block is at most one turn of a ring on");
+    static_assert(SA >= kSets, "a set's next block is at most one turn of a ring on");
+    // What lets a set wait for a copy by its parity: behind ab_empty, and in rings no shorter than that one,
+    // the block before in the slot has been multiplied, so its copy's phase is over and only this block's is open.
+    static_assert(S8 >= SA && (!ROWS8 || SR >= SA), "a copy's phase is over when its stage is asked for again");
     static constexpr int R8_BYTES = TB * BK;
     static constexpr int B_HALF_BYTES = TB * BKH * 2;
     static constexpr int B_BYTES = 2 * B_HALF_BYTES;
@@ -378,8 +381,12 @@ k_int8_tiles(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
         // Widens this set's blocks before number `to` of a tile with rows16 rows.
         auto widen = [&](int to, int rows16) -> bool {
             for (; next < to; next += kSets) {
-                bool w = (!ROWS8 || wait_bounded_inline(&r8_full[sr], phr, abort_flag, p.status)) &&
-                         wait_bounded_inline(&ab_empty[sa], pha ^ 1u, abort_flag, p.status);
+                // ab_empty first: the slot's block before is another set's, and until it has been multiplied its
+                // own rows may still be on their way (copies land in any order), one phase behind, where this
+                // block's parity passes at once.  ab_empty itself cannot be two phases behind: MMAs complete in
+                // order, and this set has seen the block after that one multiplied.
+                bool w = wait_bounded_inline(&ab_empty[sa], pha ^ 1u, abort_flag, p.status) &&
+                         (!ROWS8 || wait_bounded_inline(&r8_full[sr], phr, abort_flag, p.status));
                 if (!__all_sync(kFull, w)) return false;
                 if (ROWS8) {
                     // rows: bytes in ringR -> fp16 in ringB, 128-byte rows of 64 values.  Values 16 u .. go to
