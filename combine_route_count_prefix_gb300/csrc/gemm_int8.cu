@@ -293,7 +293,8 @@ k_int8_few(Int8FewDev p) {
             *a = 0;
             if (ch >= p.N) continue;
             const int64_t r = at.row0 + row, wn = (int64_t)at.e * p.N + ch;
-            const float s = LOCAL ? __fdiv_rn(__uint_as_float(amax[r]), 127.0f) : __ldg(p.qs + r);
+            // (with early, written while this kernel was running already: not for the read-only path)
+            const float s = LOCAL ? __fdiv_rn(__uint_as_float(amax[r]), 127.0f) : __ldcg(p.qs + r);
             float v = __fmul_rn(__fmul_rn(__int2float_rn(sum), __ldg(p.w_scales + wn)), s);
             if (p.bias) v = __fadd_rn(v, __ldg(p.bias + wn));
             if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.c)[r * p.N + ch] = __float2bfloat16_rn(v);

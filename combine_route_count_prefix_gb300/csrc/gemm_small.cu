@@ -197,8 +197,9 @@ __device__ __forceinline__ void epilogue_small(const SmallDev &p, const Tile &t,
         int64_t o = ((int64_t)t.row0 + c0) * p.Nout + ch;
 #pragma unroll
         for (int h = 0; h < EPI_COLS / 32; ++h) {
-            // one load for the scales of 32 rows
-            const float s_lane = 32 * h + lane < n ? __ldg(p.s2 + t.row0 + c0 + 32 * h + lane) : 0.0f;
+            // one load for the scales of 32 rows (written while this kernel was running already: not for the
+            // read-only path)
+            const float s_lane = 32 * h + lane < n ? __ldcg(p.s2 + t.row0 + c0 + 32 * h + lane) : 0.0f;
 #pragma unroll
             for (int i = 0; i < 32; ++i, o += p.Nout) {
                 const float s2 = __shfl_sync(0xffffffffu, s_lane, i);

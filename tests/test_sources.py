@@ -26,3 +26,33 @@ def test_no_load_is_multicast_to_a_cluster():
     for f in SOURCES:
         for copy in bulk_copies(open(f).read()):
             assert "multicast" not in copy, (os.path.basename(f), copy)
+
+
+def function_bodies(text, head):
+    """The bodies of the functions whose text before the brace matches `head`."""
+    for m in re.finditer(head, text):
+        start = at = text.index("{", m.end())
+        depth = 0
+        while True:
+            depth += {"{": 1, "}": -1}.get(text[at], 0)
+            at += 1
+            if depth == 0:
+                break
+        yield text[start:at]
+
+
+def test_row_scales_of_kernels_that_start_early_are_not_read_as_constants():
+    """A kernel that starts before the one that writes its rows' scales has ended may not
+    read them with __ldg, which is for what nobody writes while the kernel runs."""
+    def read(name):
+        return open(os.path.join(ROOT, "combine_route_count_prefix_gb300", "csrc", name)).read()
+
+    early = [b for name, head in (("gemm_int8.cu", r"\nk_int8_few\("), ("gemm_int8_tiles.cu", r"\nk_int8_tiles\("),
+                                  ("few_tokens.cu", r"\nk_few_gate_up\("), ("few_tokens.cu", r"\nk_few_down\("),
+                                  ("gemm_small.cu", r"else if \(EPI == \(int\)Epi::Linear\)"),
+                                  ("gemm_tc.cu", r"else if \(EPI == \(int\)Epi::Linear\)"))
+             for b in function_bodies(read(name), head)]
+    assert len(early) == 6
+    for body in early:
+        assert re.search(r"\b(qs|s2|row_scales)\b", body)
+        assert not re.search(r"__ldg\([^;]*\b(p\.qs|p\.s2|row_scales|s2)\b", body)
