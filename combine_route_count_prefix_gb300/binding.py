@@ -40,7 +40,7 @@ EXPORTED = [
     "moe_add_rms_norm", "moe_gate",
     "moe_grouped_gemm_fp8_workspace_size", "moe_grouped_gemm_fp8",
     "moe_grouped_ffn_fp8_workspace_size", "moe_grouped_ffn_fp8",
-    "moe_layer_few_tokens_workspace_size", "moe_layer_few_tokens",
+    "moe_layer_few_tokens_workspace_size", "moe_layer_few_tokens", "moe_layer_few_tokens_y",
     "moe_int8_packed_bytes", "moe_pack_int8",
     "moe_grouped_gemm_int8_workspace_size", "moe_grouped_gemm_int8",
     "moe_block_norm",
@@ -142,6 +142,7 @@ def lib():
         "moe_grouped_ffn_fp8": [SP, P, P, P, P, P, P, P, P, P, P, SZ, P],
         "moe_layer_few_tokens_workspace_size": [SP, ctypes.POINTER(SZ)],
         "moe_layer_few_tokens": [SP, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
+        "moe_layer_few_tokens_y": [SP, ctypes.c_int, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
         "moe_int8_packed_bytes": [I64, I64, I64, ctypes.c_int, ctypes.POINTER(SZ)],
         "moe_pack_int8": [I64, I64, I64, ctypes.c_int, P, P, P],
         "moe_grouped_gemm_int8_workspace_size": [I64, I64, I64, I64, ctypes.POINTER(SZ)],
@@ -468,10 +469,14 @@ def layer_few_tokens_workspace_size(shape: MoeShape) -> int:
 
 
 def layer_few_tokens(shape: MoeShape, x, expert_ids, expert_scales, w1p, scale1, w2p, scale2,
-                     mask=None, shared=None, ws=None, out=None, stream=None):
+                     mask=None, shared=None, ws=None, out=None, stream=None, y_dtype=torch.bfloat16):
     """moe_layer_few_tokens: :func:`layer` for at most 512 routes (T * K), the
     same results in two to four kernels.  The shape's ffn_path is "small" or
-    "auto", and the weights are packed with it.  Returns (out, workspace)."""
+    "auto", and the weights are packed with it.  y_dtype torch.float32
+    (moe_layer_few_tokens_y) keeps the experts' outputs in fp32 up to the weighted sum,
+    nearer to the formulas, instead of :func:`layer`'s bits.  Returns (out, workspace)."""
+    if y_dtype not in _DTYPES:
+        raise TypeError(f"y_dtype: {y_dtype}, expected torch.float32 or torch.bfloat16")
     T, K, H, E, N = shape.num_tokens, shape.topk, shape.hidden, shape.num_experts, shape.ffn
     dev = x.get_device()
     _check(x, torch.bfloat16, (T, H), "x", dev)
@@ -495,7 +500,10 @@ def layer_few_tokens(shape: MoeShape, x, expert_ids, expert_scales, w1p, scale1,
         _, ws = _alloc_ws(layer_few_tokens_workspace_size(shape), x.device)
     if ws.get_device() != dev:
         _check_device(ws, "ws", dev)
-    _call("moe_layer_few_tokens", shape, x.data_ptr(), expert_ids.data_ptr(),
+    name, choice = "moe_layer_few_tokens", ()
+    if y_dtype is not torch.bfloat16:
+        name, choice = "moe_layer_few_tokens_y", (_DTYPES[y_dtype],)
+    _call(name, shape, *choice, x.data_ptr(), expert_ids.data_ptr(),
           expert_scales.data_ptr(), _addr(mask), _addr(shared), w1p.data_ptr(), scale1.data_ptr(),
           w2p.data_ptr(), scale2.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(),
           _raw_stream(stream, dev))

@@ -134,7 +134,19 @@ moe_status moe_layer_few_tokens(const moe_shape *shape, const void *x, const int
                                 const float *scale1, const void *w2_packed, const float *scale2,
                                 void *x_out, void *workspace, size_t workspace_bytes,
                                 cudaStream_t stream) {
+    return moe_layer_few_tokens_y(shape, MOE_DTYPE_BF16, x, expert_ids, expert_scales, x_active_mask,
+                                  shared_expert_x, w1_packed, scale1, w2_packed, scale2, x_out, workspace,
+                                  workspace_bytes, stream);
+}
+
+moe_status moe_layer_few_tokens_y(const moe_shape *shape, int y_dtype, const void *x,
+                                  const int32_t *expert_ids, const float *expert_scales,
+                                  const uint8_t *x_active_mask, const void *shared_expert_x,
+                                  const void *w1_packed, const float *scale1, const void *w2_packed,
+                                  const float *scale2, void *x_out, void *workspace,
+                                  size_t workspace_bytes, cudaStream_t stream) {
     MOE_TRY(check_few(shape));
+    if (y_dtype != MOE_DTYPE_F32 && y_dtype != MOE_DTYPE_BF16) return MOE_FAIL(MOE_ERR_PARAM_INVALID);
     const moe_shape &s = *shape;
     const bool empty = s.num_tokens == 0;   // the per-token and per-route arrays may then be NULL
     if (!w1_packed || !scale1 || !w2_packed || !scale2 || !workspace) return MOE_FAIL(MOE_ERR_NULLPTR);
@@ -166,6 +178,7 @@ moe_status moe_layer_few_tokens(const moe_shape *shape, const void *x, const int
     a.q = at<int8_t>(workspace, L.q);
     a.qs = at<float>(workspace, L.qs);
     a.status = at<int32_t>(workspace, L.status);
+    a.y_f32 = y_dtype == MOE_DTYPE_F32;
     return launch_layer_few_tokens(s, a, stream);
 }
 

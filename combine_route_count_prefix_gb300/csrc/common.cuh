@@ -347,6 +347,7 @@ struct FewTokensArgs {
     int8_t *q;                 // T * H (rounded up to kAlign) + T * K * N/2 bytes
     float *qs;                 // [T + T*K]
     int32_t *status;
+    bool y_f32;                // an expert's output goes into the weighted sum as it is, not as bf16
 };
 // Product with few rows a group, the weights (biased bytes, [E, N, Kd]) streamed
 // per warp.  rows: bf16 [cap_rows, Kd] to be quantised (only where int8_few_local()),

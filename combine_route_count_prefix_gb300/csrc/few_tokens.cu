@@ -5,7 +5,8 @@
 // same bit for bit (y's rounding to bf16 among them):
 //   q1, s1 = quantised x[t];  h = (float(q1 . W1[e]) * scale1) * s1
 //   g = silu(h_a) * h_b;      q2, s2 = quantised g
-//   y = bf16((float(q2 . W2[e]) * scale2) * s2)
+//   y = bf16((float(q2 . W2[e]) * scale2) * s2), or, where the caller chose it, the
+//   fp32 value itself, so that the output is rounded once
 // ("PTO MegaMoE Dispatch + Combine Fusion Example": GMM1, SwiGLU, GMM2, Unpermute;
 // "aclnnMoeDistributeCombineV4": masks, shared, zero and copy experts.)
 //
@@ -94,7 +95,7 @@ struct FewDev {
     const int8_t *q;           // codes of the rows (not LOCAL): [T, H] or [T*K, Nh]
     const float *qs;           // and their scales
     int32_t *status;
-    int T, K, R, E, Z, C, H, Nh, mask_kind;
+    int T, K, R, E, Z, C, H, Nh, mask_kind, y_f32;
     Divisor by_k, by_units, by_stages1, by_stages2;   // K, Nh / 8, stages of H and of Nh
 };
 
@@ -643,8 +644,10 @@ k_few_down(FewDev p) {
         for (int i = tid; i < sums; i += kThreads) {
             const int at = i / kChannels;
             const float w2s = i == tid ? sc : scale2_of(i, batch);
-            const float y = __bfloat162float(
-                __float2bfloat16_rn(__fmul_rn(__fmul_rn(__int2float_rn(a[i]), w2s), scale[at])));
+            float y = __fmul_rn(__fmul_rn(__int2float_rn(a[i]), w2s), scale[at]);
+            // the layer's other kernels hand y over in memory, as bf16: rounded here too unless told
+            // otherwise, so that prefill and decoding agree (against 64 bits 2.4e-3 off, without 1.65e-3)
+            if (!p.y_f32) y = __bfloat162float(__float2bfloat16_rn(y));
             a[i] = __float_as_int(__fmul_rn(probs[r.list[at]], y));
         }
         __syncthreads();
@@ -821,6 +824,7 @@ moe_status launch_layer_few_tokens(const moe_shape &s, const FewTokensArgs &a, c
     p.H = (int)H;
     p.Nh = (int)Nh;
     p.mask_kind = s.mask_kind;
+    p.y_f32 = a.y_f32;
     p.by_k = Divisor((uint32_t)K);
     p.by_units = Divisor((uint32_t)(Nh / 8));
     p.by_stages1 = Divisor((uint32_t)(padded((int)H) / kDepth));

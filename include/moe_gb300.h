@@ -298,6 +298,16 @@ moe_status moe_layer_few_tokens(const moe_shape *shape, const void *x, const int
                                 const float *scale1, const void *w2_packed, const float *scale2,
                                 void *x_out, void *workspace, size_t workspace_bytes,
                                 cudaStream_t stream);
+/* The same with a choice of what an expert's output y is before the weighted sum:
+ * y_dtype MOE_DTYPE_BF16, rounded to bf16 as moe_layer's is (moe_layer_few_tokens), or
+ * MOE_DTYPE_F32, kept in fp32, so that the output is rounded once: nearer to the
+ * formulas, for a caller who does not need moe_layer's bits.  Same workspace, same time. */
+moe_status moe_layer_few_tokens_y(const moe_shape *shape, int y_dtype, const void *x,
+                                  const int32_t *expert_ids, const float *expert_scales,
+                                  const uint8_t *x_active_mask, const void *shared_expert_x,
+                                  const void *w1_packed, const float *scale1, const void *w2_packed,
+                                  const float *scale2, void *x_out, void *workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
 
 /* Device pointers into a workspace used by moe_layer or moe_grouped_ffn, for
  * inspection of the intermediate stages after the stream has finished.  Any
