@@ -294,7 +294,8 @@ def _own_layer(s):
     from combine_route_count_prefix_gb300 import binding as B
     out, s["ws"] = B.layer_few_tokens(s["shape"], s["x"], s["ids"], s["probs"], s["w1"],
                                       s["scale1"], s["w2"], s["scale2"], mask=s["mask"],
-                                      shared=s["shared"], ws=s.get("ws"), out=s["out"])
+                                      shared=s["shared"], ws=s.get("ws"), out=s["out"],
+                                      y_dtype=torch.float32)      # rounded once, as the operator is stated
     return out
 
 
