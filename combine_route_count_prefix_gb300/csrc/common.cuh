@@ -330,7 +330,7 @@ moe_status launch_grouped_gemm_small(Epi epi, const GemmArgs &a, cudaStream_t st
 
 // ---------------------------------------------------------------- a few tokens
 // Rows [rows, n] in bf16 or fp32 -> int8 codes and one scale a row.  nan_scale (bf16): a
-// NaN makes its row's scale NaN, else it stays out of it.
+// NaN or an infinity makes its row's scale NaN; else a NaN stays out of it.
 moe_status launch_quant_rows_i8(const void *src, bool bf16, bool nan_scale, int64_t rows, int64_t n,
                                 int8_t *q, float *scales, cudaStream_t stream);
 // The whole layer for at most MOE_FEW_TOKENS_MAX_ROUTES routes.

@@ -675,7 +675,8 @@ k_few_down(FewDev p) {
 
 // ---------------------------------------------------------------- codes of rows, once for all CTAs
 // bf16 or fp32 rows -> int8 codes and scales, a CTA a row.  A NaN stays out of its
-// row's maximum, as in the layer's other kernels, or (NAN_SCALE) makes the scale NaN.
+// row's maximum, as in the layer's other kernels, or (NAN_SCALE) it and an infinity make
+// the scale NaN.
 template <typename T, bool NAN_SCALE>
 __global__ void __launch_bounds__(kQuantThreads)
 k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, float *__restrict__ s_out) {
@@ -730,7 +731,7 @@ k_quant_rows_i8(const T *__restrict__ src, int64_t n, int8_t *__restrict__ q, fl
 #pragma unroll
     for (int w = 0; w < kQuantThreads / 32; ++w)
         m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(part[w])));
-    const float s = __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
+    const float s = NAN_SCALE ? strict_scale(__float_as_uint(m)) : __fdiv_rn(m, 127.0f), rs = __frcp_rn(s);
     uint2 *out = reinterpret_cast<uint2 *>(q + row * n);
 #pragma unroll
     for (int u = 0; u < kOwn; ++u) {

@@ -61,8 +61,7 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
         f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
-// The largest magnitude as bits; a NaN counts above all, so that it makes its row's
-// scale, and with it the row's outputs, NaN.
+// The largest magnitude as bits; a NaN counts above all (strict_scale).
 __device__ __forceinline__ uint32_t max8(const float (&f)[8], uint32_t m) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
@@ -241,7 +240,7 @@ k_int8_few(Int8FewDev p) {
         }
         __syncthreads();
         if (xt < p.cap_rows) {
-            const float s = __fdiv_rn(__uint_as_float(amax[xt]), 127.0f), rs = __frcp_rn(s);
+            const float s = strict_scale(amax[xt]), rs = __frcp_rn(s);
             auto put = [&](int i, uint2 q) {
                 *reinterpret_cast<uint2 *>(codes + (size_t)xt * pitch + (i >> 4) * kDepth +
                                            unit_at(xt, (i >> 1) & 7) + (i & 1) * 8) = q;
@@ -294,7 +293,7 @@ k_int8_few(Int8FewDev p) {
             if (ch >= p.N) continue;
             const int64_t r = at.row0 + row, wn = (int64_t)at.e * p.N + ch;
             // (with early, written while this kernel was running already: not for the read-only path)
-            const float s = LOCAL ? __fdiv_rn(__uint_as_float(amax[r]), 127.0f) : __ldcg(p.qs + r);
+            const float s = LOCAL ? strict_scale(amax[r]) : __ldcg(p.qs + r);
             float v = __fmul_rn(__fmul_rn(__int2float_rn(sum), __ldg(p.w_scales + wn)), s);
             if (p.bias) v = __fadd_rn(v, __ldg(p.bias + wn));
             if (p.out_bf16) static_cast<__nv_bfloat16 *>(p.c)[r * p.N + ch] = __float2bfloat16_rn(v);
@@ -346,7 +345,7 @@ k_rows_to_f16(const void *__restrict__ rows, const float *__restrict__ scales,
             __syncthreads();
 #pragma unroll
             for (int w = 0; w < kImgThreads / 32; ++w) m = max(m, part[w]);
-            const float s = __fdiv_rn(__uint_as_float(m), 127.0f), rs = __frcp_rn(s);
+            const float s = strict_scale(m), rs = __frcp_rn(s);
             auto put = [&](int i, const uint4 &x) {
                 float v[8], c[8];
                 unpack8(x, v);

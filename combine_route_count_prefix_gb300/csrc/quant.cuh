@@ -93,4 +93,11 @@ __device__ __forceinline__ uint2 quant8(const float (&v)[8], float s, float rs) 
                       __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410));
 }
 
+// The scale of a row whose largest magnitude has the bits `m`, where one that is no number
+// has to show: NaN for an infinity too, whose own quotient is none.  (Left infinite it
+// would make the infinity's code -127 and the row's outputs infinite, of either sign.)
+__device__ __forceinline__ float strict_scale(uint32_t m) {
+    return __fdiv_rn(__uint_as_float(m >= 0x7f800000u ? 0x7fffffffu : m), 127.0f);
+}
+
 }  // namespace moe

@@ -550,8 +550,8 @@ moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
  * A               int8 [rows, Kd] (MOE_DTYPE_I8) with a_scales fp32 [rows]: q and s;
  *                 or bf16 [rows, Kd] (MOE_DTYPE_BF16) with a_scales NULL: each row is
  *                 quantised in the call, s = max|a| / 127, q = clamp(rint(a / s), -127,
- *                 127), q = 0 where s = 0, in fp32 with IEEE rounding; a NaN makes its
- *                 row's s and outputs NaN
+ *                 127), q = 0 where s = 0, in fp32 with IEEE rounding; a NaN or an
+ *                 infinity makes its row's s and outputs NaN
  * w_packed        from moe_pack_int8 with the same E, N, Kd and path
  * w_scales        fp32 [E, N]; bias fp32 [E, N] or NULL
  * C               [rows, N] in out_dtype (MOE_DTYPE_F32 or MOE_DTYPE_BF16); rows
