@@ -100,15 +100,6 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
             smem_u32(bar))
         : "memory");
 }
-// Arrives once on the barrier at `bar`'s offset in every CTA of `cta_mask` when all
-// earlier MMAs of this thread have completed.
-__device__ __forceinline__ void mma_commit_all(uint64_t *bar, uint16_t cta_mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"(cta_mask)
-        : "memory");
-}
 // CTA-pair (cta_group::2) forms: a 256-row MMA whose A rows and B columns are
 // split between the two CTAs of a cluster pair, each CTA holding its half at
 // the same shared-memory offsets and its 128 accumulator rows in its own TMEM.

@@ -56,3 +56,14 @@ def test_row_scales_of_kernels_that_start_early_are_not_read_as_constants():
     for body in early:
         assert re.search(r"\b(qs|s2|row_scales)\b", body)
         assert not re.search(r"__ldg\([^;]*\b(p\.qs|p\.s2|row_scales|s2)\b", body)
+
+
+def test_nothing_in_the_sources_is_without_a_user():
+    """Device functions, constants and macros that only their definition names."""
+    text = re.sub(r"//[^\n]*", "", "\n".join(open(f).read() for f in SOURCES))
+    names = set()
+    for pattern in (r"__device__\s+(?:__forceinline__|__noinline__|inline)\s+[\w:<> ]+?[\s&*](\w+)\s*\(",
+                    r"constexpr\s+[\w:<> ]+?\s(\w+)\s*[=({]", r"#define\s+(\w+)"):
+        names.update(re.findall(pattern, text))
+    assert len(names) > 200
+    assert [n for n in sorted(names - {"operator"}) if len(re.findall(rf"\b{n}\b", text)) < 2] == []
