@@ -51,9 +51,10 @@ __device__ __forceinline__ void load_weight(const void *w, int i, float (&f)[8])
     }
 }
 
-// 1 / (1 + exp(-g)), the hardware's exponential and reciprocal (each within two
-// units in the last place, the argument rounded once): relative error about
-// 1e-7 (2 + |g|), beside bf16 gates that stand for 4e-3 of themselves.
+// 1 / (1 + exp(-g)), the hardware's exponential and reciprocal.  Relative error at most
+// 2^-22 of the exponential, 2^-24 of the sum and 2^-23 of the reciprocal, and |g| (2^-24 +
+// 2^-25) of the exponential's argument, rounded once from a rounded factor: 4.2e-7 + 0.9e-7
+// |g|, beside bf16 gates that stand for 4e-3 of themselves.
 __device__ __forceinline__ float sigmoid(float g) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));

@@ -440,8 +440,9 @@ moe_status moe_add_rms_norm(int64_t num_tokens, int64_t hidden, const void *x,
  * post_weight     [H] in weight_dtype, or NULL
  * gate            bf16 [gate_rows, H], rows gate_stride elements apart, or NULL: one
  *                 row for all tokens, one a token, or one for each T / gate_rows
- *                 consecutive tokens.  MOE_GATE_ACT_SIGMOID: 1 / (1 + exp(-gate)),
- *                 exponential and quotient within a few units in the last place.
+ *                 consecutive tokens.  MOE_GATE_ACT_SIGMOID: 1 / (1 + exp(-gate)) with a
+ *                 relative error of at most 5e-7 + 1e-7 |gate|; 0 where that is below
+ *                 fp32's normal numbers.
  * weight          [H] in weight_dtype; may be NULL when y and q are
  * residual_out    bf16 [T, H]; may be the residual buffer itself, else overlaps no
  *                 input
