@@ -692,7 +692,7 @@ def block_norm(x, residual, weight=None, post_weight=None, gate=None, gate_act="
         rows = gate.shape[0]
         if gate.dtype is not torch.bfloat16:
             raise TypeError(f"gate: dtype {gate.dtype}, expected torch.bfloat16")
-        if gate.dim() != 2 or gate.shape[1] != H or gate.stride(1) != 1 or (rows == 0) != (T == 0):
+        if gate.dim() != 2 or gate.shape[1] != H or gate.stride(1) != 1 or (rows == 0 and T > 0):
             raise ValueError(f"gate: shape {tuple(gate.shape)}, expected [rows, {H}] with contiguous rows")
         if gate.get_device() != dev:
             _check_device(gate, "gate", dev)

@@ -1,0 +1,25 @@
+"""block_norm's gates (tensors that only report where they are, nothing is launched)."""
+import pytest
+
+from test_devices import BF, t
+from test_devices import B as fake  # noqa: F401  (a binding that launches nothing)
+from test_int8_refusals import call, gate, norm_args
+
+
+def args(T, G):
+    kw = dict(norm_args(), gate=gate(G, 256), x=t(T, 256, dtype=BF), residual=t(T, 256, dtype=BF))
+    kw["out"] = dict(residual_out=t(T, 256, dtype=BF))
+    return kw
+
+
+@pytest.mark.parametrize("T,G", [(0, 0), (0, 1), (0, 3), (4, 1), (4, 4)])
+def test_gates_of_a_batch(fake, T, G):  # noqa: F811
+    """A batch may be empty whatever the gate's rows."""
+    call(fake, "block_norm", args(T, G))
+    assert fake.called == ["moe_block_norm"]
+
+
+def test_tokens_need_a_gate_row(fake):  # noqa: F811
+    with pytest.raises(ValueError, match="gate"):
+        call(fake, "block_norm", args(4, 0))
+    assert not fake.called
