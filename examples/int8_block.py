@@ -8,7 +8,8 @@ builds random weights, runs the block and prints its time per call, for T
 tokens and for one.  The functions below are what a model would call:
 `quantise_weights` once when the weights are loaded, `Int8Block.__call__` in
 every step.  Steps of a few tokens take the few-token layer, whose results are
-those of the whole layer bit for bit, from the same packed weights.
+those of the whole layer bit for bit, from the same packed weights.  Nothing is kept
+per length, so that a call of any length can be captured in a graph.
 """
 import argparse
 import os
@@ -41,7 +42,6 @@ class Int8Block:
         self.post_weight, self.weight, self.next_weight, self.gate = post_weight, weight, next_weight, gate
         self.router = router
         self.E, self.N, self.H = w1.shape
-        self.offsets = {}
         self.o_owner, self.o_packed = B.pack_int8(o_proj)
         shape = B.make_shape(1, 1, self.H, self.E, topk, self.N, ffn_path="auto")
         (self.w1_owner, self.w1), (self.w2_owner, self.w2) = B.pack_weights(shape, w1, w2)
@@ -51,9 +51,8 @@ class Int8Block:
         Returns the new residual stream and the next block's input, bf16 [T, H].
         `stages`, a dict, collects the intermediate tensors."""
         T = attention.shape[0]
-        if T not in self.offsets:       # one group of T rows
-            self.offsets[T] = torch.tensor([0, T], dtype=torch.int32, device=attention.device)
-        o, _ = B.grouped_gemm_int8(self.offsets[T], attention, self.o_packed, self.o_scale)
+        one_group = torch.linspace(0, T, 2, dtype=torch.int32, device=attention.device)      # [0, T], on the GPU
+        o, _ = B.grouped_gemm_int8(one_group, attention, self.o_packed, self.o_scale)
         n = B.block_norm(o, residual, self.weight, post_weight=self.post_weight, gate=self.gate,
                          gate_act="sigmoid", with_q=False)
         logits = n["y"].float() @ self.router.t()
