@@ -21,6 +21,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from combine_route_count_prefix_gb300 import binding as B  # noqa: E402
 
 FEW_ROUTES = 512         # what moe_layer_few_tokens takes
+FEW_PER_EXPERT = 16      # above so many routes an expert, on average, the whole layer is faster
 
 
 def quantise_weights(w):
@@ -58,7 +59,8 @@ class Int8Block:
         logits = n["y"].float() @ self.router.t()
         r = B.gate(logits, self.topk, mask=mask)
         shape = B.make_shape(T, 1, self.H, self.E, self.topk, self.N, mask_kind=2, ffn_path="auto")
-        layer = B.layer_few_tokens if T * self.topk <= FEW_ROUTES else B.layer
+        few = T * self.topk <= min(FEW_ROUTES, FEW_PER_EXPERT * self.E)
+        layer = B.layer_few_tokens if few else B.layer
         y, _ = layer(shape, n["y"], r["expert_ids"], r["expert_scales"], self.w1, self.scale1, self.w2,
                      self.scale2, mask=r["route_mask"])
         out = B.block_norm(y, n["residual_out"], self.next_weight, with_q=False)

@@ -1,5 +1,5 @@
 """Calls of the int8 block of examples/ that its documentation allows: a length first met in a
-graph's capture, no tokens."""
+graph's capture, no tokens, and which layer a call takes."""
 import pytest
 import torch
 
@@ -37,3 +37,18 @@ def test_no_tokens(ex):  # noqa: F811
     block = ex.random_block(512, 512, 16, 4, 512, seed=7)
     for v in block(*inputs(0, 512, 512, 0)[:2]):
         assert v.shape == (0, 512)
+
+
+@pytest.mark.parametrize("T,E,K,few", [(1, 16, 4, True), (64, 16, 4, True), (65, 16, 4, False), (128, 64, 4, True),
+                                       (129, 64, 4, False)])
+def test_the_layer_that_is_faster(ex, T, E, K, few, monkeypatch):  # noqa: F811
+    """The few-token layer up to its 512 routes, and up to 16 an expert."""
+    block = ex.random_block(512, 512, E, K, 256, seed=7)
+    used = []
+    for name in ("layer", "layer_few_tokens"):
+        def wrap(*a, name=name, real=getattr(ex.B, name), **kw):
+            used.append(name)
+            return real(*a, **kw)
+        monkeypatch.setattr(ex.B, name, wrap)
+    block(*inputs(T, 512, 512, 0)[:2])
+    assert used == ["layer_few_tokens" if few else "layer"]
