@@ -54,6 +54,7 @@ bool has_bytes(int path) { return path == MOE_FFN_PATH_SMALL || path == MOE_FFN_
 size_t image_bytes(int64_t E, int64_t N, int64_t Kd) { return align_up((size_t)E * N * Kd * 2, kAlign); }
 
 constexpr int64_t kMaxDepth = 131056;     // products of 2^14 at most: sums below 2^31
+constexpr int64_t kMaxRows = INT32_MAX - 255;   // the end of a tile of 256 rows is a 32-bit number too
 moe_status check_int8(int64_t E, int64_t N, int64_t Kd) {
     if (E < 1 || E > kMaxExperts || N < 8 || N % 8 != 0 || N > (1 << 20) || Kd < 16 || Kd % 16 != 0 ||
         Kd > kMaxDepth)
@@ -207,7 +208,7 @@ moe_status moe_grouped_gemm_int8_workspace_size(int64_t rows, int64_t E, int64_t
                                                 size_t *bytes) {
     if (!bytes) return MOE_FAIL(MOE_ERR_NULLPTR);
     MOE_TRY(check_int8(E, N, Kd));
-    if (rows < 0 || rows > INT32_MAX || rows * Kd >= (int64_t)1 << 40) return MOE_FAIL(MOE_ERR_SHAPE);
+    if (rows < 0 || rows > kMaxRows || rows * Kd >= (int64_t)1 << 40) return MOE_FAIL(MOE_ERR_SHAPE);
     *bytes = int8_layout(rows, Kd).total;
     return MOE_OK;
 }

@@ -561,7 +561,7 @@ moe_status moe_grouped_gemm_fp8(int64_t rows, int64_t E, int64_t N, int64_t Kd,
  *                 nearest that are, the last one before all (no call reaches behind
  *                 its arrays for them)
  * N % 8 == 0, N <= 1048576, Kd % 16 == 0, 16 <= Kd <= 131056 (any int8 codes' sum
- * fits 32 bits), rows * Kd < 2^40.
+ * fits 32 bits), rows <= 2^31 - 256, rows * Kd < 2^40.
  * path: MOE_FFN_PATH_* as in moe_shape.  moe_pack_int8 writes w int8 [E, N, Kd] as
  * fp16 images (LARGE, LARGE_PAIR; 2 bytes a weight), as biased bytes (SMALL; 1
  * byte) or both (AUTO; 3 bytes, the call picks by its rows). */
