@@ -715,8 +715,9 @@ def block_norm(x, residual, weight=None, post_weight=None, gate=None, gate_act="
         if v is not None and (v.dtype is not torch.bfloat16 or v.shape != shape or
                               not v.is_contiguous() or v.get_device() != dev):
             _check(v, torch.bfloat16, shape, name, dev)
-    desc = _block_norm_desc(T, H, rows, stride, dtype, gate_act, float(residual_scale),
-                            float(branch_scale), float(eps))
+    # 0.0 and -0.0 are one key to the cache, but not to the sums' signs
+    make = _block_norm_desc if residual_scale and branch_scale else _block_norm_desc.__wrapped__
+    desc = make(T, H, rows, stride, dtype, gate_act, float(residual_scale), float(branch_scale), float(eps))
     _call("moe_block_norm", desc, x.data_ptr(), residual.data_ptr(), _addr(post_weight), _addr(gate),
           _addr(weight), out["residual_out"].data_ptr(), _addr(y), _addr(out.get("q")),
           _addr(out.get("scales")), _raw_stream(stream, dev))

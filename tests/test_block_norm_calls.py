@@ -1,4 +1,6 @@
-"""block_norm's gates (tensors that only report where they are, nothing is launched)."""
+"""block_norm's gates and factors (tensors that only report where they are, nothing is launched)."""
+import math
+
 import pytest
 
 from test_devices import BF, t
@@ -23,3 +25,12 @@ def test_tokens_need_a_gate_row(fake):  # noqa: F811
     with pytest.raises(ValueError, match="gate"):
         call(fake, "block_norm", args(4, 0))
     assert not fake.called
+
+
+@pytest.mark.parametrize("name", ["residual_scale", "branch_scale"])
+def test_zeros_of_either_sign_reach_the_call(fake, name, monkeypatch):  # noqa: F811
+    seen = []
+    monkeypatch.setattr(fake, "_call", lambda entry, desc, *a: seen.append(math.copysign(1.0, getattr(desc, name))))
+    for v in (0.0, -0.0, 0.0, -0.0):
+        call(fake, "block_norm", dict(args(4, 1), **{name: v}))
+    assert seen == [1.0, -1.0, 1.0, -1.0]
