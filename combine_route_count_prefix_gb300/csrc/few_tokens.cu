@@ -23,9 +23,10 @@
 //                  expert and route, so the weighted sum needs no other CTA.
 // Every CTA finds the experts' rows from expert_ids by itself: up to 32 routes by
 // one warp's votes, up to 512 by counts and sums.
-// With one or two tokens the CTAs also quantise by themselves (LOCAL): the tokens
-// from registers that are loaded before the routes are known, g a row to a warp.
-// Otherwise a small kernel before each product quantises the rows once, and the codes
+// With few and short rows the CTAs also quantise by themselves (LOCAL): the tokens, each
+// in the registers of its share of the eight warps (one token of any width, two up to 7168,
+// four to 3584, eight to 1792), loaded before the routes are known; g, of 16384 values at
+// most, a row to a warp.  Otherwise a small kernel before each product quantises the rows once, and the codes
 // travel through the rings with the weights.
 //
 // Measured, 128 experts, top-8, in a graph (us, moe_layer's small-batch path, the

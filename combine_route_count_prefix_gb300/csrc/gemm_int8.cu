@@ -9,8 +9,10 @@
 // units.  Reading the weights bounds it up to about 8 rows a group, and beyond that the
 // widening of the rows and the mma (products) and the rows' stores.
 // Rows come with the weights through the rings, or, LOCAL, are quantised from
-// bf16 by every CTA into its own memory (one or two rows of one group; more take a
-// kernel before: 4096 x 7168, 8 rows, 22 us in every CTA, 10.5 with it).
+// bf16 by every CTA into its own memory: up to 8 rows of one group, each of which fits the
+// registers of its share of the twelve warps (one row up to a depth of 15360, two to
+// 7680, four to 3840, eight to 1280).  The others take a kernel before (4096 x 7168, 8 rows,
+// 22 us in every CTA, 10.5 with it).
 // One bf16 row (us, of which the weights at the HBM rate): 4096 x 7168 7.0 (4.3), 7168 x
 // 2048 4.8 (2.2), 1536 x 2048 4.0 (0.5); one int8 row 6.8, 4.6, 3.0; 16 bf16 rows 12.0, 8.0, 5.9.
 #include "common.cuh"

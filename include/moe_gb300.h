@@ -278,8 +278,8 @@ moe_status moe_layer(const moe_shape *shape, const void *x, const int32_t *exper
                      void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* The whole layer for a few tokens: moe_layer's arguments and, for finite
- * inputs and scales, its results bit for bit, in two kernels (four with more
- * than a token or two) and without its workspace's row images.  For the steps of a
+ * inputs and scales, its results bit for bit, in two kernels (one token; up to eight of
+ * small shapes) or four, and without its workspace's row images.  For the steps of a
  * decoding batch, where the time is that of reading the chosen experts' weights;
  * with more than about 16 routes an expert moe_layer is faster.
  *   - T * K <= MOE_FEW_TOKENS_MAX_ROUTES; more return MOE_ERR_SHAPE.
