@@ -160,6 +160,15 @@ Layout layout_for(const moe_shape &s, Op op);
 __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
     return __uint_as_float(((uint32_t)b) << 16);
 }
+// Eight bf16 values -> fp32.
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
 __device__ __forceinline__ uint32_t lanemask_lt() {
     uint32_t m;
     asm("mov.u32 %0, %%lanemask_lt;" : "=r"(m));

@@ -55,14 +55,6 @@ struct Cfg {
     static constexpr int kMaxRows = NB * kRows;
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
 // The largest magnitude as bits; a NaN counts above all (strict_scale).
 __device__ __forceinline__ uint32_t max8(const float (&f)[8], uint32_t m) {
 #pragma unroll

@@ -153,11 +153,6 @@ __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, vol
         }
     }
 }
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
 // 16 bytes into a cluster CTA's shared memory, counted by the barrier there.  Only in
 // launches with a cluster: without one it is an illegal instruction.
 __device__ __forceinline__ void store_part(uint32_t addr, int32_t a, int32_t b, int32_t c, int32_t d, uint32_t bar) {

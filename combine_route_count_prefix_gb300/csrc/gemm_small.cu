@@ -286,21 +286,7 @@ k_gemm_small(const __grid_constant__ CUtensorMap tmRows, const __grid_constant__
     __syncthreads();
     if (warp == 0) {
         if (EPI == (int)Epi::Linear) bound_offsets(s_off, p.E, p.cap_rows);
-        // s_sched[e] = TB-row blocks of the experts before e (warp scan)
-        int carry = 0;
-        for (int base = 0; base < p.E; base += 32) {
-            const int e = base + lane;
-            const int c = e < p.E ? (s_off[e + 1] - s_off[e] + TB - 1) / TB : 0;
-            int x = c;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += y;
-            }
-            if (e < p.E) s_sched[e] = carry + x - c;
-            carry += __shfl_sync(0xffffffffu, x, 31);
-        }
-        if (lane == 0) s_sched[p.E] = carry;
+        count_blocks(s_off, s_sched, p.E, TB);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, TMEM_COLS);

@@ -524,21 +524,7 @@ k_grouped_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     __syncthreads();
     if (warp == 0) {
         if (EPI == (int)Epi::Linear) bound_offsets(s_off, p.E, p.cap_rows);
-        // s_psched[e] = 256-row blocks of the experts before e (warp scan)
-        int carry = 0;
-        for (int base = 0; base < p.E; base += 32) {
-            const int e = base + lane;
-            const int c = e < p.E ? (s_off[e + 1] - s_off[e] + 2 * BM - 1) / (2 * BM) : 0;
-            int x = c;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += y;
-            }
-            if (e < p.E) s_psched[e] = carry + x - c;
-            carry += __shfl_sync(0xffffffffu, x, 31);
-        }
-        if (lane == 0) s_psched[p.E] = carry;
+        count_blocks(s_off, s_psched, p.E, 2 * BM);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, TMEM_COLS);
@@ -754,9 +740,9 @@ GemmDev gemm_dev(const GemmArgs &a) {
     d.scale2 = a.scale2;
     d.s2 = a.s2;
     d.status = a.status;
-    // 32-byte stores need every y row to start on a 32-byte boundary
     d.bias = a.bias;
     d.y32 = a.y_f32 ? static_cast<float *>(a.y) : nullptr;
+    // 32-byte stores need every y row to start on a 32-byte boundary
     d.y_vec32 = a.y != nullptr && ((uintptr_t)a.y % 32) == 0 && ((a.Nout * 2) % 32) == 0;
     return d;
 }

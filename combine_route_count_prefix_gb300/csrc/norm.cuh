@@ -1,4 +1,4 @@
-// norm.cuh -- what the two norm kernels share: bf16 vectors, a sum over the CTA.
+// norm.cuh -- what the two norm kernels share: packed bf16 vectors, a sum over the CTA.
 #pragma once
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -9,14 +9,6 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kF32Max = 3.402823466e38f;
 constexpr int kNormMaxThreads = 512;
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);

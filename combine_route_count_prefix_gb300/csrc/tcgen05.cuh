@@ -46,9 +46,7 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
 }
 // shared::cluster address of the object at `p`'s offset in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
+    return map_rank(smem_u32(p), rank);
 }
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
