@@ -26,8 +26,8 @@
 // With few and short rows the CTAs also quantise by themselves (LOCAL): the tokens, each
 // in the registers of its share of the eight warps (one token of any width, two up to 7168,
 // four to 3584, eight to 1792), loaded before the routes are known; g, of 16384 values at
-// most, a row to a warp.  Otherwise a small kernel before each product quantises the rows once, and the codes
-// travel through the rings with the weights.
+// most, a row to a warp.  Otherwise a small kernel before each product quantises the rows
+// once, and the codes travel through the rings with the weights.
 //
 // Measured, 128 experts, top-8, in a graph (us, moe_layer's small-batch path, the
 // weights at the HBM rate), slower and faster boxes 5 % apart:
